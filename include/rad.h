@@ -291,6 +291,169 @@ int rad_kv_quant_i8(const uint16_t *x, int8_t *codes, uint16_t *scale, int64_t r
 int rad_kv_dequant_i8(const int8_t *codes, const uint16_t *scale, uint16_t *y, int64_t rows,
                       int64_t D, rad_stream_t stream);
 
+/* Value types of the calls below. */
+enum rad_dtype { RAD_DT_F32 = 0, RAD_DT_BF16 = 1, RAD_DT_F16 = 2 };
+
+/*
+ * rad_add_rmsnorm_quant_i8 -- the step in front of a linear of this library:
+ * add a sublayer's output to the residual stream, normalise, rotate, quantise.
+ *
+ *   x             [M][K] of `dtype`, 16-byte aligned.
+ *   residual      [M][K] of `dtype`, 16-byte aligned, or NULL (x is normalised alone).
+ *   residual_out  [M][K] of `dtype`, 16-byte aligned; may be `residual` itself (in
+ *                 place).  NULL exactly when residual is NULL.
+ *   gamma         f32 [K], 16-byte aligned.
+ *   eps           >= 0, finite.
+ *   q, scale      int8 [M][K] (16-byte aligned) and f32 [M] outputs, what the
+ *                 contraction calls take.
+ *   rotate        1: rotated as by rad_fwht128; 0: not.
+ *   M >= 0; K > 0, K % 128 == 0, K <= RAD_QUANT_MAX_K.
+ *
+ * Per token: h = residual + x (f32 sum rounded to `dtype`, stored to
+ * residual_out and used as stored; h = x without a residual);
+ * r = 1 / sqrt(mean(h^2) + eps); n = (h * r) * gamma in f32; then codes and
+ * scale of n exactly as rad_quant_act_i8 gives them.  The f32 sum of squares
+ * has an unspecified (but fixed) order.  An all-zero row gives scale 0 and
+ * zero codes when eps > 0.
+ *
+ * Errors: RAD_E_FMT (unknown dtype), RAD_E_SHAPE, RAD_E_RANGE (K, M, eps or
+ * rotate), RAD_E_NULL (residual without residual_out or the reverse among
+ * them), RAD_E_ALIGN, RAD_E_ALIAS (any overlap but residual_out == residual).
+ */
+int rad_add_rmsnorm_quant_i8(const void *x, const void *residual, void *residual_out, const float *gamma,
+                             float eps, int8_t *q, float *scale, int64_t M, int64_t K, int32_t dtype,
+                             int rotate, rad_stream_t stream);
+
+/*
+ * A paged attention cache in 4 bits.  A page holds page_size consecutive tokens
+ * of one sequence for every KV head.  A head's vector of D values is kept as
+ * e2m1 codes (sign bit 3, then levels 0, 0.5, 1, 1.5, 2, 3, 4, 6) under one
+ * f16 scale per (token, head): value = level * scale.  Keys lie row by row;
+ * values lie in octets of tokens, so that a 32-bit word holds one dimension of
+ * eight tokens, the order in which the matrix cores take them:
+ *
+ *   k_codes  uint8 [pages][heads][page_size][D/2]       byte j: dims 2j (low nibble), 2j + 1
+ *   v_codes  uint8 [pages][heads][page_size/8][D][4]    byte j: tokens 2j (low nibble), 2j + 1 of the octet
+ *   k_scale, v_scale  f16 bits [pages][heads][page_size]
+ *
+ * All four 16-byte aligned; D is 64, 128 or 256; page_size is 32, 64, 128 or
+ * 256; pages, heads >= 1, heads <= 1024, pages < 2^31.  Fresh memory needs no
+ * clearing: nothing past a sequence's length is used.
+ */
+typedef struct rad_kv4_cache {
+    uint8_t *k_codes;
+    uint16_t *k_scale;
+    uint8_t *v_codes;
+    uint16_t *v_scale;
+    int64_t pages, heads, page_size, D;
+} rad_kv4_cache;
+
+/*
+ * Which tokens a call is about: a ragged batch of B sequences.  All arrays are
+ * device memory, 4-byte aligned, and are read by the kernels, so a captured
+ * graph follows new contents.
+ *
+ *   block_table  int32 [B][max_pages]: the page that holds tokens j * page_size ..
+ *                of sequence b.  An entry outside 0 .. pages - 1 is an absent page:
+ *                nothing is appended to it and attention does not see its tokens.
+ *   seq_len      int32 [B]: tokens of the sequence, the call's own among them
+ *                (read as clamped to 0 .. max_pages * page_size).
+ *   q_start      int32 [B + 1], ascending: rows q_start[b] .. q_start[b + 1] - 1 of the
+ *                call's row arrays are the last tokens of sequence b, in order; rows
+ *                from q_start[B] on are padding and are left as they were.  A row whose
+ *                position would be negative is no token: it is not appended, and
+ *                attention gives zeros for it.  NULL: one row per sequence (rows == B).
+ *   rows         rows of the call's row arrays; B, rows, max_pages >= 0.
+ *   max_q        no sequence has more rows than this (1 when q_start is NULL); later
+ *                rows of a longer one are left as they were by rad_attn_kv4.
+ *
+ * Limits: B, rows < 2^24; max_pages * page_size < 2^30.
+ */
+typedef struct rad_kv_batch {
+    const int32_t *block_table;
+    const int32_t *seq_len;
+    const int32_t *q_start;
+    int64_t B, max_pages, rows, max_q;
+} rad_kv_batch;
+
+/*
+ * Rotary angles by table: f32 [rows][dim], 16-byte aligned; row p holds dim / 2
+ * cosines, then dim / 2 sines, of position p.  dim is a multiple of 8, 8 <= dim
+ * <= D; the first dim values of a head are turned, the others kept.  style 0
+ * pairs values d and d + dim / 2, style 1 values 2d and 2d + 1.  Tokens at
+ * positions from `rows` on are skipped like rows that are no token.
+ */
+typedef struct rad_rope {
+    const float *table;
+    int64_t rows;
+    int32_t dim, style;
+} rad_rope;
+
+/*
+ * rad_kv4_append -- append a batch's new keys and values to the paged cache,
+ * with the position rotation and the 128-point rotation on the way, and turn
+ * the queries alike.
+ *
+ *   k, v      [rows][heads][D] of `dtype`; token rows ldk and ldv values apart (>= heads
+ *             * D), so that they can be columns of one projection's output; 16-byte
+ *             aligned, as is each row.
+ *   q         [rows][q_heads][D] of `dtype`, rows ldq apart, or NULL (then q_out is NULL
+ *             and q_heads and ldq are 0).
+ *   q_out     [rows][q_heads][D] of `dtype`, dense, 16-byte aligned.
+ *   rope      NULL: no position rotation.
+ *   rotate    1: every contiguous 128 of k, v and q is multiplied by H as by
+ *             rad_fwht128 after the position rotation, and q by 2^-7, so that q.k is
+ *             kept; needs D % 128 == 0.  Attention over such a cache yields outputs in
+ *             the rotated domain, which rad_quant_act_i8 with rotate = 0 turns into the
+ *             codes of the output projection.  0: not.
+ *
+ * In f32, each operation rounded by itself: (a, b) of a pair become (a * cos -
+ * b * sin, b * cos + a * sin); then the rotation; scale = f16(amax / 6) over the
+ * head's D values (f32 division, nearest f16, ties to even, saturating at
+ * 65504), code = the level nearest to |x| / scale (f32 division), ties to the
+ * even level index, magnitudes above 6 to 6, the sign of x, zero without a
+ * sign; scale 0 gives zero codes.  Only the appended tokens' codes and scales
+ * change; two sequences of one call must not append to the same page.
+ * Non-finite inputs give unspecified codes for their own head vector.
+ */
+int rad_kv4_append(const rad_kv4_cache *cache, const rad_kv_batch *batch, const void *k, int64_t ldk,
+                   const void *v, int64_t ldv, const void *q, int64_t ldq, int64_t q_heads, void *q_out,
+                   const rad_rope *rope, int rotate, int32_t dtype, rad_stream_t stream);
+
+/*
+ * rad_kv4_read -- the cached keys and values of the batch's rows as bf16
+ * (level * scale, exact in f32, rounded to nearest even): k_out and v_out bf16
+ * bits [rows][heads][D], 16-byte aligned.  Rows that are no token, and tokens
+ * on absent pages, are left as they were.
+ */
+int rad_kv4_read(const rad_kv4_cache *cache, const rad_kv_batch *batch, uint16_t *k_out, uint16_t *v_out,
+                 rad_stream_t stream);
+
+/*
+ * rad_attn_kv4 -- attention of the batch's query rows over the paged cache:
+ * o = softmax(sm_scale * q.k) v, query head j reading KV head j / (q_heads /
+ * heads).
+ *
+ *   q, o      [rows][q_heads][D] of `dtype`, dense, 16-byte aligned; q_heads a multiple
+ *             of the cache's heads.
+ *   sm_scale  finite, > 0.
+ *   causal    1: the row at position p sees tokens t <= p; 0: every token of its sequence.
+ *   window    > 0: only tokens t > p - window; 0: no window.
+ *   workspace device memory, 16-byte aligned, of at least the bytes that
+ *             rad_attn_kv4_workspace gives for the same cache, batch sizes, q_heads and
+ *             dtype (NULL when that is 0); free to reuse once the call's work is done.
+ *             Calls that may run at the same time need one each.
+ *
+ * Every row of a sequence is written; a row that sees no token becomes zeros.
+ * Scores, statistics and sums are held in f32.  Queries and probabilities meet
+ * the matrix cores as pairs of bf16 (16 bits) for RAD_DT_F32.
+ */
+int rad_attn_kv4_workspace(const rad_kv4_cache *cache, const rad_kv_batch *batch, int64_t q_heads,
+                           int32_t dtype, int64_t *bytes);
+int rad_attn_kv4(const rad_kv4_cache *cache, const rad_kv_batch *batch, const void *q, int64_t q_heads,
+                 float sm_scale, int causal, int64_t window, void *o, void *workspace,
+                 int64_t workspace_bytes, int32_t dtype, rad_stream_t stream);
+
 /*
  * rad_probe_mfma_i8 -- a measurement aid, not a step of the layer: what the
  * int8 matrix cores sustain on given operand bytes.  Its callers are

@@ -39,8 +39,14 @@ RAD_PROBE_MAX_KSTEPS = 1073741824
 
 EXPORTS = ("rad_fwht128", "rad_quant_act_i8", "rad_w8a8_gemv", "rad_w8a8_gemm", "rad_w8a8_linear",
            "rad_quant_weight_i8", "rad_kv_quant_i8", "rad_kv_dequant_i8", "rad_w8a8_rescore",
-           "rad_probe_mfma_i8", "rad_strerror")
+           "rad_add_rmsnorm_quant_i8", "rad_kv4_append", "rad_kv4_read", "rad_attn_kv4_workspace",
+           "rad_attn_kv4", "rad_probe_mfma_i8", "rad_strerror")
 KV_HEAD_DIMS = (64, 128, 256)
+KV4_PAGE_SIZES = (32, 64, 128, 256)
+# enum rad_dtype
+RAD_DT_F32 = 0
+RAD_DT_BF16 = 1
+RAD_DT_F16 = 2
 
 
 class RadError(RuntimeError):
@@ -58,6 +64,43 @@ class WeightDesc(ctypes.Structure):
         ("N", ctypes.c_int64),
         ("K", ctypes.c_int64),
         ("fmt", ctypes.c_int32),
+    ]
+
+
+class KV4CacheDesc(ctypes.Structure):
+    """struct rad_kv4_cache."""
+    _fields_ = [
+        ("k_codes", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p),
+        ("v_codes", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("pages", ctypes.c_int64),
+        ("heads", ctypes.c_int64),
+        ("page_size", ctypes.c_int64),
+        ("D", ctypes.c_int64),
+    ]
+
+
+class KVBatchDesc(ctypes.Structure):
+    """struct rad_kv_batch."""
+    _fields_ = [
+        ("block_table", ctypes.c_void_p),
+        ("seq_len", ctypes.c_void_p),
+        ("q_start", ctypes.c_void_p),
+        ("B", ctypes.c_int64),
+        ("max_pages", ctypes.c_int64),
+        ("rows", ctypes.c_int64),
+        ("max_q", ctypes.c_int64),
+    ]
+
+
+class RopeDesc(ctypes.Structure):
+    """struct rad_rope."""
+    _fields_ = [
+        ("table", ctypes.c_void_p),
+        ("rows", ctypes.c_int64),
+        ("dim", ctypes.c_int32),
+        ("style", ctypes.c_int32),
     ]
 
 
@@ -82,9 +125,17 @@ def lib() -> ctypes.CDLL:
         L.rad_kv_dequant_i8.argtypes = [vp, vp, vp, i64, i64, vp]
         L.rad_w8a8_rescore.argtypes = [vp, vp, ctypes.POINTER(WeightDesc), vp, i64, vp, i64, vp]
         L.rad_probe_mfma_i8.argtypes = [vp, vp, i64, i64, ci, vp]
+        i32, f32, cache, batch = ctypes.c_int32, ctypes.c_float, ctypes.POINTER(KV4CacheDesc), ctypes.POINTER(KVBatchDesc)
+        L.rad_add_rmsnorm_quant_i8.argtypes = [vp, vp, vp, vp, f32, vp, vp, i64, i64, i32, ci, vp]
+        L.rad_kv4_append.argtypes = [cache, batch, vp, i64, vp, i64, vp, i64, i64, vp, ctypes.POINTER(RopeDesc), ci,
+                                     i32, vp]
+        L.rad_kv4_read.argtypes = [cache, batch, vp, vp, vp]
+        L.rad_attn_kv4_workspace.argtypes = [cache, batch, i64, i32, ctypes.POINTER(i64)]
+        L.rad_attn_kv4.argtypes = [cache, batch, vp, i64, f32, ci, i64, vp, vp, i64, i32, vp]
         for f in (L.rad_fwht128, L.rad_quant_act_i8, L.rad_w8a8_gemv, L.rad_w8a8_gemm,
                   L.rad_w8a8_linear, L.rad_quant_weight_i8, L.rad_kv_quant_i8, L.rad_kv_dequant_i8,
-                  L.rad_w8a8_rescore, L.rad_probe_mfma_i8):
+                  L.rad_w8a8_rescore, L.rad_probe_mfma_i8, L.rad_add_rmsnorm_quant_i8, L.rad_kv4_append,
+                  L.rad_kv4_read, L.rad_attn_kv4_workspace, L.rad_attn_kv4):
             f.restype = ci
         L.rad_strerror.argtypes = [ci]
         L.rad_strerror.restype = ctypes.c_char_p
@@ -393,3 +444,238 @@ def probe_mfma_i8(src, blocks: int, ksteps: int, lds_fed: bool, out=None):
     _check(lib().rad_probe_mfma_i8(src.data_ptr(), out.data_ptr(), blocks, ksteps, 1 if lds_fed else 0,
                                    _stream(src)), "rad_probe_mfma_i8")
     return out
+
+
+# ------------------------------------------------- between a layer's linears --
+
+def _dtypes():
+    torch = _torch()
+    return {torch.float32: RAD_DT_F32, torch.bfloat16: RAD_DT_BF16, torch.float16: RAD_DT_F16}
+
+
+def _values(t, name):
+    """A GPU tensor of f32, bf16 or f16 values: its enum rad_dtype."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a GPU tensor" % name)
+    dt = _dtypes().get(t.dtype)
+    if dt is None:
+        raise TypeError("%s must hold f32, bf16 or f16 values, got %s" % (name, t.dtype))
+    return dt
+
+
+def _enqueue(name, device, fn, *args):
+    """Call `fn` on the current stream of `device`, with that device current."""
+    torch = _torch()
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        _check(fn(*args, stream), name)
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, stream), name)
+
+
+def add_rmsnorm_quant_i8(x, gamma, residual=None, eps: float = 1e-6, rotate: bool = True, q=None, scale=None,
+                         residual_out=None):
+    """Residual addition, RMS norm, rotation and int8 codes in one call, in front of a linear.
+
+    ``x`` [M][K] (f32, bf16 or f16), ``gamma`` f32 [K].  With ``residual`` [M][K] of the same type the sum
+    goes to ``residual_out`` (default: in place, into ``residual``).  Returns (q, scale, the sum or None)."""
+    torch = _torch()
+    dt = _values(x, "x")
+    _dev(x, x.dtype, "x")
+    _dev(gamma, torch.float32, "gamma")
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D, got shape %s" % (tuple(x.shape),))
+    M, K = x.shape
+    _shape(gamma, (K,), "gamma")
+    if q is None:
+        q = torch.empty((M, K), dtype=torch.int8, device=x.device)
+    if scale is None:
+        scale = torch.empty((M,), dtype=torch.float32, device=x.device)
+    _dev(q, torch.int8, "q")
+    _dev(scale, torch.float32, "scale")
+    _shape(q, (M, K), "q")
+    _shape(scale, (M,), "scale")
+    if residual is not None:
+        _dev(residual, x.dtype, "residual")
+        _shape(residual, (M, K), "residual")
+        if residual_out is None:
+            residual_out = residual
+        _dev(residual_out, x.dtype, "residual_out")
+        _shape(residual_out, (M, K), "residual_out")
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    _same_device(x, (gamma, "gamma"), (residual, "residual"), (residual_out, "residual_out"), (q, "q"),
+                 (scale, "scale"))
+    _enqueue("rad_add_rmsnorm_quant_i8", x.device, lib().rad_add_rmsnorm_quant_i8, x.data_ptr(),
+             None if residual is None else residual.data_ptr(),
+             None if residual_out is None else residual_out.data_ptr(), gamma.data_ptr(), eps, q.data_ptr(),
+             scale.data_ptr(), M, K, dt, 1 if rotate else 0)
+    return q, scale, residual_out
+
+
+class KV4Cache:
+    """Device tensors of a paged attention cache in 4 bits (layouts in include/rad.h), checked once:
+
+    k_codes uint8 [pages][heads][page_size][D/2], v_codes uint8 [pages][heads][page_size/8][D][4],
+    k_scale and v_scale f16 [pages][heads][page_size].
+    """
+
+    def __init__(self, k_codes, k_scale, v_codes, v_scale):
+        torch = _torch()
+        _dev(k_codes, torch.uint8, "k_codes")
+        _dev(v_codes, torch.uint8, "v_codes")
+        _dev(k_scale, torch.float16, "k_scale")
+        _dev(v_scale, torch.float16, "v_scale")
+        if k_codes.dim() != 4:
+            raise ValueError("k_codes must be 4-D, got shape %s" % (tuple(k_codes.shape),))
+        pages, heads, page, half = k_codes.shape
+        if page not in KV4_PAGE_SIZES or 2 * half not in KV_HEAD_DIMS:
+            raise ValueError("page size %d must be one of %s and head size %d one of %s"
+                             % (page, KV4_PAGE_SIZES, 2 * half, KV_HEAD_DIMS))
+        _shape(v_codes, (pages, heads, page // 8, 2 * half, 4), "v_codes")
+        _shape(k_scale, (pages, heads, page), "k_scale")
+        _shape(v_scale, (pages, heads, page), "v_scale")
+        _same_device(k_codes, (k_scale, "k_scale"), (v_codes, "v_codes"), (v_scale, "v_scale"))
+        self.k_codes, self.k_scale, self.v_codes, self.v_scale = k_codes, k_scale, v_codes, v_scale
+        self.pages, self.heads, self.page_size, self.D = pages, heads, page, 2 * half
+        self._desc = KV4CacheDesc(k_codes.data_ptr(), k_scale.data_ptr(), v_codes.data_ptr(), v_scale.data_ptr(),
+                                  pages, heads, page, 2 * half)
+
+    @classmethod
+    def empty(cls, pages: int, heads: int, page_size: int, D: int, device="cuda") -> "KV4Cache":
+        """A cache over fresh memory (it needs no clearing)."""
+        torch = _torch()
+
+        def make(shape, dtype):
+            return torch.empty(shape, dtype=dtype, device=device)
+        return cls(make((pages, heads, page_size, D // 2), torch.uint8), make((pages, heads, page_size), torch.float16),
+                   make((pages, heads, page_size // 8, D, 4), torch.uint8),
+                   make((pages, heads, page_size), torch.float16))
+
+
+class KVBatch:
+    """Which tokens a call is about: ``block_table`` int32 [B][max_pages], ``seq_len`` int32 [B] (the call's own
+    tokens counted), ``q_start`` int32 [B + 1] or None (one row per sequence), all on the GPU and read there.
+    ``rows``: rows of the call's arrays, padding included (default B); ``max_q``: no sequence has more rows
+    (default ``rows``)."""
+
+    def __init__(self, block_table, seq_len, q_start=None, rows=None, max_q=None):
+        torch = _torch()
+        _dev(block_table, torch.int32, "block_table")
+        _dev(seq_len, torch.int32, "seq_len")
+        if block_table.dim() != 2:
+            raise ValueError("block_table must be 2-D, got shape %s" % (tuple(block_table.shape),))
+        B, max_pages = block_table.shape
+        _shape(seq_len, (B,), "seq_len")
+        if q_start is not None:
+            _dev(q_start, torch.int32, "q_start")
+            _shape(q_start, (B + 1,), "q_start")
+            if rows is None:
+                raise ValueError("a ragged batch (q_start) needs rows")
+        rows = B if rows is None else int(rows)
+        _same_device(block_table, (seq_len, "seq_len"), (q_start, "q_start"))
+        self.block_table, self.seq_len, self.q_start, self.rows = block_table, seq_len, q_start, rows
+        self.max_q = (rows if max_q is None else int(max_q)) if q_start is not None else 1
+        self._desc = KVBatchDesc(block_table.data_ptr(), seq_len.data_ptr(),
+                                 None if q_start is None else q_start.data_ptr(), B, max_pages, rows, self.max_q)
+
+
+def _head_rows(t, rows, heads, D, name):
+    """[rows][heads][D] values whose token rows may lie apart: the distance in values."""
+    if t.dim() != 3 or tuple(t.shape) != (rows, heads, D):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), (rows, heads, D)))
+    if (D > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != D):
+        raise ValueError("%s must be contiguous in its last two dims" % name)
+    return t.stride(0) if rows > 1 else heads * D
+
+
+def kv4_append(cache: KV4Cache, batch: KVBatch, k, v, q=None, rope=None, rope_style: int = 0, rotate: bool = True,
+               q_out=None):
+    """Append ``k`` and ``v`` [rows][heads][D] to the cache at their positions, turned by ``rope`` (f32
+    [positions][dim]: dim/2 cosines, then dim/2 sines) and rotated per 128; returns the queries ``q``
+    [rows][q_heads][D] turned alike (q.k kept), or None."""
+    torch = _torch()
+    rows, H, D = batch.rows, cache.heads, cache.D
+    dt = _values(k, "k")
+    ldk = _head_rows(k, rows, H, D, "k")
+    if _values(v, "v") != dt:
+        raise TypeError("v is %s, k is %s" % (v.dtype, k.dtype))
+    ldv = _head_rows(v, rows, H, D, "v")
+    q_heads, ldq = 0, 0
+    if q is not None:
+        if _values(q, "q") != dt:
+            raise TypeError("q is %s, k is %s" % (q.dtype, k.dtype))
+        if q.dim() != 3:
+            raise ValueError("q must be 3-D, got shape %s" % (tuple(q.shape),))
+        q_heads = int(q.shape[1])
+        ldq = _head_rows(q, rows, q_heads, D, "q")
+        if q_out is None:
+            q_out = torch.empty((rows, q_heads, D), dtype=q.dtype, device=q.device)
+        _dev(q_out, q.dtype, "q_out")
+        _shape(q_out, (rows, q_heads, D), "q_out")
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    table = None
+    if rope is not None:
+        _dev(rope, torch.float32, "rope")
+        if rope.dim() != 2:
+            raise ValueError("rope must be 2-D, got shape %s" % (tuple(rope.shape),))
+        table = ctypes.byref(RopeDesc(rope.data_ptr(), rope.shape[0], rope.shape[1], rope_style))
+    _same_device(cache.k_codes, (batch.seq_len, "batch"), (k, "k"), (v, "v"), (q, "q"), (q_out, "q_out"),
+                 (rope, "rope"))
+    _enqueue("rad_kv4_append", k.device, lib().rad_kv4_append, cache._desc, batch._desc, k.data_ptr(), ldk,
+             v.data_ptr(), ldv, None if q is None else q.data_ptr(), ldq, q_heads,
+             None if q is None else q_out.data_ptr(), table, 1 if rotate else 0, dt)
+    return q_out
+
+
+def kv4_read(cache: KV4Cache, batch: KVBatch, k=None, v=None):
+    """The cached keys and values of the batch's rows as bf16 [rows][heads][D]."""
+    torch = _torch()
+    shape = (batch.rows, cache.heads, cache.D)
+    if k is None:
+        k = torch.empty(shape, dtype=torch.bfloat16, device=cache.k_codes.device)
+    if v is None:
+        v = torch.empty(shape, dtype=torch.bfloat16, device=cache.k_codes.device)
+    _dev(k, torch.bfloat16, "k")
+    _dev(v, torch.bfloat16, "v")
+    _shape(k, shape, "k")
+    _shape(v, shape, "v")
+    _same_device(cache.k_codes, (batch.seq_len, "batch"), (k, "k"), (v, "v"))
+    _enqueue("rad_kv4_read", k.device, lib().rad_kv4_read, cache._desc, batch._desc, k.data_ptr(), v.data_ptr())
+    return k, v
+
+
+def attn_kv4_workspace(cache: KV4Cache, batch: KVBatch, q_heads: int, dtype) -> int:
+    """Bytes of workspace that attn_kv4 needs for these sizes."""
+    n = ctypes.c_int64(0)
+    _check(lib().rad_attn_kv4_workspace(cache._desc, batch._desc, q_heads, _dtypes()[dtype], ctypes.byref(n)),
+           "rad_attn_kv4_workspace")
+    return n.value
+
+
+def attn_kv4(cache: KV4Cache, batch: KVBatch, q, sm_scale: float, causal: bool = True, window: int = 0, o=None,
+             workspace=None):
+    """Attention of ``q`` [rows][q_heads][D] over the paged 4-bit cache; rows that see nothing give zeros."""
+    torch = _torch()
+    dt = _values(q, "q")
+    _dev(q, q.dtype, "q")
+    if q.dim() != 3 or q.shape[0] != batch.rows or q.shape[2] != cache.D:
+        raise ValueError("q has shape %s, expected (%d, heads, %d)" % (tuple(q.shape), batch.rows, cache.D))
+    if o is None:
+        o = torch.empty_like(q)
+    _dev(o, q.dtype, "o")
+    _shape(o, q.shape, "o")
+    q_heads = int(q.shape[1])
+    n = attn_kv4_workspace(cache, batch, q_heads, q.dtype)
+    if workspace is None and n:
+        workspace = torch.empty((n,), dtype=torch.uint8, device=q.device)
+    if workspace is not None:
+        _dev(workspace, torch.uint8, "workspace")
+    _same_device(cache.k_codes, (batch.seq_len, "batch"), (q, "q"), (o, "o"), (workspace, "workspace"))
+    _enqueue("rad_attn_kv4", q.device, lib().rad_attn_kv4, cache._desc, batch._desc, q.data_ptr(), q_heads, sm_scale,
+             1 if causal else 0, window, o.data_ptr(), None if workspace is None else workspace.data_ptr(),
+             0 if workspace is None else workspace.numel(), dt)
+    return o

@@ -1,0 +1,179 @@
+// norm_quant.hip -- residual addition, root-mean-square norm, 128-point
+// rotation and per-token int8 quantisation in one pass (gfx950).
+//
+// Per token of K values: h = round_to_type(residual + x); r = 1 / sqrt(mean(h^2)
+// + eps); n = (h * r) * gamma; n~ = n rotated per 128; s = max |n~| / 127;
+// codes = rne(n~ / s).  The rotation mixes gamma's products, so two reductions
+// over the row are needed, the sum of squares before it and the maximum after
+// it; the row stays in registers between them.  The call reads x, the residual
+// and gamma and writes h, codes and a scale: an HBM stream for many tokens, a
+// chain of two reductions for few.
+//
+// A workgroup holds one token, each wave four 128-blocks a step (the lane
+// layout of rotate_quant.h), NITER steps.
+#include "layer_launch.h"
+#include "rotate_quant.h"
+#include "value_types.h"
+
+namespace rad {
+namespace {
+
+template <int DT, int NITER, int MAXT, bool NT>
+__global__ __launch_bounds__(MAXT) void norm_quant_kernel(const void *x, const void *res, void *res_out,
+                                                          const float *__restrict__ gamma, float eps,
+                                                          int8_t *__restrict__ q, float *__restrict__ scale, int K,
+                                                          int rotate) {
+    __shared__ float red_sum[MAXT / 64], red_max[MAXT / 64];
+    const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const int l16 = lane & 15, nblk = K >> 7;
+    const int64_t m = blockIdx.x, row = m * K;
+
+    Blk8 v[NITER];
+    float ss = 0.0f;
+#pragma unroll
+    for (int it = 0; it < NITER; ++it) {
+        const int blk = (it * waves + wid) * 4 + (lane >> 4);
+        if (blk < nblk) {
+            const int64_t at = row + blk * 128 + 4 * l16;
+            v[it].lo = load4<DT, NT>(x, at);
+            v[it].hi = load4<DT, NT>(x, at + 64);
+        } else {
+            v[it].lo = make_float4(0.f, 0.f, 0.f, 0.f);
+            v[it].hi = v[it].lo;
+        }
+    }
+    if (res) {
+#pragma unroll
+        for (int it = 0; it < NITER; ++it) {
+            const int blk = (it * waves + wid) * 4 + (lane >> 4);
+            if (blk < nblk) {
+                const int64_t at = row + blk * 128 + 4 * l16;
+                const float4 a = load4<DT, NT>(res, at), b = load4<DT, NT>(res, at + 64);
+                v[it].lo = make_float4(rounded<DT>(v[it].lo.x + a.x), rounded<DT>(v[it].lo.y + a.y),
+                                       rounded<DT>(v[it].lo.z + a.z), rounded<DT>(v[it].lo.w + a.w));
+                v[it].hi = make_float4(rounded<DT>(v[it].hi.x + b.x), rounded<DT>(v[it].hi.y + b.y),
+                                       rounded<DT>(v[it].hi.z + b.z), rounded<DT>(v[it].hi.w + b.w));
+                store4<DT, NT>(res_out, at, v[it].lo);
+                store4<DT, NT>(res_out, at + 64, v[it].hi);
+            }
+        }
+    }
+#pragma unroll
+    for (int it = 0; it < NITER; ++it) {
+        const float4 a = v[it].lo, b = v[it].hi;
+        ss += ((a.x * a.x + a.y * a.y) + (a.z * a.z + a.w * a.w)) + ((b.x * b.x + b.y * b.y) + (b.z * b.z + b.w * b.w));
+    }
+    ss = wave_sum_f32(ss);
+    if (lane == 0) red_sum[wid] = ss;
+    __syncthreads();
+    float total = 0.0f;
+    for (int w = 0; w < waves; ++w) total += red_sum[w];
+    const float r = 1.0f / __builtin_sqrtf(total / static_cast<float>(K) + eps);
+
+    float amax = 0.0f;
+#pragma unroll
+    for (int it = 0; it < NITER; ++it) {
+        const int blk = (it * waves + wid) * 4 + (lane >> 4);
+        if (blk < nblk) {
+            const float4 g = load4<kDtF32>(gamma, blk * 128 + 4 * l16), k = load4<kDtF32>(gamma, blk * 128 + 64 + 4 * l16);
+            float4 &a = v[it].lo, &b = v[it].hi;
+            a = make_float4(a.x * r * g.x, a.y * r * g.y, a.z * r * g.z, a.w * r * g.w);
+            b = make_float4(b.x * r * k.x, b.y * r * k.y, b.z * r * k.z, b.w * r * k.w);
+        }
+        if (rotate) fwht128_regs_signed(v[it], l16);           // values times the lane sign c
+        amax = fmaxf(amax, fmaxf(amax4(v[it].lo), amax4(v[it].hi)));
+    }
+    amax = wave_max_f32(amax);
+    if (lane == 0) red_max[wid] = amax;
+    __syncthreads();
+    float a = red_max[0];
+    for (int w = 1; w < waves; ++w) a = fmaxf(a, red_max[w]);
+    const float s = a / 127.0f;
+    if (threadIdx.x == 0) scale[m] = s;
+
+    // codes as in quant_act_kernel: through the reciprocal, near-half ones redone
+    // with the division, scales too small for a finite reciprocal divided throughout
+    const bool fast = s >= 0x1p-120f;
+    const float c = rotate ? fwht_lane_sign(l16) : 1.0f;
+    const float rs_c = c * (1.0f / s);
+#pragma unroll
+    for (int it = 0; it < NITER; ++it) {
+        const int blk = (it * waves + wid) * 4 + (lane >> 4);
+        if (blk < nblk) {
+            uint32_t lo = 0, hi = 0;
+            if (fast) {
+                lo = pack4_rcp_signed(v[it].lo, s, rs_c, c);
+                hi = pack4_rcp_signed(v[it].hi, s, rs_c, c);
+            } else if (s != 0.0f) {
+                lo = pack4_signed(v[it].lo, s, c);
+                hi = pack4_signed(v[it].hi, s, c);
+            }
+            uint32_t *p = reinterpret_cast<uint32_t *>(q + row + blk * 128 + 4 * l16);
+            if constexpr (NT) {
+                __builtin_nontemporal_store(lo, p);
+                __builtin_nontemporal_store(hi, p + 16);
+            } else {
+                p[0] = lo;
+                p[16] = hi;
+            }
+        }
+    }
+}
+
+struct Args {
+    const void *x, *res;
+    void *res_out;
+    const float *gamma;
+    float eps;
+    int8_t *q;
+    float *scale;
+    int64_t M;
+    int K, rotate;
+    hipStream_t st;
+};
+
+template <int DT, int NITER, int MAXT, bool NT>
+hipError_t go(const Args &a, int waves) {
+    hipLaunchKernelGGL((norm_quant_kernel<DT, NITER, MAXT, NT>), dim3(static_cast<uint32_t>(a.M)), dim3(waves * 64), 0,
+                       a.st, a.x, a.res, a.res_out, a.gamma, a.eps, a.q, a.scale, a.K, a.rotate);
+    return hipGetLastError();
+}
+
+template <int DT>
+hipError_t launch(const Args &a) {
+    const int nblk = a.K / 128, niter4 = (nblk + 15) / 16;
+    // Few tokens, or long rows: as many waves as the row has groups of four
+    // blocks, up to 16, so that each holds few steps.  Many tokens: 4 waves each.
+    if (a.M < 256 || niter4 > 12) {
+        const int niter = (nblk + 63) / 64, waves = (nblk + 4 * niter - 1) / (4 * niter);
+        if (niter <= 1) return go<DT, 1, 1024, false>(a, waves);
+        if (niter <= 2) return go<DT, 2, 1024, false>(a, waves);
+        if (niter <= 4) return go<DT, 4, 1024, false>(a, waves);
+        return go<DT, 8, 1024, false>(a, waves);               // K <= 65536
+    }
+    switch (niter4) {
+        case 1: return go<DT, 1, 256, true>(a, 4);
+        case 2: return go<DT, 2, 256, true>(a, 4);
+        case 3: return go<DT, 3, 256, true>(a, 4);
+        case 4: return go<DT, 4, 256, true>(a, 4);
+        case 5: return go<DT, 5, 256, true>(a, 4);
+        case 6: return go<DT, 6, 256, true>(a, 4);
+        case 7:
+        case 8: return go<DT, 8, 256, true>(a, 4);
+        case 9:
+        case 10: return go<DT, 10, 256, true>(a, 4);
+        default: return go<DT, 12, 256, true>(a, 4);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_norm_quant(const void *x, const void *res, void *res_out, const float *gamma, float eps,
+                             int8_t *q, float *scale, int64_t M, int K, int dtype, int rotate, hipStream_t st) {
+    const Args a{x, res, res_out, gamma, eps, q, scale, M, K, rotate, st};
+    if (dtype == kDtF32) return launch<kDtF32>(a);
+    if (dtype == kDtBf16) return launch<kDtBf16>(a);
+    return launch<kDtF16>(a);
+}
+
+}  // namespace rad

@@ -6,41 +6,17 @@
 // pointers -> alignment -> aliasing.
 #include <stdint.h>
 
-#include <initializer_list>
-
 #include "../../include/rad.h"
+#include "rad_check.h"
 #include "rad_launch.h"
 
 namespace {
 
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-struct Span {
-    uintptr_t lo, hi;  // [lo, hi)
-};
-// [p, p + bytes), the end clamped to the top of the address space (no real
-// buffer wraps; the clamp only keeps the comparison below meaningful).
-Span span(const void *p, int64_t bytes) {
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    const uintptr_t n = static_cast<uintptr_t>(bytes);
-    return Span{lo, n > UINTPTR_MAX - lo ? UINTPTR_MAX : lo + n};
-}
-bool overlap(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi && a.hi > a.lo && b.hi > b.lo; }
-
-constexpr int64_t kI32Max = 2147483647;
 // Group-scale arrays are addressed with 32-bit byte offsets in the kernels.
 constexpr int64_t kMaxScaleBytes = int64_t(1) << 31;
 static_assert(int64_t(255) * RAD_LINEAR_MAX_K + 128 < (int64_t(1) << 32),
               "a 256-row tile's lane offsets (row * K + chunk) fit 32 bits");
 
-// Product of non-negative sizes, or -1 when it does not fit int64 (no buffer
-// is that large, so such sizes are out of range).
-int64_t checked_mul(std::initializer_list<int64_t> xs) {
-    int64_t r = 1;
-    for (int64_t x : xs)
-        if (__builtin_mul_overflow(r, x, &r)) return -1;
-    return r;
-}
 static_assert(RAD_QUANT_WEIGHT_MAX_K == rad::kQuantWeightMaxK, "header and kernel agree on the largest K");
 static_assert(RAD_PROBE_BLOCK_BYTES == rad::kProbeBlockBytes, "header and kernel agree on a probe block");
 
@@ -51,8 +27,6 @@ int group_width(int32_t fmt) {
 }
 // bytes of weight codes per row
 int64_t code_bytes(int32_t fmt, int64_t K) { return fmt == RAD_FMT_TBL4_BF16G128 ? K / 2 : K; }
-
-int hip_status(hipError_t e) { return e == hipSuccess ? RAD_OK : RAD_E_HIP; }
 
 // Shared validation of the two contraction entry points.
 int check_linear(const int8_t *q, const float *scale, const rad_w8a8_weight *w, const float *y,
@@ -270,7 +244,7 @@ const char *rad_strerror(int status) {
         case RAD_E_NULL: return "a required pointer is NULL";
         case RAD_E_SHAPE: return "invalid shape (negative size, or K not a multiple of 128 / the group width)";
         case RAD_E_ALIGN: return "a pointer is not aligned as required";
-        case RAD_E_FMT: return "unknown weight format or wrong scale pointers for the format";
+        case RAD_E_FMT: return "unknown weight format or value type, or wrong scale pointers for the format";
         case RAD_E_RANGE: return "a size or flag is beyond what the call supports";
         case RAD_E_ALIAS: return "an output overlaps another argument";
         case RAD_E_HIP: return "the HIP runtime reported an error";

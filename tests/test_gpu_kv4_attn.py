@@ -1,0 +1,201 @@
+"""GPU: rad_attn_kv4 against attention in 64 bits over the same cache, every element within a derived tolerance:
+types, head sizes and groupings, lengths from none to many pages, ragged batches, masks, absent pages, stale memory."""
+import numpy as np
+import pytest
+
+import layer_cases as C
+from oracle import layer as O
+from rotated_w8a8_int8_amd import binding as B
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def torch():
+    import torch as _t
+    if not _t.cuda.is_available():
+        pytest.fail("GPU tests need a GPU")
+    return _t
+
+
+def run(torch, new, ctx, heads, G, D, page, dtype, causal=True, window=0, seed=0, pad=0, table_edit=None, width=None,
+        q_size=2.0, k_size=1.0, max_q=None, plain=False):
+    rng = np.random.default_rng(seed)
+    start = C.ragged(new)
+    T = int(start[-1]) + pad
+    seq_len = np.array(new) + np.array(ctx)
+    table, pages = C.page_table(rng, np.maximum(seq_len, 0), page, width)
+    if table_edit is not None:
+        table_edit(table, pages)
+    ref = O.Cache(pages, heads, page, D, rng)
+    C.fill_cache(rng, ref, table, np.maximum(seq_len, 0), k_size)
+    q = O.to_dtype(q_size * rng.standard_normal((T, heads * G, D)), dtype)
+    one = all(n == 1 for n in new) and pad == 0 and not plain
+    batch = C.device_batch(torch, table, seq_len, None if one else start, T, max_q)
+    sm = D ** -0.5
+    o = torch.full((T, heads * G, D), 33.0, dtype=C.torch_dtype(torch, dtype), device="cuda")
+    B.attn_kv4(C.device_cache(torch, ref), batch, C.put(torch, q, dtype), sm, causal=causal, window=window, o=o)
+    got = C.host(o)
+    want, mass, reach = O.attention(q, ref, table, seq_len, start, sm, causal, window)
+    padding = np.isnan(want)
+    assert np.array_equal(padding[:, 0, 0], np.arange(T) >= start[-1])
+    assert np.all(got[padding] == 33.0), "padding rows were written"
+    tol = C.attention_tolerance(dtype, np.nan_to_num(want), mass, reach, max(1, int(seq_len.max())))
+    off = np.abs(got - want)
+    off[padding] = 0
+    assert np.all(off <= tol), "off by %g of the tolerance at %s" % (np.max(off / tol), np.unravel_index(np.argmax(off / tol), off.shape))
+
+
+@pytest.mark.parametrize("dtype", C.DTYPES)
+@pytest.mark.parametrize("D", B.KV_HEAD_DIMS)
+@pytest.mark.parametrize("G", [1, 4, 5, 8, 11, 16, 20])
+def test_one_token_a_sequence(torch, G, D, dtype):
+    print("decode", G, D, dtype, flush=True)
+    run(torch, [1, 1, 1, 1, 1], [0, 1, 31, 77, 300], 2, G, D, 32, dtype, seed=G + D)
+
+
+@pytest.mark.parametrize("dtype", C.DTYPES)
+@pytest.mark.parametrize("n", [1, 2, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 1000])
+def test_every_length_near_a_tile(torch, n, dtype):
+    print("length", n, dtype, flush=True)
+    run(torch, [1], [n - 1], 1, 5, 128, 64, dtype, seed=n)
+
+
+@pytest.mark.parametrize("dtype", C.DTYPES)
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("D,G,page", [(64, 8, 32), (128, 5, 64), (256, 3, 128), (128, 1, 256)])
+def test_ragged_blocks(torch, D, G, page, causal, dtype):
+    print("blocks", D, G, page, causal, dtype, flush=True)
+    run(torch, [16, 3, 0, 7, 1], [100, 0, 50, 61, 33], 2, G, D, page, dtype, causal, seed=D + G, pad=3)
+
+
+@pytest.mark.parametrize("dtype", C.DTYPES)
+@pytest.mark.parametrize("n,ctx", [(97, 0), (130, 5), (200, 128), (257, 40)])
+def test_prompts(torch, n, ctx, dtype):
+    print("prompt", n, ctx, dtype, flush=True)
+    run(torch, [n, 1], [ctx, 90], 2, 5, 128, 64, dtype, seed=n)
+    run(torch, [n], [ctx], 1, 2, 64, 32, dtype, causal=False, seed=n + 1)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("window", [1, 7, 32, 100, 5000])
+def test_windows(torch, window, dtype):
+    print("window", window, dtype, flush=True)
+    run(torch, [1, 1], [200, 3], 2, 4, 128, 32, dtype, window=window, seed=window)
+    run(torch, [40, 9], [150, 0], 1, 5, 64, 32, dtype, window=window, seed=window + 1)
+    run(torch, [20, 9], [150, 0], 1, 5, 128, 64, dtype, causal=False, window=window, seed=window + 2)
+    run(torch, [160], [90], 1, 3, 128, 64, dtype, window=window, seed=window + 3)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_absent_pages_and_empty_rows(torch, dtype):
+    def edit(table, pages):
+        table[0, 0] = -1                                       # the first tokens are gone
+        table[1, :] = pages + 5                                # all of them are
+        table[2, 1] = -7
+    run(torch, [1, 1, 1], [100, 60, 90], 2, 5, 128, 32, dtype, table_edit=edit)
+    run(torch, [20, 4, 30], [100, 60, 70], 2, 5, 128, 32, dtype, table_edit=edit)
+    run(torch, [20, 4, 30], [20, 60, 70], 2, 5, 64, 32, dtype, causal=False, table_edit=edit)
+    run(torch, [6, 40], [-3, -25], 2, 5, 128, 32, dtype)       # rows before the first token: zeros
+    run(torch, [1, 1], [-1, 10], 2, 5, 128, 32, dtype)         # an empty sequence
+
+
+def test_lengths_past_the_table_are_cut(torch):
+    rng = np.random.default_rng(1)
+    ref = O.Cache(3, 1, 32, 128, rng)
+    table = np.array([[0, 2]], np.int32)
+    C.fill_cache(rng, ref, table, [64])
+    q = rng.standard_normal((1, 4, 128)).astype(np.float32)
+    dev = C.device_cache(torch, ref)
+    a = B.attn_kv4(dev, C.device_batch(torch, table, [64], None, 1), C.put(torch, q), 0.1)
+    b = B.attn_kv4(dev, C.device_batch(torch, table, [2 ** 31 - 1], None, 1), C.put(torch, q), 0.1)
+    assert torch.equal(a, b)
+    z = B.attn_kv4(dev, C.device_batch(torch, table, [-5], None, 1), C.put(torch, q), 0.1)
+    assert not z.any()
+
+
+@pytest.mark.parametrize("dtype", C.DTYPES)
+def test_peaked_and_flat_scores(torch, dtype):
+    # one token takes all, or all are alike; scores far beyond exp's range
+    run(torch, [1, 1], [500, 90], 1, 5, 128, 64, dtype, q_size=30.0, k_size=4.0, seed=3)
+    run(torch, [1, 1], [500, 90], 1, 5, 128, 64, dtype, q_size=0.0, seed=4)
+    run(torch, [130], [70], 1, 5, 128, 64, dtype, q_size=30.0, k_size=4.0, seed=5)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_scores_that_rise_with_the_context(torch, dtype):
+    # every tile brings a new maximum: the running sums are rescaled each time
+    rng = np.random.default_rng(7)
+    n, D, page = 700, 128, 64
+    ref = O.Cache(11, 1, page, D, rng)
+    table = rng.permutation(11).astype(np.int32)[None]
+    for t in range(n):
+        k = np.full((1, D), 0.02 * t) + 0.1 * rng.standard_normal((1, D))
+        v = rng.standard_normal((1, D)) * np.exp(rng.uniform(-6, 6))
+        ref.put(int(table[0, t // page]), t % page, O.quantise_f32(k.astype(np.float32)),
+                O.quantise_f32(v.astype(np.float32)))
+    for rows in (1, 30):
+        q = O.to_dtype(np.full((rows, 5, D), 1.0) + 0.1 * rng.standard_normal((rows, 5, D)), dtype)
+        start = C.ragged([rows])
+        got = C.host(B.attn_kv4(C.device_cache(torch, ref), C.device_batch(torch, table, [n], start, rows),
+                                C.put(torch, q, dtype), 0.5))
+        want, mass, reach = O.attention(q, ref, table, np.array([n]), start, 0.5, True, 0)
+        assert np.all(np.abs(got - want) <= C.attention_tolerance(dtype, want, mass, reach, n))
+
+
+def test_a_long_context(torch):
+    # 70,001 tokens: codes of a pool past 2^31 bits of offsets are not needed for the split over the context
+    rng = np.random.default_rng(11)
+    n, D, page, H, G = 70001, 128, 256, 1, 5
+    pages = (n + page - 1) // page
+    ref = O.Cache(pages, H, page, D, rng)
+    ref.k_scale[:] = (0.2 * np.exp(rng.uniform(-0.3, 0.3, ref.k_scale.shape))).astype(np.float16)
+    ref.v_scale[:] = (0.5 * np.exp(rng.uniform(-1, 1, ref.v_scale.shape))).astype(np.float16)
+    table = rng.permutation(pages).astype(np.int32)[None]
+    q = rng.standard_normal((1, G, D)).astype(np.float32)
+    got = C.host(B.attn_kv4(C.device_cache(torch, ref), C.device_batch(torch, table, [n], None, 1), C.put(torch, q),
+                            D ** -0.5))
+    want, mass, reach = O.attention(q, ref, table, np.array([n]), C.ragged([1]), D ** -0.5, True, 0)
+    assert np.all(np.abs(got - want) <= C.attention_tolerance("f32", want, mass, reach, n))
+
+
+def test_rows_past_max_q_are_left(torch):
+    rng = np.random.default_rng(2)
+    ref = O.Cache(4, 1, 32, 64, rng)
+    table = np.array([[0, 1]], np.int32)
+    C.fill_cache(rng, ref, table, [50])
+    q = C.put(torch, rng.standard_normal((10, 2, 64)).astype(np.float32))
+    dev, o = C.device_cache(torch, ref), torch.full((10, 2, 64), 5.0, device="cuda")
+    B.attn_kv4(dev, C.device_batch(torch, table, [50], C.ragged([10]), 10, max_q=4), q, 0.1, o=o)
+    full = B.attn_kv4(dev, C.device_batch(torch, table, [50], C.ragged([10]), 10), q, 0.1)
+    assert bool((o[4:] == 5).all())
+    assert float((o[:4] - full[:4]).abs().max()) <= 1e-4
+
+
+def test_the_same_call_twice_gives_the_same_bits(torch):
+    rng = np.random.default_rng(12)
+    ref = O.Cache(40, 2, 64, 128, rng)
+    ref.k_scale[:], ref.v_scale[:] = np.float16(0.1), np.float16(0.3)
+    table = rng.permutation(40).reshape(2, 20).astype(np.int32)
+    dev = C.device_cache(torch, ref)
+    for new in ([1, 1], [16, 5], [300, 200]):
+        q = C.put(torch, rng.standard_normal((sum(new), 10, 128)).astype(np.float32))
+        batch = C.device_batch(torch, table, [1200, 900], C.ragged(new), sum(new))
+        assert torch.equal(B.attn_kv4(dev, batch, q, 0.1), B.attn_kv4(dev, batch, q, 0.1))
+
+
+def test_binding_refusals(torch):
+    dev = B.KV4Cache.empty(2, 2, 32, 64)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    batch = B.KVBatch(torch.zeros(1, 1, **i32), torch.ones(1, **i32))
+    q = torch.zeros(1, 4, 64, device="cuda")
+    with pytest.raises(ValueError, match="q has shape"):
+        B.attn_kv4(dev, batch, torch.zeros(2, 4, 64, device="cuda"), 0.1)
+    with pytest.raises(B.RadError):
+        B.attn_kv4(dev, batch, torch.zeros(1, 3, 64, device="cuda"), 0.1)
+    with pytest.raises(TypeError, match="o must be"):
+        B.attn_kv4(dev, batch, q, 0.1, o=q.half())
+    with pytest.raises(B.RadError):
+        B.attn_kv4(dev, batch, q, 0.0)
+    with pytest.raises(B.RadError):
+        B.attn_kv4(dev, batch, q, 0.1, window=-3)

@@ -1,0 +1,167 @@
+"""The calls between a layer's linears refuse bad arguments on the host, before any HIP call (every call here fails
+its checks or is empty).  Fake, never dereferenced addresses stand in for device pointers."""
+import ctypes
+import os
+
+import pytest
+
+from rotated_w8a8_int8_amd import binding as B
+
+pytestmark = pytest.mark.skipif(not os.path.exists(B.LIB_PATH), reason="librad.so not built")
+
+P = [0x7F0000000000 + i * 0x10000000000 for i in range(16)]     # aligned, far apart
+F32, BF16, F16 = B.RAD_DT_F32, B.RAD_DT_BF16, B.RAD_DT_F16
+
+
+def test_dtype_constants_match_header():
+    h = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "rad.h")).read()
+    for name in ("RAD_DT_F32", "RAD_DT_BF16", "RAD_DT_F16"):
+        assert "%s = %d" % (name, getattr(B, name)) in h
+
+
+def norm(x=P[0], r=P[1], ro=P[1], g=P[2], eps=1e-6, q=P[3], s=P[4], M=4, K=256, dt=F32, rot=1):
+    return B.lib().rad_add_rmsnorm_quant_i8(x, r, ro, g, eps, q, s, M, K, dt, rot, None)
+
+
+@pytest.mark.parametrize("kw,rc", [
+    (dict(dt=3), B.RAD_E_FMT), (dict(dt=-1), B.RAD_E_FMT),
+    (dict(K=200), B.RAD_E_SHAPE), (dict(K=0), B.RAD_E_SHAPE), (dict(M=-1), B.RAD_E_SHAPE),
+    (dict(K=B.RAD_QUANT_MAX_K + 128), B.RAD_E_RANGE), (dict(M=1 << 31), B.RAD_E_RANGE), (dict(rot=2), B.RAD_E_RANGE),
+    (dict(eps=-1e-6), B.RAD_E_RANGE), (dict(eps=float("nan")), B.RAD_E_RANGE), (dict(eps=float("inf")), B.RAD_E_RANGE),
+    (dict(r=None), B.RAD_E_NULL), (dict(ro=None), B.RAD_E_NULL), (dict(x=None), B.RAD_E_NULL),
+    (dict(g=None), B.RAD_E_NULL), (dict(q=None), B.RAD_E_NULL), (dict(s=None), B.RAD_E_NULL),
+    (dict(x=P[0] + 8), B.RAD_E_ALIGN), (dict(r=P[1] + 8, ro=P[5]), B.RAD_E_ALIGN), (dict(ro=P[5] + 4), B.RAD_E_ALIGN),
+    (dict(g=P[2] + 4), B.RAD_E_ALIGN), (dict(q=P[3] + 4), B.RAD_E_ALIGN), (dict(s=P[4] + 2), B.RAD_E_ALIGN),
+    (dict(q=P[0] + 1024), B.RAD_E_ALIAS), (dict(s=P[3] + 512), B.RAD_E_ALIAS), (dict(ro=P[1] + 2048), B.RAD_E_ALIAS),
+    (dict(ro=P[0]), B.RAD_E_ALIAS), (dict(x=P[1]), B.RAD_E_ALIAS), (dict(g=P[1] + 256), B.RAD_E_ALIAS),
+    (dict(q=P[1] + 4 * 256 * 4 - 16), B.RAD_E_ALIAS),
+    (dict(M=0, x=None, r=None, ro=None, g=None, q=None, s=None), B.RAD_OK),
+])
+def test_norm_refusals(kw, rc):
+    assert norm(**kw) == rc
+
+
+def cache(k=P[0], ks=P[1], v=P[2], vs=P[3], pages=10, heads=2, page=64, D=128):
+    return B.KV4CacheDesc(k, ks, v, vs, pages, heads, page, D)
+
+
+def batch(table=P[4], n=P[5], start=P[6], seqs=3, max_pages=4, rows=7, max_q=7):
+    return B.KVBatchDesc(table, n, start, seqs, max_pages, rows, max_q)
+
+
+CACHE_REFUSALS = [
+    (dict(D=96), B.RAD_E_SHAPE), (dict(D=0), B.RAD_E_SHAPE), (dict(page=16), B.RAD_E_SHAPE),
+    (dict(page=48), B.RAD_E_SHAPE), (dict(page=512), B.RAD_E_SHAPE), (dict(pages=0), B.RAD_E_SHAPE),
+    (dict(heads=0), B.RAD_E_SHAPE), (dict(heads=1025), B.RAD_E_RANGE), (dict(pages=1 << 31), B.RAD_E_RANGE),
+    (dict(k=None), B.RAD_E_NULL), (dict(ks=None), B.RAD_E_NULL), (dict(v=None), B.RAD_E_NULL),
+    (dict(vs=None), B.RAD_E_NULL), (dict(k=P[0] + 8), B.RAD_E_ALIGN), (dict(ks=P[1] + 2), B.RAD_E_ALIGN),
+    (dict(v=P[2] + 4), B.RAD_E_ALIGN), (dict(vs=P[3] + 8), B.RAD_E_ALIGN),
+]
+BATCH_REFUSALS = [
+    (dict(seqs=-1), B.RAD_E_SHAPE), (dict(rows=-1), B.RAD_E_SHAPE), (dict(max_pages=-1), B.RAD_E_SHAPE),
+    (dict(max_q=-1), B.RAD_E_SHAPE), (dict(start=None), B.RAD_E_SHAPE),       # rows != B without q_start
+    (dict(seqs=1 << 24), B.RAD_E_RANGE), (dict(rows=1 << 24), B.RAD_E_RANGE),
+    (dict(max_pages=1 << 24), B.RAD_E_RANGE), (dict(max_pages=1 << 40), B.RAD_E_RANGE),
+    (dict(table=None), B.RAD_E_NULL), (dict(n=None), B.RAD_E_NULL),
+    (dict(table=P[4] + 2), B.RAD_E_ALIGN), (dict(n=P[5] + 1), B.RAD_E_ALIGN), (dict(start=P[6] + 2), B.RAD_E_ALIGN),
+]
+
+
+def append(c={}, b={}, k=P[7], ldk=256, v=P[8], ldv=256, q=P[9], ldq=512, q_heads=4, qo=P[10], rope=None, rot=1,
+           dt=BF16):
+    return B.lib().rad_kv4_append(cache(**c), batch(**b), k, ldk, v, ldv, q, ldq, q_heads, qo,
+                                  None if rope is None else B.RopeDesc(*rope), rot, dt, None)
+
+
+def read(c={}, b={}, k=P[7], v=P[8]):
+    return B.lib().rad_kv4_read(cache(**c), batch(**b), k, v, None)
+
+
+def attn(c={}, b={}, q=P[7], q_heads=4, scale=0.1, causal=1, window=0, o=P[8], ws=P[9], ws_bytes=1 << 40, dt=BF16):
+    return B.lib().rad_attn_kv4(cache(**c), batch(**b), q, q_heads, scale, causal, window, o, ws, ws_bytes, dt, None)
+
+
+@pytest.mark.parametrize("call", [append, read, attn])
+@pytest.mark.parametrize("kw,rc", CACHE_REFUSALS)
+def test_cache_refusals(call, kw, rc):
+    assert call(c=kw) == rc
+
+
+@pytest.mark.parametrize("call", [append, read, attn])
+@pytest.mark.parametrize("kw,rc", BATCH_REFUSALS)
+def test_batch_refusals(call, kw, rc):
+    assert call(b=kw) == rc
+
+
+@pytest.mark.parametrize("call", [append, read, attn])
+@pytest.mark.parametrize("kw", [dict(rows=0), dict(seqs=0)])
+def test_empty_batches_enqueue_nothing(call, kw):
+    assert call(b=dict(kw, table=None, n=None)) == B.RAD_OK
+
+
+@pytest.mark.parametrize("call", ["append", "read", "attn", "workspace"])
+def test_missing_descriptors(call):
+    L, n = B.lib(), ctypes.c_int64(0)
+    for c, b in ((None, batch()), (cache(), None)):
+        rc = {"append": lambda: L.rad_kv4_append(c, b, P[7], 256, P[8], 256, None, 0, 0, None, None, 0, BF16, None),
+              "read": lambda: L.rad_kv4_read(c, b, P[7], P[8], None),
+              "attn": lambda: L.rad_attn_kv4(c, b, P[7], 4, 0.1, 1, 0, P[8], P[9], 1 << 40, BF16, None),
+              "workspace": lambda: L.rad_attn_kv4_workspace(c, b, 4, BF16, ctypes.byref(n))}[call]()
+        assert rc == B.RAD_E_NULL
+
+
+@pytest.mark.parametrize("kw,rc", [
+    (dict(dt=5), B.RAD_E_FMT), (dict(rot=2), B.RAD_E_RANGE),
+    (dict(c=dict(D=64), rot=1), B.RAD_E_SHAPE),                               # the rotation needs 128s
+    (dict(ldk=255), B.RAD_E_SHAPE), (dict(ldv=0), B.RAD_E_SHAPE), (dict(ldq=511), B.RAD_E_SHAPE),
+    (dict(q_heads=-1), B.RAD_E_SHAPE), (dict(q_heads=16385, ldq=1 << 22), B.RAD_E_RANGE),
+    (dict(ldk=1 << 31), B.RAD_E_RANGE),
+    (dict(rope=(P[11], 100, 12, 0)), B.RAD_E_SHAPE), (dict(rope=(P[11], 100, 136, 0)), B.RAD_E_SHAPE),
+    (dict(rope=(P[11], 100, 0, 0)), B.RAD_E_SHAPE), (dict(rope=(P[11], -1, 64, 0)), B.RAD_E_SHAPE),
+    (dict(rope=(P[11], 100, 64, 2)), B.RAD_E_RANGE), (dict(rope=(P[11], 1 << 31, 64, 0)), B.RAD_E_RANGE),
+    (dict(rope=(None, 100, 64, 0)), B.RAD_E_NULL), (dict(rope=(P[11] + 4, 100, 64, 0)), B.RAD_E_ALIGN),
+    (dict(q=None), B.RAD_E_NULL), (dict(qo=None), B.RAD_E_NULL), (dict(q=None, q_heads=0), B.RAD_E_NULL),
+    (dict(k=None), B.RAD_E_NULL), (dict(v=None), B.RAD_E_NULL),
+    (dict(k=P[7] + 8), B.RAD_E_ALIGN), (dict(v=P[8] + 2), B.RAD_E_ALIGN), (dict(q=P[9] + 4), B.RAD_E_ALIGN),
+    (dict(qo=P[10] + 8), B.RAD_E_ALIGN), (dict(ldk=260), B.RAD_E_ALIGN), (dict(ldq=518, dt=F32), B.RAD_E_ALIGN),
+    (dict(qo=P[9] + 1024), B.RAD_E_ALIAS), (dict(qo=P[7]), B.RAD_E_ALIAS), (dict(k=P[0] + 4096), B.RAD_E_ALIAS),
+    (dict(v=P[3]), B.RAD_E_ALIAS), (dict(qo=P[2]), B.RAD_E_ALIAS), (dict(qo=P[5]), B.RAD_E_ALIAS),
+    (dict(b=dict(n=P[1] + 64)), B.RAD_E_ALIAS), (dict(c=dict(ks=P[0] + 1024)), B.RAD_E_ALIAS),
+    (dict(rope=(P[2], 100, 64, 0)), B.RAD_E_ALIAS), (dict(rope=(P[10], 100, 64, 0)), B.RAD_E_ALIAS),
+])
+def test_append_refusals(kw, rc):
+    assert append(**kw) == rc
+
+
+@pytest.mark.parametrize("kw,rc", [
+    (dict(k=None), B.RAD_E_NULL), (dict(v=None), B.RAD_E_NULL), (dict(k=P[7] + 8), B.RAD_E_ALIGN),
+    (dict(v=P[8] + 4), B.RAD_E_ALIGN), (dict(v=P[7] + 256), B.RAD_E_ALIAS), (dict(k=P[2]), B.RAD_E_ALIAS),
+    (dict(v=P[4]), B.RAD_E_ALIAS),
+])
+def test_read_refusals(kw, rc):
+    assert read(**kw) == rc
+
+
+@pytest.mark.parametrize("kw,rc", [
+    (dict(dt=3), B.RAD_E_FMT), (dict(q_heads=0), B.RAD_E_SHAPE), (dict(q_heads=5), B.RAD_E_SHAPE),
+    (dict(q_heads=1 << 15), B.RAD_E_RANGE), (dict(b=dict(rows=(1 << 24) - 1), q_heads=1024), B.RAD_E_RANGE),
+    (dict(scale=0.0), B.RAD_E_RANGE), (dict(scale=-1.0), B.RAD_E_RANGE), (dict(scale=float("nan")), B.RAD_E_RANGE),
+    (dict(scale=float("inf")), B.RAD_E_RANGE), (dict(causal=2), B.RAD_E_RANGE), (dict(window=-1), B.RAD_E_SHAPE),
+    (dict(q=None), B.RAD_E_NULL), (dict(o=None), B.RAD_E_NULL), (dict(q=P[7] + 8), B.RAD_E_ALIGN),
+    (dict(o=P[8] + 4), B.RAD_E_ALIGN), (dict(ws=P[9] + 8), B.RAD_E_ALIGN), (dict(o=P[7] + 64), B.RAD_E_ALIAS),
+    (dict(o=P[0] + 64), B.RAD_E_ALIAS), (dict(o=P[6]), B.RAD_E_ALIAS),
+])
+def test_attention_refusals(kw, rc):
+    assert attn(**kw) == rc
+
+
+def test_binding_refuses_host_tensors():
+    import torch
+    x, g = torch.zeros(2, 256), torch.ones(256)
+    with pytest.raises(TypeError, match="GPU tensor"):
+        B.add_rmsnorm_quant_i8(x, g)
+    u8 = torch.zeros(1, 1, 32, 64, dtype=torch.uint8)
+    with pytest.raises(TypeError, match="GPU tensor"):
+        B.KV4Cache(u8, torch.zeros(1, 1, 32).half(), u8.view(1, 1, 4, 128, 4), torch.zeros(1, 1, 32).half())
+    with pytest.raises(TypeError, match="GPU tensor"):
+        B.KVBatch(torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
