@@ -101,18 +101,460 @@ __global__ __launch_bounds__(256) void attn_plain_kernel(Kv4Cache c, KvBatch b, 
     }
 }
 
+// ---- few rows: the context split over workgroups ---------------------------
+//
+// A wave takes 32 tokens a step and all the call's (row, head) pairs of one KV
+// head as the columns of its matrix products (16 at most), transposed so that
+// nothing crosses lanes between them:
+//
+//   S^T [32 tokens][16 cols] = K Q^T    two 16x16x32 tiles; A: a lane holds D/4 dims of
+//                                       one token, one dword (8 dims) per product
+//   O^T [D][16 cols]        += V^T P^T  D/16 tiles; A: a lane holds one dim of eight
+//                                       tokens, one dword
+//
+// Row r of score tile u is token 8 (r / 4) + 4 u + r % 4 of the step, so lane (g, c)
+// (g = lane / 16, c = lane % 16) comes out of S^T with the scores of tokens 8 g ..
+// 8 g + 7 of column c: the B operand that O^T needs against the value octets.
+//
+// e2m1 levels are exact in f16; the f16 scales meet the scores (keys) and the
+// probabilities (values) in f32.  A query row is taken times a power of two that puts
+// its largest value in [2^9, 2^10), where f16 holds bf16 and f16 queries exactly (what
+// lies 2^-24 below the largest aside).  f32 queries and their weights are split in two
+// f16 parts, 22 bits: with at most 8 columns the low parts ride in columns 8 .. 15 of
+// the same products (HL 1), otherwise in products of their own (HL 2).  For bf16 and f16
+// queries a weight is one f16 (HL 0).
+//
+// The reference exponent m of a column keeps its weights p * scale, p = 2^(score - m),
+// inside f16: it is set so that the largest weight met comes to 2^kRoom, and raised only
+// when one passes 2^kMost (one vote a step); then scores and scale exponents are looked at
+// one by one.  A weight is thus held to 2^-24 of a scale on which the column's largest is at
+// least 2^(kRoom - 1).
+typedef unsigned int u4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u2 __attribute__((ext_vector_type(2)));
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+
+constexpr float kRoom = 4.0f;                       // log2
+constexpr float kMost = 0x1p14f;                    // twice this is below 65504
+constexpr float kMostP = 0x1p60f;                   // values of scale 0 weigh nothing, but count
+constexpr float kLowest = -3.4028234663852886e38f;
+
+// Eight e2m1 codes -> eight f16 levels.
+__device__ __forceinline__ u4 levels8(uint32_t w) {
+    return u4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0)),
+              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1)),
+              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2)),
+              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3))};
+}
+__device__ __forceinline__ f4 mma16(u4 a, u4 b, f4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, a), __builtin_bit_cast(h8, b), c, 0, 0, 0);
+}
+
+typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+// two values to f16: to the nearest, and cut (the rest a - cut is exact in f32)
+__device__ __forceinline__ uint32_t f16_pack2(float a, float b) {
+    return __builtin_bit_cast(uint32_t, h2{static_cast<_Float16>(a), static_cast<_Float16>(b)});
+}
+__device__ __forceinline__ uint32_t f16_cut2(float a, float b) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a, b));
+}
+__device__ __forceinline__ u4 f16_pack8(const float (&w)[8]) {
+    return u4{f16_pack2(w[0], w[1]), f16_pack2(w[2], w[3]), f16_pack2(w[4], w[5]), f16_pack2(w[6], w[7])};
+}
+// high and low f16 parts of eight values
+__device__ __forceinline__ void f16_split8(const float (&w)[8], u4 &hi, u4 &low) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t cut = f16_cut2(w[2 * i], w[2 * i + 1]);
+        const h2 h = __builtin_bit_cast(h2, cut);
+        hi[i] = cut;
+        low[i] = f16_pack2(fmaf(static_cast<float>(h[0]), -1.0f, w[2 * i]), fmaf(static_cast<float>(h[1]), -1.0f, w[2 * i + 1]));
+    }
+}
+
+__device__ __forceinline__ float max8(const float (&s)[8]) {
+    return fmaxf(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])), fmaxf(fmaxf(s[4], s[5]), fmaxf(s[6], s[7])));
+}
+__device__ __forceinline__ float amax4(float4 v) {
+    return fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+}
+
+// Maximum (sum) over the four lanes that hold one column.
+__device__ __forceinline__ float col_max(float v) {
+    v = fmaxf(v, __shfl_xor(v, 16));
+    return fmaxf(v, __shfl_xor(v, 32));
+}
+__device__ __forceinline__ float col_sum(float v) {
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+}
+
+// How the context [lo, hi) of one sequence (a union over its rows) is shared out:
+// steps of 32 tokens, `chunk` of them a workgroup, in at most `splits` workgroups.
+struct Share {
+    int first, steps, chunk, parts;       // first step, number of steps, steps a part, parts in use
+};
+constexpr int kMinChunk = 4;              // steps: one for each wave
+__device__ __forceinline__ Share share(int lo, int hi, int splits) {
+    Share s;
+    s.first = lo >> 5;
+    s.steps = hi > lo ? ((hi + 31) >> 5) - s.first : 0;
+    s.chunk = max(kMinChunk, (s.steps + splits - 1) / splits);
+    s.parts = (s.steps + s.chunk - 1) / s.chunk;
+    return s;
+}
+
+// A step's codes and scales, one lane's share.
+template <int D>
+struct Step {
+    uint32_t k[2][D / 32];      // D / 4 dims of a token of each tile
+    u4 v[D / 64];               // one octet of tokens, dims 64 j + 4 r ..
+    u4 ks, vs;                  // f16 scales of the octet
+};
+
+template <int D>
+__device__ __forceinline__ void load_step(Step<D> &s, const Kv4Cache &c, int64_t tok, int g, int r) {
+    // tok: index of the step's first token in the cache's [pages][heads][page] order
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const uint8_t *p = c.k_codes + (tok + 8 * (r >> 2) + 4 * u + (r & 3)) * (D / 2) + g * (D / 8);
+        if constexpr (D == 64) {
+            const u2 x = __builtin_nontemporal_load(reinterpret_cast<const u2 *>(p));
+            s.k[u][0] = x.x;
+            s.k[u][1] = x.y;
+        } else {
+#pragma unroll
+            for (int j = 0; j < D / 128; ++j) {
+                const u4 x = __builtin_nontemporal_load(reinterpret_cast<const u4 *>(p) + j);
+                s.k[u][4 * j] = x.x;
+                s.k[u][4 * j + 1] = x.y;
+                s.k[u][4 * j + 2] = x.z;
+                s.k[u][4 * j + 3] = x.w;
+            }
+        }
+    }
+    const u4 *vp = reinterpret_cast<const u4 *>(c.v_codes) + (((tok >> 3) + g) * D + 4 * r) / 4;
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) s.v[j] = __builtin_nontemporal_load(vp + 16 * j);
+    s.ks = *reinterpret_cast<const u4 *>(c.k_scale + tok + 8 * g);
+    s.vs = *reinterpret_cast<const u4 *>(c.v_scale + tok + 8 * g);
+}
+
+// f times the i-th of eight f16 values, as one mixed-precision multiply-add
+__device__ __forceinline__ float times_half(float f, const u4 &x, int i) {
+    const h2 h = __builtin_bit_cast(h2, static_cast<uint32_t>(x[i >> 1]));
+    return fmaf(f, static_cast<float>(h[i & 1]), 0.0f);
+}
+
+// blockIdx: x sequence * splits + part of its context, y KV head.  cols = max_q * G <= 16
+// (HL 1: <= 8).  Partial sums go to part_o [B][heads][splits][cols][D] and
+// part_ml [..][cols][2], or the outputs straight to a.o where one part is in use.
+template <int DT, int D, int HL>
+__global__ __launch_bounds__(256, 2) void attn_split_kernel(Kv4Cache c, KvBatch b, Kv4Attn a, int cols, int splits,
+                                                         float *part_o, float *part_ml) {
+    constexpr int W = 4;
+    __shared__ float lds_o[W][16][D + 4], lds_ml[W][16][2];
+    const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int g = lane >> 4, col = lane & 15;
+    const int h = blockIdx.y, seq = blockIdx.x / splits, part = blockIdx.x % splits, G = a.q_heads / c.heads;
+    const RowRange rr = kv_rows(b, seq);
+    const int n = min(rr.n, b.max_q), len = kv_len(b, seq), pos0 = len - rr.n;
+    if (n == 0) return;
+    // the union of what the rows see: the last row's end, the first row's beginning
+    const int lo_all = seen(max(pos0, 0), len, a.causal, a.window).lo;
+    const int hi_all = a.causal ? pos0 + n : (pos0 + n > 0 ? len : 0);
+    const Share sh = share(lo_all, hi_all, splits);
+    if (part >= max(sh.parts, 1)) return;
+
+    // this lane's column: row `ci` of the sequence, head h * G + cg
+    const int cq = HL == 1 ? col & 7 : col;
+    const bool used = cq < n * G;
+    const int ci = used ? cq / G : 0, cg = used ? cq % G : 0;
+    const TokenRange tr = seen(pos0 + ci, len, a.causal, a.window);
+    const int64_t qrow = (static_cast<int64_t>(rr.first + ci) * a.q_heads + h * G + cg) * D;
+    constexpr int NK = D / 32;
+    u4 qf[NK], ql[HL == 2 ? NK : 1];
+    float scale = a.sm_scale * kLog2e;
+    {
+        float v[NK][8], big = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NK; ++j) {
+            const int64_t at = qrow + g * (D / 4) + 8 * j;
+            const float4 x = load4<DT>(a.q, at), y = load4<DT>(a.q, at + 4);
+            v[j][0] = x.x; v[j][1] = x.y; v[j][2] = x.z; v[j][3] = x.w;
+            v[j][4] = y.x; v[j][5] = y.y; v[j][6] = y.z; v[j][7] = y.w;
+            big = fmaxf(big, fmaxf(amax4(x), amax4(y)));
+        }
+        big = col_max(big);
+        // largest value to [2^9, 2^10), undone in the scores' factor (both exact)
+        const int e = big > 0.0f ? 10 - __builtin_amdgcn_frexp_expf(big) : 0;
+#pragma unroll
+        for (int j = 0; j < NK; ++j) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[j][i] = used ? __builtin_amdgcn_ldexpf(v[j][i], e) : 0.0f;
+            if constexpr (HL == 0) {
+                qf[j] = f16_pack8(v[j]);
+            } else {
+                u4 hi, low;
+                f16_split8(v[j], hi, low);
+                if constexpr (HL == 2) ql[j] = low;
+                qf[j] = HL == 1 && col >= 8 ? low : hi;
+            }
+        }
+        scale = fmaxf(__builtin_amdgcn_ldexpf(scale, -e), 1e-30f);      // never 0: a masked score is -inf
+    }
+
+    float m = kLowest, l = 0.0f;
+    f4 acc[D / 16];
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) acc[j] = f4{0.f, 0.f, 0.f, 0.f};
+
+    const int begin = sh.first + part * sh.chunk, end = min(begin + sh.chunk, sh.first + sh.steps);
+    const int per_page = b.page_shift - 5;                    // log2 of steps a page
+    const int32_t *table = b.block_table + static_cast<int64_t>(seq) * b.max_pages;
+    auto page_of = [&](int step) { return step < end ? table[step >> per_page] : -1; };
+    auto token_of = [&](int page, int step) {
+        const int64_t p = page >= 0 && page < c.pages ? page : 0;
+        return ((p * c.heads + h) << c.page_shift) + ((step << 5) & ((1 << c.page_shift) - 1));
+    };
+
+    Step<D> cur, nxt;
+    int page = page_of(begin + wid), page_n = page_of(begin + wid + W);
+    if (begin + wid < end) load_step<D>(cur, c, token_of(page, begin + wid), g, col);
+    for (int step = begin + wid; step < end; step += W) {
+        const int page_nn = page_of(step + 2 * W);
+        if (step + W < end) load_step<D>(nxt, c, token_of(page_n, step + W), g, col);
+        if (page >= 0 && page < c.pages) {
+            float s[8];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                f4 t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int j = 0; j < NK; ++j) {
+                    const u4 kf = levels8(cur.k[u][j]);
+                    if constexpr (HL == 2) t = mma16(kf, ql[j], t);
+                    t = mma16(kf, qf[j], t);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float x = t[i];
+                    if constexpr (HL == 1) x += lane_xor<8>(x);          // high and low part of the query
+                    s[4 * u + i] = times_half(x, cur.ks, 4 * u + i);
+                }
+            }
+            const int t0 = (step << 5) + 8 * g;
+            if (__any(t0 < tr.lo || t0 + 8 > tr.hi)) {
+                asm volatile("");                              // a branch of its own: most steps need no mask
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const bool on = t0 + i >= tr.lo && t0 + i < tr.hi;
+                    s[i] = on ? s[i] : -INFINITY;
+                    cur.vs[i >> 1] &= on ? 0xFFFFFFFFu : (i & 1 ? 0x0000FFFFu : 0xFFFF0000u);
+                }
+            }
+            float w[8], sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float p = __builtin_amdgcn_exp2f(fmaf(s[i], scale, -m));
+                sum += p;
+                w[i] = times_half(p, cur.vs, i);
+            }
+            if (__any(!(max8(w) <= kMost && sum <= kMostP))) {         // also the first step: m is the lowest
+                float most = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float vs = times_half(1.0f, cur.vs, i);
+                    most = fmaxf(most, fmaf(s[i], scale, vs > 0.0f ? static_cast<float>(__builtin_amdgcn_frexp_expf(vs)) : -24.0f));
+                }
+                const float mn = fmaxf(m, col_max(most) - kRoom), shrink = __builtin_amdgcn_exp2f(m - mn);
+                m = mn;
+                l *= shrink;
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j) acc[j] *= shrink;
+                sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float p = __builtin_amdgcn_exp2f(fmaf(s[i], scale, -m));
+                    sum += p;
+                    w[i] = times_half(p, cur.vs, i);
+                }
+            }
+            l += sum;
+            u4 wf, wl;
+            if constexpr (HL == 0) {
+                wf = f16_pack8(w);
+            } else {
+                u4 hi;
+                f16_split8(w, hi, wl);
+                wf = HL == 1 && col >= 8 ? wl : hi;
+            }
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const u4 vf = levels8(cur.v[j][x]);
+                    if constexpr (HL == 2) acc[4 * j + x] = mma16(vf, wl, acc[4 * j + x]);
+                    acc[4 * j + x] = mma16(vf, wf, acc[4 * j + x]);
+                }
+            }
+        }
+        cur = nxt;
+        page = page_n;
+        page_n = page_nn;
+    }
+
+    // The four waves' sums become one.
+    l = col_sum(l);
+    if (g == 0) {
+        lds_ml[wid][col][0] = m;
+        lds_ml[wid][col][1] = l;
+    }
+    __syncthreads();
+    const float mw[4] = {lds_ml[0][col][0], lds_ml[1][col][0], lds_ml[2][col][0], lds_ml[3][col][0]};
+    const float top = fmaxf(fmaxf(mw[0], mw[1]), fmaxf(mw[2], mw[3]));
+    const float mine = __builtin_amdgcn_exp2f(m - top);
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f4 o{acc[4 * j][i], acc[4 * j + 1][i], acc[4 * j + 2][i], acc[4 * j + 3][i]};
+            if constexpr (HL == 1) o = f4{o.x + lane_xor<8>(o.x), o.y + lane_xor<8>(o.y), o.z + lane_xor<8>(o.z), o.w + lane_xor<8>(o.w)};
+            *reinterpret_cast<f4 *>(&lds_o[wid][col][64 * j + 16 * g + 4 * i]) = o * mine;
+        }
+    __syncthreads();
+    for (int e = threadIdx.x; e < n * G * (D / 4); e += 256) {
+        const int cc = e / (D / 4), d = 4 * (e % (D / 4));
+        f4 o{0.f, 0.f, 0.f, 0.f};
+        float mt = lds_ml[0][cc][0], lt = 0.0f;
+#pragma unroll
+        for (int w = 1; w < W; ++w) mt = fmaxf(mt, lds_ml[w][cc][0]);
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            o += *reinterpret_cast<const f4 *>(&lds_o[w][cc][d]);
+            lt += lds_ml[w][cc][1] * __builtin_amdgcn_exp2f(lds_ml[w][cc][0] - mt);
+        }
+        if (sh.parts <= 1) {
+            const float inv = lt > 0.0f ? 1.0f / lt : 0.0f;
+            const int64_t at = (static_cast<int64_t>(rr.first + cc / G) * a.q_heads + h * G + cc % G) * D + d;
+            store4<DT>(a.o, at, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+        } else {
+            const int64_t slot = ((static_cast<int64_t>(seq) * c.heads + h) * splits + part) * cols + cc;
+            *reinterpret_cast<f4 *>(part_o + slot * D + d) = o;
+            if (d == 0) *reinterpret_cast<float2 *>(part_ml + 2 * slot) = make_float2(mt, lt);
+        }
+    }
+}
+
+// The parts' sums of one (sequence, KV head, column) become its output: 256 / (D / 4)
+// groups of threads share the parts, then LDS.
+template <int DT, int D>
+__global__ __launch_bounds__(256) void attn_join_kernel(Kv4Cache c, KvBatch b, Kv4Attn a, int cols, int splits,
+                                                        const float *part_o, const float *part_ml) {
+    constexpr int L = D / 4, GR = 256 / L;
+    __shared__ f4 lds_o[GR][L];
+    __shared__ float lds_l[GR];
+    const int seq = blockIdx.x, h = blockIdx.y, cc = blockIdx.z, G = a.q_heads / c.heads;
+    const RowRange rr = kv_rows(b, seq);
+    const int n = min(rr.n, b.max_q), len = kv_len(b, seq), pos0 = len - rr.n;
+    if (cc >= n * G) return;
+    const int lo_all = seen(max(pos0, 0), len, a.causal, a.window).lo;
+    const int hi_all = a.causal ? pos0 + n : (pos0 + n > 0 ? len : 0);
+    const Share sh = share(lo_all, hi_all, splits);
+    if (sh.parts <= 1) return;
+    const int64_t first = ((static_cast<int64_t>(seq) * c.heads + h) * splits) * cols + cc;
+    float top = kLowest;
+    for (int p = threadIdx.x & 63; p < sh.parts; p += 64) top = fmaxf(top, part_ml[2 * (first + static_cast<int64_t>(p) * cols)]);
+    top = wave_max_f32(top);
+    const int gr = threadIdx.x / L, d = 4 * (threadIdx.x % L);
+    f4 o{0.f, 0.f, 0.f, 0.f};
+    float l = 0.0f;
+    for (int p = gr; p < sh.parts; p += GR) {
+        const int64_t slot = first + static_cast<int64_t>(p) * cols;
+        const float2 ml = *reinterpret_cast<const float2 *>(part_ml + 2 * slot);
+        const float f = __builtin_amdgcn_exp2f(ml.x - top);
+        l += ml.y * f;
+        o += *reinterpret_cast<const f4 *>(part_o + slot * D + d) * f;
+    }
+    lds_o[gr][threadIdx.x % L] = o;
+    if (d == 0) lds_l[gr] = l;
+    __syncthreads();
+    if (gr == 0) {
+#pragma unroll
+        for (int k = 1; k < GR; ++k) {
+            o += lds_o[k][threadIdx.x];
+            l += lds_l[k];
+        }
+        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        const int64_t at = (static_cast<int64_t>(rr.first + cc / G) * a.q_heads + h * G + cc % G) * D + d;
+        store4<DT>(a.o, at, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+    }
+}
+
+// Parts of the context in a launch of the split kernel: enough workgroups for
+// several on each of the chip's 256 CUs, never parts of fewer than kMinChunk steps.
+constexpr int kSplitTarget = 2048, kMaxSplits = 256;
+struct SplitPlan {
+    int cols, splits;
+    int64_t part_o, part_ml;       // bytes
+};
+bool split_applies(const KvBatch &b, const Kv4Cache &c, int q_heads) { return static_cast<int64_t>(b.max_q) * (q_heads / c.heads) <= 16; }
+SplitPlan split_plan(const KvBatch &b, const Kv4Cache &c, int q_heads) {
+    SplitPlan p;
+    p.cols = b.max_q * (q_heads / c.heads);
+    const int64_t groups = static_cast<int64_t>(b.B) * c.heads;
+    const int64_t steps = (static_cast<int64_t>(b.max_pages) << b.page_shift) >> 5;
+    int64_t s = (kSplitTarget + groups - 1) / groups;
+    const int64_t most = (steps + kMinChunk - 1) / kMinChunk;
+    s = s < most ? s : most;
+    s = s < kMaxSplits ? s : kMaxSplits;
+    p.splits = static_cast<int>(s < 1 ? 1 : s);
+    const int64_t slots = p.splits > 1 ? groups * p.splits * p.cols : 0;
+    p.part_o = slots * c.D * 4;
+    p.part_ml = slots * 8;
+    return p;
+}
+
+template <int DT, int D>
+hipError_t launch_split(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, hipStream_t st) {
+    const SplitPlan p = split_plan(b, c, a.q_heads);
+    float *part_o = static_cast<float *>(a.workspace), *part_ml = part_o + p.part_o / 4;
+    const dim3 grid(static_cast<uint32_t>(b.B) * p.splits, c.heads), block(256);
+    if constexpr (DT != kDtF32) {
+        hipLaunchKernelGGL((attn_split_kernel<DT, D, 0>), grid, block, 0, st, c, b, a, p.cols, p.splits, part_o, part_ml);
+    } else {
+        if (p.cols <= 8)
+            hipLaunchKernelGGL((attn_split_kernel<DT, D, 1>), grid, block, 0, st, c, b, a, p.cols, p.splits, part_o, part_ml);
+        else
+            hipLaunchKernelGGL((attn_split_kernel<DT, D, 2>), grid, block, 0, st, c, b, a, p.cols, p.splits, part_o, part_ml);
+    }
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.splits == 1) return e;
+    hipLaunchKernelGGL((attn_join_kernel<DT, D>), dim3(b.B, c.heads, p.cols), block, 0, st, c, b, a, p.cols, p.splits,
+                       part_o, part_ml);
+    return hipGetLastError();
+}
+
+template <int DT, int D>
+hipError_t launch_d(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, hipStream_t st) {
+    if (split_applies(b, c, a.q_heads)) return launch_split<DT, D>(c, b, a, st);
+    hipLaunchKernelGGL((attn_plain_kernel<DT, D>), dim3(b.rows, a.q_heads), dim3(256), 0, st, c, b, a);
+    return hipGetLastError();
+}
+
 template <int DT>
 hipError_t launch_t(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, hipStream_t st) {
-    const dim3 grid(b.rows, a.q_heads), block(256);
-    if (c.D == 64) hipLaunchKernelGGL((attn_plain_kernel<DT, 64>), grid, block, 0, st, c, b, a);
-    else if (c.D == 128) hipLaunchKernelGGL((attn_plain_kernel<DT, 128>), grid, block, 0, st, c, b, a);
-    else hipLaunchKernelGGL((attn_plain_kernel<DT, 256>), grid, block, 0, st, c, b, a);
-    return hipGetLastError();
+    if (c.D == 64) return launch_d<DT, 64>(c, b, a, st);
+    if (c.D == 128) return launch_d<DT, 128>(c, b, a, st);
+    return launch_d<DT, 256>(c, b, a, st);
 }
 
 }  // namespace
 
-int64_t kv4_attn_workspace(const Kv4Cache &, const KvBatch &, int, int) { return 0; }
+int64_t kv4_attn_workspace(const Kv4Cache &c, const KvBatch &b, int q_heads, int) {
+    if (!split_applies(b, c, q_heads)) return 0;
+    const SplitPlan p = split_plan(b, c, q_heads);
+    return p.part_o + p.part_ml;
+}
 
 hipError_t launch_kv4_attn(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, int dtype, hipStream_t st) {
     if (dtype == kDtF32) return launch_t<kDtF32>(c, b, a, st);

@@ -70,16 +70,19 @@ def attention_tolerance(dtype, out, mass, reach, n_tokens):
     """How far an output may be from the 64-bit one, element by element.
 
     reach = max_t sm_scale sum_d |q_d k_d|: a query element enters the products with a relative error of at most
-    2^-16 (f32: two bf16 parts, each rounded to the nearest or cut: 8 + 8 bits) or 0 (bf16 and f16 queries are taken
+    2^-16 (f32: two 16-bit parts) or 0 (bf16 and f16 queries are taken
     exactly), the products are exact, the f32 sum of D of them rounds at most D times (D <= 256: 2^-16), and three more
     f32 roundings (scales, exponent) count 2^-22: a score is off by at most e = 2^-14.9 reach < 2^-14 reach, and
     every probability by a factor of at most exp(2 e) (its own score and the normaliser's).  The weight p * scale enters
-    with 2^-16 (f32, two parts) or 2^-8 (one bf16), exp2 and its products with 2^-21, and the f32 sum over n tokens, in
+    with 2^-16 (f32, two parts) or 2^-8 (one 16-bit part), exp2 and its products with 2^-21, and the f32 sum over n tokens, in
     partial sums, rounds at most 2 sqrt(n) + 64 times to first order (tiles of tokens, splits, waves).  The division and the
-    output's own rounding end it.  All are relative to mass = sum_t p_t |v_t|.  An f16 output below 2^-14 is a multiple of
+    output's own rounding end it.  Weights are f16 (f32: a sum of two) on a scale that puts the row's largest weight so
+    far at 2^3 or more, so each is off by up to f16's smallest step, 2^-24, in itself: 2^-27 of the largest, whose token
+    has a value of the highest level, 6, in some dimension, and thus n 2^-27 of the row's largest mass for n tokens.  All are relative to mass = sum_t p_t |v_t|.  An f16 output below 2^-14 is a multiple of
     2^-24, so its rounding is off by up to 2^-25 however small the value (f32 and bf16 reach down to 2^-126: 1e-30 covers
     them).
     """
     e = 2.0 ** -14 * reach[..., None]
     weight = (2.0 ** -16 if dtype == "f32" else 2.0 ** -8) + 2.0 ** -21 + (2 * np.sqrt(n_tokens) + 64) * 2.0 ** -24
-    return (np.expm1(2 * e) + 2 * weight) * mass + (O.EPS[dtype] / 2 + 2.0 ** -22) * np.abs(out) + (2.0 ** -25 if dtype == "f16" else 1e-30)
+    least = n_tokens * 2.0 ** -27 * np.max(mass, axis=-1, keepdims=True)
+    return (np.expm1(2 * e) + 2 * weight) * mass + (O.EPS[dtype] / 2 + 2.0 ** -22) * np.abs(out) + least + (2.0 ** -25 if dtype == "f16" else 1e-30)
