@@ -367,7 +367,7 @@ typedef struct rad_kv4_cache {
  *   max_q        no sequence has more rows than this (1 when q_start is NULL); later
  *                rows of a longer one are left as they were by rad_attn_kv4.
  *
- * Limits: B, rows < 2^24; max_pages * page_size < 2^30.
+ * Limits: B, rows < 2^22; max_pages * page_size < 2^30.
  */
 typedef struct rad_kv_batch {
     const int32_t *block_table;
@@ -435,7 +435,7 @@ int rad_kv4_read(const rad_kv4_cache *cache, const rad_kv_batch *batch, uint16_t
  * heads).
  *
  *   q, o      [rows][q_heads][D] of `dtype`, dense, 16-byte aligned; q_heads a multiple
- *             of the cache's heads.
+ *             of the cache's heads, at most 16384; rows * q_heads < 2^29.
  *   sm_scale  finite, > 0.
  *   causal    1: the row at position p sees tokens t <= p; 0: every token of its sequence.
  *   window    > 0: only tokens t > p - window; 0: no window.

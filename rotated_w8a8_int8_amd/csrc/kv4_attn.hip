@@ -175,10 +175,6 @@ __device__ __forceinline__ void f16_split8(const float (&w)[8], u4 &hi, u4 &low)
 __device__ __forceinline__ float max8(const float (&s)[8]) {
     return fmaxf(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])), fmaxf(fmaxf(s[4], s[5]), fmaxf(s[6], s[7])));
 }
-__device__ __forceinline__ float amax4(float4 v) {
-    return fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
-}
-
 // Maximum (sum) over the four lanes that hold one column.
 __device__ __forceinline__ float col_max(float v) {
     v = fmaxf(v, __shfl_xor(v, 16));
@@ -189,19 +185,124 @@ __device__ __forceinline__ float col_sum(float v) {
     return v + __shfl_xor(v, 32);
 }
 
-// How the context [lo, hi) of one sequence (a union over its rows) is shared out:
-// steps of 32 tokens, `chunk` of them a workgroup, in at most `splits` workgroups.
-struct Share {
-    int first, steps, chunk, parts;       // first step, number of steps, steps a part, parts in use
+// ---- how a call's work is shared out --------------------------------------
+//
+// A sequence's (row, head of the group) pairs of one KV head form tiles of TM; a tile's
+// context, in steps of 32 tokens, is cut into equal parts, one workgroup each.  Lengths
+// are known on the device alone, so every workgroup works out the same cut: `chunk`
+// steps a part such that about `target` workgroups result over all sequences and KV
+// heads (as many as the chip holds at once), the same number of parts for each tile of
+// a sequence.  With the sum over sequences of tiles * steps at most target / heads *
+// chunk, there are at most target / heads + tiles pieces a head, and at most target /
+// heads tiles in several parts, of 2 * target / heads parts together.  Each lane looks
+// at one sequence, 64 at a time; beyond kMostScanned sequences nothing is split.
+constexpr int kMostScanned = 512;
+struct Plan {
+    int tm, target, min_chunk, split;     // rows a tile; workgroups wanted; least steps a part; 0: one part a tile
+    int pieces, items, slots;             // bounds a KV head: workgroups, tiles in several parts, parts of those
 };
-constexpr int kMinChunk = 4;              // steps: one for each wave
-__device__ __forceinline__ Share share(int lo, int hi, int splits) {
-    Share s;
-    s.first = lo >> 5;
-    s.steps = hi > lo ? ((hi + 31) >> 5) - s.first : 0;
-    s.chunk = max(kMinChunk, (s.steps + splits - 1) / splits);
-    s.parts = (s.steps + s.chunk - 1) / s.chunk;
+struct Piece {
+    int seq, tile, part, parts, slot;     // parts 0: none.  slot: place among the parts kept apart
+};
+
+// Rows of a sequence that a call handles, and what they see together.
+struct SeqWork {
+    RowRange rr;
+    int n, len, pos0, lo, hi;             // rows handled, tokens, first row's position, tokens [lo, hi)
+};
+__device__ __forceinline__ SeqWork seq_work(const KvBatch &b, const Kv4Attn &a, int seq) {
+    SeqWork s;
+    s.rr = kv_rows(b, seq);
+    s.n = min(s.rr.n, b.max_q);
+    s.len = kv_len(b, seq);
+    s.pos0 = s.len - s.rr.n;
+    s.lo = seen(max(s.pos0, 0), s.len, a.causal, a.window).lo;
+    s.hi = a.causal ? s.pos0 + s.n : (s.pos0 + s.n > 0 ? s.len : 0);
+    if (s.hi < s.lo) s.hi = s.lo;
     return s;
+}
+__device__ __forceinline__ int steps_of(int lo, int hi) { return hi > lo ? ((hi + 31) >> 5) - (lo >> 5) : 0; }
+
+// Inclusive sum over the lanes of a wave: inside rows of 16, then row 0 into 1 and 2 into
+// 3, then rows 0 .. 1 into 2 .. 3.
+__device__ __forceinline__ int wave_scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);     // row_shr 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);    // row_bcast 15
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);    // row_bcast 31
+    return v;
+}
+
+// Steps a part: about `target` parts over all sequences and KV heads, rounded up.
+__device__ __forceinline__ int chunk_of(uint64_t total, const Plan &pl, int heads) {
+    const uint64_t all = total * static_cast<uint32_t>(heads) + static_cast<uint32_t>(pl.target - 1);
+    const int even = all >> 32 ? static_cast<int>(all / static_cast<uint32_t>(pl.target))
+                               : static_cast<int>(static_cast<uint32_t>(all) / static_cast<uint32_t>(pl.target));
+    return max(even, pl.min_chunk);
+}
+
+// The x-th piece of a KV head (ITEMS false), or the x-th tile in several parts (true).
+// Every lane of the wave calls it and gets the same answer.
+template <bool ITEMS>
+__device__ __forceinline__ Piece find_piece(const KvBatch &b, const Kv4Attn &a, const Plan &pl, int heads, int G, int x) {
+    const int lane = threadIdx.x & 63;
+    if (b.B == 1 && !ITEMS) {
+        const SeqWork s = seq_work(b, a, 0);
+        const int tiles = (s.n * G + pl.tm - 1) / pl.tm, steps = steps_of(s.lo, s.hi);
+        const int chunk = chunk_of(static_cast<uint64_t>(tiles) * static_cast<uint32_t>(steps), pl, heads);
+        const int parts = pl.split ? max(1, (steps + chunk - 1) / chunk) : 1;
+        const int tile = x / parts;
+        if (tile >= tiles || (parts > 1 && x >= pl.slots)) return Piece{0, 0, 0, 0, 0};
+        return Piece{0, tiles - 1 - tile, x % parts, parts, x};
+    }
+    uint64_t total = 0;
+    if (pl.split) {
+        for (int b0 = 0; b0 < b.B; b0 += 64) {
+            uint64_t t = 0;
+            if (b0 + lane < b.B) {
+                const SeqWork s = seq_work(b, a, b0 + lane);
+                t = static_cast<uint64_t>((s.n * G + pl.tm - 1) / pl.tm) * static_cast<uint32_t>(steps_of(s.lo, s.hi));
+            }
+            // in two parts, so that 64 of each fit 32 bits
+            const int low = wave_scan(static_cast<int>(t & 0xFFFFFFu)), high = wave_scan(static_cast<int>(t >> 24));
+            total += static_cast<uint32_t>(__builtin_amdgcn_readlane(low, 63)) +
+                     (static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(high, 63))) << 24);
+        }
+    }
+    const int chunk = chunk_of(total, pl, heads);
+    int before = 0, kept = 0;
+    for (int b0 = 0; b0 < b.B; b0 += 64) {
+        int tiles = 0, parts = 0;
+        if (b0 + lane < b.B) {
+            const SeqWork s = seq_work(b, a, b0 + lane);
+            tiles = (s.n * G + pl.tm - 1) / pl.tm;
+            parts = pl.split ? max(1, (steps_of(s.lo, s.hi) + chunk - 1) / chunk) : 1;
+        }
+        const int many = parts > 1 ? tiles : 0, mine = ITEMS ? many : tiles * parts, keep = many * parts;
+        const int sum = wave_scan(mine), sum_keep = wave_scan(keep);
+        const uint64_t hit = __ballot(mine > 0 && x >= before + sum - mine && x < before + sum);
+        if (hit) {
+            const int src = __builtin_ctzll(hit);
+            Piece p;
+            p.seq = b0 + src;
+            p.parts = __builtin_amdgcn_readlane(parts, src);
+            const int local = x - (before + __builtin_amdgcn_readlane(sum - mine, src));
+            const int slot0 = kept + __builtin_amdgcn_readlane(sum_keep - keep, src);
+            const int tile = ITEMS ? local : local / p.parts;
+            p.part = ITEMS ? 0 : local % p.parts;
+            p.slot = slot0 + tile * p.parts + p.part;
+            // holds for every ascending q_start; another must not leave the workspace
+            if (p.parts > 1 && (p.slot < 0 || p.slot + (ITEMS ? p.parts : 1) > pl.slots)) break;
+            // the last rows of a causal prompt see most: they go first
+            p.tile = __builtin_amdgcn_readlane(tiles, src) - 1 - tile;
+            return p;
+        }
+        before += __builtin_amdgcn_readlane(sum, 63);
+        kept += __builtin_amdgcn_readlane(sum_keep, 63);
+    }
+    return Piece{0, 0, 0, 0, 0};
 }
 
 // A step's codes and scales, one lane's share.
@@ -246,25 +347,23 @@ __device__ __forceinline__ float times_half(float f, const u4 &x, int i) {
     return fmaf(f, static_cast<float>(h[i & 1]), 0.0f);
 }
 
-// blockIdx: x sequence * splits + part of its context, y KV head.  cols = max_q * G <= 16
-// (HL 1: <= 8).  Partial sums go to part_o [B][heads][splits][cols][D] and
-// part_ml [..][cols][2], or the outputs straight to a.o where one part is in use.
+// blockIdx: x piece, y KV head.  cols = max_q * G <= 16 (HL 1: <= 8), one tile a
+// sequence.  Parts of a tile in several leave their sums in part_o [heads][slots][cols][D]
+// and part_ml [..][cols][2]; the others write the outputs.
 template <int DT, int D, int HL>
-__global__ __launch_bounds__(256, 2) void attn_split_kernel(Kv4Cache c, KvBatch b, Kv4Attn a, int cols, int splits,
-                                                         float *part_o, float *part_ml) {
+__global__ __launch_bounds__(256, 2) void attn_split_kernel(Kv4Cache c, KvBatch b, Kv4Attn a, Plan pl, int cols,
+                                                            float *part_o, float *part_ml) {
     constexpr int W = 4;
     __shared__ float lds_o[W][16][D + 4], lds_ml[W][16][2];
     const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 4, col = lane & 15;
-    const int h = blockIdx.y, seq = blockIdx.x / splits, part = blockIdx.x % splits, G = a.q_heads / c.heads;
-    const RowRange rr = kv_rows(b, seq);
-    const int n = min(rr.n, b.max_q), len = kv_len(b, seq), pos0 = len - rr.n;
-    if (n == 0) return;
-    // the union of what the rows see: the last row's end, the first row's beginning
-    const int lo_all = seen(max(pos0, 0), len, a.causal, a.window).lo;
-    const int hi_all = a.causal ? pos0 + n : (pos0 + n > 0 ? len : 0);
-    const Share sh = share(lo_all, hi_all, splits);
-    if (part >= max(sh.parts, 1)) return;
+    const int h = blockIdx.y, G = a.q_heads / c.heads;
+    const Piece pc = find_piece<false>(b, a, pl, c.heads, G, blockIdx.x);
+    if (pc.parts == 0) return;
+    const int seq = __builtin_amdgcn_readfirstlane(pc.seq);
+    const SeqWork sw = seq_work(b, a, seq);
+    const RowRange rr = sw.rr;
+    const int n = sw.n, len = sw.len, pos0 = sw.pos0;
 
     // this lane's column: row `ci` of the sequence, head h * G + cg
     const int cq = HL == 1 ? col & 7 : col;
@@ -272,31 +371,58 @@ __global__ __launch_bounds__(256, 2) void attn_split_kernel(Kv4Cache c, KvBatch 
     const int ci = used ? cq / G : 0, cg = used ? cq % G : 0;
     const TokenRange tr = seen(pos0 + ci, len, a.causal, a.window);
     const int64_t qrow = (static_cast<int64_t>(rr.first + ci) * a.q_heads + h * G + cg) * D;
+    // the query's values are asked for first, then the first steps
     constexpr int NK = D / 32;
+    float qv[NK][8];
+#pragma unroll
+    for (int j = 0; j < NK; ++j) {
+        const int64_t at = qrow + g * (D / 4) + 8 * j;
+        const float4 x = load4<DT>(a.q, at), y = load4<DT>(a.q, at + 4);
+        qv[j][0] = x.x; qv[j][1] = x.y; qv[j][2] = x.z; qv[j][3] = x.w;
+        qv[j][4] = y.x; qv[j][5] = y.y; qv[j][6] = y.z; qv[j][7] = y.w;
+    }
+
+    const int steps = steps_of(sw.lo, sw.hi), share = (steps + pc.parts - 1) / pc.parts;
+    const int begin = __builtin_amdgcn_readfirstlane((sw.lo >> 5) + pc.part * share);
+    const int end = __builtin_amdgcn_readfirstlane((sw.lo >> 5) + min((pc.part + 1) * share, steps));
+    const int per_page = b.page_shift - 5;                    // log2 of steps a page
+    const int32_t *table = b.block_table + static_cast<int64_t>(seq) * b.max_pages;
+    auto page_of = [&](int step) { return step < end ? table[step >> per_page] : -1; };
+    auto token_of = [&](int page, int step) {
+        const int64_t p = page >= 0 && page < c.pages ? page : 0;
+        return ((p * c.heads + h) << c.page_shift) + ((step << 5) & ((1 << c.page_shift) - 1));
+    };
+
+    // A wave's steps go through a ring: two (for D = 256, whose sums fill the registers,
+    // one) on their way while one is worked on.
+    constexpr int NB = D == 256 ? 2 : 3;
+    Step<D> ring[NB];
+    int page[NB];
+#pragma unroll
+    for (int k = 0; k < NB; ++k) page[k] = page_of(begin + wid + k * W);
+#pragma unroll
+    for (int k = 0; k < NB - 1; ++k)
+        if (begin + wid + k * W < end) load_step<D>(ring[k], c, token_of(page[k], begin + wid + k * W), g, col);
     u4 qf[NK], ql[HL == 2 ? NK : 1];
     float scale = a.sm_scale * kLog2e;
     {
-        float v[NK][8], big = 0.0f;
+        float big = 0.0f;
 #pragma unroll
-        for (int j = 0; j < NK; ++j) {
-            const int64_t at = qrow + g * (D / 4) + 8 * j;
-            const float4 x = load4<DT>(a.q, at), y = load4<DT>(a.q, at + 4);
-            v[j][0] = x.x; v[j][1] = x.y; v[j][2] = x.z; v[j][3] = x.w;
-            v[j][4] = y.x; v[j][5] = y.y; v[j][6] = y.z; v[j][7] = y.w;
-            big = fmaxf(big, fmaxf(amax4(x), amax4(y)));
-        }
+        for (int j = 0; j < NK; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(qv[j][i]));
         big = col_max(big);
         // largest value to [2^9, 2^10), undone in the scores' factor (both exact)
         const int e = big > 0.0f ? 10 - __builtin_amdgcn_frexp_expf(big) : 0;
 #pragma unroll
         for (int j = 0; j < NK; ++j) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[j][i] = used ? __builtin_amdgcn_ldexpf(v[j][i], e) : 0.0f;
+            for (int i = 0; i < 8; ++i) qv[j][i] = used ? __builtin_amdgcn_ldexpf(qv[j][i], e) : 0.0f;
             if constexpr (HL == 0) {
-                qf[j] = f16_pack8(v[j]);
+                qf[j] = f16_pack8(qv[j]);
             } else {
                 u4 hi, low;
-                f16_split8(v[j], hi, low);
+                f16_split8(qv[j], hi, low);
                 if constexpr (HL == 2) ql[j] = low;
                 qf[j] = HL == 1 && col >= 8 ? low : hi;
             }
@@ -309,22 +435,7 @@ __global__ __launch_bounds__(256, 2) void attn_split_kernel(Kv4Cache c, KvBatch 
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) acc[j] = f4{0.f, 0.f, 0.f, 0.f};
 
-    const int begin = sh.first + part * sh.chunk, end = min(begin + sh.chunk, sh.first + sh.steps);
-    const int per_page = b.page_shift - 5;                    // log2 of steps a page
-    const int32_t *table = b.block_table + static_cast<int64_t>(seq) * b.max_pages;
-    auto page_of = [&](int step) { return step < end ? table[step >> per_page] : -1; };
-    auto token_of = [&](int page, int step) {
-        const int64_t p = page >= 0 && page < c.pages ? page : 0;
-        return ((p * c.heads + h) << c.page_shift) + ((step << 5) & ((1 << c.page_shift) - 1));
-    };
-
-    Step<D> cur, nxt;
-    int page = page_of(begin + wid), page_n = page_of(begin + wid + W);
-    if (begin + wid < end) load_step<D>(cur, c, token_of(page, begin + wid), g, col);
-    for (int step = begin + wid; step < end; step += W) {
-        const int page_nn = page_of(step + 2 * W);
-        if (step + W < end) load_step<D>(nxt, c, token_of(page_n, step + W), g, col);
-        if (page >= 0 && page < c.pages) {
+    auto work = [&](Step<D> &cur, int step) {
             float s[8];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
@@ -397,10 +508,19 @@ __global__ __launch_bounds__(256, 2) void attn_split_kernel(Kv4Cache c, KvBatch 
                     acc[4 * j + x] = mma16(vf, wf, acc[4 * j + x]);
                 }
             }
+    };
+    for (int step = begin + wid; step < end;) {
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+            constexpr int ahead = NB - 1;
+            const int to = (k + ahead) % NB;
+            if (step + ahead * W < end) load_step<D>(ring[to], c, token_of(page[to], step + ahead * W), g, col);
+            const int now = page[k];
+            page[k] = page_of(step + NB * W);
+            if (now >= 0 && now < c.pages) work(ring[k], step);
+            step += W;
+            if (step >= end) break;
         }
-        cur = nxt;
-        page = page_n;
-        page_n = page_nn;
     }
 
     // The four waves' sums become one.
@@ -433,104 +553,120 @@ __global__ __launch_bounds__(256, 2) void attn_split_kernel(Kv4Cache c, KvBatch 
             o += *reinterpret_cast<const f4 *>(&lds_o[w][cc][d]);
             lt += lds_ml[w][cc][1] * __builtin_amdgcn_exp2f(lds_ml[w][cc][0] - mt);
         }
-        if (sh.parts <= 1) {
+        if (pc.parts == 1) {
             const float inv = lt > 0.0f ? 1.0f / lt : 0.0f;
             const int64_t at = (static_cast<int64_t>(rr.first + cc / G) * a.q_heads + h * G + cc % G) * D + d;
             store4<DT>(a.o, at, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
         } else {
-            const int64_t slot = ((static_cast<int64_t>(seq) * c.heads + h) * splits + part) * cols + cc;
+            const int64_t slot = (static_cast<int64_t>(h) * pl.slots + pc.slot) * cols + cc;
             *reinterpret_cast<f4 *>(part_o + slot * D + d) = o;
             if (d == 0) *reinterpret_cast<float2 *>(part_ml + 2 * slot) = make_float2(mt, lt);
         }
     }
 }
 
-// The parts' sums of one (sequence, KV head, column) become its output: 256 / (D / 4)
-// groups of threads share the parts, then LDS.
+// The parts' sums of a tile and KV head become its outputs, `wide` columns (of `cols`) a
+// workgroup: D / 4 threads take a part of a column, the rest of the 512 other columns and
+// parts, each with a running maximum of its own; LDS joins the parts.
 template <int DT, int D>
-__global__ __launch_bounds__(256) void attn_join_kernel(Kv4Cache c, KvBatch b, Kv4Attn a, int cols, int splits,
-                                                        const float *part_o, const float *part_ml) {
-    constexpr int L = D / 4, GR = 256 / L;
-    __shared__ f4 lds_o[GR][L];
-    __shared__ float lds_l[GR];
-    const int seq = blockIdx.x, h = blockIdx.y, cc = blockIdx.z, G = a.q_heads / c.heads;
-    const RowRange rr = kv_rows(b, seq);
-    const int n = min(rr.n, b.max_q), len = kv_len(b, seq), pos0 = len - rr.n;
-    if (cc >= n * G) return;
-    const int lo_all = seen(max(pos0, 0), len, a.causal, a.window).lo;
-    const int hi_all = a.causal ? pos0 + n : (pos0 + n > 0 ? len : 0);
-    const Share sh = share(lo_all, hi_all, splits);
-    if (sh.parts <= 1) return;
-    const int64_t first = ((static_cast<int64_t>(seq) * c.heads + h) * splits) * cols + cc;
-    float top = kLowest;
-    for (int p = threadIdx.x & 63; p < sh.parts; p += 64) top = fmaxf(top, part_ml[2 * (first + static_cast<int64_t>(p) * cols)]);
-    top = wave_max_f32(top);
-    const int gr = threadIdx.x / L, d = 4 * (threadIdx.x % L);
+__global__ __launch_bounds__(512) void attn_join_kernel(Kv4Cache c, KvBatch b, Kv4Attn a, Plan pl, int cols, int wide,
+                                                        const float *__restrict__ part_o,
+                                                        const float *__restrict__ part_ml) {
+    constexpr int L = D / 4, N = 512 / L;
+    __shared__ f4 lds_o[N][L];
+    __shared__ float lds_ml[N][2];
+    const int h = blockIdx.y, G = a.q_heads / c.heads;
+    const Piece pc = find_piece<true>(b, a, pl, c.heads, G, blockIdx.x);
+    if (pc.parts == 0) return;
+    const SeqWork sw = seq_work(b, a, pc.seq);
+    const int64_t first = (static_cast<int64_t>(h) * pl.slots + pc.slot) * cols;
+    const int idx = threadIdx.x / L, ln = threadIdx.x % L, d = 4 * ln;
+    const int at_col = idx % wide, gr = idx / wide, groups = N / wide, cc = blockIdx.z * wide + at_col;
+    const bool on = gr < groups && cc < sw.n * G;
     f4 o{0.f, 0.f, 0.f, 0.f};
-    float l = 0.0f;
-    for (int p = gr; p < sh.parts; p += GR) {
-        const int64_t slot = first + static_cast<int64_t>(p) * cols;
-        const float2 ml = *reinterpret_cast<const float2 *>(part_ml + 2 * slot);
-        const float f = __builtin_amdgcn_exp2f(ml.x - top);
-        l += ml.y * f;
-        o += *reinterpret_cast<const f4 *>(part_o + slot * D + d) * f;
+    float m = kLowest, l = 0.0f;
+    if (on) {
+#pragma unroll 4
+        for (int p = gr; p < pc.parts; p += groups) {
+            const int64_t slot = first + static_cast<int64_t>(p) * cols + cc;
+            const float2 ml = *reinterpret_cast<const float2 *>(part_ml + 2 * slot);
+            const f4 x = *reinterpret_cast<const f4 *>(part_o + slot * D + d);
+            const float mn = fmaxf(m, ml.x), f = __builtin_amdgcn_exp2f(m - mn), e = __builtin_amdgcn_exp2f(ml.x - mn);
+            l = l * f + ml.y * e;
+            o = o * f + x * e;
+            m = mn;
+        }
     }
-    lds_o[gr][threadIdx.x % L] = o;
-    if (d == 0) lds_l[gr] = l;
+    lds_o[idx][ln] = o;
+    if (ln == 0) {
+        lds_ml[idx][0] = m;
+        lds_ml[idx][1] = l;
+    }
     __syncthreads();
-    if (gr == 0) {
-#pragma unroll
-        for (int k = 1; k < GR; ++k) {
-            o += lds_o[k][threadIdx.x];
-            l += lds_l[k];
+    if (on && gr == 0) {
+        float top = m;
+        for (int k = 1; k < groups; ++k) top = fmaxf(top, lds_ml[k * wide + at_col][0]);
+        const float f = __builtin_amdgcn_exp2f(m - top);
+        o = o * f;
+        l = l * f;
+        for (int k = 1; k < groups; ++k) {
+            const float e = __builtin_amdgcn_exp2f(lds_ml[k * wide + at_col][0] - top);
+            l += lds_ml[k * wide + at_col][1] * e;
+            o += lds_o[k * wide + at_col][ln] * e;
         }
         const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-        const int64_t at = (static_cast<int64_t>(rr.first + cc / G) * a.q_heads + h * G + cc % G) * D + d;
+        const int64_t at = (static_cast<int64_t>(sw.rr.first + cc / G) * a.q_heads + h * G + cc % G) * D + d;
         store4<DT>(a.o, at, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
     }
 }
 
-// Parts of the context in a launch of the split kernel: enough workgroups for
-// several on each of the chip's 256 CUs, never parts of fewer than kMinChunk steps.
-constexpr int kSplitTarget = 2048, kMaxSplits = 256;
-struct SplitPlan {
-    int cols, splits;
-    int64_t part_o, part_ml;       // bytes
-};
-bool split_applies(const KvBatch &b, const Kv4Cache &c, int q_heads) { return static_cast<int64_t>(b.max_q) * (q_heads / c.heads) <= 16; }
-SplitPlan split_plan(const KvBatch &b, const Kv4Cache &c, int q_heads) {
-    SplitPlan p;
-    p.cols = b.max_q * (q_heads / c.heads);
-    const int64_t groups = static_cast<int64_t>(b.B) * c.heads;
-    const int64_t steps = (static_cast<int64_t>(b.max_pages) << b.page_shift) >> 5;
-    int64_t s = (kSplitTarget + groups - 1) / groups;
-    const int64_t most = (steps + kMinChunk - 1) / kMinChunk;
-    s = s < most ? s : most;
-    s = s < kMaxSplits ? s : kMaxSplits;
-    p.splits = static_cast<int>(s < 1 ? 1 : s);
-    const int64_t slots = p.splits > 1 ? groups * p.splits * p.cols : 0;
-    p.part_o = slots * c.D * 4;
-    p.part_ml = slots * 8;
+// The bounds of a plan (see above) for tiles of tm rows of `per` (row, head) pairs a row.
+Plan make_plan(const KvBatch &b, int heads, int G, int tm, int target, int min_chunk) {
+    Plan p{tm, target, min_chunk, 0, 0, 0, 0};
+    const int64_t steps = ((static_cast<int64_t>(b.max_pages) << b.page_shift) + 31) >> 5;
+    const int64_t rows = static_cast<int64_t>(b.max_q) * G < tm ? b.B : static_cast<int64_t>(b.rows) * G / tm + b.B;
+    p.split = b.B <= kMostScanned && steps > min_chunk;
+    const int64_t even = (target + heads - 1) / heads, cuts = (steps + min_chunk - 1) / min_chunk;
+    const int64_t extra = p.split ? (even < rows * cuts ? even : rows * cuts) : 0;
+    p.pieces = static_cast<int>(rows + extra);
+    p.items = static_cast<int>(extra < rows ? extra : rows);
+    p.slots = static_cast<int>(2 * extra < rows + extra ? 2 * extra : rows + extra);
     return p;
 }
 
+// Workgroups of the split kernel that the chip's 256 CUs hold at once (by registers
+// and LDS: 5, 3 and 2 a CU for heads of 64, 128 and 256).
+bool split_applies(const KvBatch &b, const Kv4Cache &c, int q_heads) {
+    return static_cast<int64_t>(b.max_q) * (q_heads / c.heads) <= 16;
+}
+Plan split_plan(const KvBatch &b, const Kv4Cache &c, int q_heads) {
+    const int target = 256 * (c.D == 64 ? 5 : c.D == 128 ? 3 : 2) * (b.B > 1 ? 2 : 1);
+    return make_plan(b, c.heads, q_heads / c.heads, 16, target, 4);
+}
+// Bytes of the parts' sums and of their statistics.
+int64_t sums_bytes(const Plan &p, const Kv4Cache &c, int cols) { return static_cast<int64_t>(c.heads) * p.slots * cols * c.D * 4; }
+int64_t stats_bytes(const Plan &p, const Kv4Cache &c, int cols) { return static_cast<int64_t>(c.heads) * p.slots * cols * 8; }
+
 template <int DT, int D>
 hipError_t launch_split(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, hipStream_t st) {
-    const SplitPlan p = split_plan(b, c, a.q_heads);
-    float *part_o = static_cast<float *>(a.workspace), *part_ml = part_o + p.part_o / 4;
-    const dim3 grid(static_cast<uint32_t>(b.B) * p.splits, c.heads), block(256);
+    const int cols = b.max_q * (a.q_heads / c.heads);
+    const Plan p = split_plan(b, c, a.q_heads);
+    float *part_o = static_cast<float *>(a.workspace), *part_ml = part_o + sums_bytes(p, c, cols) / 4;
+    const dim3 grid(p.pieces, c.heads), block(256);
     if constexpr (DT != kDtF32) {
-        hipLaunchKernelGGL((attn_split_kernel<DT, D, 0>), grid, block, 0, st, c, b, a, p.cols, p.splits, part_o, part_ml);
+        hipLaunchKernelGGL((attn_split_kernel<DT, D, 0>), grid, block, 0, st, c, b, a, p, cols, part_o, part_ml);
     } else {
-        if (p.cols <= 8)
-            hipLaunchKernelGGL((attn_split_kernel<DT, D, 1>), grid, block, 0, st, c, b, a, p.cols, p.splits, part_o, part_ml);
+        if (cols <= 8)
+            hipLaunchKernelGGL((attn_split_kernel<DT, D, 1>), grid, block, 0, st, c, b, a, p, cols, part_o, part_ml);
         else
-            hipLaunchKernelGGL((attn_split_kernel<DT, D, 2>), grid, block, 0, st, c, b, a, p.cols, p.splits, part_o, part_ml);
+            hipLaunchKernelGGL((attn_split_kernel<DT, D, 2>), grid, block, 0, st, c, b, a, p, cols, part_o, part_ml);
     }
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.splits == 1) return e;
-    hipLaunchKernelGGL((attn_join_kernel<DT, D>), dim3(b.B, c.heads, p.cols), block, 0, st, c, b, a, p.cols, p.splits,
-                       part_o, part_ml);
+    if (e != hipSuccess || p.items == 0) return e;
+    // few tiles: a workgroup a column, so that many parts are read side by side
+    const int most = 2048 / D, wide = p.items * c.heads < 256 ? 1 : cols < most ? cols : most;
+    hipLaunchKernelGGL((attn_join_kernel<DT, D>), dim3(p.items, c.heads, (cols + wide - 1) / wide), dim3(512), 0, st, c, b,
+                       a, p, cols, wide, part_o, part_ml);
     return hipGetLastError();
 }
 
@@ -552,8 +688,9 @@ hipError_t launch_t(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, hipSt
 
 int64_t kv4_attn_workspace(const Kv4Cache &c, const KvBatch &b, int q_heads, int) {
     if (!split_applies(b, c, q_heads)) return 0;
-    const SplitPlan p = split_plan(b, c, q_heads);
-    return p.part_o + p.part_ml;
+    const int cols = b.max_q * (q_heads / c.heads);
+    const Plan p = split_plan(b, c, q_heads);
+    return sums_bytes(p, c, cols) + stats_bytes(p, c, cols);
 }
 
 hipError_t launch_kv4_attn(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, int dtype, hipStream_t st) {

@@ -13,7 +13,7 @@ int dtype_bytes(int32_t dtype) {
     return 0;
 }
 
-constexpr int64_t kMaxRows = int64_t(1) << 24, kMaxTokens = int64_t(1) << 30;
+constexpr int64_t kMaxRows = int64_t(1) << 22, kMaxTokens = int64_t(1) << 30;
 
 // Shape and range of a cache descriptor (no pointers).
 int check_cache(const rad_kv4_cache *c) {
@@ -188,7 +188,7 @@ int check_attn(const rad_kv4_cache *c, const rad_kv_batch *b, int64_t q_heads, i
     const int empty = check_batch(c, b);
     if (empty < 0) return empty;
     if (q_heads < 1 || q_heads % c->heads != 0) return RAD_E_SHAPE;
-    if (q_heads > 16384 || b->rows * q_heads >= (int64_t(1) << 31)) return RAD_E_RANGE;
+    if (q_heads > 16384 || b->rows * q_heads >= (int64_t(1) << 29)) return RAD_E_RANGE;
     return empty;
 }
 }  // namespace
