@@ -154,9 +154,15 @@ def _check(status: int, call: str) -> None:
 
 # ---------------------------------------------------------------- tensors --
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dev(t, dtype, name):
@@ -194,7 +200,7 @@ def _same_device(ref, *named):
 
 
 def _stream(t):
-    return _torch().cuda.current_stream(t.device).cuda_stream
+    return _torch()._C._cuda_getCurrentRawStream(t.get_device())
 
 
 @dataclass
@@ -448,9 +454,14 @@ def probe_mfma_i8(src, blocks: int, ksteps: int, lds_fed: bool, out=None):
 
 # ------------------------------------------------- between a layer's linears --
 
+_dtype_codes = {}
+
+
 def _dtypes():
-    torch = _torch()
-    return {torch.float32: RAD_DT_F32, torch.bfloat16: RAD_DT_BF16, torch.float16: RAD_DT_F16}
+    if not _dtype_codes:
+        torch = _torch()
+        _dtype_codes.update({torch.float32: RAD_DT_F32, torch.bfloat16: RAD_DT_BF16, torch.float16: RAD_DT_F16})
+    return _dtype_codes
 
 
 def _values(t, name):
@@ -464,15 +475,28 @@ def _values(t, name):
     return dt
 
 
-def _enqueue(name, device, fn, *args):
-    """Call `fn` on the current stream of `device`, with that device current."""
+def _ptr(t, dtype, shape, ref, name):
+    """The address of a contiguous tensor of this type and shape on ref's GPU; raises what is wrong with another."""
+    if (isinstance(t, _torch().Tensor) and t.dtype == dtype and t.shape == shape and t.is_contiguous()
+            and t.is_cuda and t.get_device() == ref.get_device()):
+        return t.data_ptr()
+    _dev(t, dtype, name)
+    _shape(t, shape, name)
+    _same_device(ref, (t, name))
+    raise AssertionError(name)
+
+
+def _enqueue(name, index, fn, *args):
+    """Call `fn` on the current stream of GPU `index`, with that GPU current."""
     torch = _torch()
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() == device.index:
-        _check(fn(*args, stream), name)
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if torch.cuda.current_device() == index:
+        status = fn(*args, stream)
     else:
-        with torch.cuda.device(device):
-            _check(fn(*args, stream), name)
+        with torch.cuda.device(index):
+            status = fn(*args, stream)
+    if status != RAD_OK:
+        raise RadError(status, name)
 
 
 def add_rmsnorm_quant_i8(x, gamma, residual=None, eps: float = 1e-6, rotate: bool = True, q=None, scale=None,
@@ -482,36 +506,28 @@ def add_rmsnorm_quant_i8(x, gamma, residual=None, eps: float = 1e-6, rotate: boo
     ``x`` [M][K] (f32, bf16 or f16), ``gamma`` f32 [K].  With ``residual`` [M][K] of the same type the sum
     goes to ``residual_out`` (default: in place, into ``residual``).  Returns (q, scale, the sum or None)."""
     torch = _torch()
-    dt = _values(x, "x")
-    _dev(x, x.dtype, "x")
-    _dev(gamma, torch.float32, "gamma")
+    dt, dtype = _values(x, "x"), x.dtype
     if x.dim() != 2:
         raise ValueError("x must be 2-D, got shape %s" % (tuple(x.shape),))
     M, K = x.shape
-    _shape(gamma, (K,), "gamma")
+    xp = _ptr(x, dtype, (M, K), x, "x")
+    gp = _ptr(gamma, torch.float32, (K,), x, "gamma")
     if q is None:
         q = torch.empty((M, K), dtype=torch.int8, device=x.device)
     if scale is None:
         scale = torch.empty((M,), dtype=torch.float32, device=x.device)
-    _dev(q, torch.int8, "q")
-    _dev(scale, torch.float32, "scale")
-    _shape(q, (M, K), "q")
-    _shape(scale, (M,), "scale")
+    qp = _ptr(q, torch.int8, (M, K), x, "q")
+    sp = _ptr(scale, torch.float32, (M,), x, "scale")
+    rp = op = None
     if residual is not None:
-        _dev(residual, x.dtype, "residual")
-        _shape(residual, (M, K), "residual")
+        rp = _ptr(residual, dtype, (M, K), x, "residual")
         if residual_out is None:
             residual_out = residual
-        _dev(residual_out, x.dtype, "residual_out")
-        _shape(residual_out, (M, K), "residual_out")
+        op = _ptr(residual_out, dtype, (M, K), x, "residual_out")
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
-    _same_device(x, (gamma, "gamma"), (residual, "residual"), (residual_out, "residual_out"), (q, "q"),
-                 (scale, "scale"))
-    _enqueue("rad_add_rmsnorm_quant_i8", x.device, lib().rad_add_rmsnorm_quant_i8, x.data_ptr(),
-             None if residual is None else residual.data_ptr(),
-             None if residual_out is None else residual_out.data_ptr(), gamma.data_ptr(), eps, q.data_ptr(),
-             scale.data_ptr(), M, K, dt, 1 if rotate else 0)
+    _enqueue("rad_add_rmsnorm_quant_i8", x.get_device(), lib().rad_add_rmsnorm_quant_i8, xp, rp, op, gp, eps, qp, sp,
+             M, K, dt, 1 if rotate else 0)
     return q, scale, residual_out
 
 
@@ -540,6 +556,7 @@ class KV4Cache:
         _same_device(k_codes, (k_scale, "k_scale"), (v_codes, "v_codes"), (v_scale, "v_scale"))
         self.k_codes, self.k_scale, self.v_codes, self.v_scale = k_codes, k_scale, v_codes, v_scale
         self.pages, self.heads, self.page_size, self.D = pages, heads, page, 2 * half
+        self.device_index = k_codes.get_device()
         self._desc = KV4CacheDesc(k_codes.data_ptr(), k_scale.data_ptr(), v_codes.data_ptr(), v_scale.data_ptr(),
                                   pages, heads, page, 2 * half)
 
@@ -578,17 +595,29 @@ class KVBatch:
         _same_device(block_table, (seq_len, "seq_len"), (q_start, "q_start"))
         self.block_table, self.seq_len, self.q_start, self.rows = block_table, seq_len, q_start, rows
         self.max_q = (rows if max_q is None else int(max_q)) if q_start is not None else 1
+        self._workspace = {}                    # sizes of a call -> bytes of its workspace
         self._desc = KVBatchDesc(block_table.data_ptr(), seq_len.data_ptr(),
                                  None if q_start is None else q_start.data_ptr(), B, max_pages, rows, self.max_q)
 
 
-def _head_rows(t, rows, heads, D, name):
-    """[rows][heads][D] values whose token rows may lie apart: the distance in values."""
-    if t.dim() != 3 or tuple(t.shape) != (rows, heads, D):
+def _head_rows(t, dtype, rows, heads, D, ref, name):
+    """[rows][heads][D] values whose token rows may lie apart: address and distance in values."""
+    if not isinstance(t, _torch().Tensor) or t.dtype != dtype:
+        _values(t, name)
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != (rows, heads, D):
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), (rows, heads, D)))
-    if (D > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != D):
+    apart, head, one = t.stride()
+    if one != 1 or (head != D and heads > 1):
         raise ValueError("%s must be contiguous in its last two dims" % name)
-    return t.stride(0) if rows > 1 else heads * D
+    if not t.is_cuda or t.get_device() != ref.device_index:
+        raise ValueError("%s is on %s, the cache on GPU %d" % (name, t.device, ref.device_index))
+    return t.data_ptr(), apart if rows > 1 else heads * D
+
+
+def _one_device(cache, batch):
+    if batch.block_table.get_device() != cache.device_index:
+        raise ValueError("the batch is on %s, the cache on GPU %d" % (batch.block_table.device, cache.device_index))
 
 
 def kv4_append(cache: KV4Cache, batch: KVBatch, k, v, q=None, rope=None, rope_style: int = 0, rotate: bool = True,
@@ -598,36 +627,27 @@ def kv4_append(cache: KV4Cache, batch: KVBatch, k, v, q=None, rope=None, rope_st
     [rows][q_heads][D] turned alike (q.k kept), or None."""
     torch = _torch()
     rows, H, D = batch.rows, cache.heads, cache.D
-    dt = _values(k, "k")
-    ldk = _head_rows(k, rows, H, D, "k")
-    if _values(v, "v") != dt:
-        raise TypeError("v is %s, k is %s" % (v.dtype, k.dtype))
-    ldv = _head_rows(v, rows, H, D, "v")
-    q_heads, ldq = 0, 0
+    _one_device(cache, batch)
+    dt, dtype = _values(k, "k"), k.dtype
+    kp, ldk = _head_rows(k, dtype, rows, H, D, cache, "k")
+    vp, ldv = _head_rows(v, dtype, rows, H, D, cache, "v")
+    q_heads, ldq, qp, op = 0, 0, None, None
     if q is not None:
-        if _values(q, "q") != dt:
-            raise TypeError("q is %s, k is %s" % (q.dtype, k.dtype))
-        if q.dim() != 3:
-            raise ValueError("q must be 3-D, got shape %s" % (tuple(q.shape),))
-        q_heads = int(q.shape[1])
-        ldq = _head_rows(q, rows, q_heads, D, "q")
+        q_heads = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else -1
+        qp, ldq = _head_rows(q, dtype, rows, q_heads, D, cache, "q")
         if q_out is None:
-            q_out = torch.empty((rows, q_heads, D), dtype=q.dtype, device=q.device)
-        _dev(q_out, q.dtype, "q_out")
-        _shape(q_out, (rows, q_heads, D), "q_out")
+            q_out = torch.empty((rows, q_heads, D), dtype=dtype, device=q.device)
+        op = _ptr(q_out, dtype, (rows, q_heads, D), cache.k_codes, "q_out")
     elif q_out is not None:
         raise ValueError("q_out needs q")
     table = None
     if rope is not None:
-        _dev(rope, torch.float32, "rope")
-        if rope.dim() != 2:
-            raise ValueError("rope must be 2-D, got shape %s" % (tuple(rope.shape),))
-        table = ctypes.byref(RopeDesc(rope.data_ptr(), rope.shape[0], rope.shape[1], rope_style))
-    _same_device(cache.k_codes, (batch.seq_len, "batch"), (k, "k"), (v, "v"), (q, "q"), (q_out, "q_out"),
-                 (rope, "rope"))
-    _enqueue("rad_kv4_append", k.device, lib().rad_kv4_append, cache._desc, batch._desc, k.data_ptr(), ldk,
-             v.data_ptr(), ldv, None if q is None else q.data_ptr(), ldq, q_heads,
-             None if q is None else q_out.data_ptr(), table, 1 if rotate else 0, dt)
+        if not isinstance(rope, torch.Tensor) or rope.dim() != 2:
+            raise ValueError("rope must be a 2-D tensor")
+        table = RopeDesc(_ptr(rope, torch.float32, rope.shape, cache.k_codes, "rope"), rope.shape[0], rope.shape[1],
+                         rope_style)
+    _enqueue("rad_kv4_append", cache.device_index, lib().rad_kv4_append, cache._desc, batch._desc, kp, ldk, vp, ldv,
+             qp, ldq, q_heads, op, table, 1 if rotate else 0, dt)
     return q_out
 
 
@@ -635,25 +655,26 @@ def kv4_read(cache: KV4Cache, batch: KVBatch, k=None, v=None):
     """The cached keys and values of the batch's rows as bf16 [rows][heads][D]."""
     torch = _torch()
     shape = (batch.rows, cache.heads, cache.D)
+    _one_device(cache, batch)
     if k is None:
         k = torch.empty(shape, dtype=torch.bfloat16, device=cache.k_codes.device)
     if v is None:
         v = torch.empty(shape, dtype=torch.bfloat16, device=cache.k_codes.device)
-    _dev(k, torch.bfloat16, "k")
-    _dev(v, torch.bfloat16, "v")
-    _shape(k, shape, "k")
-    _shape(v, shape, "v")
-    _same_device(cache.k_codes, (batch.seq_len, "batch"), (k, "k"), (v, "v"))
-    _enqueue("rad_kv4_read", k.device, lib().rad_kv4_read, cache._desc, batch._desc, k.data_ptr(), v.data_ptr())
+    kp = _ptr(k, torch.bfloat16, shape, cache.k_codes, "k")
+    vp = _ptr(v, torch.bfloat16, shape, cache.k_codes, "v")
+    _enqueue("rad_kv4_read", cache.device_index, lib().rad_kv4_read, cache._desc, batch._desc, kp, vp)
     return k, v
 
 
 def attn_kv4_workspace(cache: KV4Cache, batch: KVBatch, q_heads: int, dtype) -> int:
     """Bytes of workspace that attn_kv4 needs for these sizes."""
-    n = ctypes.c_int64(0)
-    _check(lib().rad_attn_kv4_workspace(cache._desc, batch._desc, q_heads, _dtypes()[dtype], ctypes.byref(n)),
-           "rad_attn_kv4_workspace")
-    return n.value
+    key = (cache.heads, cache.page_size, cache.D, q_heads, dtype)
+    if key not in batch._workspace:
+        n = ctypes.c_int64(0)
+        _check(lib().rad_attn_kv4_workspace(cache._desc, batch._desc, q_heads, _dtypes()[dtype], ctypes.byref(n)),
+               "rad_attn_kv4_workspace")
+        batch._workspace[key] = n.value
+    return batch._workspace[key]
 
 
 def attn_kv4(cache: KV4Cache, batch: KVBatch, q, sm_scale: float, causal: bool = True, window: int = 0, o=None,
@@ -661,21 +682,21 @@ def attn_kv4(cache: KV4Cache, batch: KVBatch, q, sm_scale: float, causal: bool =
     """Attention of ``q`` [rows][q_heads][D] over the paged 4-bit cache; rows that see nothing give zeros."""
     torch = _torch()
     dt = _values(q, "q")
-    _dev(q, q.dtype, "q")
-    if q.dim() != 3 or q.shape[0] != batch.rows or q.shape[2] != cache.D:
-        raise ValueError("q has shape %s, expected (%d, heads, %d)" % (tuple(q.shape), batch.rows, cache.D))
+    shape, dtype = q.shape, q.dtype
+    if len(shape) != 3 or shape[0] != batch.rows or shape[2] != cache.D:
+        raise ValueError("q has shape %s, expected (%d, heads, %d)" % (tuple(shape), batch.rows, cache.D))
+    _one_device(cache, batch)
+    qp = _ptr(q, dtype, shape, cache.k_codes, "q")
     if o is None:
         o = torch.empty_like(q)
-    _dev(o, q.dtype, "o")
-    _shape(o, q.shape, "o")
-    q_heads = int(q.shape[1])
-    n = attn_kv4_workspace(cache, batch, q_heads, q.dtype)
-    if workspace is None and n:
-        workspace = torch.empty((n,), dtype=torch.uint8, device=q.device)
+    op = _ptr(o, dtype, shape, cache.k_codes, "o")
+    n = attn_kv4_workspace(cache, batch, shape[1], dtype)
+    wp, size = None, 0
     if workspace is not None:
-        _dev(workspace, torch.uint8, "workspace")
-    _same_device(cache.k_codes, (batch.seq_len, "batch"), (q, "q"), (o, "o"), (workspace, "workspace"))
-    _enqueue("rad_attn_kv4", q.device, lib().rad_attn_kv4, cache._desc, batch._desc, q.data_ptr(), q_heads, sm_scale,
-             1 if causal else 0, window, o.data_ptr(), None if workspace is None else workspace.data_ptr(),
-             0 if workspace is None else workspace.numel(), dt)
+        wp, size = _ptr(workspace, torch.uint8, workspace.shape, cache.k_codes, "workspace"), workspace.numel()
+    elif n:
+        workspace = torch.empty((n,), dtype=torch.uint8, device=q.device)
+        wp, size = workspace.data_ptr(), n
+    _enqueue("rad_attn_kv4", cache.device_index, lib().rad_attn_kv4, cache._desc, batch._desc, qp, shape[1], sm_scale,
+             1 if causal else 0, window, op, wp, size, dt)
     return o

@@ -177,7 +177,7 @@ def test_binding_refusals(torch):
     k = torch.zeros(3, 2, 64, device="cuda")
     with pytest.raises(ValueError, match="shape"):
         B.kv4_append(dev, batch, k[:2], k)
-    with pytest.raises(TypeError, match="v is"):
+    with pytest.raises(TypeError, match="v must be"):
         B.kv4_append(dev, batch, k, k.half())
     with pytest.raises(ValueError, match="contiguous"):
         B.kv4_append(dev, batch, torch.zeros(3, 64, 2, device="cuda").transpose(1, 2), k)
