@@ -20,92 +20,9 @@ __device__ __forceinline__ TokenRange seen(int pos, int len, int causal, int win
     return r;
 }
 
-// One workgroup per (row, query head); tiles of 256 tokens, a thread a token
-// for the scores and a thread a dimension (of 256 / D token groups) for the sum.
-template <int DT, int D>
-__global__ __launch_bounds__(256) void attn_plain_kernel(Kv4Cache c, KvBatch b, Kv4Attn a) {
-    __shared__ float qs[D], ps[256], red[8], part[256];
-    const int row = blockIdx.x, hq = blockIdx.y, tid = threadIdx.x;
-    const int h = hq / (a.q_heads / c.heads);
-    const int seq = kv_seq_of(b, row);
-    if (seq < 0) return;
-    const RowRange rr = kv_rows(b, seq);
-    if (row - rr.first >= b.max_q) return;
-    const int len = kv_len(b, seq), pos = len - rr.n + (row - rr.first);
-    const TokenRange tr = seen(pos, len, a.causal, a.window);
-    const int64_t at = (static_cast<int64_t>(row) * a.q_heads + hq) * D;
-    if (tid < D / 4) {
-        const float4 x = load4<DT>(a.q, at + 4 * tid);
-        const float f = a.sm_scale * kLog2e;
-        qs[4 * tid] = x.x * f; qs[4 * tid + 1] = x.y * f; qs[4 * tid + 2] = x.z * f; qs[4 * tid + 3] = x.w * f;
-    }
-    __syncthreads();
-    float m = -INFINITY, l = 0.0f, acc = 0.0f;
-    const int d = tid % D, group = tid / D, per = 256 / (256 / D);         // tokens of a tile for a group
-    for (int t0 = tr.lo & ~31; t0 < tr.hi; t0 += 256) {
-        const int t = t0 + tid;
-        const int page = t < tr.hi && t >= tr.lo ? kv_page(b, seq, t, c.pages) : -1;
-        float s = -INFINITY, sv = 0.0f;
-        if (page >= 0) {
-            const int64_t vec = (static_cast<int64_t>(page) * c.heads + h) << c.page_shift;
-            const int64_t tok = vec + (t & ((1 << c.page_shift) - 1));
-            const uint32_t *kp = reinterpret_cast<const uint32_t *>(c.k_codes + tok * (D / 2));
-            float sum = 0.0f;
-            for (int j = 0; j < D / 8; ++j) {
-                const uint32_t w = kp[j];
-                const f2v x0 = e2m1_pair<0>(w), x1 = e2m1_pair<1>(w), x2 = e2m1_pair<2>(w), x3 = e2m1_pair<3>(w);
-                const float *qq = qs + 8 * j;
-                sum += qq[0] * x0[0] + qq[1] * x0[1] + qq[2] * x1[0] + qq[3] * x1[1] + qq[4] * x2[0] + qq[5] * x2[1] +
-                       qq[6] * x3[0] + qq[7] * x3[1];
-            }
-            s = sum * f16_widen(c.k_scale[tok]);
-            sv = f16_widen(c.v_scale[tok]);
-        }
-        const float wm = wave_max_f32(s);
-        if ((tid & 63) == 0) red[tid >> 6] = wm;
-        __syncthreads();
-        const float mt = fmaxf(m, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-        const float p = s > -INFINITY ? __builtin_amdgcn_exp2f(s - mt) : 0.0f;
-        const float ws = wave_sum_f32(p);
-        if ((tid & 63) == 0) red[4 + (tid >> 6)] = ws;
-        ps[tid] = s > -INFINITY ? p * sv : 0.0f;
-        __syncthreads();
-        const float scale = m > -INFINITY ? __builtin_amdgcn_exp2f(m - mt) : 0.0f;
-        l = l * scale + ((red[4] + red[5]) + (red[6] + red[7]));
-        acc *= scale;
-        m = mt;
-        for (int j = 0; j < per; j += 8) {
-            const int tj = t0 + group * per + j;
-            const int pg = tj < tr.hi ? kv_page(b, seq, tj, c.pages) : -1;
-            if (pg < 0) continue;
-            const int64_t vec = (static_cast<int64_t>(pg) * c.heads + h) << c.page_shift;
-            const int64_t oct = (vec + (tj & ((1 << c.page_shift) - 1))) >> 3;
-            const uint32_t w = reinterpret_cast<const uint32_t *>(c.v_codes)[oct * D + d];
-            const f2v x0 = e2m1_pair<0>(w), x1 = e2m1_pair<1>(w), x2 = e2m1_pair<2>(w), x3 = e2m1_pair<3>(w);
-            const float *pp = ps + group * per + j;
-            acc += pp[0] * x0[0] + pp[1] * x0[1] + pp[2] * x1[0] + pp[3] * x1[1] + pp[4] * x2[0] + pp[5] * x2[1] +
-                   pp[6] * x3[0] + pp[7] * x3[1];
-        }
-        __syncthreads();
-    }
-    part[tid] = acc;
-    __syncthreads();
-    if (tid < D / 4) {
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int g = 0; g < 256 / D; ++g) {
-            const float *pp = part + g * D + 4 * tid;
-            o.x += pp[0]; o.y += pp[1]; o.z += pp[2]; o.w += pp[3];
-        }
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-        store4<DT>(a.o, at + 4 * tid, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-    }
-}
-
-// ---- few rows: the context split over workgroups ---------------------------
-//
-// A wave takes 32 tokens a step and all the call's (row, head) pairs of one KV
-// head as the columns of its matrix products (16 at most), transposed so that
-// nothing crosses lanes between them:
+// The (row, head) pairs of a sequence that share a KV head are the columns of transposed
+// matrix products, 16 a product, NT of them a wave, so that nothing crosses lanes between
+// the two products of a step of 32 tokens:
 //
 //   S^T [32 tokens][16 cols] = K Q^T    two 16x16x32 tiles; A: a lane holds D/4 dims of
 //                                       one token, one dword (8 dims) per product
@@ -115,6 +32,8 @@ __global__ __launch_bounds__(256) void attn_plain_kernel(Kv4Cache c, KvBatch b, 
 // Row r of score tile u is token 8 (r / 4) + 4 u + r % 4 of the step, so lane (g, c)
 // (g = lane / 16, c = lane % 16) comes out of S^T with the scores of tokens 8 g ..
 // 8 g + 7 of column c: the B operand that O^T needs against the value octets.
+// Codes go from memory to registers to the products; a workgroup's four waves take
+// WC groups of columns and 4 / WC groups of steps (joined through LDS at the end).
 //
 // e2m1 levels are exact in f16; the f16 scales meet the scores (keys) and the
 // probabilities (values) in f32.  A query row is taken times a power of two that puts
@@ -313,20 +232,26 @@ struct Step {
     u4 ks, vs;                  // f16 scales of the octet
 };
 
-template <int D>
+// NT: nontemporal, for codes that only one workgroup reads
+template <bool NT>
+__device__ __forceinline__ u4 load16(const u4 *p) {
+    if constexpr (NT) return __builtin_nontemporal_load(p);
+    else return *p;
+}
+template <int D, bool NT>
 __device__ __forceinline__ void load_step(Step<D> &s, const Kv4Cache &c, int64_t tok, int g, int r) {
     // tok: index of the step's first token in the cache's [pages][heads][page] order
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
         const uint8_t *p = c.k_codes + (tok + 8 * (r >> 2) + 4 * u + (r & 3)) * (D / 2) + g * (D / 8);
         if constexpr (D == 64) {
-            const u2 x = __builtin_nontemporal_load(reinterpret_cast<const u2 *>(p));
+            const u2 x = *reinterpret_cast<const u2 *>(p);
             s.k[u][0] = x.x;
             s.k[u][1] = x.y;
         } else {
 #pragma unroll
             for (int j = 0; j < D / 128; ++j) {
-                const u4 x = __builtin_nontemporal_load(reinterpret_cast<const u4 *>(p) + j);
+                const u4 x = load16<NT>(reinterpret_cast<const u4 *>(p) + j);
                 s.k[u][4 * j] = x.x;
                 s.k[u][4 * j + 1] = x.y;
                 s.k[u][4 * j + 2] = x.z;
@@ -336,7 +261,7 @@ __device__ __forceinline__ void load_step(Step<D> &s, const Kv4Cache &c, int64_t
     }
     const u4 *vp = reinterpret_cast<const u4 *>(c.v_codes) + (((tok >> 3) + g) * D + 4 * r) / 4;
 #pragma unroll
-    for (int j = 0; j < D / 64; ++j) s.v[j] = __builtin_nontemporal_load(vp + 16 * j);
+    for (int j = 0; j < D / 64; ++j) s.v[j] = load16<NT>(vp + 16 * j);
     s.ks = *reinterpret_cast<const u4 *>(c.k_scale + tok + 8 * g);
     s.vs = *reinterpret_cast<const u4 *>(c.v_scale + tok + 8 * g);
 }
@@ -347,44 +272,65 @@ __device__ __forceinline__ float times_half(float f, const u4 &x, int i) {
     return fmaf(f, static_cast<float>(h[i & 1]), 0.0f);
 }
 
-// blockIdx: x piece, y KV head.  cols = max_q * G <= 16 (HL 1: <= 8), one tile a
-// sequence.  Parts of a tile in several leave their sums in part_o [heads][slots][cols][D]
+// blockIdx: x piece, y KV head.  A tile has TM = 16 * NT * WC columns, `cols` of them in
+// use at most.  Parts of a tile in several leave their sums in part_o [heads][slots][cols][D]
 // and part_ml [..][cols][2]; the others write the outputs.
-template <int DT, int D, int HL>
-__global__ __launch_bounds__(256, 2) void attn_split_kernel(Kv4Cache c, KvBatch b, Kv4Attn a, Plan pl, int cols,
-                                                            float *part_o, float *part_ml) {
-    constexpr int W = 4;
-    __shared__ float lds_o[W][16][D + 4], lds_ml[W][16][2];
+template <int DT, int D, int HL, int NT, int WC>
+__global__ __launch_bounds__(256, 2) void attn_kernel(Kv4Cache c, KvBatch b, Kv4Attn a, Plan pl, int cols,
+                                                      float *part_o, float *part_ml) {
+    constexpr int TG = 4 / WC, TC = 16 * NT, TM = TC * WC;
+    static_assert(HL != 1 || (NT == 1 && WC == 1), "low parts ride along in one product of columns");
+    __shared__ float lds_o[TG > 1 ? TG : 1][TG > 1 ? TM : 1][D + 4], lds_ml[TG > 1 ? TG : 1][TM][2];
     const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int g = lane >> 4, col = lane & 15;
+    const int g = lane >> 4, col = lane & 15, tg = wid / WC, wc = wid % WC;
     const int h = blockIdx.y, G = a.q_heads / c.heads;
     const Piece pc = find_piece<false>(b, a, pl, c.heads, G, blockIdx.x);
     if (pc.parts == 0) return;
     const int seq = __builtin_amdgcn_readfirstlane(pc.seq);
     const SeqWork sw = seq_work(b, a, seq);
     const RowRange rr = sw.rr;
-    const int n = sw.n, len = sw.len, pos0 = sw.pos0;
+    const int len = sw.len, pos0 = sw.pos0, pairs = sw.n * G, tile0 = pc.tile * TM;   // first pair of the tile
 
-    // this lane's column: row `ci` of the sequence, head h * G + cg
-    const int cq = HL == 1 ? col & 7 : col;
-    const bool used = cq < n * G;
-    const int ci = used ? cq / G : 0, cg = used ? cq % G : 0;
-    const TokenRange tr = seen(pos0 + ci, len, a.causal, a.window);
-    const int64_t qrow = (static_cast<int64_t>(rr.first + ci) * a.q_heads + h * G + cg) * D;
-    // the query's values are asked for first, then the first steps
-    constexpr int NK = D / 32;
-    float qv[NK][8];
+    // the tile's and this wave's share of the context
+    const int tile_last = min(tile0 + TM, pairs) - 1, wave0 = tile0 + wc * TC, wave_last = min(wave0 + TC, pairs) - 1;
+    const bool idle = wave0 >= pairs;
+    auto range = [&](int first, int last) {
+        const int p0 = pos0 + first / G, p1 = pos0 + last / G;
+        TokenRange r{seen(max(p0, 0), len, a.causal, a.window).lo, seen(p1, len, a.causal, a.window).hi};
+        if (r.hi < r.lo) r.hi = r.lo;
+        return r;
+    };
+    const TokenRange tile_r = range(tile0, tile_last), wave_r = range(idle ? tile0 : wave0, idle ? tile_last : wave_last);
+    const int steps = steps_of(tile_r.lo, tile_r.hi), share = (steps + pc.parts - 1) / pc.parts;
+    const int from = (tile_r.lo >> 5) + pc.part * share, to = (tile_r.lo >> 5) + min((pc.part + 1) * share, steps);
+    const int begin = __builtin_amdgcn_readfirstlane(max(from, wave_r.lo >> 5) + tg);
+    const int end = __builtin_amdgcn_readfirstlane(idle ? 0 : min(to, (wave_r.hi + 31) >> 5));
+
+    // this lane's columns: pair cp is row cp / G of the sequence, head h * G + cp % G
+    bool used[NT];
+    TokenRange tr[NT];
+    int64_t qrow[NT];
 #pragma unroll
-    for (int j = 0; j < NK; ++j) {
-        const int64_t at = qrow + g * (D / 4) + 8 * j;
-        const float4 x = load4<DT>(a.q, at), y = load4<DT>(a.q, at + 4);
-        qv[j][0] = x.x; qv[j][1] = x.y; qv[j][2] = x.z; qv[j][3] = x.w;
-        qv[j][4] = y.x; qv[j][5] = y.y; qv[j][6] = y.z; qv[j][7] = y.w;
+    for (int t = 0; t < NT; ++t) {
+        const int cp = wave0 + 16 * t + (HL == 1 ? col & 7 : col);
+        used[t] = cp < pairs;
+        const int ci = used[t] ? cp / G : 0, cg = used[t] ? cp % G : 0;
+        tr[t] = used[t] ? seen(pos0 + ci, len, a.causal, a.window) : wave_r;
+        qrow[t] = (static_cast<int64_t>(rr.first + ci) * a.q_heads + h * G + cg) * D;
     }
+    // the queries' values are asked for first, then the first steps
+    constexpr int NK = D / 32;
+    float qv[NT][NK][8];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int j = 0; j < NK; ++j) {
+            const int64_t at = qrow[t] + g * (D / 4) + 8 * j;
+            const float4 x = load4<DT>(a.q, at), y = load4<DT>(a.q, at + 4);
+            qv[t][j][0] = x.x; qv[t][j][1] = x.y; qv[t][j][2] = x.z; qv[t][j][3] = x.w;
+            qv[t][j][4] = y.x; qv[t][j][5] = y.y; qv[t][j][6] = y.z; qv[t][j][7] = y.w;
+        }
 
-    const int steps = steps_of(sw.lo, sw.hi), share = (steps + pc.parts - 1) / pc.parts;
-    const int begin = __builtin_amdgcn_readfirstlane((sw.lo >> 5) + pc.part * share);
-    const int end = __builtin_amdgcn_readfirstlane((sw.lo >> 5) + min((pc.part + 1) * share, steps));
     const int per_page = b.page_shift - 5;                    // log2 of steps a page
     const int32_t *table = b.block_table + static_cast<int64_t>(seq) * b.max_pages;
     auto page_of = [&](int step) { return step < end ? table[step >> per_page] : -1; };
@@ -393,174 +339,240 @@ __global__ __launch_bounds__(256, 2) void attn_split_kernel(Kv4Cache c, KvBatch 
         return ((p * c.heads + h) << c.page_shift) + ((step << 5) & ((1 << c.page_shift) - 1));
     };
 
-    // A wave's steps go through a ring: two (for D = 256, whose sums fill the registers,
-    // one) on their way while one is worked on.
-    constexpr int NB = D == 256 ? 2 : 3;
+    // A wave's steps go through a ring: two (one, where the columns' sums fill the
+    // registers) on their way while one is worked on.
+    constexpr int NB = D == 256 || NT > 1 ? 2 : 3;
+    constexpr bool ONCE = WC == 1;                            // no other wave reads these codes
     Step<D> ring[NB];
     int page[NB];
 #pragma unroll
-    for (int k = 0; k < NB; ++k) page[k] = page_of(begin + wid + k * W);
+    for (int k = 0; k < NB; ++k) page[k] = page_of(begin + k * TG);
 #pragma unroll
     for (int k = 0; k < NB - 1; ++k)
-        if (begin + wid + k * W < end) load_step<D>(ring[k], c, token_of(page[k], begin + wid + k * W), g, col);
-    u4 qf[NK], ql[HL == 2 ? NK : 1];
-    float scale = a.sm_scale * kLog2e;
-    {
+        if (begin + k * TG < end) load_step<D, ONCE>(ring[k], c, token_of(page[k], begin + k * TG), g, col);
+
+    u4 qf[NT][NK], ql[HL == 2 ? NT : 1][HL == 2 ? NK : 1];
+    float scale[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
         float big = 0.0f;
 #pragma unroll
         for (int j = 0; j < NK; ++j)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(qv[j][i]));
+            for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(qv[t][j][i]));
         big = col_max(big);
         // largest value to [2^9, 2^10), undone in the scores' factor (both exact)
         const int e = big > 0.0f ? 10 - __builtin_amdgcn_frexp_expf(big) : 0;
 #pragma unroll
         for (int j = 0; j < NK; ++j) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) qv[j][i] = used ? __builtin_amdgcn_ldexpf(qv[j][i], e) : 0.0f;
+            for (int i = 0; i < 8; ++i) qv[t][j][i] = used[t] ? __builtin_amdgcn_ldexpf(qv[t][j][i], e) : 0.0f;
             if constexpr (HL == 0) {
-                qf[j] = f16_pack8(qv[j]);
+                qf[t][j] = f16_pack8(qv[t][j]);
             } else {
                 u4 hi, low;
-                f16_split8(qv[j], hi, low);
-                if constexpr (HL == 2) ql[j] = low;
-                qf[j] = HL == 1 && col >= 8 ? low : hi;
+                f16_split8(qv[t][j], hi, low);
+                if constexpr (HL == 2) ql[t][j] = low;
+                qf[t][j] = HL == 1 && col >= 8 ? low : hi;
             }
         }
-        scale = fmaxf(__builtin_amdgcn_ldexpf(scale, -e), 1e-30f);      // never 0: a masked score is -inf
+        scale[t] = fmaxf(__builtin_amdgcn_ldexpf(a.sm_scale * kLog2e, -e), 1e-30f);   // never 0: a masked score is -inf
     }
 
-    float m = kLowest, l = 0.0f;
-    f4 acc[D / 16];
+    float m[NT], l[NT];
+    f4 acc[NT][D / 16];
 #pragma unroll
-    for (int j = 0; j < D / 16; ++j) acc[j] = f4{0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < NT; ++t) {
+        m[t] = kLowest;
+        l[t] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) acc[t][j] = f4{0.f, 0.f, 0.f, 0.f};
+    }
 
     auto work = [&](Step<D> &cur, int step) {
-            float s[8];
+        float s[NT][8];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                f4 t{0.f, 0.f, 0.f, 0.f};
+        for (int u = 0; u < 2; ++u) {
+            f4 x[NT];
 #pragma unroll
-                for (int j = 0; j < NK; ++j) {
-                    const u4 kf = levels8(cur.k[u][j]);
-                    if constexpr (HL == 2) t = mma16(kf, ql[j], t);
-                    t = mma16(kf, qf[j], t);
+            for (int t = 0; t < NT; ++t) x[t] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < NK; ++j) {
+                const u4 kf = levels8(cur.k[u][j]);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    if constexpr (HL == 2) x[t] = mma16(kf, ql[t][j], x[t]);
+                    x[t] = mma16(kf, qf[t][j], x[t]);
                 }
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float x = t[i];
-                    if constexpr (HL == 1) x += lane_xor<8>(x);          // high and low part of the query
-                    s[4 * u + i] = times_half(x, cur.ks, 4 * u + i);
+                    float y = x[t][i];
+                    if constexpr (HL == 1) y += lane_xor<8>(y);          // high and low part of the query
+                    s[t][4 * u + i] = times_half(y, cur.ks, 4 * u + i);
                 }
-            }
-            const int t0 = (step << 5) + 8 * g;
-            if (__any(t0 < tr.lo || t0 + 8 > tr.hi)) {
-                asm volatile("");                              // a branch of its own: most steps need no mask
+        }
+        const int t0 = (step << 5) + 8 * g;
+        bool edge = false;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const bool on = t0 + i >= tr.lo && t0 + i < tr.hi;
-                    s[i] = on ? s[i] : -INFINITY;
-                    cur.vs[i >> 1] &= on ? 0xFFFFFFFFu : (i & 1 ? 0x0000FFFFu : 0xFFFF0000u);
-                }
-            }
-            float w[8], sum = 0.0f;
+        for (int t = 0; t < NT; ++t) edge = edge || t0 < tr[t].lo || t0 + 8 > tr[t].hi;
+        if (__any(edge)) {
+            asm volatile("");                              // a branch of its own: most steps need no mask
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float p = __builtin_amdgcn_exp2f(fmaf(s[i], scale, -m));
-                sum += p;
-                w[i] = times_half(p, cur.vs, i);
+                bool any = false;
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const bool on = t0 + i >= tr[t].lo && t0 + i < tr[t].hi;
+                    s[t][i] = on ? s[t][i] : -INFINITY;
+                    any = any || on;
+                }
+                // a scale past the sequence's end may be anything
+                cur.vs[i >> 1] &= any ? 0xFFFFFFFFu : (i & 1 ? 0x0000FFFFu : 0xFFFF0000u);
             }
-            if (__any(!(max8(w) <= kMost && sum <= kMostP))) {         // also the first step: m is the lowest
+        }
+        float w[NT][8], sum[NT];
+        bool pass = false;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            sum[t] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float p = __builtin_amdgcn_exp2f(fmaf(s[t][i], scale[t], -m[t]));
+                sum[t] += p;
+                w[t][i] = times_half(p, cur.vs, i);
+            }
+            pass = pass || !(max8(w[t]) <= kMost && sum[t] <= kMostP);
+        }
+        if (__any(pass)) {                                 // also the first step: m is the lowest
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
                 float most = -INFINITY;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float vs = times_half(1.0f, cur.vs, i);
-                    most = fmaxf(most, fmaf(s[i], scale, vs > 0.0f ? static_cast<float>(__builtin_amdgcn_frexp_expf(vs)) : -24.0f));
+                    most = fmaxf(most, fmaf(s[t][i], scale[t], vs > 0.0f ? static_cast<float>(__builtin_amdgcn_frexp_expf(vs)) : -24.0f));
                 }
-                const float mn = fmaxf(m, col_max(most) - kRoom), shrink = __builtin_amdgcn_exp2f(m - mn);
-                m = mn;
-                l *= shrink;
+                const float mn = fmaxf(m[t], col_max(most) - kRoom), shrink = __builtin_amdgcn_exp2f(m[t] - mn);
+                m[t] = mn;
+                l[t] *= shrink;
 #pragma unroll
-                for (int j = 0; j < D / 16; ++j) acc[j] *= shrink;
-                sum = 0.0f;
+                for (int j = 0; j < D / 16; ++j) acc[t][j] *= shrink;
+                sum[t] = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float p = __builtin_amdgcn_exp2f(fmaf(s[i], scale, -m));
-                    sum += p;
-                    w[i] = times_half(p, cur.vs, i);
+                    const float p = __builtin_amdgcn_exp2f(fmaf(s[t][i], scale[t], -m[t]));
+                    sum[t] += p;
+                    w[t][i] = times_half(p, cur.vs, i);
                 }
             }
-            l += sum;
-            u4 wf, wl;
+        }
+        u4 wf[NT], wl[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            l[t] += sum[t];
             if constexpr (HL == 0) {
-                wf = f16_pack8(w);
+                wf[t] = f16_pack8(w[t]);
             } else {
                 u4 hi;
-                f16_split8(w, hi, wl);
-                wf = HL == 1 && col >= 8 ? wl : hi;
+                f16_split8(w[t], hi, wl[t]);
+                wf[t] = HL == 1 && col >= 8 ? wl[t] : hi;
             }
+        }
 #pragma unroll
-            for (int j = 0; j < D / 64; ++j) {
+        for (int j = 0; j < D / 64; ++j) {
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const u4 vf = levels8(cur.v[j][x]);
-                    if constexpr (HL == 2) acc[4 * j + x] = mma16(vf, wl, acc[4 * j + x]);
-                    acc[4 * j + x] = mma16(vf, wf, acc[4 * j + x]);
+            for (int x = 0; x < 4; ++x) {
+                const u4 vf = levels8(cur.v[j][x]);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    if constexpr (HL == 2) acc[t][4 * j + x] = mma16(vf, wl[t], acc[t][4 * j + x]);
+                    acc[t][4 * j + x] = mma16(vf, wf[t], acc[t][4 * j + x]);
                 }
             }
+        }
     };
-    for (int step = begin + wid; step < end;) {
+    for (int step = begin; step < end;) {
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
             constexpr int ahead = NB - 1;
-            const int to = (k + ahead) % NB;
-            if (step + ahead * W < end) load_step<D>(ring[to], c, token_of(page[to], step + ahead * W), g, col);
+            const int in = (k + ahead) % NB;
+            if (step + ahead * TG < end) load_step<D, ONCE>(ring[in], c, token_of(page[in], step + ahead * TG), g, col);
             const int now = page[k];
-            page[k] = page_of(step + NB * W);
+            page[k] = page_of(step + NB * TG);
             if (now >= 0 && now < c.pages) work(ring[k], step);
-            step += W;
+            step += TG;
             if (step >= end) break;
         }
     }
 
-    // The four waves' sums become one.
-    l = col_sum(l);
-    if (g == 0) {
-        lds_ml[wid][col][0] = m;
-        lds_ml[wid][col][1] = l;
-    }
-    __syncthreads();
-    const float mw[4] = {lds_ml[0][col][0], lds_ml[1][col][0], lds_ml[2][col][0], lds_ml[3][col][0]};
-    const float top = fmaxf(fmaxf(mw[0], mw[1]), fmaxf(mw[2], mw[3]));
-    const float mine = __builtin_amdgcn_exp2f(m - top);
-#pragma unroll
-    for (int j = 0; j < D / 64; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f4 o{acc[4 * j][i], acc[4 * j + 1][i], acc[4 * j + 2][i], acc[4 * j + 3][i]};
-            if constexpr (HL == 1) o = f4{o.x + lane_xor<8>(o.x), o.y + lane_xor<8>(o.y), o.z + lane_xor<8>(o.z), o.w + lane_xor<8>(o.w)};
-            *reinterpret_cast<f4 *>(&lds_o[wid][col][64 * j + 16 * g + 4 * i]) = o * mine;
-        }
-    __syncthreads();
-    for (int e = threadIdx.x; e < n * G * (D / 4); e += 256) {
-        const int cc = e / (D / 4), d = 4 * (e % (D / 4));
-        f4 o{0.f, 0.f, 0.f, 0.f};
-        float mt = lds_ml[0][cc][0], lt = 0.0f;
-#pragma unroll
-        for (int w = 1; w < W; ++w) mt = fmaxf(mt, lds_ml[w][cc][0]);
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-            o += *reinterpret_cast<const f4 *>(&lds_o[w][cc][d]);
-            lt += lds_ml[w][cc][1] * __builtin_amdgcn_exp2f(lds_ml[w][cc][0] - mt);
-        }
+    // lane (g, c) holds dims 64 j + 16 g .. + 15 of column c: acc[4 j + x][i] is 4 i + x of them
+    auto dims4 = [&](int t, int j, int i) { return f4{acc[t][4 * j][i], acc[t][4 * j + 1][i], acc[t][4 * j + 2][i], acc[t][4 * j + 3][i]}; };
+    auto put = [&](int cc, int d, f4 o, float mt, float lt) {
+        // sums of the tile's column cc
         if (pc.parts == 1) {
             const float inv = lt > 0.0f ? 1.0f / lt : 0.0f;
-            const int64_t at = (static_cast<int64_t>(rr.first + cc / G) * a.q_heads + h * G + cc % G) * D + d;
+            const int cp = tile0 + cc;
+            const int64_t at = (static_cast<int64_t>(rr.first + cp / G) * a.q_heads + h * G + cp % G) * D + d;
             store4<DT>(a.o, at, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
         } else {
             const int64_t slot = (static_cast<int64_t>(h) * pl.slots + pc.slot) * cols + cc;
             *reinterpret_cast<f4 *>(part_o + slot * D + d) = o;
             if (d == 0) *reinterpret_cast<float2 *>(part_ml + 2 * slot) = make_float2(mt, lt);
+        }
+    };
+#pragma unroll
+    for (int t = 0; t < NT; ++t) l[t] = col_sum(l[t]);
+    if constexpr (TG == 1) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            if (!used[t]) continue;
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) put(wc * TC + 16 * t + col, 64 * j + 16 * g + 4 * i, dims4(t, j, i), m[t], l[t]);
+        }
+    } else {
+        // the step groups' sums of a column become one
+        const int lc = wc * TC + col;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+            if (g == 0) {
+                lds_ml[tg][lc + 16 * t][0] = m[t];
+                lds_ml[tg][lc + 16 * t][1] = l[t];
+            }
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            float top = kLowest;
+#pragma unroll
+            for (int k = 0; k < TG; ++k) top = fmaxf(top, lds_ml[k][lc + 16 * t][0]);
+            const float mine = __builtin_amdgcn_exp2f(m[t] - top);
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    f4 o = dims4(t, j, i);
+                    if constexpr (HL == 1) o = f4{o.x + lane_xor<8>(o.x), o.y + lane_xor<8>(o.y), o.z + lane_xor<8>(o.z), o.w + lane_xor<8>(o.w)};
+                    *reinterpret_cast<f4 *>(&lds_o[tg][lc + 16 * t][64 * j + 16 * g + 4 * i]) = o * mine;
+                }
+        }
+        __syncthreads();
+        const int n = min(TM, pairs - tile0);
+        for (int e = threadIdx.x; e < n * (D / 4); e += 256) {
+            const int cc = e / (D / 4), d = 4 * (e % (D / 4));
+            f4 o{0.f, 0.f, 0.f, 0.f};
+            float mt = kLowest, lt = 0.0f;
+#pragma unroll
+            for (int k = 0; k < TG; ++k) mt = fmaxf(mt, lds_ml[k][cc][0]);
+#pragma unroll
+            for (int k = 0; k < TG; ++k) {
+                o += *reinterpret_cast<const f4 *>(&lds_o[k][cc][d]);
+                lt += lds_ml[k][cc][1] * __builtin_amdgcn_exp2f(lds_ml[k][cc][0] - mt);
+            }
+            put(cc, d, o, mt, lt);
         }
     }
 }
@@ -582,7 +594,7 @@ __global__ __launch_bounds__(512) void attn_join_kernel(Kv4Cache c, KvBatch b, K
     const int64_t first = (static_cast<int64_t>(h) * pl.slots + pc.slot) * cols;
     const int idx = threadIdx.x / L, ln = threadIdx.x % L, d = 4 * ln;
     const int at_col = idx % wide, gr = idx / wide, groups = N / wide, cc = blockIdx.z * wide + at_col;
-    const bool on = gr < groups && cc < sw.n * G;
+    const bool on = gr < groups && cc < cols && pc.tile * pl.tm + cc < sw.n * G;
     f4 o{0.f, 0.f, 0.f, 0.f};
     float m = kLowest, l = 0.0f;
     if (on) {
@@ -615,7 +627,8 @@ __global__ __launch_bounds__(512) void attn_join_kernel(Kv4Cache c, KvBatch b, K
             o += lds_o[k * wide + at_col][ln] * e;
         }
         const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-        const int64_t at = (static_cast<int64_t>(sw.rr.first + cc / G) * a.q_heads + h * G + cc % G) * D + d;
+        const int cp = pc.tile * pl.tm + cc;
+        const int64_t at = (static_cast<int64_t>(sw.rr.first + cp / G) * a.q_heads + h * G + cp % G) * D + d;
         store4<DT>(a.o, at, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
     }
 }
@@ -634,46 +647,70 @@ Plan make_plan(const KvBatch &b, int heads, int G, int tm, int target, int min_c
     return p;
 }
 
-// Workgroups of the split kernel that the chip's 256 CUs hold at once (by registers
-// and LDS: 5, 3 and 2 a CU for heads of 64, 128 and 256).
-bool split_applies(const KvBatch &b, const Kv4Cache &c, int q_heads) {
-    return static_cast<int64_t>(b.max_q) * (q_heads / c.heads) <= 16;
+// The kernel's shape for a call: by the pairs of one sequence and KV head, the most columns
+// a workgroup is offered, so that no wave multiplies mostly padding and short prompts keep
+// their waves busy on the context.  Heads of 256 fill the registers with one product of
+// columns a wave.
+struct Shape {
+    int nt, wc;             // products of 16 columns a wave, groups of columns
+    Plan plan;
+    int cols;               // columns kept for a part
+    int64_t sums, stats;    // bytes of the parts' sums and of their statistics
+};
+Shape attn_shape(const KvBatch &b, const Kv4Cache &c, int q_heads) {
+    Shape s;
+    const int G = q_heads / c.heads;
+    const int64_t pairs = static_cast<int64_t>(b.max_q) * G;
+    s.nt = c.D == 256 || pairs <= 16 ? 1 : 2;
+    s.wc = pairs <= 16 * s.nt ? 1 : pairs <= 32 * s.nt ? 2 : 4;
+    const int tm = 16 * s.nt * s.wc;
+    // workgroups wanted: what the chip's 256 CUs hold at once, twice that where sequences of
+    // different lengths leave parts uneven
+    const int held = c.D == 64 && s.nt == 1 ? 5 : c.D == 128 && s.nt == 1 ? 3 : 2;
+    s.plan = make_plan(b, c.heads, G, tm, 256 * held * (b.B > 1 && s.wc == 1 ? 2 : 1), s.wc == 1 ? 4 : 8);
+    s.cols = static_cast<int>(pairs < tm ? pairs : tm);
+    s.sums = static_cast<int64_t>(c.heads) * s.plan.slots * s.cols * c.D * 4;
+    s.stats = static_cast<int64_t>(c.heads) * s.plan.slots * s.cols * 8;
+    return s;
 }
-Plan split_plan(const KvBatch &b, const Kv4Cache &c, int q_heads) {
-    const int target = 256 * (c.D == 64 ? 5 : c.D == 128 ? 3 : 2) * (b.B > 1 ? 2 : 1);
-    return make_plan(b, c.heads, q_heads / c.heads, 16, target, 4);
-}
-// Bytes of the parts' sums and of their statistics.
-int64_t sums_bytes(const Plan &p, const Kv4Cache &c, int cols) { return static_cast<int64_t>(c.heads) * p.slots * cols * c.D * 4; }
-int64_t stats_bytes(const Plan &p, const Kv4Cache &c, int cols) { return static_cast<int64_t>(c.heads) * p.slots * cols * 8; }
 
-template <int DT, int D>
-hipError_t launch_split(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, hipStream_t st) {
-    const int cols = b.max_q * (a.q_heads / c.heads);
-    const Plan p = split_plan(b, c, a.q_heads);
-    float *part_o = static_cast<float *>(a.workspace), *part_ml = part_o + sums_bytes(p, c, cols) / 4;
-    const dim3 grid(p.pieces, c.heads), block(256);
+template <int DT, int D, int NT, int WC>
+void launch_shape(const Shape &s, const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, float *part_o, float *part_ml,
+                  hipStream_t st) {
+    const dim3 grid(s.plan.pieces, c.heads), block(256);
     if constexpr (DT != kDtF32) {
-        hipLaunchKernelGGL((attn_split_kernel<DT, D, 0>), grid, block, 0, st, c, b, a, p, cols, part_o, part_ml);
+        hipLaunchKernelGGL((attn_kernel<DT, D, 0, NT, WC>), grid, block, 0, st, c, b, a, s.plan, s.cols, part_o, part_ml);
     } else {
-        if (cols <= 8)
-            hipLaunchKernelGGL((attn_split_kernel<DT, D, 1>), grid, block, 0, st, c, b, a, p, cols, part_o, part_ml);
-        else
-            hipLaunchKernelGGL((attn_split_kernel<DT, D, 2>), grid, block, 0, st, c, b, a, p, cols, part_o, part_ml);
+        if constexpr (NT == 1 && WC == 1) {
+            if (s.cols <= 8) {
+                hipLaunchKernelGGL((attn_kernel<DT, D, 1, NT, WC>), grid, block, 0, st, c, b, a, s.plan, s.cols, part_o, part_ml);
+                return;
+            }
+        }
+        hipLaunchKernelGGL((attn_kernel<DT, D, 2, NT, WC>), grid, block, 0, st, c, b, a, s.plan, s.cols, part_o, part_ml);
     }
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.items == 0) return e;
-    // few tiles: a workgroup a column, so that many parts are read side by side
-    const int most = 2048 / D, wide = p.items * c.heads < 256 ? 1 : cols < most ? cols : most;
-    hipLaunchKernelGGL((attn_join_kernel<DT, D>), dim3(p.items, c.heads, (cols + wide - 1) / wide), dim3(512), 0, st, c, b,
-                       a, p, cols, wide, part_o, part_ml);
-    return hipGetLastError();
 }
 
 template <int DT, int D>
 hipError_t launch_d(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, hipStream_t st) {
-    if (split_applies(b, c, a.q_heads)) return launch_split<DT, D>(c, b, a, st);
-    hipLaunchKernelGGL((attn_plain_kernel<DT, D>), dim3(b.rows, a.q_heads), dim3(256), 0, st, c, b, a);
+    const Shape s = attn_shape(b, c, a.q_heads);
+    float *part_o = static_cast<float *>(a.workspace), *part_ml = part_o + s.sums / 4;
+    if constexpr (D == 256) {
+        if (s.wc == 1) launch_shape<DT, D, 1, 1>(s, c, b, a, part_o, part_ml, st);
+        else if (s.wc == 2) launch_shape<DT, D, 1, 2>(s, c, b, a, part_o, part_ml, st);
+        else launch_shape<DT, D, 1, 4>(s, c, b, a, part_o, part_ml, st);
+    } else {
+        if (s.nt == 1) launch_shape<DT, D, 1, 1>(s, c, b, a, part_o, part_ml, st);
+        else if (s.wc == 1) launch_shape<DT, D, 2, 1>(s, c, b, a, part_o, part_ml, st);
+        else if (s.wc == 2) launch_shape<DT, D, 2, 2>(s, c, b, a, part_o, part_ml, st);
+        else launch_shape<DT, D, 2, 4>(s, c, b, a, part_o, part_ml, st);
+    }
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || s.plan.items == 0) return e;
+    // few tiles: a workgroup a column, so that many parts are read side by side
+    const int most = 2048 / D, wide = static_cast<int64_t>(s.plan.items) * c.heads < 256 ? 1 : s.cols < most ? s.cols : most;
+    hipLaunchKernelGGL((attn_join_kernel<DT, D>), dim3(s.plan.items, c.heads, (s.cols + wide - 1) / wide), dim3(512), 0, st,
+                       c, b, a, s.plan, s.cols, wide, part_o, part_ml);
     return hipGetLastError();
 }
 
@@ -687,10 +724,8 @@ hipError_t launch_t(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, hipSt
 }  // namespace
 
 int64_t kv4_attn_workspace(const Kv4Cache &c, const KvBatch &b, int q_heads, int) {
-    if (!split_applies(b, c, q_heads)) return 0;
-    const int cols = b.max_q * (q_heads / c.heads);
-    const Plan p = split_plan(b, c, q_heads);
-    return sums_bytes(p, c, cols) + stats_bytes(p, c, cols);
+    const Shape s = attn_shape(b, c, q_heads);
+    return s.sums + s.stats;
 }
 
 hipError_t launch_kv4_attn(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, int dtype, hipStream_t st) {
