@@ -707,8 +707,10 @@ hipError_t launch_d(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, hipSt
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || s.plan.items == 0) return e;
-    // few tiles: a workgroup a column, so that many parts are read side by side
-    const int most = 2048 / D, wide = static_cast<int64_t>(s.plan.items) * c.heads < 256 ? 1 : s.cols < most ? s.cols : most;
+    // columns a workgroup: few where there are few tiles, so that many parts are read side
+    // by side, up to what its threads hold
+    const int64_t most = s.cols < 2048 / D ? s.cols : 2048 / D, even = static_cast<int64_t>(s.plan.items) * c.heads * s.cols / 512;
+    const int wide = static_cast<int>(even < 1 ? 1 : even < most ? even : most);
     hipLaunchKernelGGL((attn_join_kernel<DT, D>), dim3(s.plan.items, c.heads, (s.cols + wide - 1) / wide), dim3(512), 0, st,
                        c, b, a, s.plan, s.cols, wide, part_o, part_ml);
     return hipGetLastError();
