@@ -332,7 +332,10 @@ __global__ __launch_bounds__(256, 2) void attn_kernel(Kv4Cache c, KvBatch b, Kv4
         }
 
     const int per_page = b.page_shift - 5;                    // log2 of steps a page
-    const int32_t *table = b.block_table + static_cast<int64_t>(seq) * b.max_pages;
+    // Page ids come through the scalar cache (no kernel writes them while this one runs): a
+    // vector load here would wait for every code on its way.
+    typedef const __attribute__((address_space(4))) int32_t *scalar_ids;
+    const scalar_ids table = (scalar_ids)(b.block_table + static_cast<int64_t>(seq) * b.max_pages);
     auto page_of = [&](int step) { return step < end ? table[step >> per_page] : -1; };
     auto token_of = [&](int page, int step) {
         const int64_t p = page >= 0 && page < c.pages ? page : 0;
