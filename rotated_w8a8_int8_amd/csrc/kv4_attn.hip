@@ -339,11 +339,13 @@ __global__ __launch_bounds__(256, 2) void attn_kernel(Kv4Cache c, KvBatch b, Kv4
     auto page_of = [&](int step) { return step < end ? table[step >> per_page] : -1; };
     auto token_of = [&](int page, int step) {
         const int64_t p = page >= 0 && page < c.pages ? page : 0;
-        return ((p * c.heads + h) << c.page_shift) + ((step << 5) & ((1 << c.page_shift) - 1));
+        return ((p * c.heads + h) << c.page_shift) + (step < end ? (step << 5) & ((1 << c.page_shift) - 1) : 0);
     };
 
     // A wave's steps go through a ring: two (one, where the columns' sums fill the
-    // registers) on their way while one is worked on.
+    // registers) on their way while one is worked on.  Past the end the loads go on, to the
+    // start of page 0 (cached, unused): were they conditional, the wait for a step's codes
+    // would have to be a wait for the later ones too.
     constexpr int NB = D == 256 || NT > 1 ? 2 : 3;
     constexpr bool ONCE = WC == 1;                            // no other wave reads these codes
     Step<D> ring[NB];
@@ -351,8 +353,7 @@ __global__ __launch_bounds__(256, 2) void attn_kernel(Kv4Cache c, KvBatch b, Kv4
 #pragma unroll
     for (int k = 0; k < NB; ++k) page[k] = page_of(begin + k * TG);
 #pragma unroll
-    for (int k = 0; k < NB - 1; ++k)
-        if (begin + k * TG < end) load_step<D, ONCE>(ring[k], c, token_of(page[k], begin + k * TG), g, col);
+    for (int k = 0; k < NB - 1; ++k) load_step<D, ONCE>(ring[k], c, token_of(page[k], begin + k * TG), g, col);
 
     u4 qf[NT][NK], ql[HL == 2 ? NT : 1][HL == 2 ? NK : 1];
     float scale[NT];
@@ -502,7 +503,7 @@ __global__ __launch_bounds__(256, 2) void attn_kernel(Kv4Cache c, KvBatch b, Kv4
         for (int k = 0; k < NB; ++k) {
             constexpr int ahead = NB - 1;
             const int in = (k + ahead) % NB;
-            if (step + ahead * TG < end) load_step<D, ONCE>(ring[in], c, token_of(page[in], step + ahead * TG), g, col);
+            load_step<D, ONCE>(ring[in], c, token_of(page[in], step + ahead * TG), g, col);
             const int now = page[k];
             page[k] = page_of(step + NB * TG);
             if (now >= 0 && now < c.pages) work(ring[k], step);
