@@ -306,6 +306,11 @@ __global__ __launch_bounds__(256, 2) void attn_kernel(Kv4Cache c, KvBatch b, Kv4
     const int begin = __builtin_amdgcn_readfirstlane(max(from, wave_r.lo >> 5) + tg);
     const int end = __builtin_amdgcn_readfirstlane(idle ? 0 : min(to, (wave_r.hi + 31) >> 5));
 
+    // steps [open_lo, open_hi) that all of the wave's rows see whole: rows see ever later tokens
+    const TokenRange first_r = range(idle ? tile0 : wave0, idle ? tile0 : wave0);
+    const int open_lo = __builtin_amdgcn_readfirstlane((seen(max(pos0 + (idle ? tile_last : wave_last) / G, 0), len, a.causal, a.window).lo + 31) >> 5);
+    const int open_hi = __builtin_amdgcn_readfirstlane(first_r.hi >> 5);
+
     // this lane's columns: pair cp is row cp / G of the sequence, head h * G + cp % G
     bool used[NT];
     TokenRange tr[NT];
@@ -418,12 +423,8 @@ __global__ __launch_bounds__(256, 2) void attn_kernel(Kv4Cache c, KvBatch b, Kv4
                     s[t][4 * u + i] = times_half(y, cur.ks, 4 * u + i);
                 }
         }
-        const int t0 = (step << 5) + 8 * g;
-        bool edge = false;
-#pragma unroll
-        for (int t = 0; t < NT; ++t) edge = edge || t0 < tr[t].lo || t0 + 8 > tr[t].hi;
-        if (__any(edge)) {
-            asm volatile("");                              // a branch of its own: most steps need no mask
+        if (step < open_lo || step >= open_hi) {
+            const int t0 = (step << 5) + 8 * g;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 bool any = false;
@@ -639,9 +640,13 @@ __global__ __launch_bounds__(512) void attn_join_kernel(Kv4Cache c, KvBatch b, K
 
 // The bounds of a plan (see above) for tiles of tm rows of `per` (row, head) pairs a row.
 Plan make_plan(const KvBatch &b, int heads, int G, int tm, int target, int min_chunk) {
-    Plan p{tm, target, min_chunk, 0, 0, 0, 0};
     const int64_t steps = ((static_cast<int64_t>(b.max_pages) << b.page_shift) + 31) >> 5;
-    const int64_t rows = static_cast<int64_t>(b.max_q) * G < tm ? b.B : static_cast<int64_t>(b.rows) * G / tm + b.B;
+    const int64_t rows = static_cast<int64_t>(b.max_q) * G <= tm ? b.B : static_cast<int64_t>(b.rows) * G / tm + b.B;
+    // Each tile may add a part to the even share: where tiles are few, the parts still fit one
+    // round of workgroups; where they are many, twice as many parts even the rounds out.
+    const int64_t tiles = rows * heads;
+    target = 2 * tiles <= target ? target - static_cast<int>(tiles) : 2 * target;
+    Plan p{tm, target, min_chunk, 0, 0, 0, 0};
     p.split = b.B <= kMostScanned && steps > min_chunk;
     const int64_t even = (target + heads - 1) / heads, cuts = (steps + min_chunk - 1) / min_chunk;
     const int64_t extra = p.split ? (even < rows * cuts ? even : rows * cuts) : 0;
@@ -668,10 +673,9 @@ Shape attn_shape(const KvBatch &b, const Kv4Cache &c, int q_heads) {
     s.nt = c.D == 256 || pairs <= 16 ? 1 : 2;
     s.wc = pairs <= 16 * s.nt ? 1 : pairs <= 32 * s.nt ? 2 : 4;
     const int tm = 16 * s.nt * s.wc;
-    // workgroups wanted: what the chip's 256 CUs hold at once, twice that where sequences of
-    // different lengths leave parts uneven
+    // workgroups that the chip's 256 CUs hold at once
     const int held = c.D == 64 && s.nt == 1 ? 5 : c.D == 128 && s.nt == 1 ? 3 : 2;
-    s.plan = make_plan(b, c.heads, G, tm, 256 * held * (b.B > 1 && s.wc == 1 ? 2 : 1), s.wc == 1 ? 4 : 8);
+    s.plan = make_plan(b, c.heads, G, tm, 256 * held, s.wc == 1 ? 4 : 8);
     s.cols = static_cast<int>(pairs < tm ? pairs : tm);
     s.sums = static_cast<int64_t>(c.heads) * s.plan.slots * s.cols * c.D * 4;
     s.stats = static_cast<int64_t>(c.heads) * s.plan.slots * s.cols * 8;
