@@ -21,6 +21,8 @@
 namespace rad {
 namespace {
 
+constexpr int kSpan = 7;      // groups of heads a workgroup, many rows
+
 // (a cos - b sin, b cos + a sin), every operation rounded by itself.
 __device__ __forceinline__ float turn_first(float a, float b, float cs, float sn) {
 #pragma clang fp contract(off)
@@ -31,28 +33,80 @@ __device__ __forceinline__ float turn_second(float a, float b, float cs, float s
     return b * cs + a * sn;
 }
 
-// Four consecutive values d .. d + 3 (d % 4 == 0) of the head at `base` after
-// the position rotation; tab is the position's table row.
+// A lane's two runs of four values of a head vector.
+struct Runs {
+    float4 lo, hi;
+};
+
+// The position rotation of a lane's runs at d0 and d1.  Where a pair's halves lie d1 - d0
+// apart (style 0, dim = 2 (d1 - d0): the usual whole-head rotation for D = 64 and 128)
+// the lane holds both, and lo and hi share one set of angles; style 1 pairs neighbours;
+// otherwise the other half is read again.
+struct Angles {
+    float4 c0, s0, c1, s1;      // cosines and sines for lo and for hi
+};
+template <int D>
+__device__ __forceinline__ Angles angles(const float *tab, int dim, int style, int d0, int d1) {
+    const int half = dim >> 1;
+    Angles a{};
+    if (style == 1) {
+        auto two = [&](int d, float4 &c, float4 &s) {
+            if (d >= dim) return;
+            const float2 x = *reinterpret_cast<const float2 *>(tab + (d >> 1)), y = *reinterpret_cast<const float2 *>(tab + half + (d >> 1));
+            c = make_float4(x.x, x.y, 0.f, 0.f);
+            s = make_float4(y.x, y.y, 0.f, 0.f);
+        };
+        two(d0, a.c0, a.s0);
+        two(d1, a.c1, a.s1);
+    } else {
+        if (d0 < dim) {
+            const int j = d0 < half ? d0 : d0 - half;
+            a.c0 = load4<kDtF32>(tab, j);
+            a.s0 = load4<kDtF32>(tab, half + j);
+        }
+        if (half == d1 - d0) return a;
+        if (d1 < dim) {
+            const int j = d1 < half ? d1 : d1 - half;
+            a.c1 = load4<kDtF32>(tab, j);
+            a.s1 = load4<kDtF32>(tab, half + j);
+        }
+    }
+    return a;
+}
+__device__ __forceinline__ float4 firsts(float4 a, float4 b, float4 c, float4 s) {
+    return make_float4(turn_first(a.x, b.x, c.x, s.x), turn_first(a.y, b.y, c.y, s.y), turn_first(a.z, b.z, c.z, s.z),
+                       turn_first(a.w, b.w, c.w, s.w));
+}
+__device__ __forceinline__ float4 seconds(float4 a, float4 b, float4 c, float4 s) {
+    return make_float4(turn_second(a.x, b.x, c.x, s.x), turn_second(a.y, b.y, c.y, s.y), turn_second(a.z, b.z, c.z, s.z),
+                       turn_second(a.w, b.w, c.w, s.w));
+}
 template <int DT>
-__device__ __forceinline__ float4 turned4(const void *src, int64_t base, int d, const float *tab, int dim, int style) {
-    const float4 x = load4<DT>(src, base + d);
-    if (d >= dim) return x;
+__device__ __forceinline__ void turn(Runs &v, const Angles &a, const void *src, int64_t base, int dim, int style, int d0,
+                                     int d1) {
     const int half = dim >> 1;
     if (style == 1) {
-        const float2 cs = *reinterpret_cast<const float2 *>(tab + (d >> 1));
-        const float2 sn = *reinterpret_cast<const float2 *>(tab + half + (d >> 1));
-        return make_float4(turn_first(x.x, x.y, cs.x, sn.x), turn_second(x.x, x.y, cs.x, sn.x),
-                           turn_first(x.z, x.w, cs.y, sn.y), turn_second(x.z, x.w, cs.y, sn.y));
+        auto two = [](float4 x, float4 c, float4 s) {
+            return make_float4(turn_first(x.x, x.y, c.x, s.x), turn_second(x.x, x.y, c.x, s.x),
+                               turn_first(x.z, x.w, c.y, s.y), turn_second(x.z, x.w, c.y, s.y));
+        };
+        if (d0 < dim) v.lo = two(v.lo, a.c0, a.s0);
+        if (d1 < dim) v.hi = two(v.hi, a.c1, a.s1);
+    } else if (half == d1 - d0) {
+        if (d0 < half) {                                      // heads of 256: the first 128 alone
+            const float4 x = v.lo, y = v.hi;
+            v.lo = firsts(x, y, a.c0, a.s0);
+            v.hi = seconds(x, y, a.c0, a.s0);
+        }
+    } else {
+        auto one = [&](float4 x, int d, float4 c, float4 s) {
+            if (d >= dim) return x;
+            const float4 o = load4<DT>(src, base + (d < half ? d + half : d - half));
+            return d < half ? firsts(x, o, c, s) : seconds(o, x, c, s);
+        };
+        v.lo = one(v.lo, d0, a.c0, a.s0);
+        v.hi = one(v.hi, d1, a.c1, a.s1);
     }
-    const bool first = d < half;
-    const int j = first ? d : d - half;
-    const float4 o = load4<DT>(src, base + (first ? d + half : j));
-    const float4 cs = load4<kDtF32>(tab, j), sn = load4<kDtF32>(tab, half + j);
-    if (first)
-        return make_float4(turn_first(x.x, o.x, cs.x, sn.x), turn_first(x.y, o.y, cs.y, sn.y),
-                           turn_first(x.z, o.z, cs.z, sn.z), turn_first(x.w, o.w, cs.w, sn.w));
-    return make_float4(turn_second(o.x, x.x, cs.x, sn.x), turn_second(o.y, x.y, cs.y, sn.y),
-                       turn_second(o.z, x.z, cs.z, sn.z), turn_second(o.w, x.w, cs.w, sn.w));
 }
 
 // Maximum over the L lanes of a head vector (L = 8, 16 or 32).
@@ -66,117 +120,144 @@ __device__ __forceinline__ float head_max(float a) {
     return a;
 }
 
-// blockIdx.x: `chunk` consecutive rows; blockIdx.y: HPB heads of the q_heads +
-// 2 * heads in the order queries, keys, values.
+// blockIdx.x: `chunk` consecutive rows, of which the workgroup takes the octets that begin
+// there; blockIdx.y: `span` groups of HPB heads of the q_heads + 2 * heads in the order
+// queries, keys, values.  A thread's token, and with it its angles, stays while the heads
+// go by, the next head's values being on their way.
 template <int DT, int D>
-__global__ __launch_bounds__(256) void kv4_append_kernel(Kv4Cache c, KvBatch b, Kv4New nw, int chunk) {
+__global__ __launch_bounds__(256) void kv4_append_kernel(Kv4Cache c, KvBatch b, Kv4New nw, int chunk, int span) {
     constexpr int L = D / 8, HPB = 32 / L;
     __shared__ uint32_t codes[HPB][8][L];                 // [head][token of the octet][lane]: 8 codes of a lane
     const int lane = threadIdx.x % L, tok = (threadIdx.x / L) % 8, hs = threadIdx.x / (8 * L);
     const int l16 = lane & 15;
     // a lane's two runs of four values: d0 .. d0 + 3 and d1 .. d1 + 3
     const int d0 = D == 64 ? 4 * lane : (lane >> 4) * 128 + 4 * l16, d1 = d0 + (D == 64 ? 32 : 64);
-    const int hx = blockIdx.y * HPB + hs, H = c.heads, HQ = nw.q_heads;
-    const int kind = hx < HQ ? 0 : hx < HQ + H ? 1 : hx < HQ + 2 * H ? 2 : 3;       // query, key, value, none
-    const int h = kind == 0 ? hx : kind == 1 ? hx - HQ : hx - HQ - H;
-    const void *src = kind == 0 ? nw.q : kind == 1 ? nw.k : nw.v;
-    const int64_t ld = kind == 0 ? nw.ldq : kind == 1 ? nw.ldk : nw.ldv;
+    const int H = c.heads, HQ = nw.q_heads, heads = HQ + 2 * H;
+    const int hb0 = blockIdx.y * span, hb1 = min(hb0 + span, (heads + HPB - 1) / HPB);
+    const bool turned_too = D % 128 == 0 && nw.rotate;
+    const float sign = turned_too ? fwht_lane_sign(l16) : 1.0f;        // what fwht128_regs_signed leaves on a lane
 
     const int row_end = min(static_cast<int>(blockIdx.x + 1) * chunk, b.rows);
-    for (int row = blockIdx.x * chunk; row < row_end; ++row) {
-        // this row's octet is the workgroup's if the row is its first token in the call
+    for (int row = blockIdx.x * chunk; row < row_end;) {
         const int seq = kv_seq_of(b, row);
-        if (seq < 0) continue;
+        if (seq < 0) {
+            ++row;
+            continue;
+        }
         const RowRange rr = kv_rows(b, seq);
         const int pos0 = kv_len(b, seq) - rr.n;              // position of the sequence's first row
-        const int pos = pos0 + (row - rr.first);
-        if (pos < 0 || !((pos & 7) == 0 || pos == max(pos0, 0))) continue;
-        const int octet = pos >> 3, last = pos0 + rr.n - 1;   // tokens pos .. min(last, 8 * octet + 7)
-        const int t = octet * 8 + tok;
-        const bool live = t >= pos && t <= last && kind < 3 && (!nw.rope || t < nw.rope_rows);
-        const int page = kv_page(b, seq, octet * 8, c.pages);
-        const int off = (octet * 8) & ((1 << c.page_shift) - 1);
-
-        float r[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (live) {
-            const int64_t base = static_cast<int64_t>(rr.first + (t - pos0)) * ld + static_cast<int64_t>(h) * D;
-            Blk8 v;
-            if (kind < 2 && nw.rope) {
-                const float *tab = nw.rope + static_cast<int64_t>(t) * nw.rope_dim;
-                v.lo = turned4<DT>(src, base, d0, tab, nw.rope_dim, nw.rope_style);
-                v.hi = turned4<DT>(src, base, d1, tab, nw.rope_dim, nw.rope_style);
-            } else {
-                v.lo = load4<DT>(src, base + d0);
-                v.hi = load4<DT>(src, base + d1);
-            }
-            if (D % 128 == 0 && nw.rotate) fwht128_regs(v, l16);
-            if (kind == 0) {
-                const float m = D % 128 == 0 && nw.rotate ? 0x1p-7f : 1.0f;
-                const int64_t at = (static_cast<int64_t>(rr.first + (t - pos0)) * HQ + h) * D;
-                store4<DT>(nw.q_out, at + d0, make_float4(v.lo.x * m, v.lo.y * m, v.lo.z * m, v.lo.w * m));
-                store4<DT>(nw.q_out, at + d1, make_float4(v.hi.x * m, v.hi.y * m, v.hi.z * m, v.hi.w * m));
-            } else {
-                r[0] = v.lo.x; r[1] = v.lo.y; r[2] = v.lo.z; r[3] = v.lo.w;
-                r[4] = v.hi.x; r[5] = v.hi.y; r[6] = v.hi.z; r[7] = v.hi.w;
-            }
-        }
-        // a head vector's lanes are live together, so its reduction sees only live lanes
-        uint32_t w = 0;
-        if (live && kind != 0) {
-            float a = 0.0f;
+        const int seq_end = min(rr.first + rr.n, row_end), last = pos0 + rr.n - 1;
+        // the first row here that begins an octet or the sequence's tokens
+        int p = max(pos0 + (row - rr.first), 0);
+        if ((p & 7) != 0 && p != max(pos0, 0)) p = (p | 7) + 1;
+        for (; rr.first + (p - pos0) < seq_end; p = (p | 7) + 1) {
+            const int octet = p >> 3;                         // tokens p .. min(last, 8 * octet + 7)
+            const int t = octet * 8 + tok;
+            const bool here = t >= p && t <= last && (!nw.rope || t < nw.rope_rows);
+            const int64_t trow = rr.first + (t - pos0);
+            const int page = kv_page(b, seq, octet * 8, c.pages);
+            const int off = (octet * 8) & ((1 << c.page_shift) - 1);
+            const Angles ang = here && nw.rope ? angles<D>(nw.rope + static_cast<int64_t>(t) * nw.rope_dim, nw.rope_dim, nw.rope_style, d0, d1)
+                                               : Angles{};
+            auto base_of = [&](int hx) {
+                return hx < HQ ? trow * nw.ldq + static_cast<int64_t>(hx) * D
+                               : hx < HQ + H ? trow * nw.ldk + static_cast<int64_t>(hx - HQ) * D
+                                             : trow * nw.ldv + static_cast<int64_t>(hx - HQ - H) * D;
+            };
+            auto source = [&](int hx) { return hx < HQ ? nw.q : hx < HQ + H ? nw.k : nw.v; };
+            auto fetch = [&](int hx) {
+                Runs v{};
+                if (here && hx < heads) {
+                    v.lo = load4<DT>(source(hx), base_of(hx) + d0);
+                    v.hi = load4<DT>(source(hx), base_of(hx) + d1);
+                }
+                return v;
+            };
+            Runs next = fetch(hb0 * HPB + hs);
+            for (int hb = hb0; hb < hb1; ++hb) {
+                const int hx = hb * HPB + hs;
+                Runs v = next;
+                if (hb + 1 < hb1) next = fetch(hx + HPB);
+                const int kind = hx < HQ ? 0 : hx < HQ + H ? 1 : hx < heads ? 2 : 3;       // query, key, value, none
+                const int h = kind == 0 ? hx : kind == 1 ? hx - HQ : hx - HQ - H;
+                const bool live = here && kind < 3;
+                uint32_t w = 0;
+                if (live) {                                  // a head vector's lanes are live together
+                    if (kind < 2 && nw.rope) turn<DT>(v, ang, source(hx), base_of(hx), nw.rope_dim, nw.rope_style, d0, d1);
+                    if (turned_too) {
+                        Blk8 x{v.lo, v.hi};
+                        fwht128_regs_signed(x, l16);
+                        v = Runs{x.lo, x.hi};
+                    }
+                    if (kind == 0) {
+                        const float m = turned_too ? sign * 0x1p-7f : 1.0f;
+                        const int64_t at = (trow * HQ + h) * D;
+                        store4<DT>(nw.q_out, at + d0, make_float4(v.lo.x * m, v.lo.y * m, v.lo.z * m, v.lo.w * m));
+                        store4<DT>(nw.q_out, at + d1, make_float4(v.hi.x * m, v.hi.y * m, v.hi.z * m, v.hi.w * m));
+                    } else {
+                        float r[8] = {v.lo.x, v.lo.y, v.lo.z, v.lo.w, v.hi.x, v.hi.y, v.hi.z, v.hi.w};
+                        float a = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(r[i]));
-            a = head_max<L>(a);
-            const uint32_t sb = kv4_scale_bits(a / 6.0f);
-            const float s = f16_widen(sb);
-            if (s > 0.0f) {
+                        for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(r[i]));
+                        a = head_max<L>(a);
+                        const uint32_t sb = kv4_scale_bits(a / 6.0f);
+                        const float s = f16_widen(sb);
+                        if (s > 0.0f) {
+                            const float d = sign * s;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) r[i] = r[i] / s;
-                w = e2m1_pack8(r);
-            }
-            if (page >= 0) {
-                const int64_t vec = (static_cast<int64_t>(page) * H + h) << c.page_shift;    // first token of (page, head)
-                if (lane == 0) (kind == 1 ? c.k_scale : c.v_scale)[vec + off + tok] = static_cast<uint16_t>(sb);
-                if (kind == 1) {
-                    uint16_t *p = reinterpret_cast<uint16_t *>(c.k_codes + (vec + off + tok) * (D / 2));
-                    p[d0 >> 2] = static_cast<uint16_t>(w);
-                    p[d1 >> 2] = static_cast<uint16_t>(w >> 16);
+                            for (int i = 0; i < 8; ++i) r[i] = r[i] / d;
+                            w = e2m1_pack8(r);
+                        }
+                        if (page >= 0) {
+                            const int64_t vec = (static_cast<int64_t>(page) * H + h) << c.page_shift;    // first token of (page, head)
+                            if (lane == 0) (kind == 1 ? c.k_scale : c.v_scale)[vec + off + tok] = static_cast<uint16_t>(sb);
+                            if (kind == 1) {
+                                uint16_t *q = reinterpret_cast<uint16_t *>(c.k_codes + (vec + off + tok) * (D / 2));
+                                q[d0 >> 2] = static_cast<uint16_t>(w);
+                                q[d1 >> 2] = static_cast<uint16_t>(w >> 16);
+                            }
+                        }
+                    }
+                }
+                if ((hb + 1) * HPB <= HQ + H || page < 0) continue;   // no values among the workgroup's heads
+                __syncthreads();                              // the group before is read
+                if (kind == 2) codes[hs][tok][lane] = w;
+                __syncthreads();
+                if (kind == 2) {
+                    // one thread per dword: dimension d of head hs, the octet's eight tokens
+                    const int d = threadIdx.x % D;
+                    const int dl = d % 128, ln = D == 64 ? (d % 32) / 4 : (d / 128) * 16 + (dl % 64) / 4;
+                    const int nib = 4 * (d % 4) + (D == 64 ? (d >= 32 ? 16 : 0) : (dl >= 64 ? 16 : 0));
+                    uint32_t word = 0, mask = 0;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int tj = octet * 8 + j;
+                        const bool on = tj >= p && tj <= last && (!nw.rope || tj < nw.rope_rows);
+                        word |= ((codes[hs][j][ln] >> nib) & 15u) << (4 * j);
+                        mask |= on ? 15u << (4 * j) : 0u;
+                    }
+                    const int64_t vec = (static_cast<int64_t>(page) * H + h) << c.page_shift;
+                    uint32_t *q = reinterpret_cast<uint32_t *>(c.v_codes) + ((vec + off) >> 3) * D + d;
+                    *q = mask == 0xFFFFFFFFu ? word : (*q & ~mask) | (word & mask);
                 }
             }
         }
-        __syncthreads();                                     // the last octet's codes are read
-        if (kind == 2) codes[hs][tok][lane] = w;
-        __syncthreads();
-        if (kind == 2 && page >= 0) {
-            // one thread per dword: dimension d of head hs, the octet's eight tokens
-            const int d = threadIdx.x % D;
-            const int dl = d % 128, ln = D == 64 ? (d % 32) / 4 : (d / 128) * 16 + (dl % 64) / 4;
-            const int nib = 4 * (d % 4) + (D == 64 ? (d >= 32 ? 16 : 0) : (dl >= 64 ? 16 : 0));
-            uint32_t word = 0, mask = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int tj = octet * 8 + j;
-                const bool on = tj >= pos && tj <= last && (!nw.rope || tj < nw.rope_rows);
-                word |= ((codes[hs][j][ln] >> nib) & 15u) << (4 * j);
-                mask |= on ? 15u << (4 * j) : 0u;
-            }
-            const int64_t vec = (static_cast<int64_t>(page) * H + h) << c.page_shift;
-            uint32_t *p = reinterpret_cast<uint32_t *>(c.v_codes) + ((vec + off) >> 3) * D + d;
-            *p = mask == 0xFFFFFFFFu ? word : (*p & ~mask) | (word & mask);
-        }
+        row = rr.first + rr.n;
     }
 }
 
 template <int DT>
 hipError_t append_t(const Kv4Cache &c, const KvBatch &b, const Kv4New &n, hipStream_t st) {
-    // Few rows: a workgroup for each, so that no octet waits for another.  Many:
-    // one for every eight, so that most find one octet to do.
-    const int chunk = b.rows <= 512 ? 1 : 8;
-    const int hpb = 256 / c.D, heads = n.q_heads + 2 * c.heads;
-    const dim3 grid((b.rows + chunk - 1) / chunk, (heads + hpb - 1) / hpb), block(256);
-    if (c.D == 64) hipLaunchKernelGGL((kv4_append_kernel<DT, 64>), grid, block, 0, st, c, b, n, chunk);
-    else if (c.D == 128) hipLaunchKernelGGL((kv4_append_kernel<DT, 128>), grid, block, 0, st, c, b, n, chunk);
-    else hipLaunchKernelGGL((kv4_append_kernel<DT, 256>), grid, block, 0, st, c, b, n, chunk);
+    // Few rows: a workgroup for each and for every group of heads, so that none waits for
+    // another.  Many: one for every eight rows, most with one octet to do, and for several
+    // groups of heads.
+    const bool many = b.rows > 512;
+    const int chunk = many ? 8 : 1, hpb = 256 / c.D, groups = (n.q_heads + 2 * c.heads + hpb - 1) / hpb;
+    const int span = many ? (groups < kSpan ? groups : kSpan) : 1;
+    const dim3 grid((b.rows + chunk - 1) / chunk, (groups + span - 1) / span), block(256);
+    if (c.D == 64) hipLaunchKernelGGL((kv4_append_kernel<DT, 64>), grid, block, 0, st, c, b, n, chunk, span);
+    else if (c.D == 128) hipLaunchKernelGGL((kv4_append_kernel<DT, 128>), grid, block, 0, st, c, b, n, chunk, span);
+    else hipLaunchKernelGGL((kv4_append_kernel<DT, 256>), grid, block, 0, st, c, b, n, chunk, span);
     return hipGetLastError();
 }
 
