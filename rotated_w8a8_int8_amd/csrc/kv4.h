@@ -64,6 +64,34 @@ __device__ __forceinline__ int kv_seq_of(const KvBatch &b, int row) {
     return row >= r.first && row < r.first + r.n ? lo : -1;
 }
 
+// A row's sequence with its rows and tokens, for a row that a whole wave (all lanes on)
+// asks about: up to 64 sequences are looked at by a lane each, in one trip to memory.
+struct SeqOfRow {
+    int seq, len;
+    RowRange rr;
+};
+__device__ __forceinline__ SeqOfRow kv_seq_of_wave(const KvBatch &b, int row) {
+    SeqOfRow s{-1, 0, RowRange{0, 0}};
+    if (b.q_start && b.B <= 64) {
+        const int i = min(static_cast<int>(threadIdx.x & 63), b.B - 1);
+        const int lo = b.q_start[i], hi = b.q_start[i + 1], len = kv_len(b, i);
+        const uint64_t hit = __ballot(row >= lo && row < hi);
+        if (hit == 0) return s;
+        const int src = __builtin_ctzll(hit);
+        s.rr.first = __builtin_amdgcn_readlane(lo, src);
+        s.rr.n = __builtin_amdgcn_readlane(hi, src) - s.rr.first;
+        if (s.rr.first < 0 || s.rr.first + s.rr.n > b.rows) return s;
+        s.seq = src;
+        s.len = __builtin_amdgcn_readlane(len, src);
+        return s;
+    }
+    s.seq = kv_seq_of(b, row);
+    if (s.seq < 0) return s;
+    s.rr = kv_rows(b, s.seq);
+    s.len = kv_len(b, s.seq);
+    return s;
+}
+
 // The page that holds token t of sequence seq, or -1 (absent).  0 <= t < kv_len.
 __device__ __forceinline__ int kv_page(const KvBatch &b, int seq, int t, int pages) {
     const int id = b.block_table[static_cast<int64_t>(seq) * b.max_pages + (t >> b.page_shift)];

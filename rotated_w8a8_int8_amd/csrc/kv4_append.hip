@@ -139,13 +139,14 @@ __global__ __launch_bounds__(256) void kv4_append_kernel(Kv4Cache c, KvBatch b, 
 
     const int row_end = min(static_cast<int>(blockIdx.x + 1) * chunk, b.rows);
     for (int row = blockIdx.x * chunk; row < row_end;) {
-        const int seq = kv_seq_of(b, row);
+        const SeqOfRow found = kv_seq_of_wave(b, row);
+        const int seq = found.seq;
         if (seq < 0) {
             ++row;
             continue;
         }
-        const RowRange rr = kv_rows(b, seq);
-        const int pos0 = kv_len(b, seq) - rr.n;              // position of the sequence's first row
+        const RowRange rr = found.rr;
+        const int pos0 = found.len - rr.n;                   // position of the sequence's first row
         const int seq_end = min(rr.first + rr.n, row_end), last = pos0 + rr.n - 1;
         // the first row here that begins an octet or the sequence's tokens
         int p = max(pos0 + (row - rr.first), 0);
