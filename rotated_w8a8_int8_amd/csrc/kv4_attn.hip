@@ -21,8 +21,8 @@ __device__ __forceinline__ TokenRange seen(int pos, int len, int causal, int win
 }
 
 // The (row, head) pairs of a sequence that share a KV head are the columns of transposed
-// matrix products, 16 a product, NT of them a wave, so that nothing crosses lanes between
-// the two products of a step of 32 tokens:
+// matrix products, 16 a wave (32 where there are more), so that nothing crosses lanes
+// between the two products of a step of 32 tokens:
 //
 //   S^T [32 tokens][16 cols] = K Q^T    two 16x16x32 tiles; A: a lane holds D/4 dims of
 //                                       one token, one dword (8 dims) per product
@@ -272,14 +272,113 @@ __device__ __forceinline__ float times_half(float f, const u4 &x, int i) {
     return fmaf(f, static_cast<float>(h[i & 1]), 0.0f);
 }
 
-// blockIdx: x piece, y KV head.  A tile has TM = 16 * NT * WC columns, `cols` of them in
-// use at most.  Parts of a tile in several leave their sums in part_o [heads][slots][cols][D]
-// and part_ml [..][cols][2]; the others write the outputs.
-template <int DT, int D, int HL, int NT, int WC>
+// A wave's share of a piece: its columns and its steps.
+struct Share {
+    int first_row, len, pos0, pairs;      // the sequence: first row, tokens, first row's position, (row, head) pairs
+    int tile0, wave0;                     // first pair of the tile and of this wave
+    int begin, end;                       // steps: begin, begin + TG, .. below end
+    int open_lo, open_hi;                 // steps [open_lo, open_hi) that all the wave's rows see whole
+    TokenRange wave_r;                    // what the wave's rows see together
+};
+template <int TC, int TM, int TG>
+__device__ __forceinline__ Share wave_share(const KvBatch &b, const Kv4Attn &a, const Piece &pc, int seq, int G, int wc,
+                                            int tg) {
+    const SeqWork sw = seq_work(b, a, seq);
+    Share s;
+    s.first_row = sw.rr.first;
+    s.len = sw.len;
+    s.pos0 = sw.pos0;
+    s.pairs = sw.n * G;
+    s.tile0 = pc.tile * TM;
+    s.wave0 = s.tile0 + wc * TC;
+    const int tile_last = min(s.tile0 + TM, s.pairs) - 1;
+    const bool idle = s.wave0 >= s.pairs;                     // a wave without columns has no steps
+    const int first = idle ? s.tile0 : s.wave0, last = idle ? tile_last : min(s.wave0 + TC, s.pairs) - 1;
+    // rows see ever later tokens: the first pair's beginning and the last pair's end
+    auto one = [&](int pair) { return seen(s.pos0 + pair / G, s.len, a.causal, a.window); };
+    auto range = [&](int p, int q) {
+        TokenRange r{seen(max(s.pos0 + p / G, 0), s.len, a.causal, a.window).lo, one(q).hi};
+        if (r.hi < r.lo) r.hi = r.lo;
+        return r;
+    };
+    const TokenRange tile_r = range(s.tile0, tile_last);
+    s.wave_r = range(first, last);
+    const int steps = steps_of(tile_r.lo, tile_r.hi), each = (steps + pc.parts - 1) / pc.parts;
+    const int from = (tile_r.lo >> 5) + pc.part * each, to = (tile_r.lo >> 5) + min((pc.part + 1) * each, steps);
+    s.begin = __builtin_amdgcn_readfirstlane(max(from, s.wave_r.lo >> 5) + tg);
+    s.end = __builtin_amdgcn_readfirstlane(idle ? 0 : min(to, (s.wave_r.hi + 31) >> 5));
+    s.open_lo = __builtin_amdgcn_readfirstlane((seen(max(s.pos0 + last / G, 0), s.len, a.causal, a.window).lo + 31) >> 5);
+    s.open_hi = __builtin_amdgcn_readfirstlane(range(first, first).hi >> 5);
+    return s;
+}
+
+// Where a step's tokens lie.  Page ids come through the scalar cache (no kernel writes them
+// while this one runs): a vector load here would wait for every code on its way.
+struct Pages {
+    typedef const __attribute__((address_space(4))) int32_t *Ids;
+    Ids table;
+    int per_page, end, pages, heads, h, shift;
+    __device__ __forceinline__ Pages(const Kv4Cache &c, const KvBatch &b, int seq, int h_, int end_)
+        : table((Ids)(b.block_table + static_cast<int64_t>(seq) * b.max_pages)), per_page(b.page_shift - 5), end(end_),
+          pages(c.pages), heads(c.heads), h(h_), shift(c.page_shift) {}
+    // page of a step, -1 past the end
+    __device__ __forceinline__ int id(int step) const { return step < end ? table[step >> per_page] : -1; }
+    // index of the step's first token in the cache's [pages][heads][page] order; for a step past the
+    // end or on an absent page one that exists
+    __device__ __forceinline__ int64_t token(int page, int step) const {
+        const int64_t p = page >= 0 && page < pages ? page : 0;
+        return ((p * heads + h) << shift) + (step < end ? (step << 5) & ((1 << shift) - 1) : 0);
+    }
+};
+
+// Where a column's sums go: the output, or among the parts kept apart.
+template <int DT, int D>
+struct Output {
+    const Kv4Attn &a;
+    const Plan &pl;
+    const Piece &pc;
+    float *part_o, *part_ml;
+    int first_row, tile0, cols, h, G;
+    // four dims from d of the tile's column cc, with its reference exponent and normaliser
+    __device__ __forceinline__ void put(int cc, int d, f4 o, float m, float l) const {
+        if (pc.parts == 1) {
+            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+            const int cp = tile0 + cc;
+            const int64_t at = (static_cast<int64_t>(first_row + cp / G) * a.q_heads + h * G + cp % G) * D + d;
+            store4<DT>(a.o, at, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+        } else {
+            const int64_t slot = (static_cast<int64_t>(h) * pl.slots + pc.slot) * cols + cc;
+            *reinterpret_cast<f4 *>(part_o + slot * D + d) = o;
+            if (d == 0) *reinterpret_cast<float2 *>(part_ml + 2 * slot) = make_float2(m, l);
+        }
+    }
+};
+// The step groups' sums of n columns become one (each group's taken to the common maximum).
+template <int TG, int TM, int D, class Out>
+__device__ __forceinline__ void join_groups(const Out &out, float (&lds_o)[TG][TM][D + 4], float (&lds_ml)[TG][TM][2], int n) {
+    for (int e = threadIdx.x; e < n * (D / 4); e += 256) {
+        const int cc = e / (D / 4), d = 4 * (e % (D / 4));
+        f4 o{0.f, 0.f, 0.f, 0.f};
+        float m = kLowest, l = 0.0f;
+#pragma unroll
+        for (int k = 0; k < TG; ++k) m = fmaxf(m, lds_ml[k][cc][0]);
+#pragma unroll
+        for (int k = 0; k < TG; ++k) {
+            o += *reinterpret_cast<const f4 *>(&lds_o[k][cc][d]);
+            l += lds_ml[k][cc][1] * __builtin_amdgcn_exp2f(lds_ml[k][cc][0] - m);
+        }
+        out.put(cc, d, o, m, l);
+    }
+}
+
+// blockIdx: x piece, y KV head.  A tile has TM = 16 * WC columns, `cols` of them in use at
+// most.  Parts of a tile in several leave their sums in part_o [heads][slots][cols][D] and
+// part_ml [..][cols][2]; the others write the outputs.
+template <int DT, int D, int HL, int WC>
 __global__ __launch_bounds__(256, 2) void attn_kernel(Kv4Cache c, KvBatch b, Kv4Attn a, Plan pl, int cols,
                                                       float *part_o, float *part_ml) {
-    constexpr int TG = 4 / WC, TC = 16 * NT, TM = TC * WC;
-    static_assert(HL != 1 || (NT == 1 && WC == 1), "low parts ride along in one product of columns");
+    constexpr int TG = 4 / WC, TC = 16, TM = TC * WC, NK = D / 32;
+    static_assert(HL != 1 || WC == 1, "low parts ride along in one product of columns");
     __shared__ float lds_o[TG > 1 ? TG : 1][TG > 1 ? TM : 1][D + 4], lds_ml[TG > 1 ? TG : 1][TM][2];
     const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 4, col = lane & 15, tg = wid / WC, wc = wid % WC;
@@ -287,298 +386,432 @@ __global__ __launch_bounds__(256, 2) void attn_kernel(Kv4Cache c, KvBatch b, Kv4
     const Piece pc = find_piece<false>(b, a, pl, c.heads, G, blockIdx.x);
     if (pc.parts == 0) return;
     const int seq = __builtin_amdgcn_readfirstlane(pc.seq);
-    const SeqWork sw = seq_work(b, a, seq);
-    const RowRange rr = sw.rr;
-    const int len = sw.len, pos0 = sw.pos0, pairs = sw.n * G, tile0 = pc.tile * TM;   // first pair of the tile
+    const Share sh = wave_share<TC, TM, TG>(b, a, pc, seq, G, wc, tg);
 
-    // the tile's and this wave's share of the context
-    const int tile_last = min(tile0 + TM, pairs) - 1, wave0 = tile0 + wc * TC, wave_last = min(wave0 + TC, pairs) - 1;
-    const bool idle = wave0 >= pairs;
-    auto range = [&](int first, int last) {
-        const int p0 = pos0 + first / G, p1 = pos0 + last / G;
-        TokenRange r{seen(max(p0, 0), len, a.causal, a.window).lo, seen(p1, len, a.causal, a.window).hi};
-        if (r.hi < r.lo) r.hi = r.lo;
-        return r;
-    };
-    const TokenRange tile_r = range(tile0, tile_last), wave_r = range(idle ? tile0 : wave0, idle ? tile_last : wave_last);
-    const int steps = steps_of(tile_r.lo, tile_r.hi), share = (steps + pc.parts - 1) / pc.parts;
-    const int from = (tile_r.lo >> 5) + pc.part * share, to = (tile_r.lo >> 5) + min((pc.part + 1) * share, steps);
-    const int begin = __builtin_amdgcn_readfirstlane(max(from, wave_r.lo >> 5) + tg);
-    const int end = __builtin_amdgcn_readfirstlane(idle ? 0 : min(to, (wave_r.hi + 31) >> 5));
-
-    // steps [open_lo, open_hi) that all of the wave's rows see whole: rows see ever later tokens
-    const TokenRange first_r = range(idle ? tile0 : wave0, idle ? tile0 : wave0);
-    const int open_lo = __builtin_amdgcn_readfirstlane((seen(max(pos0 + (idle ? tile_last : wave_last) / G, 0), len, a.causal, a.window).lo + 31) >> 5);
-    const int open_hi = __builtin_amdgcn_readfirstlane(first_r.hi >> 5);
-
-    // this lane's columns: pair cp is row cp / G of the sequence, head h * G + cp % G
-    bool used[NT];
-    TokenRange tr[NT];
-    int64_t qrow[NT];
+    // this lane's column: pair cp is row cp / G of the sequence, head h * G + cp % G
+    const int cp = sh.wave0 + (HL == 1 ? col & 7 : col);
+    const bool used = cp < sh.pairs;
+    const int ci = used ? cp / G : 0, cg = used ? cp % G : 0;
+    const TokenRange tr = used ? seen(sh.pos0 + ci, sh.len, a.causal, a.window) : sh.wave_r;
+    const int64_t qrow = (static_cast<int64_t>(sh.first_row + ci) * a.q_heads + h * G + cg) * D;
+    // the query's values are asked for first, then the first steps
+    float qv[NK][8];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const int cp = wave0 + 16 * t + (HL == 1 ? col & 7 : col);
-        used[t] = cp < pairs;
-        const int ci = used[t] ? cp / G : 0, cg = used[t] ? cp % G : 0;
-        tr[t] = used[t] ? seen(pos0 + ci, len, a.causal, a.window) : wave_r;
-        qrow[t] = (static_cast<int64_t>(rr.first + ci) * a.q_heads + h * G + cg) * D;
+    for (int j = 0; j < NK; ++j) {
+        const int64_t at = qrow + g * (D / 4) + 8 * j;
+        const float4 x = load4<DT>(a.q, at), y = load4<DT>(a.q, at + 4);
+        qv[j][0] = x.x; qv[j][1] = x.y; qv[j][2] = x.z; qv[j][3] = x.w;
+        qv[j][4] = y.x; qv[j][5] = y.y; qv[j][6] = y.z; qv[j][7] = y.w;
     }
-    // the queries' values are asked for first, then the first steps
-    constexpr int NK = D / 32;
-    float qv[NT][NK][8];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int j = 0; j < NK; ++j) {
-            const int64_t at = qrow[t] + g * (D / 4) + 8 * j;
-            const float4 x = load4<DT>(a.q, at), y = load4<DT>(a.q, at + 4);
-            qv[t][j][0] = x.x; qv[t][j][1] = x.y; qv[t][j][2] = x.z; qv[t][j][3] = x.w;
-            qv[t][j][4] = y.x; qv[t][j][5] = y.y; qv[t][j][6] = y.z; qv[t][j][7] = y.w;
-        }
 
-    const int per_page = b.page_shift - 5;                    // log2 of steps a page
-    // Page ids come through the scalar cache (no kernel writes them while this one runs): a
-    // vector load here would wait for every code on its way.
-    typedef const __attribute__((address_space(4))) int32_t *scalar_ids;
-    const scalar_ids table = (scalar_ids)(b.block_table + static_cast<int64_t>(seq) * b.max_pages);
-    auto page_of = [&](int step) { return step < end ? table[step >> per_page] : -1; };
-    auto token_of = [&](int page, int step) {
-        const int64_t p = page >= 0 && page < c.pages ? page : 0;
-        return ((p * c.heads + h) << c.page_shift) + (step < end ? (step << 5) & ((1 << c.page_shift) - 1) : 0);
-    };
-
-    // A wave's steps go through a ring: two (one, where the columns' sums fill the
-    // registers) on their way while one is worked on.  Past the end the loads go on, to the
-    // start of page 0 (cached, unused): were they conditional, the wait for a step's codes
-    // would have to be a wait for the later ones too.
-    constexpr int NB = D == 256 || NT > 1 ? 2 : 3;
+    // A wave's steps go through a ring: two (one, where the sums fill the registers) on
+    // their way while one is worked on.  Past the end the loads go on, to a page that exists
+    // (cached, unused): were they conditional, the wait for a step's codes would have to be
+    // a wait for the later ones too.
+    const Pages pages(c, b, seq, h, sh.end);
+    constexpr int NB = D == 256 ? 2 : 3;
     constexpr bool ONCE = WC == 1;                            // no other wave reads these codes
     Step<D> ring[NB];
     int page[NB];
 #pragma unroll
-    for (int k = 0; k < NB; ++k) page[k] = page_of(begin + k * TG);
+    for (int k = 0; k < NB; ++k) page[k] = pages.id(sh.begin + k * TG);
 #pragma unroll
-    for (int k = 0; k < NB - 1; ++k) load_step<D, ONCE>(ring[k], c, token_of(page[k], begin + k * TG), g, col);
+    for (int k = 0; k < NB - 1; ++k) load_step<D, ONCE>(ring[k], c, pages.token(page[k], sh.begin + k * TG), g, col);
 
-    u4 qf[NT][NK], ql[HL == 2 ? NT : 1][HL == 2 ? NK : 1];
-    float scale[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
+    u4 qf[NK], ql[HL == 2 ? NK : 1];
+    float scale;
+    {
         float big = 0.0f;
 #pragma unroll
         for (int j = 0; j < NK; ++j)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(qv[t][j][i]));
+            for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(qv[j][i]));
         big = col_max(big);
         // largest value to [2^9, 2^10), undone in the scores' factor (both exact)
         const int e = big > 0.0f ? 10 - __builtin_amdgcn_frexp_expf(big) : 0;
 #pragma unroll
         for (int j = 0; j < NK; ++j) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) qv[t][j][i] = used[t] ? __builtin_amdgcn_ldexpf(qv[t][j][i], e) : 0.0f;
+            for (int i = 0; i < 8; ++i) qv[j][i] = used ? __builtin_amdgcn_ldexpf(qv[j][i], e) : 0.0f;
             if constexpr (HL == 0) {
-                qf[t][j] = f16_pack8(qv[t][j]);
+                qf[j] = f16_pack8(qv[j]);
             } else {
                 u4 hi, low;
-                f16_split8(qv[t][j], hi, low);
-                if constexpr (HL == 2) ql[t][j] = low;
-                qf[t][j] = HL == 1 && col >= 8 ? low : hi;
+                f16_split8(qv[j], hi, low);
+                if constexpr (HL == 2) ql[j] = low;
+                qf[j] = HL == 1 && col >= 8 ? low : hi;
             }
         }
-        scale[t] = fmaxf(__builtin_amdgcn_ldexpf(a.sm_scale * kLog2e, -e), 1e-30f);   // never 0: a masked score is -inf
+        scale = fmaxf(__builtin_amdgcn_ldexpf(a.sm_scale * kLog2e, -e), 1e-30f);   // never 0: a masked score is -inf
     }
 
-    float m[NT], l[NT];
-    f4 acc[NT][D / 16];
+    float m = kLowest, l = 0.0f;
+    f4 acc[D / 16];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        m[t] = kLowest;
-        l[t] = 0.0f;
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) acc[t][j] = f4{0.f, 0.f, 0.f, 0.f};
-    }
+    for (int j = 0; j < D / 16; ++j) acc[j] = f4{0.f, 0.f, 0.f, 0.f};
 
     auto work = [&](Step<D> &cur, int step) {
-        float s[NT][8];
+        float s[8];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            f4 x[NT];
-#pragma unroll
-            for (int t = 0; t < NT; ++t) x[t] = f4{0.f, 0.f, 0.f, 0.f};
+            f4 x{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int j = 0; j < NK; ++j) {
                 const u4 kf = levels8(cur.k[u][j]);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    if constexpr (HL == 2) x[t] = mma16(kf, ql[t][j], x[t]);
-                    x[t] = mma16(kf, qf[t][j], x[t]);
-                }
+                if constexpr (HL == 2) x = mma16(kf, ql[j], x);
+                x = mma16(kf, qf[j], x);
             }
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float y = x[t][i];
-                    if constexpr (HL == 1) y += lane_xor<8>(y);          // high and low part of the query
-                    s[t][4 * u + i] = times_half(y, cur.ks, 4 * u + i);
-                }
+            for (int i = 0; i < 4; ++i) {
+                float y = x[i];
+                if constexpr (HL == 1) y += lane_xor<8>(y);          // high and low part of the query
+                s[4 * u + i] = times_half(y, cur.ks, 4 * u + i);
+            }
         }
-        if (step < open_lo || step >= open_hi) {
+        if (step < sh.open_lo || step >= sh.open_hi) {
             const int t0 = (step << 5) + 8 * g;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                bool any = false;
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const bool on = t0 + i >= tr[t].lo && t0 + i < tr[t].hi;
-                    s[t][i] = on ? s[t][i] : -INFINITY;
-                    any = any || on;
-                }
+                const bool on = t0 + i >= tr.lo && t0 + i < tr.hi;
+                s[i] = on ? s[i] : -INFINITY;
                 // a scale past the sequence's end may be anything
-                cur.vs[i >> 1] &= any ? 0xFFFFFFFFu : (i & 1 ? 0x0000FFFFu : 0xFFFF0000u);
+                cur.vs[i >> 1] &= on ? 0xFFFFFFFFu : (i & 1 ? 0x0000FFFFu : 0xFFFF0000u);
             }
         }
-        float w[NT][8], sum[NT];
-        bool pass = false;
+        float w[8], sum = 0.0f;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            sum[t] = 0.0f;
+        for (int i = 0; i < 8; ++i) {
+            const float p = __builtin_amdgcn_exp2f(fmaf(s[i], scale, -m));
+            sum += p;
+            w[i] = times_half(p, cur.vs, i);
+        }
+        if (__any(!(max8(w) <= kMost && sum <= kMostP))) {         // also the first step: m is the lowest
+            float most = -INFINITY;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float p = __builtin_amdgcn_exp2f(fmaf(s[t][i], scale[t], -m[t]));
-                sum[t] += p;
-                w[t][i] = times_half(p, cur.vs, i);
+                const float vs = times_half(1.0f, cur.vs, i);
+                most = fmaxf(most, fmaf(s[i], scale, vs > 0.0f ? static_cast<float>(__builtin_amdgcn_frexp_expf(vs)) : -24.0f));
             }
-            pass = pass || !(max8(w[t]) <= kMost && sum[t] <= kMostP);
-        }
-        if (__any(pass)) {                                 // also the first step: m is the lowest
+            const float mn = fmaxf(m, col_max(most) - kRoom), shrink = __builtin_amdgcn_exp2f(m - mn);
+            m = mn;
+            l *= shrink;
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                float most = -INFINITY;
+            for (int j = 0; j < D / 16; ++j) acc[j] *= shrink;
+            sum = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float vs = times_half(1.0f, cur.vs, i);
-                    most = fmaxf(most, fmaf(s[t][i], scale[t], vs > 0.0f ? static_cast<float>(__builtin_amdgcn_frexp_expf(vs)) : -24.0f));
-                }
-                const float mn = fmaxf(m[t], col_max(most) - kRoom), shrink = __builtin_amdgcn_exp2f(m[t] - mn);
-                m[t] = mn;
-                l[t] *= shrink;
-#pragma unroll
-                for (int j = 0; j < D / 16; ++j) acc[t][j] *= shrink;
-                sum[t] = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float p = __builtin_amdgcn_exp2f(fmaf(s[t][i], scale[t], -m[t]));
-                    sum[t] += p;
-                    w[t][i] = times_half(p, cur.vs, i);
-                }
+            for (int i = 0; i < 8; ++i) {
+                const float p = __builtin_amdgcn_exp2f(fmaf(s[i], scale, -m));
+                sum += p;
+                w[i] = times_half(p, cur.vs, i);
             }
         }
-        u4 wf[NT], wl[NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            l[t] += sum[t];
-            if constexpr (HL == 0) {
-                wf[t] = f16_pack8(w[t]);
-            } else {
-                u4 hi;
-                f16_split8(w[t], hi, wl[t]);
-                wf[t] = HL == 1 && col >= 8 ? wl[t] : hi;
-            }
+        l += sum;
+        u4 wf, wl;
+        if constexpr (HL == 0) {
+            wf = f16_pack8(w);
+        } else {
+            u4 hi;
+            f16_split8(w, hi, wl);
+            wf = HL == 1 && col >= 8 ? wl : hi;
         }
 #pragma unroll
         for (int j = 0; j < D / 64; ++j) {
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 const u4 vf = levels8(cur.v[j][x]);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    if constexpr (HL == 2) acc[t][4 * j + x] = mma16(vf, wl[t], acc[t][4 * j + x]);
-                    acc[t][4 * j + x] = mma16(vf, wf[t], acc[t][4 * j + x]);
-                }
+                if constexpr (HL == 2) acc[4 * j + x] = mma16(vf, wl, acc[4 * j + x]);
+                acc[4 * j + x] = mma16(vf, wf, acc[4 * j + x]);
             }
         }
     };
-    for (int step = begin; step < end;) {
+    for (int step = sh.begin; step < sh.end;) {
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
             constexpr int ahead = NB - 1;
             const int in = (k + ahead) % NB;
-            load_step<D, ONCE>(ring[in], c, token_of(page[in], step + ahead * TG), g, col);
+            load_step<D, ONCE>(ring[in], c, pages.token(page[in], step + ahead * TG), g, col);
             const int now = page[k];
-            page[k] = page_of(step + NB * TG);
+            page[k] = pages.id(step + NB * TG);
             if (now >= 0 && now < c.pages) work(ring[k], step);
             step += TG;
-            if (step >= end) break;
+            if (step >= sh.end) break;
         }
     }
 
     // lane (g, c) holds dims 64 j + 16 g .. + 15 of column c: acc[4 j + x][i] is 4 i + x of them
-    auto dims4 = [&](int t, int j, int i) { return f4{acc[t][4 * j][i], acc[t][4 * j + 1][i], acc[t][4 * j + 2][i], acc[t][4 * j + 3][i]}; };
-    auto put = [&](int cc, int d, f4 o, float mt, float lt) {
-        // sums of the tile's column cc
-        if (pc.parts == 1) {
-            const float inv = lt > 0.0f ? 1.0f / lt : 0.0f;
-            const int cp = tile0 + cc;
-            const int64_t at = (static_cast<int64_t>(rr.first + cp / G) * a.q_heads + h * G + cp % G) * D + d;
-            store4<DT>(a.o, at, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+    auto dims4 = [&](int j, int i) { return f4{acc[4 * j][i], acc[4 * j + 1][i], acc[4 * j + 2][i], acc[4 * j + 3][i]}; };
+    const Output<DT, D> out{a, pl, pc, part_o, part_ml, sh.first_row, sh.tile0, cols, h, G};
+    l = col_sum(l);
+    if constexpr (TG == 1) {
+        if (!used) return;
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) out.put(wc * TC + col, 64 * j + 16 * g + 4 * i, dims4(j, i), m, l);
+    } else {
+        const int lc = wc * TC + col;
+        if (g == 0) {
+            lds_ml[tg][lc][0] = m;
+            lds_ml[tg][lc][1] = l;
+        }
+        __syncthreads();
+        float top = kLowest;
+#pragma unroll
+        for (int k = 0; k < TG; ++k) top = fmaxf(top, lds_ml[k][lc][0]);
+        const float mine = __builtin_amdgcn_exp2f(m - top);
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f4 o = dims4(j, i);
+                if constexpr (HL == 1) o = f4{o.x + lane_xor<8>(o.x), o.y + lane_xor<8>(o.y), o.z + lane_xor<8>(o.z), o.w + lane_xor<8>(o.w)};
+                *reinterpret_cast<f4 *>(&lds_o[tg][lc][64 * j + 16 * g + 4 * i]) = o * mine;
+            }
+        __syncthreads();
+        join_groups<TG, TM, D>(out, lds_o, lds_ml, min(TM, sh.pairs - sh.tile0));
+    }
+}
+
+// ---- 32 columns a wave -------------------------------------------------------
+//
+// The same two products with 32x32x16 matrix operations, half as many, one column and 16
+// tokens a lane (g = lane / 32, c = lane % 32):
+//
+//   S^T [32 tokens][32 cols]: A: a lane holds D/2 dims of one token, one dword a product
+//   O^T [D][32 cols]: D/32 tiles, two products each of 16 tokens; A: a lane holds one dim of
+//                     eight tokens, one dword
+//
+// Row r of S^T is token 16 (r / 16) + 8 (r / 4 % 2) + 4 (r / 8 % 2) + r % 4, so that lane (g,
+// c) comes out with octets g and 2 + g of column c, what O^T's two products take.
+typedef float f16v __attribute__((ext_vector_type(16)));
+__device__ __forceinline__ f16v mma32(u4 a, u4 b, f16v c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, a), __builtin_bit_cast(h8, b), c, 0, 0, 0);
+}
+
+template <int D>
+struct WideStep {
+    uint32_t k[D / 16];         // D / 2 dims of a token
+    uint32_t v[2][D / 32];      // octets g and 2 + g: dims D / 32 * r ..
+    u4 ks[2], vs[2];            // f16 scales of the octets
+};
+template <int D>
+__device__ __forceinline__ void load_step(WideStep<D> &s, const Kv4Cache &c, int64_t tok, int g, int r) {
+    const int row = 16 * (r >> 4) + 8 * ((r >> 2) & 1) + 4 * ((r >> 3) & 1) + (r & 3);
+    const u4 *kp = reinterpret_cast<const u4 *>(c.k_codes + (tok + row) * (D / 2) + g * (D / 4));
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) {
+        const u4 x = kp[j];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s.k[4 * j + i] = x[i];
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const uint32_t *vp = reinterpret_cast<const uint32_t *>(c.v_codes) + ((tok >> 3) + 2 * e + g) * D + D / 32 * r;
+        if constexpr (D == 64) {
+            const u2 x = *reinterpret_cast<const u2 *>(vp);
+            s.v[e][0] = x.x;
+            s.v[e][1] = x.y;
         } else {
-            const int64_t slot = (static_cast<int64_t>(h) * pl.slots + pc.slot) * cols + cc;
-            *reinterpret_cast<f4 *>(part_o + slot * D + d) = o;
-            if (d == 0) *reinterpret_cast<float2 *>(part_ml + 2 * slot) = make_float2(mt, lt);
+            const u4 x = *reinterpret_cast<const u4 *>(vp);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s.v[e][i] = x[i];
+        }
+        s.ks[e] = *reinterpret_cast<const u4 *>(c.k_scale + tok + 16 * e + 8 * g);
+        s.vs[e] = *reinterpret_cast<const u4 *>(c.v_scale + tok + 16 * e + 8 * g);
+    }
+}
+__device__ __forceinline__ float max16(const float (&s)[16]) {
+    float m = fmaxf(s[0], s[1]);
+#pragma unroll
+    for (int i = 2; i < 16; i += 2) m = fmaxf(m, fmaxf(s[i], s[i + 1]));
+    return m;
+}
+
+// Four dims in a row of a lane's column, from register r of the tiles.
+template <int D>
+__device__ __forceinline__ f4 wide_dims(const f16v (&acc)[D / 32], int r) {
+    if constexpr (D == 64) return f4{acc[0][r], acc[1][r], acc[0][r + 1], acc[1][r + 1]};
+    else return f4{acc[0][r], acc[1][r], acc[2][r], acc[3][r]};
+}
+
+// As attn_kernel, with TM = 32 * WC columns a tile.  SP: f32 queries and weights in two parts.
+template <int DT, int D, bool SP, int WC>
+__global__ __launch_bounds__(256, 2) void attn_wide_kernel(Kv4Cache c, KvBatch b, Kv4Attn a, Plan pl, int cols,
+                                                           float *part_o, float *part_ml) {
+    constexpr int TG = 4 / WC, TC = 32, TM = TC * WC, NK = D / 16, ND = D / 32;
+    __shared__ float lds_o[TG > 1 ? TG : 1][TG > 1 ? TM : 1][D + 4], lds_ml[TG > 1 ? TG : 1][TM][2];
+    const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int g = lane >> 5, col = lane & 31, tg = wid / WC, wc = wid % WC;
+    const int h = blockIdx.y, G = a.q_heads / c.heads;
+    const Piece pc = find_piece<false>(b, a, pl, c.heads, G, blockIdx.x);
+    if (pc.parts == 0) return;
+    const int seq = __builtin_amdgcn_readfirstlane(pc.seq);
+    const Share sh = wave_share<TC, TM, TG>(b, a, pc, seq, G, wc, tg);
+
+    // this lane's column: pair cp is row cp / G of the sequence, head h * G + cp % G
+    const int cp = sh.wave0 + col;
+    const bool used = cp < sh.pairs;
+    const int ci = used ? cp / G : 0, cg = used ? cp % G : 0;
+    const TokenRange tr = used ? seen(sh.pos0 + ci, sh.len, a.causal, a.window) : sh.wave_r;
+    const int64_t qrow = (static_cast<int64_t>(sh.first_row + ci) * a.q_heads + h * G + cg) * D;
+    float qv[NK][8];
+#pragma unroll
+    for (int j = 0; j < NK; ++j) {
+        const int64_t at = qrow + g * (D / 2) + 8 * j;
+        const float4 x = load4<DT>(a.q, at), y = load4<DT>(a.q, at + 4);
+        qv[j][0] = x.x; qv[j][1] = x.y; qv[j][2] = x.z; qv[j][3] = x.w;
+        qv[j][4] = y.x; qv[j][5] = y.y; qv[j][6] = y.z; qv[j][7] = y.w;
+    }
+
+    const Pages pages(c, b, seq, h, sh.end);
+    constexpr int NB = 2;
+    WideStep<D> ring[NB];
+    int page[NB];
+#pragma unroll
+    for (int k = 0; k < NB; ++k) page[k] = pages.id(sh.begin + k * TG);
+#pragma unroll
+    for (int k = 0; k < NB - 1; ++k) load_step<D>(ring[k], c, pages.token(page[k], sh.begin + k * TG), g, col);
+
+    u4 qf[NK], ql[SP ? NK : 1];
+    float scale;
+    {
+        float big = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NK; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(qv[j][i]));
+        big = fmaxf(big, __shfl_xor(big, 32));
+        const int e = big > 0.0f ? 10 - __builtin_amdgcn_frexp_expf(big) : 0;
+#pragma unroll
+        for (int j = 0; j < NK; ++j) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) qv[j][i] = used ? __builtin_amdgcn_ldexpf(qv[j][i], e) : 0.0f;
+            if constexpr (SP) f16_split8(qv[j], qf[j], ql[j]);
+            else qf[j] = f16_pack8(qv[j]);
+        }
+        scale = fmaxf(__builtin_amdgcn_ldexpf(a.sm_scale * kLog2e, -e), 1e-30f);   // never 0: a masked score is -inf
+    }
+
+    float m = kLowest, l = 0.0f;
+    f16v acc[ND];
+#pragma unroll
+    for (int x = 0; x < ND; ++x)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[x][i] = 0.0f;
+
+    auto work = [&](WideStep<D> &cur, int step) {
+        f16v st;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) st[i] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NK; ++j) {
+            const u4 kf = levels8(cur.k[j]);
+            if constexpr (SP) st = mma32(kf, ql[j], st);
+            st = mma32(kf, qf[j], st);
+        }
+        float s[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = times_half(st[i], cur.ks[i >> 3], i & 7);
+        if (step < sh.open_lo || step >= sh.open_hi) {
+            const int t0 = (step << 5) + 8 * g;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int t = t0 + 16 * (i >> 3) + (i & 7);
+                const bool on = t >= tr.lo && t < tr.hi;
+                s[i] = on ? s[i] : -INFINITY;
+                // a scale past the sequence's end may be anything
+                cur.vs[i >> 3][(i & 7) >> 1] &= on ? 0xFFFFFFFFu : (i & 1 ? 0x0000FFFFu : 0xFFFF0000u);
+            }
+        }
+        float w[16], sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float p = __builtin_amdgcn_exp2f(fmaf(s[i], scale, -m));
+            sum += p;
+            w[i] = times_half(p, cur.vs[i >> 3], i & 7);
+        }
+        if (__any(!(max16(w) <= kMost && sum <= kMostP))) {                        // also the first step: m is the lowest
+            float most = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float vs = times_half(1.0f, cur.vs[i >> 3], i & 7);
+                most = fmaxf(most, fmaf(s[i], scale, vs > 0.0f ? static_cast<float>(__builtin_amdgcn_frexp_expf(vs)) : -24.0f));
+            }
+            most = fmaxf(most, __shfl_xor(most, 32));
+            const float mn = fmaxf(m, most - kRoom), shrink = __builtin_amdgcn_exp2f(m - mn);
+            m = mn;
+            l *= shrink;
+#pragma unroll
+            for (int x = 0; x < ND; ++x) acc[x] *= shrink;
+            sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float p = __builtin_amdgcn_exp2f(fmaf(s[i], scale, -m));
+                sum += p;
+                w[i] = times_half(p, cur.vs[i >> 3], i & 7);
+            }
+        }
+        l += sum;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float we[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) we[i] = w[8 * e + i];
+            u4 wf, wl;
+            if constexpr (SP) f16_split8(we, wf, wl);
+            else wf = f16_pack8(we);
+#pragma unroll
+            for (int x = 0; x < ND; ++x) {
+                const u4 vf = levels8(cur.v[e][x]);
+                if constexpr (SP) acc[x] = mma32(vf, wl, acc[x]);
+                acc[x] = mma32(vf, wf, acc[x]);
+            }
         }
     };
+    for (int step = sh.begin; step < sh.end;) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) l[t] = col_sum(l[t]);
+        for (int k = 0; k < NB; ++k) {
+            constexpr int ahead = NB - 1;
+            const int in = (k + ahead) % NB;
+            load_step<D>(ring[in], c, pages.token(page[in], step + ahead * TG), g, col);
+            const int now = page[k];
+            page[k] = pages.id(step + NB * TG);
+            if (now >= 0 && now < c.pages) work(ring[k], step);
+            step += TG;
+            if (step >= sh.end) break;
+        }
+    }
+
+    // lane (g, c): tile x's row 8 q + 4 g + i is dim D / 32 * row + x; four dims in a row from (q, i)
+    l += __shfl_xor(l, 32);
+    const Output<DT, D> out{a, pl, pc, part_o, part_ml, sh.first_row, sh.tile0, cols, h, G};
     if constexpr (TG == 1) {
+        if (!used) return;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            if (!used[t]) continue;
+        for (int q = 0; q < 4; ++q)
 #pragma unroll
-            for (int j = 0; j < D / 64; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) put(wc * TC + 16 * t + col, 64 * j + 16 * g + 4 * i, dims4(t, j, i), m[t], l[t]);
-        }
+            for (int i = 0; i < 4; i += 128 / D) {
+                const f4 o = wide_dims<D>(acc, 4 * q + i);
+                out.put(wc * TC + col, D / 32 * (8 * q + 4 * g + i), o, m, l);
+            }
     } else {
-        // the step groups' sums of a column become one
         const int lc = wc * TC + col;
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-            if (g == 0) {
-                lds_ml[tg][lc + 16 * t][0] = m[t];
-                lds_ml[tg][lc + 16 * t][1] = l[t];
-            }
-        __syncthreads();
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            float top = kLowest;
-#pragma unroll
-            for (int k = 0; k < TG; ++k) top = fmaxf(top, lds_ml[k][lc + 16 * t][0]);
-            const float mine = __builtin_amdgcn_exp2f(m[t] - top);
-#pragma unroll
-            for (int j = 0; j < D / 64; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    f4 o = dims4(t, j, i);
-                    if constexpr (HL == 1) o = f4{o.x + lane_xor<8>(o.x), o.y + lane_xor<8>(o.y), o.z + lane_xor<8>(o.z), o.w + lane_xor<8>(o.w)};
-                    *reinterpret_cast<f4 *>(&lds_o[tg][lc + 16 * t][64 * j + 16 * g + 4 * i]) = o * mine;
-                }
+        if (g == 0) {
+            lds_ml[tg][lc][0] = m;
+            lds_ml[tg][lc][1] = l;
         }
         __syncthreads();
-        const int n = min(TM, pairs - tile0);
-        for (int e = threadIdx.x; e < n * (D / 4); e += 256) {
-            const int cc = e / (D / 4), d = 4 * (e % (D / 4));
-            f4 o{0.f, 0.f, 0.f, 0.f};
-            float mt = kLowest, lt = 0.0f;
+        float top = kLowest;
 #pragma unroll
-            for (int k = 0; k < TG; ++k) mt = fmaxf(mt, lds_ml[k][cc][0]);
+        for (int k = 0; k < TG; ++k) top = fmaxf(top, lds_ml[k][lc][0]);
+        const float mine = __builtin_amdgcn_exp2f(m - top);
 #pragma unroll
-            for (int k = 0; k < TG; ++k) {
-                o += *reinterpret_cast<const f4 *>(&lds_o[k][cc][d]);
-                lt += lds_ml[k][cc][1] * __builtin_amdgcn_exp2f(lds_ml[k][cc][0] - mt);
-            }
-            put(cc, d, o, mt, lt);
-        }
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int i = 0; i < 4; i += 128 / D)
+                *reinterpret_cast<f4 *>(&lds_o[tg][lc][D / 32 * (8 * q + 4 * g + i)]) = wide_dims<D>(acc, 4 * q + i) * mine;
+        __syncthreads();
+        join_groups<TG, TM, D>(out, lds_o, lds_ml, min(TM, sh.pairs - sh.tile0));
     }
 }
 
@@ -658,10 +891,10 @@ Plan make_plan(const KvBatch &b, int heads, int G, int tm, int target, int min_c
 
 // The kernel's shape for a call: by the pairs of one sequence and KV head, the most columns
 // a workgroup is offered, so that no wave multiplies mostly padding and short prompts keep
-// their waves busy on the context.  Heads of 256 fill the registers with one product of
-// columns a wave.
+// their waves busy on the context.  Heads of 256 fill the registers with 16 columns a wave.
 struct Shape {
-    int nt, wc;             // products of 16 columns a wave, groups of columns
+    bool wide;              // 32 columns a wave
+    int wc;                 // groups of columns
     Plan plan;
     int cols;               // columns kept for a part
     int64_t sums, stats;    // bytes of the parts' sums and of their statistics
@@ -670,11 +903,12 @@ Shape attn_shape(const KvBatch &b, const Kv4Cache &c, int q_heads) {
     Shape s;
     const int G = q_heads / c.heads;
     const int64_t pairs = static_cast<int64_t>(b.max_q) * G;
-    s.nt = c.D == 256 || pairs <= 16 ? 1 : 2;
-    s.wc = pairs <= 16 * s.nt ? 1 : pairs <= 32 * s.nt ? 2 : 4;
-    const int tm = 16 * s.nt * s.wc;
+    s.wide = c.D != 256 && pairs > 16;
+    const int tc = s.wide ? 32 : 16;
+    s.wc = pairs <= tc ? 1 : pairs <= 2 * tc ? 2 : 4;
+    const int tm = tc * s.wc;
     // workgroups that the chip's 256 CUs hold at once
-    const int held = c.D == 64 && s.nt == 1 ? 5 : c.D == 128 && s.nt == 1 ? 3 : 2;
+    const int held = s.wide || c.D == 256 ? 2 : c.D == 128 ? 3 : 5;
     s.plan = make_plan(b, c.heads, G, tm, 256 * held, s.wc == 1 ? 4 : 8);
     s.cols = static_cast<int>(pairs < tm ? pairs : tm);
     s.sums = static_cast<int64_t>(c.heads) * s.plan.slots * s.cols * c.D * 4;
@@ -682,21 +916,27 @@ Shape attn_shape(const KvBatch &b, const Kv4Cache &c, int q_heads) {
     return s;
 }
 
-template <int DT, int D, int NT, int WC>
-void launch_shape(const Shape &s, const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, float *part_o, float *part_ml,
-                  hipStream_t st) {
+template <int DT, int D, int WC>
+void launch_narrow(const Shape &s, const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, float *part_o, float *part_ml,
+                   hipStream_t st) {
     const dim3 grid(s.plan.pieces, c.heads), block(256);
     if constexpr (DT != kDtF32) {
-        hipLaunchKernelGGL((attn_kernel<DT, D, 0, NT, WC>), grid, block, 0, st, c, b, a, s.plan, s.cols, part_o, part_ml);
+        hipLaunchKernelGGL((attn_kernel<DT, D, 0, WC>), grid, block, 0, st, c, b, a, s.plan, s.cols, part_o, part_ml);
     } else {
-        if constexpr (NT == 1 && WC == 1) {
+        if constexpr (WC == 1) {
             if (s.cols <= 8) {
-                hipLaunchKernelGGL((attn_kernel<DT, D, 1, NT, WC>), grid, block, 0, st, c, b, a, s.plan, s.cols, part_o, part_ml);
+                hipLaunchKernelGGL((attn_kernel<DT, D, 1, WC>), grid, block, 0, st, c, b, a, s.plan, s.cols, part_o, part_ml);
                 return;
             }
         }
-        hipLaunchKernelGGL((attn_kernel<DT, D, 2, NT, WC>), grid, block, 0, st, c, b, a, s.plan, s.cols, part_o, part_ml);
+        hipLaunchKernelGGL((attn_kernel<DT, D, 2, WC>), grid, block, 0, st, c, b, a, s.plan, s.cols, part_o, part_ml);
     }
+}
+template <int DT, int D, int WC>
+void launch_wide(const Shape &s, const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, float *part_o, float *part_ml,
+                 hipStream_t st) {
+    hipLaunchKernelGGL((attn_wide_kernel<DT, D, DT == kDtF32, WC>), dim3(s.plan.pieces, c.heads), dim3(256), 0, st, c, b, a,
+                       s.plan, s.cols, part_o, part_ml);
 }
 
 template <int DT, int D>
@@ -704,14 +944,14 @@ hipError_t launch_d(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, hipSt
     const Shape s = attn_shape(b, c, a.q_heads);
     float *part_o = static_cast<float *>(a.workspace), *part_ml = part_o + s.sums / 4;
     if constexpr (D == 256) {
-        if (s.wc == 1) launch_shape<DT, D, 1, 1>(s, c, b, a, part_o, part_ml, st);
-        else if (s.wc == 2) launch_shape<DT, D, 1, 2>(s, c, b, a, part_o, part_ml, st);
-        else launch_shape<DT, D, 1, 4>(s, c, b, a, part_o, part_ml, st);
+        if (s.wc == 1) launch_narrow<DT, D, 1>(s, c, b, a, part_o, part_ml, st);
+        else if (s.wc == 2) launch_narrow<DT, D, 2>(s, c, b, a, part_o, part_ml, st);
+        else launch_narrow<DT, D, 4>(s, c, b, a, part_o, part_ml, st);
     } else {
-        if (s.nt == 1) launch_shape<DT, D, 1, 1>(s, c, b, a, part_o, part_ml, st);
-        else if (s.wc == 1) launch_shape<DT, D, 2, 1>(s, c, b, a, part_o, part_ml, st);
-        else if (s.wc == 2) launch_shape<DT, D, 2, 2>(s, c, b, a, part_o, part_ml, st);
-        else launch_shape<DT, D, 2, 4>(s, c, b, a, part_o, part_ml, st);
+        if (!s.wide) launch_narrow<DT, D, 1>(s, c, b, a, part_o, part_ml, st);
+        else if (s.wc == 1) launch_wide<DT, D, 1>(s, c, b, a, part_o, part_ml, st);
+        else if (s.wc == 2) launch_wide<DT, D, 2>(s, c, b, a, part_o, part_ml, st);
+        else launch_wide<DT, D, 4>(s, c, b, a, part_o, part_ml, st);
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || s.plan.items == 0) return e;
