@@ -871,8 +871,8 @@ __global__ __launch_bounds__(512) void attn_join_kernel(Kv4Cache c, KvBatch b, K
     }
 }
 
-// The bounds of a plan (see above) for tiles of tm rows of `per` (row, head) pairs a row.
-Plan make_plan(const KvBatch &b, int heads, int G, int tm, int target, int min_chunk) {
+// The bounds of a plan (see above) for tiles of tm pairs; tables of at most `whole` steps are not cut.
+Plan make_plan(const KvBatch &b, int heads, int G, int tm, int target, int min_chunk, int whole) {
     const int64_t steps = ((static_cast<int64_t>(b.max_pages) << b.page_shift) + 31) >> 5;
     const int64_t rows = static_cast<int64_t>(b.max_q) * G <= tm ? b.B : static_cast<int64_t>(b.rows) * G / tm + b.B;
     // Each tile may add a part to the even share: where tiles are few, the parts still fit one
@@ -880,7 +880,7 @@ Plan make_plan(const KvBatch &b, int heads, int G, int tm, int target, int min_c
     const int64_t tiles = rows * heads;
     target = 2 * tiles <= target ? target - static_cast<int>(tiles) : 2 * target;
     Plan p{tm, target, min_chunk, 0, 0, 0, 0};
-    p.split = b.B <= kMostScanned && steps > min_chunk;
+    p.split = b.B <= kMostScanned && steps > whole;
     const int64_t even = (target + heads - 1) / heads, cuts = (steps + min_chunk - 1) / min_chunk;
     const int64_t extra = p.split ? (even < rows * cuts ? even : rows * cuts) : 0;
     p.pieces = static_cast<int>(rows + extra);
@@ -909,7 +909,9 @@ Shape attn_shape(const KvBatch &b, const Kv4Cache &c, int q_heads) {
     const int tm = tc * s.wc;
     // workgroups that the chip's 256 CUs hold at once
     const int held = s.wide || c.D == 256 ? 2 : c.D == 128 ? 3 : 5;
-    s.plan = make_plan(b, c.heads, G, tm, 256 * held, s.wc == 1 ? 4 : 8);
+    // Contexts of at most eight steps a wave are not cut: a second launch costs more (997
+    // tokens, 40 query heads: 9.5 us in one launch, 10.3 us in two)
+    s.plan = make_plan(b, c.heads, G, tm, 256 * held, s.wc == 1 ? 4 : 8, 8 * (4 / s.wc));
     s.cols = static_cast<int>(pairs < tm ? pairs : tm);
     s.sums = static_cast<int64_t>(c.heads) * s.plan.slots * s.cols * c.D * 4;
     s.stats = static_cast<int64_t>(c.heads) * s.plan.slots * s.cols * 8;
