@@ -8,6 +8,7 @@
 namespace rad {
 namespace {
 
+constexpr int kWaves = 4;                            // of a workgroup
 constexpr float kLog2e = 1.44269504088896340736f;
 
 // Tokens [lo, hi) that a row at position pos of a sequence of len tokens sees.
@@ -32,8 +33,8 @@ __device__ __forceinline__ TokenRange seen(int pos, int len, int causal, int win
 // Row r of score tile u is token 8 (r / 4) + 4 u + r % 4 of the step, so lane (g, c)
 // (g = lane / 16, c = lane % 16) comes out of S^T with the scores of tokens 8 g ..
 // 8 g + 7 of column c: the B operand that O^T needs against the value octets.
-// Codes go from memory to registers to the products; a workgroup's four waves take
-// WC groups of columns and 4 / WC groups of steps (joined through LDS at the end).
+// Codes go from memory to registers to the products; a workgroup's four waves take every
+// fourth step of its tile of columns each and are joined through LDS at the end.
 //
 // e2m1 levels are exact in f16; the f16 scales meet the scores (keys) and the
 // probabilities (values) in f32.  A query row is taken times a power of two that puts
@@ -272,17 +273,16 @@ __device__ __forceinline__ float times_half(float f, const u4 &x, int i) {
     return fmaf(f, static_cast<float>(h[i & 1]), 0.0f);
 }
 
-// A wave's share of a piece: its columns and its steps.
+// A wave's share of a piece.
 struct Share {
     int first_row, len, pos0, pairs;      // the sequence: first row, tokens, first row's position, (row, head) pairs
-    int tile0, wave0;                     // first pair of the tile and of this wave
-    int begin, end;                       // steps: begin, begin + TG, .. below end
-    int open_lo, open_hi;                 // steps [open_lo, open_hi) that all the wave's rows see whole
-    TokenRange wave_r;                    // what the wave's rows see together
+    int tile0;                            // first pair of the tile
+    int begin, end;                       // steps: begin, begin + kWaves, .. below end
+    int open_lo, open_hi;                 // steps [open_lo, open_hi) that all the tile's rows see whole
+    TokenRange tile_r;                    // what the tile's rows see together
 };
-template <int TC, int TM, int TG>
-__device__ __forceinline__ Share wave_share(const KvBatch &b, const Kv4Attn &a, const Piece &pc, int seq, int G, int wc,
-                                            int tg) {
+template <int TM>
+__device__ __forceinline__ Share wave_share(const KvBatch &b, const Kv4Attn &a, const Piece &pc, int seq, int G, int tg) {
     const SeqWork sw = seq_work(b, a, seq);
     Share s;
     s.first_row = sw.rr.first;
@@ -290,25 +290,17 @@ __device__ __forceinline__ Share wave_share(const KvBatch &b, const Kv4Attn &a, 
     s.pos0 = sw.pos0;
     s.pairs = sw.n * G;
     s.tile0 = pc.tile * TM;
-    s.wave0 = s.tile0 + wc * TC;
-    const int tile_last = min(s.tile0 + TM, s.pairs) - 1;
-    const bool idle = s.wave0 >= s.pairs;                     // a wave without columns has no steps
-    const int first = idle ? s.tile0 : s.wave0, last = idle ? tile_last : min(s.wave0 + TC, s.pairs) - 1;
-    // rows see ever later tokens: the first pair's beginning and the last pair's end
-    auto one = [&](int pair) { return seen(s.pos0 + pair / G, s.len, a.causal, a.window); };
-    auto range = [&](int p, int q) {
-        TokenRange r{seen(max(s.pos0 + p / G, 0), s.len, a.causal, a.window).lo, one(q).hi};
-        if (r.hi < r.lo) r.hi = r.lo;
-        return r;
-    };
-    const TokenRange tile_r = range(s.tile0, tile_last);
-    s.wave_r = range(first, last);
-    const int steps = steps_of(tile_r.lo, tile_r.hi), each = (steps + pc.parts - 1) / pc.parts;
-    const int from = (tile_r.lo >> 5) + pc.part * each, to = (tile_r.lo >> 5) + min((pc.part + 1) * each, steps);
-    s.begin = __builtin_amdgcn_readfirstlane(max(from, s.wave_r.lo >> 5) + tg);
-    s.end = __builtin_amdgcn_readfirstlane(idle ? 0 : min(to, (s.wave_r.hi + 31) >> 5));
-    s.open_lo = __builtin_amdgcn_readfirstlane((seen(max(s.pos0 + last / G, 0), s.len, a.causal, a.window).lo + 31) >> 5);
-    s.open_hi = __builtin_amdgcn_readfirstlane(range(first, first).hi >> 5);
+    const int first = s.tile0 / G, last = (min(s.tile0 + TM, s.pairs) - 1) / G;
+    // rows see ever later tokens: the first row's beginning and the last row's end
+    s.tile_r = TokenRange{seen(max(s.pos0 + first, 0), s.len, a.causal, a.window).lo,
+                          seen(s.pos0 + last, s.len, a.causal, a.window).hi};
+    if (s.tile_r.hi < s.tile_r.lo) s.tile_r.hi = s.tile_r.lo;
+    const int step0 = s.tile_r.lo >> 5, steps = steps_of(s.tile_r.lo, s.tile_r.hi);
+    const int each = (steps + pc.parts - 1) / pc.parts;
+    s.begin = __builtin_amdgcn_readfirstlane(step0 + pc.part * each + tg);
+    s.end = __builtin_amdgcn_readfirstlane(step0 + min((pc.part + 1) * each, steps));
+    s.open_lo = __builtin_amdgcn_readfirstlane((seen(max(s.pos0 + last, 0), s.len, a.causal, a.window).lo + 31) >> 5);
+    s.open_hi = __builtin_amdgcn_readfirstlane(seen(s.pos0 + first, s.len, a.causal, a.window).hi >> 5);
     return s;
 }
 
@@ -356,7 +348,7 @@ struct Output {
 // The step groups' sums of n columns become one (each group's taken to the common maximum).
 template <int TG, int TM, int D, class Out>
 __device__ __forceinline__ void join_groups(const Out &out, float (&lds_o)[TG][TM][D + 4], float (&lds_ml)[TG][TM][2], int n) {
-    for (int e = threadIdx.x; e < n * (D / 4); e += 256) {
+    for (int e = threadIdx.x; e < n * (D / 4); e += 64 * kWaves) {
         const int cc = e / (D / 4), d = 4 * (e % (D / 4));
         f4 o{0.f, 0.f, 0.f, 0.f};
         float m = kLowest, l = 0.0f;
@@ -371,28 +363,28 @@ __device__ __forceinline__ void join_groups(const Out &out, float (&lds_o)[TG][T
     }
 }
 
-// blockIdx: x piece, y KV head.  A tile has TM = 16 * WC columns, `cols` of them in use at
-// most.  Parts of a tile in several leave their sums in part_o [heads][slots][cols][D] and
-// part_ml [..][cols][2]; the others write the outputs.
-template <int DT, int D, int HL, int WC>
+// blockIdx: x piece, y KV head.  A tile has 16 columns, `cols` of them in use at most.  Parts of a tile in several leave their sums in part_o [heads][slots][cols][D] and
+// part_ml [..][cols][2]; the others write the outputs.  ONCE: no other workgroup reads the
+// codes, so they are loaded nontemporally (200K tokens 50 -> 46 us; with several tiles of heads
+// of 256 4096 tokens take 246 us that way, 219 us without).
+template <int DT, int D, int HL, bool ONCE>
 __global__ __launch_bounds__(256, 2) void attn_kernel(Kv4Cache c, KvBatch b, Kv4Attn a, Plan pl, int cols,
                                                       float *part_o, float *part_ml) {
-    constexpr int TG = 4 / WC, TC = 16, TM = TC * WC, NK = D / 32;
-    static_assert(HL != 1 || WC == 1, "low parts ride along in one product of columns");
-    __shared__ float lds_o[TG > 1 ? TG : 1][TG > 1 ? TM : 1][D + 4], lds_ml[TG > 1 ? TG : 1][TM][2];
-    const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int g = lane >> 4, col = lane & 15, tg = wid / WC, wc = wid % WC;
+    constexpr int TG = kWaves, TM = 16, NK = D / 32;
+    __shared__ float lds_o[TG][TM][D + 4], lds_ml[TG][TM][2];
+    const int lane = threadIdx.x & 63, tg = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int g = lane >> 4, col = lane & 15;
     const int h = blockIdx.y, G = a.q_heads / c.heads;
     const Piece pc = find_piece<false>(b, a, pl, c.heads, G, blockIdx.x);
     if (pc.parts == 0) return;
     const int seq = __builtin_amdgcn_readfirstlane(pc.seq);
-    const Share sh = wave_share<TC, TM, TG>(b, a, pc, seq, G, wc, tg);
+    const Share sh = wave_share<TM>(b, a, pc, seq, G, tg);
 
     // this lane's column: pair cp is row cp / G of the sequence, head h * G + cp % G
-    const int cp = sh.wave0 + (HL == 1 ? col & 7 : col);
+    const int cp = sh.tile0 + (HL == 1 ? col & 7 : col);
     const bool used = cp < sh.pairs;
     const int ci = used ? cp / G : 0, cg = used ? cp % G : 0;
-    const TokenRange tr = used ? seen(sh.pos0 + ci, sh.len, a.causal, a.window) : sh.wave_r;
+    const TokenRange tr = used ? seen(sh.pos0 + ci, sh.len, a.causal, a.window) : sh.tile_r;
     const int64_t qrow = (static_cast<int64_t>(sh.first_row + ci) * a.q_heads + h * G + cg) * D;
     // the query's values are asked for first, then the first steps
     float qv[NK][8];
@@ -410,7 +402,6 @@ __global__ __launch_bounds__(256, 2) void attn_kernel(Kv4Cache c, KvBatch b, Kv4
     // a wait for the later ones too.
     const Pages pages(c, b, seq, h, sh.end);
     constexpr int NB = D == 256 ? 2 : 3;
-    constexpr bool ONCE = WC == 1;                            // no other wave reads these codes
     Step<D> ring[NB];
     int page[NB];
 #pragma unroll
@@ -542,34 +533,25 @@ __global__ __launch_bounds__(256, 2) void attn_kernel(Kv4Cache c, KvBatch b, Kv4
     auto dims4 = [&](int j, int i) { return f4{acc[4 * j][i], acc[4 * j + 1][i], acc[4 * j + 2][i], acc[4 * j + 3][i]}; };
     const Output<DT, D> out{a, pl, pc, part_o, part_ml, sh.first_row, sh.tile0, cols, h, G};
     l = col_sum(l);
-    if constexpr (TG == 1) {
-        if (!used) return;
-#pragma unroll
-        for (int j = 0; j < D / 64; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) out.put(wc * TC + col, 64 * j + 16 * g + 4 * i, dims4(j, i), m, l);
-    } else {
-        const int lc = wc * TC + col;
-        if (g == 0) {
-            lds_ml[tg][lc][0] = m;
-            lds_ml[tg][lc][1] = l;
-        }
-        __syncthreads();
-        float top = kLowest;
-#pragma unroll
-        for (int k = 0; k < TG; ++k) top = fmaxf(top, lds_ml[k][lc][0]);
-        const float mine = __builtin_amdgcn_exp2f(m - top);
-#pragma unroll
-        for (int j = 0; j < D / 64; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                f4 o = dims4(j, i);
-                if constexpr (HL == 1) o = f4{o.x + lane_xor<8>(o.x), o.y + lane_xor<8>(o.y), o.z + lane_xor<8>(o.z), o.w + lane_xor<8>(o.w)};
-                *reinterpret_cast<f4 *>(&lds_o[tg][lc][64 * j + 16 * g + 4 * i]) = o * mine;
-            }
-        __syncthreads();
-        join_groups<TG, TM, D>(out, lds_o, lds_ml, min(TM, sh.pairs - sh.tile0));
+    if (g == 0) {
+        lds_ml[tg][col][0] = m;
+        lds_ml[tg][col][1] = l;
     }
+    __syncthreads();
+    float top = kLowest;
+#pragma unroll
+    for (int k = 0; k < TG; ++k) top = fmaxf(top, lds_ml[k][col][0]);
+    const float mine = __builtin_amdgcn_exp2f(m - top);
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f4 o = dims4(j, i);
+            if constexpr (HL == 1) o = f4{o.x + lane_xor<8>(o.x), o.y + lane_xor<8>(o.y), o.z + lane_xor<8>(o.z), o.w + lane_xor<8>(o.w)};
+            *reinterpret_cast<f4 *>(&lds_o[tg][col][64 * j + 16 * g + 4 * i]) = o * mine;
+        }
+    __syncthreads();
+    join_groups<TG, TM, D>(out, lds_o, lds_ml, min(TM, sh.pairs - sh.tile0));
 }
 
 // ---- 32 columns a wave -------------------------------------------------------
@@ -634,25 +616,25 @@ __device__ __forceinline__ f4 wide_dims(const f16v (&acc)[D / 32], int r) {
     else return f4{acc[0][r], acc[1][r], acc[2][r], acc[3][r]};
 }
 
-// As attn_kernel, with TM = 32 * WC columns a tile.  SP: f32 queries and weights in two parts.
-template <int DT, int D, bool SP, int WC>
+// As attn_kernel, with 32 columns a tile.  SP: f32 queries and weights in two parts.
+template <int DT, int D, bool SP>
 __global__ __launch_bounds__(256, 2) void attn_wide_kernel(Kv4Cache c, KvBatch b, Kv4Attn a, Plan pl, int cols,
                                                            float *part_o, float *part_ml) {
-    constexpr int TG = 4 / WC, TC = 32, TM = TC * WC, NK = D / 16, ND = D / 32;
-    __shared__ float lds_o[TG > 1 ? TG : 1][TG > 1 ? TM : 1][D + 4], lds_ml[TG > 1 ? TG : 1][TM][2];
-    const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int g = lane >> 5, col = lane & 31, tg = wid / WC, wc = wid % WC;
+    constexpr int TG = kWaves, TM = 32, NK = D / 16, ND = D / 32;
+    __shared__ float lds_o[TG][TM][D + 4], lds_ml[TG][TM][2];
+    const int lane = threadIdx.x & 63, tg = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int g = lane >> 5, col = lane & 31;
     const int h = blockIdx.y, G = a.q_heads / c.heads;
     const Piece pc = find_piece<false>(b, a, pl, c.heads, G, blockIdx.x);
     if (pc.parts == 0) return;
     const int seq = __builtin_amdgcn_readfirstlane(pc.seq);
-    const Share sh = wave_share<TC, TM, TG>(b, a, pc, seq, G, wc, tg);
+    const Share sh = wave_share<TM>(b, a, pc, seq, G, tg);
 
     // this lane's column: pair cp is row cp / G of the sequence, head h * G + cp % G
-    const int cp = sh.wave0 + col;
+    const int cp = sh.tile0 + col;
     const bool used = cp < sh.pairs;
     const int ci = used ? cp / G : 0, cg = used ? cp % G : 0;
-    const TokenRange tr = used ? seen(sh.pos0 + ci, sh.len, a.causal, a.window) : sh.wave_r;
+    const TokenRange tr = used ? seen(sh.pos0 + ci, sh.len, a.causal, a.window) : sh.tile_r;
     const int64_t qrow = (static_cast<int64_t>(sh.first_row + ci) * a.q_heads + h * G + cg) * D;
     float qv[NK][8];
 #pragma unroll
@@ -700,6 +682,7 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(Kv4Cache c, KvBatch b
         for (int i = 0; i < 16; ++i) acc[x][i] = 0.0f;
 
     auto work = [&](WideStep<D> &cur, int step) {
+        __builtin_amdgcn_s_setprio(1);
         f16v st;
 #pragma unroll
         for (int i = 0; i < 16; ++i) st[i] = 0.0f;
@@ -709,6 +692,7 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(Kv4Cache c, KvBatch b
             if constexpr (SP) st = mma32(kf, ql[j], st);
             st = mma32(kf, qf[j], st);
         }
+        __builtin_amdgcn_s_setprio(0);
         float s[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[i] = times_half(st[i], cur.ks[i >> 3], i & 7);
@@ -752,6 +736,7 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(Kv4Cache c, KvBatch b
             }
         }
         l += sum;
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             float we[8];
@@ -785,34 +770,22 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(Kv4Cache c, KvBatch b
     // lane (g, c): tile x's row 8 q + 4 g + i is dim D / 32 * row + x; four dims in a row from (q, i)
     l += __shfl_xor(l, 32);
     const Output<DT, D> out{a, pl, pc, part_o, part_ml, sh.first_row, sh.tile0, cols, h, G};
-    if constexpr (TG == 1) {
-        if (!used) return;
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int i = 0; i < 4; i += 128 / D) {
-                const f4 o = wide_dims<D>(acc, 4 * q + i);
-                out.put(wc * TC + col, D / 32 * (8 * q + 4 * g + i), o, m, l);
-            }
-    } else {
-        const int lc = wc * TC + col;
-        if (g == 0) {
-            lds_ml[tg][lc][0] = m;
-            lds_ml[tg][lc][1] = l;
-        }
-        __syncthreads();
-        float top = kLowest;
-#pragma unroll
-        for (int k = 0; k < TG; ++k) top = fmaxf(top, lds_ml[k][lc][0]);
-        const float mine = __builtin_amdgcn_exp2f(m - top);
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int i = 0; i < 4; i += 128 / D)
-                *reinterpret_cast<f4 *>(&lds_o[tg][lc][D / 32 * (8 * q + 4 * g + i)]) = wide_dims<D>(acc, 4 * q + i) * mine;
-        __syncthreads();
-        join_groups<TG, TM, D>(out, lds_o, lds_ml, min(TM, sh.pairs - sh.tile0));
+    if (g == 0) {
+        lds_ml[tg][col][0] = m;
+        lds_ml[tg][col][1] = l;
     }
+    __syncthreads();
+    float top = kLowest;
+#pragma unroll
+    for (int k = 0; k < TG; ++k) top = fmaxf(top, lds_ml[k][col][0]);
+    const float mine = __builtin_amdgcn_exp2f(m - top);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; i += 128 / D)
+            *reinterpret_cast<f4 *>(&lds_o[tg][col][D / 32 * (8 * q + 4 * g + i)]) = wide_dims<D>(acc, 4 * q + i) * mine;
+    __syncthreads();
+    join_groups<TG, TM, D>(out, lds_o, lds_ml, min(TM, sh.pairs - sh.tile0));
 }
 
 // The parts' sums of a tile and KV head become its outputs, `wide` columns (of `cols`) a
@@ -889,12 +862,10 @@ Plan make_plan(const KvBatch &b, int heads, int G, int tm, int target, int min_c
     return p;
 }
 
-// The kernel's shape for a call: by the pairs of one sequence and KV head, the most columns
-// a workgroup is offered, so that no wave multiplies mostly padding and short prompts keep
-// their waves busy on the context.  Heads of 256 fill the registers with 16 columns a wave.
+// The kernel's shape for a call: by the pairs of one sequence and KV head, so that no wave
+// multiplies mostly padding.  Heads of 256 fill the registers with 16 columns a wave.
 struct Shape {
-    bool wide;              // 32 columns a wave
-    int wc;                 // groups of columns
+    bool once;              // a sequence and KV head is one tile
     Plan plan;
     int cols;               // columns kept for a part
     int64_t sums, stats;    // bytes of the parts' sums and of their statistics
@@ -903,57 +874,32 @@ Shape attn_shape(const KvBatch &b, const Kv4Cache &c, int q_heads) {
     Shape s;
     const int G = q_heads / c.heads;
     const int64_t pairs = static_cast<int64_t>(b.max_q) * G;
-    s.wide = c.D != 256 && pairs > 16;
-    const int tc = s.wide ? 32 : 16;
-    s.wc = pairs <= tc ? 1 : pairs <= 2 * tc ? 2 : 4;
-    const int tm = tc * s.wc;
+    s.once = pairs <= 16;
+    const int tm = s.once || c.D == 256 ? 16 : 32;
     // workgroups that the chip's 256 CUs hold at once
-    const int held = s.wide || c.D == 256 ? 2 : c.D == 128 ? 3 : 5;
+    const int held = !s.once || c.D == 256 ? 2 : c.D == 128 ? 3 : 5;
     // Contexts of at most eight steps a wave are not cut: a second launch costs more (997
     // tokens, 40 query heads: 9.5 us in one launch, 10.3 us in two)
-    s.plan = make_plan(b, c.heads, G, tm, 256 * held, s.wc == 1 ? 4 : 8, 8 * (4 / s.wc));
+    s.plan = make_plan(b, c.heads, G, tm, 256 * held, kWaves, 8 * kWaves);
     s.cols = static_cast<int>(pairs < tm ? pairs : tm);
     s.sums = static_cast<int64_t>(c.heads) * s.plan.slots * s.cols * c.D * 4;
     s.stats = static_cast<int64_t>(c.heads) * s.plan.slots * s.cols * 8;
     return s;
 }
 
-template <int DT, int D, int WC>
-void launch_narrow(const Shape &s, const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, float *part_o, float *part_ml,
-                   hipStream_t st) {
-    const dim3 grid(s.plan.pieces, c.heads), block(256);
-    if constexpr (DT != kDtF32) {
-        hipLaunchKernelGGL((attn_kernel<DT, D, 0, WC>), grid, block, 0, st, c, b, a, s.plan, s.cols, part_o, part_ml);
-    } else {
-        if constexpr (WC == 1) {
-            if (s.cols <= 8) {
-                hipLaunchKernelGGL((attn_kernel<DT, D, 1, WC>), grid, block, 0, st, c, b, a, s.plan, s.cols, part_o, part_ml);
-                return;
-            }
-        }
-        hipLaunchKernelGGL((attn_kernel<DT, D, 2, WC>), grid, block, 0, st, c, b, a, s.plan, s.cols, part_o, part_ml);
-    }
-}
-template <int DT, int D, int WC>
-void launch_wide(const Shape &s, const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, float *part_o, float *part_ml,
-                 hipStream_t st) {
-    hipLaunchKernelGGL((attn_wide_kernel<DT, D, DT == kDtF32, WC>), dim3(s.plan.pieces, c.heads), dim3(256), 0, st, c, b, a,
-                       s.plan, s.cols, part_o, part_ml);
-}
-
 template <int DT, int D>
 hipError_t launch_d(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, hipStream_t st) {
     const Shape s = attn_shape(b, c, a.q_heads);
     float *part_o = static_cast<float *>(a.workspace), *part_ml = part_o + s.sums / 4;
-    if constexpr (D == 256) {
-        if (s.wc == 1) launch_narrow<DT, D, 1>(s, c, b, a, part_o, part_ml, st);
-        else if (s.wc == 2) launch_narrow<DT, D, 2>(s, c, b, a, part_o, part_ml, st);
-        else launch_narrow<DT, D, 4>(s, c, b, a, part_o, part_ml, st);
+    const dim3 grid(s.plan.pieces, c.heads), block(64 * kWaves);
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, st, c, b, a, s.plan, s.cols, part_o, part_ml); };
+    constexpr int HL = DT == kDtF32 ? 2 : 0;
+    if (s.once) {
+        if (DT == kDtF32 && s.cols <= 8) go(attn_kernel<DT, D, DT == kDtF32 ? 1 : 0, true>);
+        else go(attn_kernel<DT, D, HL, true>);
     } else {
-        if (!s.wide) launch_narrow<DT, D, 1>(s, c, b, a, part_o, part_ml, st);
-        else if (s.wc == 1) launch_wide<DT, D, 1>(s, c, b, a, part_o, part_ml, st);
-        else if (s.wc == 2) launch_wide<DT, D, 2>(s, c, b, a, part_o, part_ml, st);
-        else launch_wide<DT, D, 4>(s, c, b, a, part_o, part_ml, st);
+        if constexpr (D == 256) go(attn_kernel<DT, D, HL, false>);
+        else go(attn_wide_kernel<DT, D, DT == kDtF32>);
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || s.plan.items == 0) return e;
