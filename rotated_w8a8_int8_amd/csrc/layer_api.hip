@@ -130,8 +130,8 @@ int rad_kv4_append(const rad_kv4_cache *cache, const rad_kv_batch *batch, const 
         if (rope->dim < 8 || rope->dim > D || rope->dim % 8 != 0 || rope->rows < 0) return RAD_E_SHAPE;
         if ((rope->style != 0 && rope->style != 1) || rope->rows > kI32Max) return RAD_E_RANGE;
     }
-    if ((q_heads > 0) != (q != nullptr) || (q != nullptr) != (q_out != nullptr)) return RAD_E_NULL;
     if (empty) return RAD_OK;
+    if ((q_heads > 0) != (q != nullptr) || (q != nullptr) != (q_out != nullptr)) return RAD_E_NULL;
     rc = check_pointers(cache, batch);
     if (rc != RAD_OK) return rc;
     if (!k || !v || (rope && !rope->table)) return RAD_E_NULL;

@@ -99,6 +99,13 @@ def test_empty_batches_enqueue_nothing(call, kw):
     assert call(b=dict(kw, table=None, n=None)) == B.RAD_OK
 
 
+def test_an_empty_append_needs_no_arrays():
+    # empty tensors have no address
+    for kw in (dict(rows=0), dict(seqs=0)):
+        assert append(b=kw, k=None, v=None, q=None, qo=None) == B.RAD_OK
+        assert append(b=kw, q=None) == B.RAD_OK
+
+
 @pytest.mark.parametrize("call", ["append", "read", "attn", "workspace"])
 def test_missing_descriptors(call):
     L, n = B.lib(), ctypes.c_int64(0)
