@@ -307,7 +307,7 @@ enum rad_dtype { RAD_DT_F32 = 0, RAD_DT_BF16 = 1, RAD_DT_F16 = 2 };
  *   q, scale      int8 [M][K] (16-byte aligned) and f32 [M] outputs, what the
  *                 contraction calls take.
  *   rotate        1: rotated as by rad_fwht128; 0: not.
- *   M >= 0; K > 0, K % 128 == 0, K <= RAD_QUANT_MAX_K.
+ *   0 <= M < 2^24; K > 0, K % 128 == 0, K <= RAD_QUANT_MAX_K.
  *
  * Per token: h = residual + x (f32 sum rounded to `dtype`, stored to
  * residual_out and used as stored; h = x without a residual);
@@ -423,8 +423,8 @@ int rad_kv4_append(const rad_kv4_cache *cache, const rad_kv_batch *batch, const 
 /*
  * rad_kv4_read -- the cached keys and values of the batch's rows as bf16
  * (level * scale, exact in f32, rounded to nearest even): k_out and v_out bf16
- * bits [rows][heads][D], 16-byte aligned.  Rows that are no token, and tokens
- * on absent pages, are left as they were.
+ * bits [rows][heads][D], 16-byte aligned, rows * heads * D < 2^35.  Rows that
+ * are no token, and tokens on absent pages, are left as they were.
  */
 int rad_kv4_read(const rad_kv4_cache *cache, const rad_kv_batch *batch, uint16_t *k_out, uint16_t *v_out,
                  rad_stream_t stream);

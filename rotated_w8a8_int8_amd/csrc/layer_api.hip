@@ -14,6 +14,8 @@ int dtype_bytes(int32_t dtype) {
 }
 
 constexpr int64_t kMaxRows = int64_t(1) << 22, kMaxTokens = int64_t(1) << 30;
+// a launch holds fewer than 2^32 threads: 256 a token, and one for every eight values read back
+constexpr int64_t kMaxNormRows = int64_t(1) << 24, kMaxRead = int64_t(1) << 35;
 
 // Shape and range of a cache descriptor (no pointers).
 int check_cache(const rad_kv4_cache *c) {
@@ -90,7 +92,7 @@ int rad_add_rmsnorm_quant_i8(const void *x, const void *residual, void *residual
     const int e = dtype_bytes(dtype);
     if (e == 0) return RAD_E_FMT;
     if (M < 0 || K <= 0 || K % 128 != 0) return RAD_E_SHAPE;
-    if (K > RAD_QUANT_MAX_K || M > kI32Max || (rotate != 0 && rotate != 1)) return RAD_E_RANGE;
+    if (K > RAD_QUANT_MAX_K || M >= kMaxNormRows || (rotate != 0 && rotate != 1)) return RAD_E_RANGE;
     if (!(eps >= 0.0f) || eps > 3.0e38f) return RAD_E_RANGE;
     if ((residual == nullptr) != (residual_out == nullptr)) return RAD_E_NULL;
     if (M == 0) return RAD_OK;
@@ -164,7 +166,9 @@ int rad_kv4_read(const rad_kv4_cache *cache, const rad_kv_batch *batch, uint16_t
     int rc = check_cache(cache);
     if (rc != RAD_OK) return rc;
     const int empty = check_batch(cache, batch);
-    if (empty != RAD_OK) return empty < 0 ? empty : RAD_OK;
+    if (empty < 0) return empty;
+    if (batch->rows * cache->heads * cache->D >= kMaxRead) return RAD_E_RANGE;
+    if (empty) return RAD_OK;
     rc = check_pointers(cache, batch);
     if (rc != RAD_OK) return rc;
     if (!k_out || !v_out) return RAD_E_NULL;

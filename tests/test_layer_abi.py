@@ -41,6 +41,14 @@ def test_norm_refusals(kw, rc):
     assert norm(**kw) == rc
 
 
+def test_more_than_a_launch_holds():
+    assert norm(M=(1 << 24) - 1, r=None, ro=None, x=None) == B.RAD_E_NULL          # the size itself is taken
+    assert norm(M=1 << 24, r=None, ro=None) == B.RAD_E_RANGE
+    big = dict(heads=1024, D=256)
+    assert read(c=big, b=dict(rows=1 << 17)) == B.RAD_E_RANGE
+    assert read(c=big, b=dict(rows=(1 << 17) - 1), k=None) == B.RAD_E_NULL
+
+
 def cache(k=P[0], ks=P[1], v=P[2], vs=P[3], pages=10, heads=2, page=64, D=128):
     return B.KV4CacheDesc(k, ks, v, vs, pages, heads, page, D)
 
