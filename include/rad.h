@@ -436,7 +436,7 @@ int rad_kv4_read(const rad_kv4_cache *cache, const rad_kv_batch *batch, uint16_t
  *
  *   q, o      [rows][q_heads][D] of `dtype`, dense, 16-byte aligned; q_heads a multiple
  *             of the cache's heads, at most 16384; rows * q_heads < 2^29.
- *   sm_scale  finite, > 0.
+ *   sm_scale  0 < sm_scale <= 2^126.
  *   causal    1: the row at position p sees tokens t <= p; 0: every token of its sequence.
  *   window    > 0: only tokens t > p - window; 0: no window.
  *   workspace device memory, 16-byte aligned, of at least the bytes that

@@ -95,6 +95,11 @@ __device__ __forceinline__ void f16_split8(const float (&w)[8], u4 &hi, u4 &low)
 __device__ __forceinline__ float max8(const float (&s)[8]) {
     return fmaxf(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])), fmaxf(fmaxf(s[4], s[5]), fmaxf(s[6], s[7])));
 }
+// sm_scale log2(e) 2^-e, never 0 or infinite: a masked score stays -inf, a score of 0 stays 0.
+__device__ __forceinline__ float score_factor(float sm_scale, int e) {
+    return fminf(fmaxf(__builtin_amdgcn_ldexpf(sm_scale * kLog2e, -e), 1e-30f), 0x1p126f);
+}
+
 // Maximum (sum) over the four lanes that hold one column.
 __device__ __forceinline__ float col_max(float v) {
     v = fmaxf(v, __shfl_xor(v, 16));
@@ -433,7 +438,7 @@ __global__ __launch_bounds__(256, 2) void attn_kernel(Kv4Cache c, KvBatch b, Kv4
                 qf[j] = HL == 1 && col >= 8 ? low : hi;
             }
         }
-        scale = fmaxf(__builtin_amdgcn_ldexpf(a.sm_scale * kLog2e, -e), 1e-30f);   // never 0: a masked score is -inf
+        scale = score_factor(a.sm_scale, e);
     }
 
     float m = kLowest, l = 0.0f;
@@ -671,7 +676,7 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(Kv4Cache c, KvBatch b
             if constexpr (SP) f16_split8(qv[j], qf[j], ql[j]);
             else qf[j] = f16_pack8(qv[j]);
         }
-        scale = fmaxf(__builtin_amdgcn_ldexpf(a.sm_scale * kLog2e, -e), 1e-30f);   // never 0: a masked score is -inf
+        scale = score_factor(a.sm_scale, e);
     }
 
     float m = kLowest, l = 0.0f;

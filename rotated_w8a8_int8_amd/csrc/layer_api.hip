@@ -215,7 +215,7 @@ int rad_attn_kv4(const rad_kv4_cache *cache, const rad_kv_batch *batch, const vo
     int rc = check_attn(cache, batch, q_heads, dtype);
     if (rc < 0) return rc;
     const bool empty = rc > 0;
-    if (!(sm_scale > 0.0f) || sm_scale > 3.0e38f || (causal != 0 && causal != 1)) return RAD_E_RANGE;
+    if (!(sm_scale > 0.0f) || sm_scale > 0x1p126f || (causal != 0 && causal != 1)) return RAD_E_RANGE;
     if (window < 0) return RAD_E_SHAPE;
     if (empty) return RAD_OK;
     const rad::Kv4Cache ca = cache_args(cache);

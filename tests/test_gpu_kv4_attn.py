@@ -172,6 +172,73 @@ def test_rows_past_max_q_are_left(torch):
     assert float((o[:4] - full[:4]).abs().max()) <= 1e-4
 
 
+@pytest.mark.parametrize("n", [1, 40])
+def test_extreme_factors_of_zero_scores(torch, n):
+    # zero scores stay zero under the largest factor and beside a huge query element: every token weighs the same
+    rng = np.random.default_rng(13)
+    ref = O.Cache(2, 1, 32, 64)
+    table = np.array([[0, 1]], np.int32)
+    C.fill_cache(rng, ref, table, [50])
+    ref.k_codes[..., 31] &= 0x0F                               # keys have no last dimension
+    q = np.zeros((n, 2, 64), np.float32)
+    q[:, 1, 63] = 1.0e38
+    want, mass, reach = O.attention(np.zeros_like(q), ref, table, [50], C.ragged([n]), 1.0, False, 0)
+    batch = C.device_batch(torch, table, [50], C.ragged([n]), n)
+    for sm in (2.0 ** 126, 2.0 ** 20, 1e-38):
+        got = C.host(B.attn_kv4(C.device_cache(torch, ref), batch, C.put(torch, q), sm, causal=False))
+        assert np.all(np.abs(got - want) <= C.attention_tolerance("f32", want, mass, reach, 50)), sm
+
+
+@pytest.mark.parametrize("dtype", C.DTYPES)
+@pytest.mark.parametrize("n", [1, 3, 40])
+def test_rows_that_are_not_finite_keep_to_themselves(torch, n, dtype):
+    # a row and head of NaN or infinite queries shares its products with others: theirs are as without it
+    rng = np.random.default_rng(14)
+    ref = O.Cache(6, 2, 32, 128)
+    table = np.array([[4, 0, 2, 1, 5, 3]], np.int32)
+    C.fill_cache(rng, ref, table, [170])
+    q = O.to_dtype(rng.standard_normal((n, 8, 128)), dtype)
+    batch, dev = C.device_batch(torch, table, [170], C.ragged([n]), n), C.device_cache(torch, ref)
+    clean = C.host(B.attn_kv4(dev, batch, C.put(torch, q, dtype), 0.1))
+    q[n // 2, 1, 7], q[0, 6, 100] = np.nan, np.inf
+    got = C.host(B.attn_kv4(dev, batch, C.put(torch, q, dtype), 0.1))
+    keep = np.ones((n, 8), bool)
+    keep[n // 2, 1] = keep[0, 6] = False
+    want, mass, reach = O.attention(np.where(np.isfinite(q), q, 0), ref, table, [170], C.ragged([n]), 0.1, True, 0)
+    tol = C.attention_tolerance(dtype, want, mass, reach, 170)
+    assert np.all(np.abs(got - want)[keep] <= tol[keep]) and np.all(np.abs(clean - want)[keep] <= tol[keep])
+
+
+@pytest.mark.parametrize("n", [1, 24])
+def test_pages_that_sequences_share(torch, n):
+    # a common prefix, and one page twice in a row's table
+    rng = np.random.default_rng(15)
+    ref = O.Cache(5, 2, 32, 64)
+    own = np.array([[0, 1, 2, 3, 4]], np.int32)
+    C.fill_cache(rng, ref, own, [160])
+    table = np.array([[0, 1, 2, -1], [0, 1, 3, 4], [2, 2, 2, 0]], np.int32)
+    seq_len, start = np.array([90, 128, 100]), C.ragged([n] * 3)
+    q = O.to_dtype(rng.standard_normal((3 * n, 4, 64)), "bf16")
+    got = C.host(B.attn_kv4(C.device_cache(torch, ref), C.device_batch(torch, table, seq_len, start, 3 * n),
+                            C.put(torch, q, "bf16"), 0.125))
+    want, mass, reach = O.attention(q, ref, table, seq_len, start, 0.125, True, 0)
+    assert np.all(np.abs(got - want) <= C.attention_tolerance("bf16", want, mass, reach, 128))
+
+
+def test_nothing_to_attend_to(torch):
+    dev = B.KV4Cache.empty(1, 2, 32, 64)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    none = B.KVBatch(torch.zeros(0, 4, **i32), torch.zeros(0, **i32))
+    q = torch.zeros(0, 4, 64, device="cuda")
+    assert B.attn_kv4(dev, none, q, 0.1).shape == (0, 4, 64)
+    k = torch.zeros(0, 2, 64, device="cuda")
+    assert B.kv4_append(dev, none, k, k, q, rotate=False).shape == (0, 4, 64)
+    assert B.kv4_read(dev, none)[0].shape == (0, 2, 64)
+    # a table without pages: every row sees nothing
+    bare = B.KVBatch(torch.zeros(2, 0, **i32), torch.full((2,), 9, **i32))
+    assert not B.attn_kv4(dev, bare, torch.ones(2, 4, 64, device="cuda"), 0.1).any()
+
+
 def test_the_same_call_twice_gives_the_same_bits(torch):
     rng = np.random.default_rng(12)
     ref = O.Cache(40, 2, 64, 128, rng)

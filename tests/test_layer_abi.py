@@ -161,7 +161,7 @@ def test_read_refusals(kw, rc):
     (dict(dt=3), B.RAD_E_FMT), (dict(q_heads=0), B.RAD_E_SHAPE), (dict(q_heads=5), B.RAD_E_SHAPE),
     (dict(q_heads=1 << 15), B.RAD_E_RANGE), (dict(b=dict(rows=(1 << 24) - 1), q_heads=1024), B.RAD_E_RANGE),
     (dict(scale=0.0), B.RAD_E_RANGE), (dict(scale=-1.0), B.RAD_E_RANGE), (dict(scale=float("nan")), B.RAD_E_RANGE),
-    (dict(scale=float("inf")), B.RAD_E_RANGE), (dict(causal=2), B.RAD_E_RANGE), (dict(window=-1), B.RAD_E_SHAPE),
+    (dict(scale=float("inf")), B.RAD_E_RANGE), (dict(scale=2.0 ** 126.5), B.RAD_E_RANGE), (dict(causal=2), B.RAD_E_RANGE), (dict(window=-1), B.RAD_E_SHAPE),
     (dict(q=None), B.RAD_E_NULL), (dict(o=None), B.RAD_E_NULL), (dict(q=P[7] + 8), B.RAD_E_ALIGN),
     (dict(o=P[8] + 4), B.RAD_E_ALIGN), (dict(ws=P[9] + 8), B.RAD_E_ALIGN), (dict(o=P[7] + 64), B.RAD_E_ALIAS),
     (dict(o=P[0] + 64), B.RAD_E_ALIAS), (dict(o=P[6]), B.RAD_E_ALIAS),
