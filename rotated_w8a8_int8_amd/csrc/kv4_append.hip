@@ -21,8 +21,6 @@
 namespace rad {
 namespace {
 
-constexpr int kSpan = 7;      // groups of heads a workgroup, many rows
-
 // (a cos - b sin, b cos + a sin), every operation rounded by itself.
 __device__ __forceinline__ float turn_first(float a, float b, float cs, float sn) {
 #pragma clang fp contract(off)
@@ -120,6 +118,95 @@ __device__ __forceinline__ float head_max(float a) {
     return a;
 }
 
+// One head vector v of a token (kind 0: query, 1: key, 2: value, head h of its kind), by D / 8
+// lanes: the turned query stored, or scale and keys' codes; returns the lane's eight codes.
+template <int DT, int D>
+__device__ __forceinline__ uint32_t append_head(const Kv4Cache &c, const Kv4New &nw, Runs v, const Angles &ang, int kind, int h,
+                                                int64_t base, int64_t trow, int page, int off, int lane, int d0, int d1,
+                                                float sign) {
+    const bool turned_too = D % 128 == 0 && nw.rotate;
+    if (kind < 2 && nw.rope) turn<DT>(v, ang, kind == 0 ? nw.q : nw.k, base, nw.rope_dim, nw.rope_style, d0, d1);
+    if (turned_too) {
+        Blk8 x{v.lo, v.hi};
+        fwht128_regs_signed(x, lane & 15);
+        v = Runs{x.lo, x.hi};
+    }
+    if (kind == 0) {
+        const float m = turned_too ? sign * 0x1p-7f : 1.0f;
+        const int64_t at = (trow * nw.q_heads + h) * D;
+        store4<DT>(nw.q_out, at + d0, make_float4(v.lo.x * m, v.lo.y * m, v.lo.z * m, v.lo.w * m));
+        store4<DT>(nw.q_out, at + d1, make_float4(v.hi.x * m, v.hi.y * m, v.hi.z * m, v.hi.w * m));
+        return 0;
+    }
+    float r[8] = {v.lo.x, v.lo.y, v.lo.z, v.lo.w, v.hi.x, v.hi.y, v.hi.z, v.hi.w};
+    float a = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(r[i]));
+    a = head_max<D / 8>(a);
+    const uint32_t sb = kv4_scale_bits(a / 6.0f);
+    const float s = f16_widen(sb);
+    uint32_t w = 0;
+    if (s > 0.0f) {
+        const float d = sign * s;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] = r[i] / d;
+        w = e2m1_pack8(r);
+    }
+    if (page >= 0) {
+        const int64_t tok = ((static_cast<int64_t>(page) * c.heads + h) << c.page_shift) + off;
+        if (lane == 0) (kind == 1 ? c.k_scale : c.v_scale)[tok] = static_cast<uint16_t>(sb);
+        if (kind == 1) {
+            uint16_t *q = reinterpret_cast<uint16_t *>(c.k_codes + tok * (D / 2));
+            q[d0 >> 2] = static_cast<uint16_t>(w);
+            q[d1 >> 2] = static_cast<uint16_t>(w >> 16);
+        }
+    }
+    return w;
+}
+
+// A lane's runs of a head vector: d0 .. d0 + 3 and d1 .. d1 + 3.
+template <int D>
+__device__ __forceinline__ int first_dim(int lane) { return D == 64 ? 4 * lane : (lane >> 4) * 128 + 4 * (lane & 15); }
+template <int D>
+constexpr int kRunsApart = D == 64 ? 32 : 64;
+
+// One row per sequence: blockIdx.x the row, blockIdx.y 256 / L heads of it (queries, keys,
+// values), D / 8 lanes each.  A value's lane puts its eight codes into the octet's dwords itself.
+template <int DT, int D>
+__global__ __launch_bounds__(256) void kv4_append_one_kernel(Kv4Cache c, KvBatch b, Kv4New nw) {
+    constexpr int L = D / 8;
+    const int lane = threadIdx.x % L, row = blockIdx.x, hx = blockIdx.y * (256 / L) + threadIdx.x / L;
+    const int d0 = first_dim<D>(lane), d1 = d0 + kRunsApart<D>;
+    const int H = c.heads, HQ = nw.q_heads;
+    const int kind = hx < HQ ? 0 : hx < HQ + H ? 1 : hx < HQ + 2 * H ? 2 : 3;
+    if (kind == 3) return;
+    const int h = kind == 0 ? hx : kind == 1 ? hx - HQ : hx - HQ - H;
+    const int64_t base = row * (kind == 0 ? nw.ldq : kind == 1 ? nw.ldk : nw.ldv) + static_cast<int64_t>(h) * D;
+    const void *src = kind == 0 ? nw.q : kind == 1 ? nw.k : nw.v;
+    const Runs v{load4<DT>(src, base + d0), load4<DT>(src, base + d1)};
+    const int t = kv_len(b, row) - 1;
+    if (t < 0 || (nw.rope && t >= nw.rope_rows)) return;
+    const int page = kv_page(b, row, t, c.pages), off = t & ((1 << c.page_shift) - 1), sh = 4 * (t & 7);
+    const bool merge = kind == 2 && page >= 0;
+    uint4 *oct = nullptr, lo{}, hi{};
+    if (merge) {
+        oct = reinterpret_cast<uint4 *>(c.v_codes) + ((((static_cast<int64_t>(page) * H + h) << c.page_shift) + off) >> 3) * (D / 4);
+        lo = oct[d0 >> 2];
+        hi = oct[d1 >> 2];
+    }
+    const Angles ang = nw.rope && kind < 2 ? angles<D>(nw.rope + static_cast<int64_t>(t) * nw.rope_dim, nw.rope_dim, nw.rope_style, d0, d1)
+                                           : Angles{};
+    const float sign = D % 128 == 0 && nw.rotate ? fwht_lane_sign(lane & 15) : 1.0f;
+    const uint32_t w = append_head<DT, D>(c, nw, v, ang, kind, h, base, row, page, off, lane, d0, d1, sign);
+    if (merge) {
+        auto put = [&](uint32_t &word, int i) { word = (word & ~(15u << sh)) | (((w >> (4 * i)) & 15u) << sh); };
+        put(lo.x, 0); put(lo.y, 1); put(lo.z, 2); put(lo.w, 3);
+        put(hi.x, 4); put(hi.y, 5); put(hi.z, 6); put(hi.w, 7);
+        oct[d0 >> 2] = lo;
+        oct[d1 >> 2] = hi;
+    }
+}
+
 // blockIdx.x: `chunk` consecutive rows, of which the workgroup takes the octets that begin
 // there; blockIdx.y: `span` groups of HPB heads of the q_heads + 2 * heads in the order
 // queries, keys, values.  A thread's token, and with it its angles, stays while the heads
@@ -129,13 +216,10 @@ __global__ __launch_bounds__(256) void kv4_append_kernel(Kv4Cache c, KvBatch b, 
     constexpr int L = D / 8, HPB = 32 / L;
     __shared__ uint32_t codes[HPB][8][L];                 // [head][token of the octet][lane]: 8 codes of a lane
     const int lane = threadIdx.x % L, tok = (threadIdx.x / L) % 8, hs = threadIdx.x / (8 * L);
-    const int l16 = lane & 15;
-    // a lane's two runs of four values: d0 .. d0 + 3 and d1 .. d1 + 3
-    const int d0 = D == 64 ? 4 * lane : (lane >> 4) * 128 + 4 * l16, d1 = d0 + (D == 64 ? 32 : 64);
+    const int d0 = first_dim<D>(lane), d1 = d0 + kRunsApart<D>;
     const int H = c.heads, HQ = nw.q_heads, heads = HQ + 2 * H;
     const int hb0 = blockIdx.y * span, hb1 = min(hb0 + span, (heads + HPB - 1) / HPB);
-    const bool turned_too = D % 128 == 0 && nw.rotate;
-    const float sign = turned_too ? fwht_lane_sign(l16) : 1.0f;        // what fwht128_regs_signed leaves on a lane
+    const float sign = D % 128 == 0 && nw.rotate ? fwht_lane_sign(lane & 15) : 1.0f;     // what fwht128_regs_signed leaves on a lane
 
     const int row_end = min(static_cast<int>(blockIdx.x + 1) * chunk, b.rows);
     for (int row = blockIdx.x * chunk; row < row_end;) {
@@ -181,45 +265,8 @@ __global__ __launch_bounds__(256) void kv4_append_kernel(Kv4Cache c, KvBatch b, 
                 if (hb + 1 < hb1) next = fetch(hx + HPB);
                 const int kind = hx < HQ ? 0 : hx < HQ + H ? 1 : hx < heads ? 2 : 3;       // query, key, value, none
                 const int h = kind == 0 ? hx : kind == 1 ? hx - HQ : hx - HQ - H;
-                const bool live = here && kind < 3;
                 uint32_t w = 0;
-                if (live) {                                  // a head vector's lanes are live together
-                    if (kind < 2 && nw.rope) turn<DT>(v, ang, source(hx), base_of(hx), nw.rope_dim, nw.rope_style, d0, d1);
-                    if (turned_too) {
-                        Blk8 x{v.lo, v.hi};
-                        fwht128_regs_signed(x, l16);
-                        v = Runs{x.lo, x.hi};
-                    }
-                    if (kind == 0) {
-                        const float m = turned_too ? sign * 0x1p-7f : 1.0f;
-                        const int64_t at = (trow * HQ + h) * D;
-                        store4<DT>(nw.q_out, at + d0, make_float4(v.lo.x * m, v.lo.y * m, v.lo.z * m, v.lo.w * m));
-                        store4<DT>(nw.q_out, at + d1, make_float4(v.hi.x * m, v.hi.y * m, v.hi.z * m, v.hi.w * m));
-                    } else {
-                        float r[8] = {v.lo.x, v.lo.y, v.lo.z, v.lo.w, v.hi.x, v.hi.y, v.hi.z, v.hi.w};
-                        float a = 0.0f;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(r[i]));
-                        a = head_max<L>(a);
-                        const uint32_t sb = kv4_scale_bits(a / 6.0f);
-                        const float s = f16_widen(sb);
-                        if (s > 0.0f) {
-                            const float d = sign * s;
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) r[i] = r[i] / d;
-                            w = e2m1_pack8(r);
-                        }
-                        if (page >= 0) {
-                            const int64_t vec = (static_cast<int64_t>(page) * H + h) << c.page_shift;    // first token of (page, head)
-                            if (lane == 0) (kind == 1 ? c.k_scale : c.v_scale)[vec + off + tok] = static_cast<uint16_t>(sb);
-                            if (kind == 1) {
-                                uint16_t *q = reinterpret_cast<uint16_t *>(c.k_codes + (vec + off + tok) * (D / 2));
-                                q[d0 >> 2] = static_cast<uint16_t>(w);
-                                q[d1 >> 2] = static_cast<uint16_t>(w >> 16);
-                            }
-                        }
-                    }
-                }
+                if (here && kind < 3) w = append_head<DT, D>(c, nw, v, ang, kind, h, base_of(hx), trow, page, off + tok, lane, d0, d1, sign);
                 if ((hb + 1) * HPB <= HQ + H || page < 0) continue;   // no values among the workgroup's heads
                 __syncthreads();                              // the group before is read
                 if (kind == 2) codes[hs][tok][lane] = w;
@@ -247,19 +294,35 @@ __global__ __launch_bounds__(256) void kv4_append_kernel(Kv4Cache c, KvBatch b, 
     }
 }
 
+template <int DT, int D>
+hipError_t append_d(const Kv4Cache &c, const KvBatch &b, const Kv4New &n, hipStream_t st) {
+    const int heads = n.q_heads + 2 * c.heads;
+    if (!b.q_start) {
+        const dim3 grid(b.rows, (heads * (D / 8) + 255) / 256);
+        hipLaunchKernelGGL((kv4_append_one_kernel<DT, D>), grid, dim3(256), 0, st, c, b, n);
+        return hipGetLastError();
+    }
+    // Rows a workgroup: an octet where sequences have that many, else as many as they have on
+    // average, so that it does not walk from sequence to sequence (1024 of one row each: 100 us by
+    // eights, 88 us by ones; 512 rows of one: 17 us by eights, 53 us by ones).  Heads a workgroup:
+    // one group, until that gives more workgroups than the chip takes at once, then up to seven, each
+    // token's angles being read once for them (8 x 16 rows 10 us with one, 23 us with seven; 8192
+    // rows 111 us with four, 109 us with seven, 119 us with 28).
+    constexpr int kSpan = 7, kFew = 1024;
+    const int each = b.rows / b.B, chunk = each >= 8 ? 8 : each >= 4 ? 4 : each >= 2 ? 2 : 1;
+    constexpr int hpb = 256 / D;
+    const int groups = (heads + hpb - 1) / hpb;
+    const int64_t all = static_cast<int64_t>((b.rows + chunk - 1) / chunk) * groups;
+    const int span = static_cast<int>(all <= kFew ? 1 : all >= kSpan * kFew ? kSpan : all / kFew);
+    const dim3 grid((b.rows + chunk - 1) / chunk, (groups + span - 1) / span);
+    hipLaunchKernelGGL((kv4_append_kernel<DT, D>), grid, dim3(256), 0, st, c, b, n, chunk, span);
+    return hipGetLastError();
+}
 template <int DT>
 hipError_t append_t(const Kv4Cache &c, const KvBatch &b, const Kv4New &n, hipStream_t st) {
-    // Few rows: a workgroup for each and for every group of heads, so that none waits for
-    // another.  Many: one for every eight rows, most with one octet to do, and for several
-    // groups of heads.
-    const bool many = b.rows > 512;
-    const int chunk = many ? 8 : 1, hpb = 256 / c.D, groups = (n.q_heads + 2 * c.heads + hpb - 1) / hpb;
-    const int span = many ? (groups < kSpan ? groups : kSpan) : 1;
-    const dim3 grid((b.rows + chunk - 1) / chunk, (groups + span - 1) / span), block(256);
-    if (c.D == 64) hipLaunchKernelGGL((kv4_append_kernel<DT, 64>), grid, block, 0, st, c, b, n, chunk, span);
-    else if (c.D == 128) hipLaunchKernelGGL((kv4_append_kernel<DT, 128>), grid, block, 0, st, c, b, n, chunk, span);
-    else hipLaunchKernelGGL((kv4_append_kernel<DT, 256>), grid, block, 0, st, c, b, n, chunk, span);
-    return hipGetLastError();
+    if (c.D == 64) return append_d<DT, 64>(c, b, n, st);
+    if (c.D == 128) return append_d<DT, 128>(c, b, n, st);
+    return append_d<DT, 256>(c, b, n, st);
 }
 
 // One (row, head) vector by D / 8 lanes, eight consecutive values each.
