@@ -14,7 +14,14 @@
 // lanes, 8 values each (lane layout of rotate_quant.h).  The codes of a head's
 // values cross LDS once to become dwords; a dword that the call fills only
 // partly is read and merged.  No other workgroup of the call writes that dword,
-// so nothing is atomic.
+// so nothing is atomic.  Where every sequence has one row no octet has two tokens
+// to bring together: a kernel of its own holds a head a 16-lane group (1024
+// sequences 100 us by octets, 14.6 us, read-back counted).
+//
+// 8192 f32 tokens of 40 query and 8 KV heads of 128 take 94 us, 4.4 TB/s of the
+// 412 MB it moves, its mix of reads and writes being a copy's (4.9 TB/s); one
+// token of 8 sequences 3.1 us, 8 x 16 bf16 tokens 7.9 us.  The read-back is a
+// stream: 12 us for the 8192 tokens.
 #include "kv4.h"
 #include "rotate_quant.h"
 

@@ -3,6 +3,15 @@
 // Per query row and head: s_t = sm_scale * q.k_t over the tokens t that the row
 // sees, o = sum_t exp(s_t - m) v_t / sum_t exp(s_t - m) with m the running
 // maximum; k and v are level * scale.
+//
+// Few query rows leave it to the memory: the cache is read once, as it lies.  199999
+// tokens (one f32 row, 40 query and 8 KV heads of 128; 211 MB) take 38 us and 5.4 us for
+// the join, 4.9 TB/s in all; 64 bf16 sequences of up to 16000 tokens (506 MB) 89 + 5 us,
+// 5.4 TB/s, where a read-only stream reaches 5.8.  Many rows are bound by a SIMD's issue
+// of vector and matrix instructions, which overlap little: an 8192-token prompt (687
+// GFLOP, bf16) takes 0.82 ms, 0.84 PFLOP/s, where a library product of this size reaches
+// 1.2; 63% of its cycles issue vector instructions (codes to f16 and exponents first) and
+// 35% keep the matrix cores busy.  8 x 16 draft rows over 8192 tokens take 29 + 6 us.
 #include "kv4.h"
 
 namespace rad {
@@ -687,6 +696,8 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(Kv4Cache c, KvBatch b
         for (int i = 0; i < 16; ++i) acc[x][i] = 0.0f;
 
     auto work = [&](WideStep<D> &cur, int step) {
+        // the wave with products to issue goes before the one with exponents (8192 tokens
+        // 860 -> 827 us)
         __builtin_amdgcn_s_setprio(1);
         f16v st;
 #pragma unroll
@@ -868,7 +879,11 @@ Plan make_plan(const KvBatch &b, int heads, int G, int tm, int target, int min_c
 }
 
 // The kernel's shape for a call: by the pairs of one sequence and KV head, so that no wave
-// multiplies mostly padding.  Heads of 256 fill the registers with 16 columns a wave.
+// multiplies mostly padding (more than 16 pairs in tiles of 32: an 8192-token prompt 861 us,
+// 874 us in tiles of 16, which keep twice the conversions a product).  Heads of 256 fill the
+// registers with 16 columns a wave.  One tile a workgroup, its waves sharing the context, beat
+// two or four tiles side by side (8 x 16 rows 41 -> 37 us, a 4096-token window 199 -> 182 us;
+// with 80 pairs a fourth wave had none) though an 8192-token prompt takes 3% less with two.
 struct Shape {
     bool once;              // a sequence and KV head is one tile
     Plan plan;
@@ -881,7 +896,8 @@ Shape attn_shape(const KvBatch &b, const Kv4Cache &c, int q_heads) {
     const int64_t pairs = static_cast<int64_t>(b.max_q) * G;
     s.once = pairs <= 16;
     const int tm = s.once || c.D == 256 ? 16 : 32;
-    // workgroups that the chip's 256 CUs hold at once
+    // workgroups that the chip's 256 CUs hold at once; cutting finer costs more in the join (199999
+    // tokens 50 us at 3 a CU, 60 at 6, 68 at 9)
     const int held = !s.once || c.D == 256 ? 2 : c.D == 128 ? 3 : 5;
     // Contexts of at most eight steps a wave are not cut: a second launch costs more (997
     // tokens, 40 query heads: 9.5 us in one launch, 10.3 us in two)

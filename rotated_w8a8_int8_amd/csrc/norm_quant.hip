@@ -9,8 +9,13 @@
 // and gamma and writes h, codes and a scale: an HBM stream for many tokens, a
 // chain of two reductions for few.
 //
-// A workgroup holds one token, each wave four 128-blocks a step (the lane
-// layout of rotate_quant.h), NITER steps.
+// A workgroup holds one token, each wave four 128-blocks a step (the lane layout
+// of rotate_quant.h), NITER steps.  8192 tokens of 5120 f32 values with a residual
+// take 93 us, 5.9 TB/s of the 545 MB it has to move (a read-only stream reaches 5.8,
+// a copy 4.9); nontemporal accesses are no faster here and leave the codes out of the
+// caches for the contraction (the call and a pass over its codes 203 us, 210 us with
+// them).  128 bf16 tokens take 4.1 us and one f32 token 3.8 us: the launch, a trip to
+// memory and the two reductions.
 #include "layer_launch.h"
 #include "rotate_quant.h"
 #include "value_types.h"
@@ -18,12 +23,12 @@
 namespace rad {
 namespace {
 
-template <int DT, int NITER, int MAXT, bool NT>
-__global__ __launch_bounds__(MAXT) void norm_quant_kernel(const void *x, const void *res, void *res_out,
+template <int DT, int NITER>
+__global__ __launch_bounds__(1024) void norm_quant_kernel(const void *x, const void *res, void *res_out,
                                                           const float *__restrict__ gamma, float eps,
                                                           int8_t *__restrict__ q, float *__restrict__ scale, int K,
                                                           int rotate) {
-    __shared__ float red_sum[MAXT / 64], red_max[MAXT / 64];
+    __shared__ float red_sum[16], red_max[16];
     const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, waves = blockDim.x >> 6;
     const int l16 = lane & 15, nblk = K >> 7;
     const int64_t m = blockIdx.x, row = m * K;
@@ -35,8 +40,8 @@ __global__ __launch_bounds__(MAXT) void norm_quant_kernel(const void *x, const v
         const int blk = (it * waves + wid) * 4 + (lane >> 4);
         if (blk < nblk) {
             const int64_t at = row + blk * 128 + 4 * l16;
-            v[it].lo = load4<DT, NT>(x, at);
-            v[it].hi = load4<DT, NT>(x, at + 64);
+            v[it].lo = load4<DT>(x, at);
+            v[it].hi = load4<DT>(x, at + 64);
         } else {
             v[it].lo = make_float4(0.f, 0.f, 0.f, 0.f);
             v[it].hi = v[it].lo;
@@ -48,13 +53,13 @@ __global__ __launch_bounds__(MAXT) void norm_quant_kernel(const void *x, const v
             const int blk = (it * waves + wid) * 4 + (lane >> 4);
             if (blk < nblk) {
                 const int64_t at = row + blk * 128 + 4 * l16;
-                const float4 a = load4<DT, NT>(res, at), b = load4<DT, NT>(res, at + 64);
+                const float4 a = load4<DT>(res, at), b = load4<DT>(res, at + 64);
                 v[it].lo = make_float4(rounded<DT>(v[it].lo.x + a.x), rounded<DT>(v[it].lo.y + a.y),
                                        rounded<DT>(v[it].lo.z + a.z), rounded<DT>(v[it].lo.w + a.w));
                 v[it].hi = make_float4(rounded<DT>(v[it].hi.x + b.x), rounded<DT>(v[it].hi.y + b.y),
                                        rounded<DT>(v[it].hi.z + b.z), rounded<DT>(v[it].hi.w + b.w));
-                store4<DT, NT>(res_out, at, v[it].lo);
-                store4<DT, NT>(res_out, at + 64, v[it].hi);
+                store4<DT>(res_out, at, v[it].lo);
+                store4<DT>(res_out, at + 64, v[it].hi);
             }
         }
     }
@@ -109,13 +114,8 @@ __global__ __launch_bounds__(MAXT) void norm_quant_kernel(const void *x, const v
                 hi = pack4_signed(v[it].hi, s, c);
             }
             uint32_t *p = reinterpret_cast<uint32_t *>(q + row + blk * 128 + 4 * l16);
-            if constexpr (NT) {
-                __builtin_nontemporal_store(lo, p);
-                __builtin_nontemporal_store(hi, p + 16);
-            } else {
-                p[0] = lo;
-                p[16] = hi;
-            }
+            p[0] = lo;
+            p[16] = hi;
         }
     }
 }
@@ -132,38 +132,26 @@ struct Args {
     hipStream_t st;
 };
 
-template <int DT, int NITER, int MAXT, bool NT>
+template <int DT, int NITER>
 hipError_t go(const Args &a, int waves) {
-    hipLaunchKernelGGL((norm_quant_kernel<DT, NITER, MAXT, NT>), dim3(static_cast<uint32_t>(a.M)), dim3(waves * 64), 0,
+    hipLaunchKernelGGL((norm_quant_kernel<DT, NITER>), dim3(static_cast<uint32_t>(a.M)), dim3(waves * 64), 0,
                        a.st, a.x, a.res, a.res_out, a.gamma, a.eps, a.q, a.scale, a.K, a.rotate);
     return hipGetLastError();
 }
 
 template <int DT>
 hipError_t launch(const Args &a) {
-    const int nblk = a.K / 128, niter4 = (nblk + 15) / 16;
-    // Few tokens, or long rows: as many waves as the row has groups of four
-    // blocks, up to 16, so that each holds few steps.  Many tokens: 4 waves each.
-    if (a.M < 256 || niter4 > 12) {
-        const int niter = (nblk + 63) / 64, waves = (nblk + 4 * niter - 1) / (4 * niter);
-        if (niter <= 1) return go<DT, 1, 1024, false>(a, waves);
-        if (niter <= 2) return go<DT, 2, 1024, false>(a, waves);
-        if (niter <= 4) return go<DT, 4, 1024, false>(a, waves);
-        return go<DT, 8, 1024, false>(a, waves);               // K <= 65536
-    }
-    switch (niter4) {
-        case 1: return go<DT, 1, 256, true>(a, 4);
-        case 2: return go<DT, 2, 256, true>(a, 4);
-        case 3: return go<DT, 3, 256, true>(a, 4);
-        case 4: return go<DT, 4, 256, true>(a, 4);
-        case 5: return go<DT, 5, 256, true>(a, 4);
-        case 6: return go<DT, 6, 256, true>(a, 4);
-        case 7:
-        case 8: return go<DT, 8, 256, true>(a, 4);
-        case 9:
-        case 10: return go<DT, 10, 256, true>(a, 4);
-        default: return go<DT, 12, 256, true>(a, 4);
-    }
+    const int nblk = a.K / 128;
+    // As many waves as the row has groups of four blocks, so that each holds one step, up to 16
+    // (5120 values: 128 tokens 10.5 us with 10 waves, 11.8 us with 4, codes widened after).  Of many
+    // tokens a CU holds more where rows of more than 2048 take half the waves, two steps each (8192
+    // bf16 tokens 162 us, 185 us in one step; 16384 x 1024 f32 has no second step to take).
+    const int least = (nblk + 63) / 64, niter = a.M >= 1024 && nblk > 16 && least < 2 ? 2 : least;
+    const int waves = (nblk + 4 * niter - 1) / (4 * niter);
+    if (niter <= 1) return go<DT, 1>(a, waves);
+    if (niter <= 2) return go<DT, 2>(a, waves);
+    if (niter <= 4) return go<DT, 4>(a, waves);
+    return go<DT, 8>(a, waves);                                // K <= 65536
 }
 
 }  // namespace
