@@ -860,13 +860,18 @@ __global__ __launch_bounds__(512) void attn_join_kernel(Kv4Cache c, KvBatch b, K
     }
 }
 
-// The bounds of a plan (see above) for tiles of tm pairs; tables of at most `whole` steps are not cut.
-Plan make_plan(const KvBatch &b, int heads, int G, int tm, int target, int min_chunk, int whole) {
+// The bounds of a plan (see above) for tiles of tm pairs.
+Plan make_plan(const KvBatch &b, int heads, int G, int tm, int target, int min_chunk) {
     const int64_t steps = ((static_cast<int64_t>(b.max_pages) << b.page_shift) + 31) >> 5;
     const int64_t rows = static_cast<int64_t>(b.max_q) * G <= tm ? b.B : static_cast<int64_t>(b.rows) * G / tm + b.B;
     // Each tile may add a part to the even share: where tiles are few, the parts still fit one
     // round of workgroups; where they are many, twice as many parts even the rounds out.
     const int64_t tiles = rows * heads;
+    // Contexts that fit few steps a wave are not cut, the longer the more tiles there are: a second
+    // launch costs more than it saves (f32, 40 query and 8 KV heads: one sequence of 997 tokens 9.5
+    // against 10.3 us, but 14.2 against 10.7 us for 1990; 8 of 1990 14.0 against 15.6 us; 8 of 3900
+    // 20.5 against 17.4 us; 64 of 3900 34.6 against 42.9 us).
+    const int64_t whole = kWaves * (tiles < 64 ? 8 : tiles < 256 ? 16 : 32);
     target = 2 * tiles <= target ? target - static_cast<int>(tiles) : 2 * target;
     Plan p{tm, target, min_chunk, 0, 0, 0, 0};
     p.split = b.B <= kMostScanned && steps > whole;
@@ -899,9 +904,7 @@ Shape attn_shape(const KvBatch &b, const Kv4Cache &c, int q_heads) {
     // workgroups that the chip's 256 CUs hold at once; cutting finer costs more in the join (199999
     // tokens 50 us at 3 a CU, 60 at 6, 68 at 9)
     const int held = !s.once || c.D == 256 ? 2 : c.D == 128 ? 3 : 5;
-    // Contexts of at most eight steps a wave are not cut: a second launch costs more (997
-    // tokens, 40 query heads: 9.5 us in one launch, 10.3 us in two)
-    s.plan = make_plan(b, c.heads, G, tm, 256 * held, kWaves, 8 * kWaves);
+    s.plan = make_plan(b, c.heads, G, tm, 256 * held, kWaves);
     s.cols = static_cast<int>(pairs < tm ? pairs : tm);
     s.sums = static_cast<int64_t>(c.heads) * s.plan.slots * s.cols * c.D * 4;
     s.stats = static_cast<int64_t>(c.heads) * s.plan.slots * s.cols * 8;
