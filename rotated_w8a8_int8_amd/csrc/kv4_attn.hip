@@ -182,14 +182,15 @@ __device__ __forceinline__ int chunk_of(uint64_t total, const Plan &pl, int head
 template <bool ITEMS>
 __device__ __forceinline__ Piece find_piece(const KvBatch &b, const Kv4Attn &a, const Plan &pl, int heads, int G, int x) {
     const int lane = threadIdx.x & 63;
-    if (b.B == 1 && !ITEMS) {
+    if (b.B == 1) {
         const SeqWork s = seq_work(b, a, 0);
         const int tiles = (s.n * G + pl.tm - 1) / pl.tm, steps = steps_of(s.lo, s.hi);
         const int chunk = chunk_of(static_cast<uint64_t>(tiles) * static_cast<uint32_t>(steps), pl, heads);
         const int parts = pl.split ? max(1, (steps + chunk - 1) / chunk) : 1;
-        const int tile = x / parts;
-        if (tile >= tiles || (parts > 1 && x >= pl.slots)) return Piece{0, 0, 0, 0, 0};
-        return Piece{0, tiles - 1 - tile, x % parts, parts, x};
+        const int tile = ITEMS ? x : x / parts, slot = ITEMS ? x * parts : x;
+        if (tile >= tiles || (ITEMS && parts == 1)) return Piece{0, 0, 0, 0, 0};
+        if (parts > 1 && slot + (ITEMS ? parts : 1) > pl.slots) return Piece{0, 0, 0, 0, 0};
+        return Piece{0, tiles - 1 - tile, ITEMS ? 0 : x % parts, parts, slot};
     }
     uint64_t total = 0;
     if (pl.split) {
