@@ -103,6 +103,28 @@ def test_padding_rows_and_separate_arrays(torch):
     run(torch, [3, 2], [4, 30], 2, 4, 128, 32, "f16", 128, 0, True, with_q=False)
 
 
+@pytest.mark.parametrize("D,rot", [(64, False), (128, True), (256, True)])
+def test_one_row_each_of_many_sequences(torch, D, rot):
+    # lengths around octets and pages, no token at all, an absent page, a position past the table
+    def edit(table, pages):
+        table[5, -1] = -1
+        table[40] = -1
+    rng = np.random.default_rng(D)
+    ctx = rng.integers(0, 70, 90)
+    ctx[:9] = [-1, 0, 6, 7, 8, 64, 31, 32, 95]
+    print("append one row each", D, flush=True)
+    run(torch, [1] * 90, ctx, 2, 3, D, 32, "bf16", D // 2, 0, rot, table_edit=edit, rope_rows=95)
+    run(torch, [1] * 90, ctx, 2, 3, D, 32, "f32", D, 1, rot, with_q=False)
+
+
+@pytest.mark.parametrize("new", [[2, 3, 2], [4, 5, 6, 1], [1, 0, 9, 0, 30, 2], [3] * 70, [17, 16, 15] * 30])
+def test_blocks_of_every_size(torch, new):
+    # rows a workgroup go by the rows a sequence has on average: 2, 4, 8
+    print("append blocks", len(new), new[:6], flush=True)
+    rng = np.random.default_rng(len(new))
+    run(torch, new, rng.integers(0, 40, len(new)), 2, 3, 128, 32, "f16", 128, 0, True, pad=1)
+
+
 def test_absent_pages_and_rows_before_the_first_token(torch):
     def edit(table, pages):
         table[0, 1] = -1
