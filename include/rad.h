@@ -413,8 +413,7 @@ typedef struct rad_rope {
  * 65504), code = the level nearest to |x| / scale (f32 division), ties to the
  * even level index, magnitudes above 6 to 6, the sign of x, zero without a
  * sign; scale 0 gives zero codes.  Only the appended tokens' codes and scales
- * change; one call must not append to the same page
- * through two table entries.
+ * change; one call must not append to the same page through two table entries.
  * Non-finite inputs give unspecified codes for their own head vector.
  */
 int rad_kv4_append(const rad_kv4_cache *cache, const rad_kv_batch *batch, const void *k, int64_t ldk,

@@ -92,7 +92,7 @@ def test_decode_and_blocks(torch, D, rope, style, rot, dtype):
 @pytest.mark.parametrize("page", B.KV4_PAGE_SIZES)
 @pytest.mark.parametrize("ctx", [0, 1, 7, 8, 37, 250])
 def test_prompts_of_many_rows(torch, page, ctx):
-    # more than 512 rows: a workgroup walks eight rows
+    # a workgroup walks eight rows
     print("append prompt", page, ctx, flush=True)
     run(torch, [600, 0, 1, 13], [ctx, 5, 40, 2 * ctx], 1, 2, 64, page, "f32", 64, 0, False, seed=page + ctx)
 

@@ -144,7 +144,7 @@ def test_scores_that_rise_with_the_context(torch, dtype):
 
 
 def test_a_long_context(torch):
-    # 70,001 tokens: codes of a pool past 2^31 bits of offsets are not needed for the split over the context
+    # 70,001 tokens of one sequence: the context is split over workgroups and joined
     rng = np.random.default_rng(11)
     n, D, page, H, G = 70001, 128, 256, 1, 5
     pages = (n + page - 1) // page
