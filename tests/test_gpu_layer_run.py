@@ -253,3 +253,37 @@ def test_many_sequences(torch):
         assert np.all(np.abs(C.host(o) - want) <= C.attention_tolerance("f32", want, mass, reach, 60))
         o2 = B.attn_kv4(C.device_cache(torch, host), C.device_batch(torch, table, seq_len, start, T), C.put(torch, q), 0.1)
         assert np.all(np.abs(C.host(o2) - want) <= C.attention_tolerance("f32", want, mass, reach, 60))
+
+
+@pytest.mark.parametrize("inside", [True, False])
+def test_graph_replays_follow_the_block_table(torch, inside):
+    # page ids are read anew by every replay, written by the graph itself just before or by work between replays
+    rng = np.random.default_rng(21)
+    H, G, D, page, B_, width = 2, 4, 128, 32, 3, 40
+    host = O.Cache(2 * B_ * width, H, page, D, rng)
+    C.fill_cache(rng, host, np.arange(2 * B_ * width, dtype=np.int32)[None], [2 * B_ * width * page])
+    cache = C.device_cache(torch, host)
+    seq_len = np.array([1000, 1270, 33])
+    tables = [rng.permutation(2 * B_ * width)[:B_ * width].reshape(B_, width).astype(np.int32) for _ in range(4)]
+    dev = [C.put(torch, t) for t in tables]
+    batch = C.device_batch(torch, tables[0], seq_len, None, B_)
+    q = O.to_dtype(rng.standard_normal((B_, H * G, D)), "bf16")
+    qd, src, o = C.put(torch, q, "bf16"), dev[0].clone(), torch.empty((B_, H * G, D), dtype=torch.bfloat16, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        B.attn_kv4(cache, batch, qd, D ** -0.5, o=o)
+        s.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            if inside:
+                batch.block_table.copy_(src)
+            B.attn_kv4(cache, batch, qd, D ** -0.5, o=o)
+        for k in (1, 2, 3, 0, 2):
+            (src if inside else batch.block_table).copy_(dev[k])
+            o.fill_(9.0)
+            g.replay()
+            s.synchronize()
+            want, mass, reach = O.attention(q, host, tables[k], seq_len, C.ragged([1] * B_), D ** -0.5, True, 0)
+            tol = C.attention_tolerance("bf16", want, mass, reach, 1270)
+            assert np.all(np.abs(C.host(o) - want) <= tol), k
