@@ -445,9 +445,12 @@ int rad_kv4_read(const rad_kv4_cache *cache, const rad_kv_batch *batch, uint16_t
  *             Calls that may run at the same time need one each.
  *
  * Every row of a sequence is written; a row that sees no token becomes zeros.
- * Scores, statistics and sums are held in f32.  RAD_DT_F32
- * queries and the probabilities times value scales meet the matrix cores as
- * pairs of f16 (22 bits); for the 16-bit types the latter are one f16.
+ * Scores, statistics and sums are held in f32.  RAD_DT_F32 queries and the
+ * probabilities times value scales meet the matrix cores as pairs of f16 (22
+ * bits); for the 16-bit types the latter are one f16 (11 bits).  However small,
+ * such a product is off by no more than 2^-33 (f32), 2^-31 (f16) or 2^-28
+ * (bf16) of the largest of its row and head that a wave met with it (a wave
+ * takes a quarter of a part of the context).
  */
 int rad_attn_kv4_workspace(const rad_kv4_cache *cache, const rad_kv_batch *batch, int64_t q_heads,
                            int32_t dtype, int64_t *bytes);

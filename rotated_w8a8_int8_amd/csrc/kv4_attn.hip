@@ -54,17 +54,24 @@ __device__ __forceinline__ TokenRange seen(int pos, int len, int causal, int win
 // queries a weight is one f16 (HL 0).
 //
 // The reference exponent m of a column keeps its weights p * scale, p = 2^(score - m),
-// inside f16: it is set so that the largest weight met comes to 2^kRoom, and raised only
-// when one passes 2^kMost (one vote a step); then scores and scale exponents are looked at
-// one by one.  A weight is thus held to 2^-24 of a scale on which the column's largest is at
-// least 2^(kRoom - 1).
+// inside f16: it is set so that the largest weight met comes to 2^room, and raised only
+// when one passes kMost (one vote a step); then scores and scale exponents are looked at
+// one by one.  A weight is off by up to 2^-25, half of f16's smallest step, where the
+// column's largest is at least 2^(room - 1): by 2^(-24 - room) of it, however small it is
+// itself (see kRoom).
 typedef unsigned int u4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u2 __attribute__((ext_vector_type(2)));
 typedef float f4 __attribute__((ext_vector_type(4)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 
-constexpr float kRoom = 4.0f;                       // log2
-constexpr float kMost = 0x1p14f;                    // twice this is below 65504
+// log2 of the largest weight after a rise.  What a wave's n tokens lose beside a largest weight is
+// at most n 2^(-24 - kRoom) of it: for 50000 a tenth of half a step of a bf16 or f16 output, and
+// 6e-6 in f32 (1.9e-4 with 4).  The rest of f16's range is what weights may grow by before the next
+// rise, and rises cost: an 8192-token bf16 prompt takes 834 us with 4, 846 with 8, 855 with 9, 911
+// with 12; an f32 block of 16 rows 67, 69, 70 and 73 us.
+template <int DT>
+constexpr float kRoom = DT == kDtF32 ? 9.0f : DT == kDtF16 ? 7.0f : 4.0f;
+constexpr float kMost = 63488.0f;                   // f16, below its largest, 65504
 constexpr float kMostP = 0x1p60f;                   // values of scale 0 weigh nothing, but count
 constexpr float kLowest = -3.4028234663852886e38f;
 
@@ -498,7 +505,7 @@ __global__ __launch_bounds__(256, 2) void attn_kernel(Kv4Cache c, KvBatch b, Kv4
                 const float vs = times_half(1.0f, cur.vs, i);
                 most = fmaxf(most, fmaf(s[i], scale, vs > 0.0f ? static_cast<float>(__builtin_amdgcn_frexp_expf(vs)) : -24.0f));
             }
-            const float mn = fmaxf(m, col_max(most) - kRoom), shrink = __builtin_amdgcn_exp2f(m - mn);
+            const float mn = fmaxf(m, col_max(most) - kRoom<DT>), shrink = __builtin_amdgcn_exp2f(m - mn);
             m = mn;
             l *= shrink;
 #pragma unroll
@@ -739,7 +746,7 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(Kv4Cache c, KvBatch b
                 most = fmaxf(most, fmaf(s[i], scale, vs > 0.0f ? static_cast<float>(__builtin_amdgcn_frexp_expf(vs)) : -24.0f));
             }
             most = fmaxf(most, __shfl_xor(most, 32));
-            const float mn = fmaxf(m, most - kRoom), shrink = __builtin_amdgcn_exp2f(m - mn);
+            const float mn = fmaxf(m, most - kRoom<DT>), shrink = __builtin_amdgcn_exp2f(m - mn);
             m = mn;
             l *= shrink;
 #pragma unroll

@@ -266,3 +266,41 @@ def test_binding_refusals(torch):
         B.attn_kv4(dev, batch, q, 0.0)
     with pytest.raises(B.RadError):
         B.attn_kv4(dev, batch, q, 0.1, window=-3)
+
+
+@pytest.mark.parametrize("gap", [14, 16, 18, 20, 22, 24])
+@pytest.mark.parametrize("n,rows,D", [(200001, 1, 128), (200001, 12, 64), (200001, 40, 128), (1000, 1, 64), (1000, 12, 128),
+                                      (1000, 12, 256), (1000, 40, 64), (1000, 40, 128)])
+def test_a_peak_above_many_small_weights(torch, n, rows, D, gap):
+    """f32: one token `gap` nats above all others, with a value in dimension 0 alone: what the others are worth
+    together must not be lost with each of them.  The context is not cut (600 sequences, one of them long), so that a
+    wave, whose weights share a scale, has a quarter of it.
+
+    Of the mass of a dimension: the scores, 0 and `gap`, are right to 2^-21 (two f16 parts of the query, three
+    roundings), the weights to 24 * 2^-21 for that and 2^-21 for their two parts; each of a wave's tokens adds one
+    rounding to its sums, the join of the waves and the quotient at most 16, 2^-24 each.  Then a weight is off by up to
+    2^-33 of the largest that it is held with, whatever the dimension's mass: of 6 for each of the tokens."""
+    rng = np.random.default_rng(gap + D)
+    page, others = 256, 599
+    pages = (n + page - 1) // page
+    ref = O.Cache(pages, 1, page, D)
+    ref.k_scale[:], ref.v_scale[:] = 1, 1
+    ref.v_codes[:] = 0xFF                                      # level 6, negative, in every dimension
+    table = rng.permutation(pages).astype(np.int32)[None].repeat(others + 1, axis=0)
+    at = int(rng.integers(0, 32))                              # the peak comes first: all that follows meets its scale
+    key, value = np.zeros((1, D), np.uint8), np.zeros((1, D), np.uint8)
+    key[0, 0] = value[0, 0] = 7
+    ref.put(int(table[0, at // page]), at % page, (key, np.float16([1])), (value, np.float16([1])))
+    q = np.zeros((rows + others, 1, D), np.float32)
+    q[:, 0, 0] = gap / 6
+    start, seq_len = C.ragged([1] * others + [rows]), np.array([0] * others + [n])
+    got = C.host(B.attn_kv4(C.device_cache(torch, ref), C.device_batch(torch, table, seq_len, start, rows + others, rows),
+                            C.put(torch, q), 1.0, causal=False))
+    assert not got[:others].any()
+    top, rest = np.exp(float(np.float32(gap / 6)) * 6), n - 1.0
+    want, mass = np.full(D, -6 * rest / (top + rest)), np.full(D, 6 * rest / (top + rest))
+    want[0], mass[0] = 6 * (top - rest) / (top + rest), 6
+    tol = mass * (25 * 2.0 ** -21 + (n / 4 + 16) * 2.0 ** -24) + 6 * (n / 4 + 32) * 2.0 ** -33
+    off = np.max(np.abs(got[others:, 0] - want), axis=0)
+    print("peak", n, rows, D, gap, np.max(off / tol), np.max(off[1:] / mass[1:]), flush=True)
+    assert np.all(off <= tol)
