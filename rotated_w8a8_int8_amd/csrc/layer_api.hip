@@ -184,7 +184,7 @@ int rad_kv4_read(const rad_kv4_cache *cache, const rad_kv_batch *batch, uint16_t
 }  // extern "C"
 
 namespace {
-// Sizes that the attention call and its workspace call share; 1 when the batch is empty.
+// Sizes that the attention call and its workspace call share; 1 when there is no row to attend for.
 int check_attn(const rad_kv4_cache *c, const rad_kv_batch *b, int64_t q_heads, int32_t dtype) {
     if (dtype_bytes(dtype) == 0) return RAD_E_FMT;
     const int rc = check_cache(c);
@@ -193,7 +193,7 @@ int check_attn(const rad_kv4_cache *c, const rad_kv_batch *b, int64_t q_heads, i
     if (empty < 0) return empty;
     if (q_heads < 1 || q_heads % c->heads != 0) return RAD_E_SHAPE;
     if (q_heads > 16384 || b->rows * q_heads >= (int64_t(1) << 29)) return RAD_E_RANGE;
-    return empty;
+    return empty || (b->q_start && b->max_q == 0) ? 1 : RAD_OK;
 }
 }  // namespace
 

@@ -304,3 +304,19 @@ def test_a_peak_above_many_small_weights(torch, n, rows, D, gap):
     off = np.max(np.abs(got[others:, 0] - want), axis=0)
     print("peak", n, rows, D, gap, np.max(off / tol), np.max(off[1:] / mass[1:]), flush=True)
     assert np.all(off <= tol)
+
+
+@pytest.mark.parametrize("width", [2, 64])
+def test_no_rows_a_sequence(torch, width):
+    # max_q 0, as the largest row count of a batch without new rows gives it; also inside a capture
+    dev, i32 = B.KV4Cache.empty(4, 2, 64, 64), dict(dtype=torch.int32, device="cuda")
+    batch = B.KVBatch(torch.zeros(3, width, **i32), torch.full((3,), 40, **i32), torch.zeros(4, **i32), rows=5, max_q=0)
+    q, o = torch.ones(5, 4, 64, device="cuda"), torch.full((5, 4, 64), 7.0, device="cuda")
+    assert B.attn_kv4(dev, batch, q, 0.1, o=o) is o
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o.add_(1)
+        B.attn_kv4(dev, batch, q, 0.1, o=o)
+    g.replay()
+    torch.cuda.synchronize()
+    assert bool((o == 8).all())

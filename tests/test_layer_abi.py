@@ -180,3 +180,12 @@ def test_binding_refuses_host_tensors():
         B.KV4Cache(u8, torch.zeros(1, 1, 32).half(), u8.view(1, 1, 4, 128, 4), torch.zeros(1, 1, 32).half())
     with pytest.raises(TypeError, match="GPU tensor"):
         B.KVBatch(torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("max_pages", [4, 64, 4096])
+def test_attention_of_no_rows_a_sequence_is_done_at_once(max_pages):
+    # max_q 0: every row is past it and stays as it was, whatever the table's width
+    n, kw = ctypes.c_int64(-1), dict(max_q=0, max_pages=max_pages)
+    assert B.lib().rad_attn_kv4_workspace(cache(), batch(**kw), 4, BF16, ctypes.byref(n)) == B.RAD_OK and n.value == 0
+    assert attn(b=kw, ws=None, ws_bytes=0) == B.RAD_OK
+    assert attn(b=kw, q_heads=5) == B.RAD_E_SHAPE             # its sizes are still looked at
