@@ -307,7 +307,8 @@ enum rad_dtype { RAD_DT_F32 = 0, RAD_DT_BF16 = 1, RAD_DT_F16 = 2 };
  *   q, scale      int8 [M][K] (16-byte aligned) and f32 [M] outputs, what the
  *                 contraction calls take.
  *   rotate        1: rotated as by rad_fwht128; 0: not.
- *   0 <= M < 2^24; K > 0, K % 128 == 0, K <= RAD_QUANT_MAX_K.
+ *   0 <= M < 2^24; K > 0, K % 128 == 0, K <= RAD_QUANT_MAX_K; for K > 2048 also
+ *   M * min(ceil(K / 1024), 16) < 2^26 (what one launch holds).
  *
  * Per token: h = residual + x (f32 sum rounded to `dtype`, stored to
  * residual_out and used as stored; h = x without a residual);

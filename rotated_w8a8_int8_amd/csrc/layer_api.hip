@@ -14,8 +14,10 @@ int dtype_bytes(int32_t dtype) {
 }
 
 constexpr int64_t kMaxRows = int64_t(1) << 22, kMaxTokens = int64_t(1) << 30;
-// a launch holds fewer than 2^32 threads: 256 a token, and one for every eight values read back
-constexpr int64_t kMaxNormRows = int64_t(1) << 24, kMaxRead = int64_t(1) << 35;
+// A launch holds fewer than 2^32 threads: one for every eight values read back, and of the norm up to 256 a
+// token for K <= 2048, 64 for every 1024 values (1024 at most) for longer ones (norm_quant.hip, many tokens).
+constexpr int64_t kMaxNormRows = int64_t(1) << 24, kMaxRead = int64_t(1) << 35, kMaxThreads = int64_t(1) << 32;
+int64_t norm_threads(int64_t K) { return K <= 2048 ? 256 : K <= 16384 ? 64 * ((K + 1023) / 1024) : 1024; }
 
 // Shape and range of a cache descriptor (no pointers).
 int check_cache(const rad_kv4_cache *c) {
@@ -92,7 +94,7 @@ int rad_add_rmsnorm_quant_i8(const void *x, const void *residual, void *residual
     const int e = dtype_bytes(dtype);
     if (e == 0) return RAD_E_FMT;
     if (M < 0 || K <= 0 || K % 128 != 0) return RAD_E_SHAPE;
-    if (K > RAD_QUANT_MAX_K || M >= kMaxNormRows || (rotate != 0 && rotate != 1)) return RAD_E_RANGE;
+    if (K > RAD_QUANT_MAX_K || M >= kMaxNormRows || M * norm_threads(K) >= kMaxThreads || (rotate != 0 && rotate != 1)) return RAD_E_RANGE;
     if (!(eps >= 0.0f) || eps > 3.0e38f) return RAD_E_RANGE;
     if ((residual == nullptr) != (residual_out == nullptr)) return RAD_E_NULL;
     if (M == 0) return RAD_OK;

@@ -189,3 +189,12 @@ def test_attention_of_no_rows_a_sequence_is_done_at_once(max_pages):
     assert B.lib().rad_attn_kv4_workspace(cache(), batch(**kw), 4, BF16, ctypes.byref(n)) == B.RAD_OK and n.value == 0
     assert attn(b=kw, ws=None, ws_bytes=0) == B.RAD_OK
     assert attn(b=kw, q_heads=5) == B.RAD_E_SHAPE             # its sizes are still looked at
+
+
+def test_norm_of_more_threads_than_a_launch_holds():
+    # wide tokens take more threads each: up to 1024, 64 for every 1024 values
+    one = dict(r=None, ro=None)
+    for K, most in ((2048, (1 << 24) - 1), (4096, (1 << 24) - 1), (5120, (1 << 32) // 320), (8192, (1 << 23) - 1),
+                    (8320, (1 << 32) // 576), (65536, (1 << 22) - 1)):
+        assert norm(M=most, K=K, x=None, **one) == B.RAD_E_NULL, K       # the size itself is taken
+        assert norm(M=most + 1, K=K, x=None, **one) == B.RAD_E_RANGE, K
