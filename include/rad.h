@@ -424,8 +424,8 @@ int rad_kv4_append(const rad_kv4_cache *cache, const rad_kv_batch *batch, const 
 /*
  * rad_kv4_read -- the cached keys and values of the batch's rows as bf16
  * (level * scale, exact in f32, rounded to nearest even): k_out and v_out bf16
- * bits [rows][heads][D], 16-byte aligned, rows * heads * D < 2^35.  Rows that
- * are no token, and tokens on absent pages, are left as they were.
+ * bits [rows][heads][D], 16-byte aligned, rows * heads * D <= 2^35 - 2048.
+ * Rows that are no token, and tokens on absent pages, are left as they were.
  */
 int rad_kv4_read(const rad_kv4_cache *cache, const rad_kv_batch *batch, uint16_t *k_out, uint16_t *v_out,
                  rad_stream_t stream);

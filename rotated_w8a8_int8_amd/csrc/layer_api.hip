@@ -16,7 +16,7 @@ int dtype_bytes(int32_t dtype) {
 constexpr int64_t kMaxRows = int64_t(1) << 22, kMaxTokens = int64_t(1) << 30;
 // A launch holds fewer than 2^32 threads: one for every eight values read back, and of the norm up to 256 a
 // token for K <= 2048, 64 for every 1024 values (1024 at most) for longer ones (norm_quant.hip, many tokens).
-constexpr int64_t kMaxNormRows = int64_t(1) << 24, kMaxRead = int64_t(1) << 35, kMaxThreads = int64_t(1) << 32;
+constexpr int64_t kMaxNormRows = int64_t(1) << 24, kMaxRead = (int64_t(1) << 35) - 2048, kMaxThreads = int64_t(1) << 32;
 int64_t norm_threads(int64_t K) { return K <= 2048 ? 256 : K <= 16384 ? 64 * ((K + 1023) / 1024) : 1024; }
 
 // Shape and range of a cache descriptor (no pointers).
@@ -169,7 +169,7 @@ int rad_kv4_read(const rad_kv4_cache *cache, const rad_kv_batch *batch, uint16_t
     if (rc != RAD_OK) return rc;
     const int empty = check_batch(cache, batch);
     if (empty < 0) return empty;
-    if (batch->rows * cache->heads * cache->D >= kMaxRead) return RAD_E_RANGE;
+    if (batch->rows * cache->heads * cache->D > kMaxRead) return RAD_E_RANGE;
     if (empty) return RAD_OK;
     rc = check_pointers(cache, batch);
     if (rc != RAD_OK) return rc;

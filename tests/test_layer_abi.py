@@ -198,3 +198,9 @@ def test_norm_of_more_threads_than_a_launch_holds():
                     (8320, (1 << 32) // 576), (65536, (1 << 22) - 1)):
         assert norm(M=most, K=K, x=None, **one) == B.RAD_E_NULL, K       # the size itself is taken
         assert norm(M=most + 1, K=K, x=None, **one) == B.RAD_E_RANGE, K
+
+
+def test_read_back_of_more_threads_than_a_launch_holds():
+    # 2048 values a workgroup of 256 threads: one value short of 2^35 still rounds up to 2^24 workgroups
+    assert read(c=dict(heads=233, D=64), b=dict(rows=2304167)) == B.RAD_E_RANGE      # 2^35 - 64 values
+    assert read(c=dict(heads=1, D=64), b=dict(rows=(1 << 22) - 1), k=None) == B.RAD_E_NULL
