@@ -436,7 +436,10 @@ int rad_kv4_read(const rad_kv4_cache *cache, const rad_kv_batch *batch, uint16_t
  * heads).
  *
  *   q, o      [rows][q_heads][D] of `dtype`, dense, 16-byte aligned; q_heads a multiple
- *             of the cache's heads, at most 16384; rows * q_heads < 2^29.
+ *             of the cache's heads, at most 16384; rows * q_heads < 2^29, and one launch holds
+ *             fewer than 2^24 tiles of 32 (row, head) pairs of a KV head (16 for D =
+ *             256) and parts of them: rows * q_heads / heads / 32 (/ 16) + B below
+ *             2^24 - 2560 suffices.
  *   sm_scale  0 < sm_scale <= 2^126.
  *   causal    1: the row at position p sees tokens t <= p; 0: every token of its sequence.
  *   window    > 0: only tokens t > p - window; 0: no window.

@@ -953,6 +953,10 @@ hipError_t launch_t(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, hipSt
 
 }  // namespace
 
+bool kv4_attn_fits(const Kv4Cache &c, const KvBatch &b, int q_heads) {
+    return static_cast<int64_t>(attn_shape(b, c, q_heads).plan.pieces) * 64 * kWaves < int64_t(1) << 32;
+}
+
 int64_t kv4_attn_workspace(const Kv4Cache &c, const KvBatch &b, int q_heads, int) {
     const Shape s = attn_shape(b, c, q_heads);
     return s.sums + s.stats;

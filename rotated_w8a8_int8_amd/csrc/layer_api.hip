@@ -195,7 +195,8 @@ int check_attn(const rad_kv4_cache *c, const rad_kv_batch *b, int64_t q_heads, i
     if (empty < 0) return empty;
     if (q_heads < 1 || q_heads % c->heads != 0) return RAD_E_SHAPE;
     if (q_heads > 16384 || b->rows * q_heads >= (int64_t(1) << 29)) return RAD_E_RANGE;
-    return empty || (b->q_start && b->max_q == 0) ? 1 : RAD_OK;
+    if (empty || (b->q_start && b->max_q == 0)) return 1;
+    return rad::kv4_attn_fits(cache_args(c), batch_args(c, b), static_cast<int>(q_heads)) ? RAD_OK : RAD_E_RANGE;
 }
 }  // namespace
 

@@ -42,6 +42,7 @@ struct Kv4Attn {
     int causal, window;      // window 0: none
     void *workspace;
 };
+bool kv4_attn_fits(const Kv4Cache &c, const KvBatch &b, int q_heads);     // one launch holds the call
 int64_t kv4_attn_workspace(const Kv4Cache &c, const KvBatch &b, int q_heads, int dtype);
 hipError_t launch_kv4_attn(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, int dtype, hipStream_t st);
 

@@ -204,3 +204,22 @@ def test_read_back_of_more_threads_than_a_launch_holds():
     # 2048 values a workgroup of 256 threads: one value short of 2^35 still rounds up to 2^24 workgroups
     assert read(c=dict(heads=233, D=64), b=dict(rows=2304167)) == B.RAD_E_RANGE      # 2^35 - 64 values
     assert read(c=dict(heads=1, D=64), b=dict(rows=(1 << 22) - 1), k=None) == B.RAD_E_NULL
+
+
+def test_attention_of_more_workgroups_than_a_launch_holds():
+    # 256 threads a tile of 32 (row, head) pairs of a KV head, 16 for heads of 256, and a tile more a sequence
+    n, one = ctypes.c_int64(0), dict(seqs=1, max_pages=1)
+
+    def both(c, b, q_heads, rc):
+        assert attn(c=c, b=b, q_heads=q_heads, q=None, ws_bytes=1 << 60) == rc
+        assert B.lib().rad_attn_kv4_workspace(cache(**c), batch(**b), q_heads, BF16,
+                                              ctypes.byref(n)) == (B.RAD_OK if rc == B.RAD_E_NULL else rc)
+    many = dict(seqs=1024, max_pages=1)
+    both(dict(heads=1, D=64), dict(many, rows=32767, max_q=32767), 16384, B.RAD_E_RANGE)      # 2^24 + 512
+    both(dict(heads=1, D=64), dict(many, rows=32765, max_q=32765), 16384, B.RAD_E_NULL)       # 2^24 - 512
+    both(dict(heads=1, D=64), dict(one, rows=32767, max_q=32767), 16384, B.RAD_E_NULL)        # 2^24 - 511
+    both(dict(heads=1, D=256), dict(many, rows=16383, max_q=16383), 16384, B.RAD_E_RANGE)     # 2^24
+    both(dict(heads=1, D=256), dict(one, rows=32767, max_q=32767), 16384, B.RAD_E_RANGE)      # nearly 2^25
+    both(dict(heads=1, D=256), dict(many, rows=16382, max_q=16382), 16384, B.RAD_E_NULL)
+    both(dict(heads=2, D=256), dict(many, rows=32767, max_q=32767), 16384, B.RAD_E_RANGE)
+    both(dict(heads=4, D=256), dict(many, rows=32767, max_q=32767), 16384, B.RAD_E_NULL)
