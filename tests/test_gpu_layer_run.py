@@ -287,3 +287,33 @@ def test_graph_replays_follow_the_block_table(torch, inside):
             want, mass, reach = O.attention(q, host, tables[k], seq_len, C.ragged([1] * B_), D ** -0.5, True, 0)
             tol = C.attention_tolerance("bf16", want, mass, reach, 1270)
             assert np.all(np.abs(C.host(o) - want) <= tol), k
+
+
+@pytest.mark.parametrize("nseq,most,starts,H,G,D,dtype", [
+    (513, 40, True, 2, 3, 64, "bf16"), (700, 40, True, 1, 5, 128, "f32"), (600, 9, True, 2, 7, 256, "f16"),
+    (520, 1, False, 1, 40, 64, "f16"), (700, 1, False, 2, 4, 128, "bf16"), (5000, 3, True, 1, 2, 64, "f32"),
+    (70000, 2, True, 1, 20, 64, "bf16"), (70000, 1, False, 1, 33, 64, "f32"), (70000, 1, True, 1, 1, 64, "f32")])
+def test_more_sequences_than_are_looked_at_by_every_workgroup(torch, nseq, most, starts, H, G, D, dtype):
+    # every row written, and a sample of the sequences against the oracle: the first and last, empty ones, the longest
+    print("sequences", nseq, most, starts, H, G, D, dtype, flush=True)
+    rng = np.random.default_rng(nseq + G)
+    page, pool = 32, 50
+    new = rng.integers(0, most + 1, nseq) if starts else np.ones(nseq, int)
+    if starts:
+        new[[0, 7, nseq - 1]], new[[8, 9, nseq - 2]] = most, 0
+    seq_len = np.maximum(new + rng.integers(-1, 60, nseq), 0)
+    table = rng.integers(-1, pool, (nseq, 4)).astype(np.int32)         # shared pages, some absent
+    host = O.Cache(pool, H, page, D, rng)
+    host.k_scale[:], host.v_scale[:] = np.float16(0.2), np.float16(0.4)
+    start = C.ragged(new)
+    T = int(start[-1]) + (5 if starts else 0)
+    q = O.to_dtype(rng.standard_normal((T, H * G, D)), dtype)
+    o = torch.full(q.shape, float("nan"), dtype=C.torch_dtype(torch, dtype), device="cuda")
+    batch = C.device_batch(torch, table, seq_len, start if starts else None, T, most)
+    B.attn_kv4(C.device_cache(torch, host), batch, C.put(torch, q, dtype), 0.1, o=o)
+    got = C.host(o)
+    assert np.isnan(got[start[-1]:]).all() and not np.isnan(got[:start[-1]]).any()
+    some = np.unique(np.concatenate([np.arange(12), np.arange(nseq - 70, nseq), rng.integers(0, nseq, 60)]))
+    rows = np.concatenate([np.arange(start[b], start[b + 1]) for b in some])
+    want, mass, reach = O.attention(q[rows], host, table[some], seq_len[some], C.ragged(new[some]), 0.1, True, 0)
+    assert np.all(np.abs(got[rows] - want) <= C.attention_tolerance(dtype, want, mass, reach, 100))
