@@ -182,7 +182,7 @@ __device__ __forceinline__ int wave_scan(int v) {
 // Steps a part: about `target` parts over all sequences and KV heads, rounded up.
 __device__ __forceinline__ int chunk_of(uint64_t total, const Plan &pl, int heads) {
     const uint64_t all = total * static_cast<uint32_t>(heads) + static_cast<uint32_t>(pl.target - 1);
-    const int even = all >> 32 ? static_cast<int>(all / static_cast<uint32_t>(pl.target))
+    const int even = all >> 32 ? static_cast<int>(min(all / static_cast<uint32_t>(pl.target), uint64_t(1) << 30))
                                : static_cast<int>(static_cast<uint32_t>(all) / static_cast<uint32_t>(pl.target));
     return max(even, pl.min_chunk);
 }
