@@ -215,3 +215,20 @@ def test_binding_refusals(torch):
         B.KV4Cache.empty(2, 2, 48, 64)
     with pytest.raises(ValueError, match="v_scale"):
         B.KV4Cache(dev.k_codes, dev.k_scale, dev.v_codes, dev.v_scale[:1])
+
+
+@pytest.mark.parametrize("D,heads,q_heads,new,dtype,rope,style,rot", [
+    (256, 3, 9, [2000, 0, 1, 1500, 33, 466], "bf16", 256, 0, True),       # seven groups of heads a workgroup, three workgroups a row
+    (256, 3, 9, [1200, 900], "f32", 128, 1, False),                       # three groups a workgroup
+    (128, 4, 20, [3000, 9, 700, 491], "f32", 128, 0, True),               # seven groups of two heads
+    (128, 4, 19, [2500, 17, 60], "f16", 64, 1, True),                     # five, the last with one head to spare
+    (128, 4, 20, [3000, 9, 700, 491], "bf16", None, 0, False),
+    (64, 4, 20, [9001], "f16", 64, 0, False),                             # seven groups of four heads, all of a row's
+    (64, 5, 17, [2400, 2403], "f32", 24, 1, False)])
+def test_prompts_whose_workgroups_take_several_groups_of_heads(torch, D, heads, q_heads, new, dtype, rope, style, rot):
+    print("append groups", D, heads, q_heads, new, dtype, flush=True)
+    rng = np.random.default_rng(D + heads)
+
+    def edit(table, pages):
+        table[0, 3] = -1
+    run(torch, new, rng.integers(0, 50, len(new)), heads, q_heads, D, 64, dtype, rope, style, rot, pad=3, table_edit=edit)

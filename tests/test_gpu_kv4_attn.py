@@ -320,3 +320,99 @@ def test_no_rows_a_sequence(torch, width):
     g.replay()
     torch.cuda.synchronize()
     assert bool((o == 8).all())
+
+
+def run_cut(torch, new, ctx, heads, G, D, page, dtype, causal=True, window=0, seed=0, edit=None, max_q=None, width=None):
+    """As run, over contexts so long that they are cut and joined (random codes, scales past a length stale)."""
+    print("cut", new[:6], ctx[:6], heads, G, D, dtype, causal, window, flush=True)
+    rng = np.random.default_rng(seed)
+    start, seq_len = C.ragged(new), np.array(new) + np.array(ctx)
+    T = int(start[-1]) + 2
+    table, pages = C.page_table(rng, seq_len, page, width)
+    ref = O.Cache(pages, heads, page, D, rng)
+    for b, n in enumerate(seq_len):
+        for j in range((int(n) + page - 1) // page):
+            m = min(int(n) - j * page, page)
+            ref.k_scale[table[b, j], :, :m] = 0.35 * np.exp(rng.uniform(-0.5, 0.5, (heads, m)))
+            ref.v_scale[table[b, j], :, :m] = 0.4 * np.exp(rng.uniform(-1, 1, (heads, m)))
+    if edit is not None:
+        edit(table, pages)
+    q = O.to_dtype(1.5 * rng.standard_normal((T, heads * G, D)), dtype)
+    cache, batch = C.device_cache(torch, ref), C.device_batch(torch, table, seq_len, start, T, max_q or max(new))
+    assert B.attn_kv4_workspace(cache, batch, heads * G, C.torch_dtype(torch, dtype)) > 0, "not cut"
+    o = torch.full(q.shape, 33.0, dtype=C.torch_dtype(torch, dtype), device="cuda")
+    B.attn_kv4(cache, batch, C.put(torch, q, dtype), D ** -0.5, causal=causal, window=window, o=o)
+    got = C.host(o)
+    assert np.all(got[start[-1]:] == 33.0), "padding rows were written"
+    want, mass, reach = O.attention(q, ref, table, seq_len, start, D ** -0.5, causal, window)
+    n = start[-1]
+    off, tol = np.abs(got - want)[:n], C.attention_tolerance(dtype, want[:n], mass[:n], reach[:n], int(seq_len.max()))
+    assert np.all(off <= tol), "off by %g of the tolerance at %s" % (np.max(off / tol), np.unravel_index(np.argmax(off / tol), off.shape))
+
+
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 1500), (False, 4300)])
+@pytest.mark.parametrize("dtype", C.DTYPES)
+@pytest.mark.parametrize("D,G,page", [(64, 8, 32), (128, 5, 64), (256, 3, 128)])
+def test_cut_contexts_of_blocks(torch, D, G, page, dtype, causal, window):
+    # tiles of 32 columns (16 where D is 256), with rows that see nothing of a part, and a sequence without rows
+    run_cut(torch, [16, 5, 0, 16, 1], [5003, 4100, 700, 30, 1999], 2, G, D, page, dtype, causal, window, seed=D + window)
+
+
+@pytest.mark.parametrize("dtype", C.DTYPES)
+@pytest.mark.parametrize("D,G", [(64, 5), (128, 5), (256, 7), (128, 2), (64, 1)])
+def test_cut_contexts_of_few_pairs(torch, D, G, dtype):
+    # 9 to 16 (row, head) pairs of a KV head: one tile of 16 columns, f32 in two products; and up to 8
+    run_cut(torch, [3 if G == 5 else 2, 1, 2], [6001, 90, 2500], 2, G, D, 64, dtype, seed=D + G)
+
+
+@pytest.mark.parametrize("dtype", C.DTYPES)
+@pytest.mark.parametrize("D,G,n,ctx,causal,window", [(128, 5, 300, 4500, True, 0), (64, 8, 300, 4500, False, 0), (256, 3, 300, 4500, True, 0),
+                                                     (128, 5, 1200, 4800, True, 0), (128, 5, 1200, 3800, True, 2000), (64, 4, 4300, 0, True, 0)])
+def test_cut_contexts_of_prompts(torch, D, G, n, ctx, causal, window, dtype):
+    # many tiles in a few parts each, the early ones of a causal prompt in fewer; the join takes several columns a
+    # workgroup, a number that does not divide its threads
+    run_cut(torch, [n, 7], [ctx, 2000], 2 if n < 1000 else 1, G, D, 64, dtype, causal, window, seed=n + D)
+
+
+@pytest.mark.parametrize("dtype", C.DTYPES)
+@pytest.mark.parametrize("nseq,heads,G,D,most", [(65, 2, 5, 128, 1), (200, 8, 5, 128, 1), (100, 4, 8, 64, 1), (130, 2, 4, 256, 2), (512, 1, 3, 64, 1),
+                                                 (100, 2, 5, 128, 16)])
+def test_cut_contexts_of_many_sequences(torch, nseq, heads, G, D, most, dtype):
+    # more than the 64 sequences that a wave looks at at once: sums over them run on, few contexts are long
+    rng = np.random.default_rng(nseq)
+    ctx = rng.integers(0, 300, nseq)
+    ctx[[3, 64, nseq - 1]] = [9000, 5111, 4700]
+    new = np.full(nseq, most) if most == 1 else rng.integers(0, most + 1, nseq)
+    new[[3, 64, nseq - 1]] = most
+    run_cut(torch, list(new), list(ctx), heads, G, D, 64, dtype, seed=nseq + D, max_q=most)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_cut_contexts_with_absent_pages(torch, dtype):
+    def edit(table, pages):
+        table[0, 5:60] = -1                                    # a hole over whole parts
+        table[1, 0], table[1, 33] = pages, -9
+        table[2, :] = -1                                       # nothing is left: zeros
+    for new in ([1, 1, 1], [16, 16, 16], [200, 3, 40]):
+        run_cut(torch, new, [5000, 4800, 4500], 2, 5, 128, 64, dtype, seed=sum(new), edit=edit)
+
+
+def test_a_cut_context_of_many_heads_and_a_wide_table(torch):
+    # 40 heads on one KV head: two tiles a row; a table far wider than the sequences need
+    run_cut(torch, [1, 1], [3000, 77], 1, 40, 128, 64, "bf16", seed=1, width=3000)
+    run_cut(torch, [1, 1], [900, 77], 2, 5, 64, 32, "f32", seed=2, width=6000)
+
+
+def test_rows_past_max_q_of_a_cut_context(torch):
+    rng = np.random.default_rng(22)
+    ref = O.Cache(100, 2, 64, 128, rng)
+    ref.k_scale[:], ref.v_scale[:] = np.float16(0.2), np.float16(0.3)
+    table, n, rows = rng.permutation(100).astype(np.int32)[None], 6100, 20
+    q = rng.standard_normal((rows, 10, 128)).astype(np.float32)
+    batch = C.device_batch(torch, table, [n], C.ragged([rows]), rows, max_q=7)
+    dev, o = C.device_cache(torch, ref), torch.full((rows, 10, 128), 5.0, device="cuda")
+    assert B.attn_kv4_workspace(dev, batch, 10, torch.float32) > 0
+    got = C.host(B.attn_kv4(dev, batch, C.put(torch, q), 0.1, o=o))
+    want, mass, reach = O.attention(q, ref, table, np.array([n]), C.ragged([rows]), 0.1, True, 0)
+    assert np.all(got[7:] == 5)
+    assert np.all(np.abs(got - want)[:7] <= C.attention_tolerance("f32", want, mass, reach, n)[:7])

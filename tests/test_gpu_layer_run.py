@@ -317,3 +317,51 @@ def test_more_sequences_than_are_looked_at_by_every_workgroup(torch, nseq, most,
     rows = np.concatenate([np.arange(start[b], start[b + 1]) for b in some])
     want, mass, reach = O.attention(q[rows], host, table[some], seq_len[some], C.ragged(new[some]), 0.1, True, 0)
     assert np.all(np.abs(got[rows] - want) <= C.attention_tolerance(dtype, want, mass, reach, 100))
+
+
+@pytest.mark.parametrize("dtype,n,G,D", [("f32", 1, 5, 128), ("bf16", 16, 5, 128), ("f16", 7, 8, 64), ("bf16", 9, 4, 256)])
+def test_graph_replays_of_cut_contexts(torch, dtype, n, G, D):
+    # two captured calls with a workspace each; between replays lengths move so that the cut into parts is another,
+    # down to sequences of a few tokens, and the workspaces hold NaN
+    print("graph cut", dtype, n, G, D, flush=True)
+    rng = np.random.default_rng(n + D)
+    B_, H, page, width = 3, 2, 64, 140
+    host = O.Cache(B_ * width, H, page, D, rng)
+    host.k_scale[:] = 0.3 * np.exp(rng.uniform(-0.5, 0.5, host.k_scale.shape))
+    host.v_scale[:] = 0.4 * np.exp(rng.uniform(-1, 1, host.v_scale.shape))
+    cache, dt = C.device_cache(torch, host), C.torch_dtype(torch, dtype)
+    table, start = rng.permutation(B_ * width).reshape(B_, width).astype(np.int32), C.ragged([n] * B_)
+    lens = torch.zeros(B_, dtype=torch.int32, device="cuda")
+    batch = B.KVBatch(C.put(torch, table), lens, C.put(torch, start), rows=B_ * n, max_q=n)
+    q = [O.to_dtype(rng.standard_normal((B_ * n, H * G, D)), dtype) for _ in range(2)]
+    qd, o = [C.put(torch, x, dtype) for x in q], [torch.empty((B_ * n, H * G, D), dtype=dt, device="cuda") for _ in range(2)]
+    size = B.attn_kv4_workspace(cache, batch, H * G, dt)
+    assert size > 0
+    ws = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(2)]
+
+    def call(i):
+        B.attn_kv4(cache, batch, qd[i], 0.1, window=(0, 3000)[i], o=o[i], workspace=ws[i])
+    graphs = []
+    for i in range(2):
+        call(i)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(i)
+        graphs.append(g)
+    for seq_len in ([8960, 4000, 77], [n, 5, 6000], [0, 8960, 8960], [300, 200, 100], [5000, 8000, 2 * n]):
+        lens.copy_(torch.tensor(seq_len, dtype=torch.int32))
+        for i in range(2):
+            call(i)
+        torch.cuda.synchronize()
+        eager = [x.clone() for x in o]
+        for i in range(2):
+            o[i].fill_(float("nan"))
+            ws[i].fill_(255)
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert torch.equal(o[i].view(torch.uint8), eager[i].view(torch.uint8)), (seq_len, i)
+            want, mass, reach = O.attention(q[i], host, table, np.array(seq_len), start, 0.1, True, (0, 3000)[i])
+            assert np.all(np.abs(C.host(o[i]) - want) <= C.attention_tolerance(dtype, want, mass, reach, 8960)), (seq_len, i)

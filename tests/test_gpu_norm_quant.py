@@ -108,3 +108,14 @@ def test_binding_refusals(torch):
         B.add_rmsnorm_quant_i8(torch.zeros(256, 4, device="cuda").t(), g)
     with pytest.raises(B.RadError):
         B.add_rmsnorm_quant_i8(x[:, :200].contiguous(), g[:200].contiguous())
+
+
+@pytest.mark.parametrize("rot", [True, False])
+@pytest.mark.parametrize("dtype", C.DTYPES)
+@pytest.mark.parametrize("M,K", [(1023, 2176), (1024, 2176), (1025, 4096), (1024, 5120), (1100, 8192), (1024, 2048), (1024, 8320)])
+def test_many_tokens(torch, M, K, dtype, rot):
+    # from 1024 tokens on, rows of more than 2048 and up to 8192 values take half the waves, two steps each
+    print("norm", M, K, dtype, rot, flush=True)
+    x, h, g = inputs(M, K, dtype, seed=M + K)
+    q, s, out = B.add_rmsnorm_quant_i8(C.put(torch, x, dtype), C.put(torch, g), C.put(torch, h, dtype), eps=1e-6, rotate=rot)
+    check(q.cpu().numpy(), s.cpu().numpy(), C.host(out), x, h, g, 1e-6, dtype, rot)
