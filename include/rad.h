@@ -314,7 +314,8 @@ enum rad_dtype { RAD_DT_F32 = 0, RAD_DT_BF16 = 1, RAD_DT_F16 = 2 };
  * residual_out and used as stored; h = x without a residual);
  * r = 1 / sqrt(mean(h^2) + eps); n = (h * r) * gamma in f32; then codes and
  * scale of n exactly as rad_quant_act_i8 gives them.  The f32 sum of squares
- * has an unspecified (but fixed) order.  An all-zero row gives scale 0 and
+ * has an unspecified (but fixed) order; a row whose squares leave f32's range is
+ * taken times a power of two, as is eps to match.  An all-zero row gives scale 0 and
  * zero codes when eps > 0.
  *
  * Errors: RAD_E_FMT (unknown dtype), RAD_E_SHAPE, RAD_E_RANGE (K, M, eps or

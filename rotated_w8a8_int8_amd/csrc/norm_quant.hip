@@ -23,6 +23,35 @@
 namespace rad {
 namespace {
 
+// Sum of squares, and maximum, over the workgroup's row; `red` holds a value a wave.
+template <int NITER>
+__device__ __forceinline__ float row_sum_of_squares(const Blk8 (&v)[NITER], float (&red)[16]) {
+    float ss = 0.0f;
+#pragma unroll
+    for (int it = 0; it < NITER; ++it) {
+        const float4 a = v[it].lo, b = v[it].hi;
+        ss += ((a.x * a.x + a.y * a.y) + (a.z * a.z + a.w * a.w)) + ((b.x * b.x + b.y * b.y) + (b.z * b.z + b.w * b.w));
+    }
+    ss = wave_sum_f32(ss);
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = ss;
+    __syncthreads();
+    float total = 0.0f;
+    for (uint32_t w = 0; w < blockDim.x >> 6; ++w) total += red[w];
+    return total;
+}
+__device__ __forceinline__ float row_max(float a, float (&red)[16]) {
+    a = wave_max_f32(a);
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = a;
+    __syncthreads();
+    a = red[0];
+    for (uint32_t w = 1; w < blockDim.x >> 6; ++w) a = fmaxf(a, red[w]);
+    return a;
+}
+__device__ __forceinline__ float4 ldexp4(float4 f, int e) {
+    return make_float4(__builtin_amdgcn_ldexpf(f.x, e), __builtin_amdgcn_ldexpf(f.y, e), __builtin_amdgcn_ldexpf(f.z, e),
+                       __builtin_amdgcn_ldexpf(f.w, e));
+}
+
 template <int DT, int NITER>
 __global__ __launch_bounds__(1024) void norm_quant_kernel(const void *x, const void *res, void *res_out,
                                                           const float *__restrict__ gamma, float eps,
@@ -34,7 +63,6 @@ __global__ __launch_bounds__(1024) void norm_quant_kernel(const void *x, const v
     const int64_t m = blockIdx.x, row = m * K;
 
     Blk8 v[NITER];
-    float ss = 0.0f;
 #pragma unroll
     for (int it = 0; it < NITER; ++it) {
         const int blk = (it * waves + wid) * 4 + (lane >> 4);
@@ -63,16 +91,24 @@ __global__ __launch_bounds__(1024) void norm_quant_kernel(const void *x, const v
             }
         }
     }
+    float total = row_sum_of_squares(v, red_sum);
+    if constexpr (DT != kDtF16) {
+        // Squares that leave f32's range (values past 2^63 or, where eps does not cover them, below
+        // 2^-45): the row times a power of two, exactly, with eps to match.  The same for every thread.
+        if (!(total < 0x1p127f) || (total < 0x1p-90f && eps < 0x1p-120f)) {
+            float big = 0.0f;
 #pragma unroll
-    for (int it = 0; it < NITER; ++it) {
-        const float4 a = v[it].lo, b = v[it].hi;
-        ss += ((a.x * a.x + a.y * a.y) + (a.z * a.z + a.w * a.w)) + ((b.x * b.x + b.y * b.y) + (b.z * b.z + b.w * b.w));
+            for (int it = 0; it < NITER; ++it) big = fmaxf(big, fmaxf(amax4(v[it].lo), amax4(v[it].hi)));
+            const int e = max(__builtin_amdgcn_frexp_expf(row_max(big, red_max)), -100);
+#pragma unroll
+            for (int it = 0; it < NITER; ++it) {
+                v[it].lo = ldexp4(v[it].lo, -e);
+                v[it].hi = ldexp4(v[it].hi, -e);
+            }
+            total = row_sum_of_squares(v, red_sum);
+            eps = __builtin_amdgcn_ldexpf(eps, -2 * e);
+        }
     }
-    ss = wave_sum_f32(ss);
-    if (lane == 0) red_sum[wid] = ss;
-    __syncthreads();
-    float total = 0.0f;
-    for (int w = 0; w < waves; ++w) total += red_sum[w];
     const float r = 1.0f / __builtin_sqrtf(total / static_cast<float>(K) + eps);
 
     float amax = 0.0f;
@@ -88,11 +124,7 @@ __global__ __launch_bounds__(1024) void norm_quant_kernel(const void *x, const v
         if (rotate) fwht128_regs_signed(v[it], l16);           // values times the lane sign c
         amax = fmaxf(amax, fmaxf(amax4(v[it].lo), amax4(v[it].hi)));
     }
-    amax = wave_max_f32(amax);
-    if (lane == 0) red_max[wid] = amax;
-    __syncthreads();
-    float a = red_max[0];
-    for (int w = 1; w < waves; ++w) a = fmaxf(a, red_max[w]);
+    const float a = row_max(amax, red_max);
     const float s = a / 127.0f;
     if (threadIdx.x == 0) scale[m] = s;
 

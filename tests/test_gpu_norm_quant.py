@@ -119,3 +119,17 @@ def test_many_tokens(torch, M, K, dtype, rot):
     x, h, g = inputs(M, K, dtype, seed=M + K)
     q, s, out = B.add_rmsnorm_quant_i8(C.put(torch, x, dtype), C.put(torch, g), C.put(torch, h, dtype), eps=1e-6, rotate=rot)
     check(q.cpu().numpy(), s.cpu().numpy(), C.host(out), x, h, g, 1e-6, dtype, rot)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,K", [(6, 640), (5, 8320), (1024, 4096)])
+def test_rows_whose_squares_leave_f32(torch, M, K, dtype):
+    # rows of about 2^63 and more (squares pass 2^128), and of 2^-75 and less without an eps to cover them
+    print("range", M, K, dtype, flush=True)
+    x, h, g = inputs(M, K, dtype, seed=K)
+    for size, eps in ((1e25, 1e-6), (1e30, 1e-6), (1e30, 1e30), (3e18, 1e-6), (1e-25, 0.0), (1e-30, 0.0), (1e-20, 1e-40),
+                      (1e-25, 1e-45), (1e-25, 1e-6)):
+        xs, hs = O.to_dtype(x * np.float32(size), dtype), O.to_dtype(h * np.float32(size), dtype)
+        xs[1], hs[1] = x[1], h[1]                              # an ordinary row among them
+        q, s, out = B.add_rmsnorm_quant_i8(C.put(torch, xs, dtype), C.put(torch, g), C.put(torch, hs, dtype), eps=eps)
+        check(q.cpu().numpy(), s.cpu().numpy(), C.host(out), xs, hs, g, float(np.float32(eps)), dtype, True)
