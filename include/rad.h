@@ -456,6 +456,8 @@ int rad_kv4_read(const rad_kv4_cache *cache, const rad_kv_batch *batch, uint16_t
  * such a product is off by no more than 2^-33 (f32), 2^-31 (f16) or 2^-28
  * (bf16) of the largest of its row and head that a wave met with it (a wave
  * takes a quarter of a part of the context).
+ * Where a row's scores pass 2^21 in magnitude, those within 2^-17 of its largest
+ * may count alike.
  */
 int rad_attn_kv4_workspace(const rad_kv4_cache *cache, const rad_kv_batch *batch, int64_t q_heads,
                            int32_t dtype, int64_t *bytes);

@@ -111,10 +111,25 @@ __device__ __forceinline__ void f16_split8(const float (&w)[8], u4 &hi, u4 &low)
 __device__ __forceinline__ float max8(const float (&s)[8]) {
     return fmaxf(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])), fmaxf(fmaxf(s[4], s[5]), fmaxf(s[6], s[7])));
 }
-// sm_scale log2(e) 2^-e, never 0 or infinite: a masked score stays -inf, a score of 0 stays 0.
+// sm_scale log2(e) 2^-e, never 0: a masked score stays -inf.  At most 2^90: products and key scales come to
+// less than 2^37, so no score is infinite, and at more than that any difference is far past exp's range.
 __device__ __forceinline__ float score_factor(float sm_scale, int e) {
-    return fminf(fmaxf(__builtin_amdgcn_ldexpf(sm_scale * kLog2e, -e), 1e-30f), 0x1p126f);
+    return fminf(fmaxf(__builtin_amdgcn_ldexpf(sm_scale * kLog2e, -e), 1e-30f), 0x1p90f);
 }
+// log2 of a power of two above a value's scale; scales of 0 weigh nothing, but count
+__device__ __forceinline__ float scale_log2(float vs) {
+    return vs > 0.0f ? static_cast<float>(__builtin_amdgcn_frexp_expf(vs)) : -24.0f;
+}
+// The reference exponent for a largest log2 weight `most`: never above most - room by rounding.
+template <int DT>
+__device__ __forceinline__ float reference(float m, float most) {
+    return fmaxf(m, fmaf(fabsf(most), -0x1p-22f, most - kRoom<DT>));
+}
+// Beyond kNear (the lowest, the mark of nothing seen, aside) f32 holds a reference to half a unit or worse, and with
+// it what the room leaves: there 2^(score - m) is held to 1, every step.  The vote's third compare and the minimum
+// cost 1% of a prompt (816 -> 824 us) and of short calls (9.69 -> 9.81 us).
+constexpr float kNear = 0x1p22f;
+__device__ __forceinline__ float most_power(float m) { return fabsf(m) > kNear && m > -0x1.8p127f ? 0.0f : INFINITY; }
 
 // Maximum (sum) over the four lanes that hold one column.
 __device__ __forceinline__ float col_max(float v) {
@@ -415,9 +430,10 @@ __device__ __forceinline__ void join_groups(const Out &out, float (&lds_o)[TG][T
 // blockIdx: x piece, y KV head.  A tile has 16 columns, `cols` of them in use at most.  Parts of a tile in several leave their sums in part_o [heads][slots][cols][D] and
 // part_ml [..][cols][2]; the others write the outputs.  ONCE: no other workgroup reads the
 // codes, so they are loaded nontemporally (200K tokens 50 -> 46 us; with several tiles of heads
-// of 256 4096 tokens take 246 us that way, 219 us without).
+// of 256 4096 tokens take 246 us that way, 219 us without).  Three waves a SIMD where 168 registers do for
+// them (64 sequences 98 us, 102 us with two).
 template <int DT, int D, int HL, bool ONCE>
-__global__ __launch_bounds__(256, 2) void attn_kernel(Kv4Cache c, KvBatch b, Kv4Attn a, Plan pl, int cols,
+__global__ __launch_bounds__(256, D == 128 && HL != 2 ? 3 : 2) void attn_kernel(Kv4Cache c, KvBatch b, Kv4Attn a, Plan pl, int cols,
                                                       float *part_o, float *part_ml) {
     constexpr int TG = kWaves, TM = 16, NK = D / 32;
     __shared__ float lds_o[TG][TM][D + 4], lds_ml[TG][TM][2];
@@ -525,22 +541,23 @@ __global__ __launch_bounds__(256, 2) void attn_kernel(Kv4Cache c, KvBatch b, Kv4
             sum += p;
             w[i] = times_half(p, cur.vs, i);
         }
-        if (__any(!(max8(w) <= kMost && sum <= kMostP))) {         // also the first step: m is the lowest
+        if (__any(!(max8(w) <= kMost && sum <= kMostP && fabsf(m) <= kNear))) {         // also the first step: m is the lowest
             float most = -INFINITY;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float vs = times_half(1.0f, cur.vs, i);
-                most = fmaxf(most, fmaf(s[i], scale, vs > 0.0f ? static_cast<float>(__builtin_amdgcn_frexp_expf(vs)) : -24.0f));
+                most = fmaxf(most, fmaf(s[i], scale, scale_log2(vs)));
             }
-            const float mn = fmaxf(m, col_max(most) - kRoom<DT>), shrink = __builtin_amdgcn_exp2f(m - mn);
+            const float mn = reference<DT>(m, col_max(most)), shrink = __builtin_amdgcn_exp2f(m - mn);
             m = mn;
             l *= shrink;
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) acc[j] *= shrink;
+            const float top = most_power(m);
             sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float p = __builtin_amdgcn_exp2f(fmaf(s[i], scale, -m));
+                const float p = __builtin_amdgcn_exp2f(fminf(fmaf(s[i], scale, -m), top));
                 sum += p;
                 w[i] = times_half(p, cur.vs, i);
             }
@@ -765,23 +782,24 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(Kv4Cache c, KvBatch b
             sum += p;
             w[i] = times_half(p, cur.vs[i >> 3], i & 7);
         }
-        if (__any(!(max16(w) <= kMost && sum <= kMostP))) {                        // also the first step: m is the lowest
+        if (__any(!(max16(w) <= kMost && sum <= kMostP && fabsf(m) <= kNear))) {                        // also the first step: m is the lowest
             float most = -INFINITY;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const float vs = times_half(1.0f, cur.vs[i >> 3], i & 7);
-                most = fmaxf(most, fmaf(s[i], scale, vs > 0.0f ? static_cast<float>(__builtin_amdgcn_frexp_expf(vs)) : -24.0f));
+                most = fmaxf(most, fmaf(s[i], scale, scale_log2(vs)));
             }
             most = fmaxf(most, __shfl_xor(most, 32));
-            const float mn = fmaxf(m, most - kRoom<DT>), shrink = __builtin_amdgcn_exp2f(m - mn);
+            const float mn = reference<DT>(m, most), shrink = __builtin_amdgcn_exp2f(m - mn);
             m = mn;
             l *= shrink;
 #pragma unroll
             for (int x = 0; x < ND; ++x) acc[x] *= shrink;
+            const float top = most_power(m);
             sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const float p = __builtin_amdgcn_exp2f(fmaf(s[i], scale, -m));
+                const float p = __builtin_amdgcn_exp2f(fminf(fmaf(s[i], scale, -m), top));
                 sum += p;
                 w[i] = times_half(p, cur.vs[i >> 3], i & 7);
             }

@@ -416,3 +416,34 @@ def test_rows_past_max_q_of_a_cut_context(torch):
     want, mass, reach = O.attention(q, ref, table, np.array([n]), C.ragged([rows]), 0.1, True, 0)
     assert np.all(got[7:] == 5)
     assert np.all(np.abs(got - want)[:7] <= C.attention_tolerance("f32", want, mass, reach, n)[:7])
+
+
+@pytest.mark.parametrize("dtype,q_size,sm", [("f32", 1e36, 1.0), ("f32", 1e30, 2.0 ** 60), ("bf16", 1e37, 0.5), ("f32", 1.0, 2.0 ** 126),
+                                             ("f16", 3.0, 2.0 ** 126), ("f32", 1e-30, 2.0 ** 126), ("bf16", 1e20, 1e20)])
+@pytest.mark.parametrize("n,ctx", [(1, 60), (12, 60), (40, 1100)])
+def test_scores_past_f32(torch, n, ctx, dtype, q_size, sm):
+    """Scores of more than 2^128: all of a row goes to its largest score, wherever that is ahead of the next by more
+    than the products' rounding (2^-14 of the largest sum of magnitudes, far more than they lose).  Its weight, 1, is held
+    in two f16 parts (2^-21) or one (2^-11), the quotient and the output round."""
+    rng = np.random.default_rng(n)
+    H, G, D, page, total = 1, 1, 64, 32, n + ctx
+    ref = O.Cache((total + page - 1) // page, H, page, D, rng)
+    table = rng.permutation(ref.pages).astype(np.int32)[None]
+    C.fill_cache(rng, ref, table, [total])
+    q = O.to_dtype(q_size * rng.standard_normal((n, H * G, D)), dtype)
+    got = C.host(B.attn_kv4(C.device_cache(torch, ref), C.device_batch(torch, table, [total], C.ragged([n]), n),
+                            C.put(torch, q, dtype), sm))
+    K, V, _ = O.tokens_of(ref, table[0], total)
+    clear = 0
+    for i in range(n):
+        k, v = K[:ctx + i + 1, 0], V[:ctx + i + 1, 0]
+        score = k @ q[i, 0].astype(np.float64)
+        first, second = np.argsort(score)[[-1, -2]]
+        reach = np.max(np.abs(k) @ np.abs(q[i, 0].astype(np.float64)))
+        if score[first] - score[second] < 2.0 ** -13 * reach or (score[first] - score[second]) * sm < 1000:
+            continue
+        clear += 1
+        want = v[first]
+        assert np.all(np.abs(got[i, 0] - want) <= np.abs(want) * ((2.0 ** -21 if dtype == "f32" else 2.0 ** -11) + 2.0 ** -22 + O.EPS[dtype] / 2)
+                      + 2.0 ** -25), i
+    assert clear >= (n + 1) // 2
