@@ -5,13 +5,14 @@
 // maximum; k and v are level * scale.
 //
 // Few query rows leave it to the memory: the cache is read once, as it lies.  199999
-// tokens (one f32 row, 40 query and 8 KV heads of 128; 211 MB) take 38 us and 5.4 us for
+// tokens (one f32 row, 40 query and 8 KV heads of 128; 211 MB) take 39 us and 4.6 us for
 // the join, 4.9 TB/s in all; 64 bf16 sequences of up to 16000 tokens (506 MB) 89 + 5 us,
 // 5.4 TB/s, where a read-only stream reaches 5.8.  Many rows are bound by a SIMD's issue
 // of vector and matrix instructions, which overlap little: an 8192-token prompt (687
-// GFLOP, bf16) takes 0.82 ms, 0.84 PFLOP/s, where a library product of this size reaches
-// 1.2; 63% of its cycles issue vector instructions (codes to f16 and exponents first) and
-// 35% keep the matrix cores busy.  8 x 16 draft rows over 8192 tokens take 29 + 6 us.
+// GFLOP, bf16) takes 0.81 to 0.84 ms, 0.82 to 0.85 PFLOP/s, where a library product of
+// this size reaches 1.2; 77% of a SIMD's cycles issue vector instructions (codes to f16 and
+// exponents first) and 37% keep the matrix cores busy.  8 x 16 draft rows over 8192
+// tokens take 29 + 6 us.
 #include "kv4.h"
 
 namespace rad {

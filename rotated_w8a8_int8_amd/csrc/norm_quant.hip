@@ -11,11 +11,12 @@
 //
 // A workgroup holds one token, each wave four 128-blocks a step (the lane layout
 // of rotate_quant.h), NITER steps.  8192 tokens of 5120 f32 values with a residual
-// take 93 us, 5.9 TB/s of the 545 MB it has to move (a read-only stream reaches 5.8,
-// a copy 4.9); nontemporal accesses are no faster here and leave the codes out of the
-// caches for the contraction (the call and a pass over its codes 203 us, 210 us with
-// them).  128 bf16 tokens take 4.1 us and one f32 token 3.8 us: the launch, a trip to
-// memory and the two reductions.
+// take 93 to 94 us for the 545 MB that it reads and writes, 5.8 TB/s, where a copy that
+// moves as much reaches 5.3, one of 4 GB 4.9 and a read-only stream 5.8.  Nontemporal
+// accesses are no faster here and leave the codes out of the caches for the contraction
+// (the call and a pass over its codes 203 us, 210 us with them).  128 bf16 tokens take
+// 4.1 us and one f32 token 3.8 us: the launch, a trip to memory and the two reductions.
+// A row whose squares leave f32's range takes two reductions more.
 #include "layer_launch.h"
 #include "rotate_quant.h"
 #include "value_types.h"
