@@ -10,7 +10,7 @@ the library's entry points:
            the drafted tokens that it sees.
   weights  causal attention, and for each token and KV head w = factor * w + the probabilities that the last `observe`
            rows (0: every row) of its sequence gave it, summed over the query heads of the group; the call's own tokens
-           begin at 0.
+           begin at 0, a sequence without rows keeps its weights.
   evict    of each sequence and KV head the `budget` tokens of greatest weight, the first `first` and the last `recent`
            ones always among them, in their order, to pages of their own; returned with the cached values as they are
            read back.
@@ -303,7 +303,8 @@ def _run_weights(s):
     counts = (i < new[:, None]) & ((i >= new[:, None] - c["observe"]) if c["observe"] else (i >= 0))
     given = torch.matmul(counts.float()[:, None, None, None], p).sum(dim=2)[:, :, 0]   # [B][H][L]
     old = torch.where(t < base[:, None, None], c["factor"] * s["weight"], 0) if c["factor"] else 0
-    s["weight"].copy_(torch.where(t < s["seq_len"][:, None, None], old + given, s["weight"]))
+    changed = (t < s["seq_len"][:, None, None]) & (new > 0)[:, None, None]
+    s["weight"].copy_(torch.where(changed, old + given, s["weight"]))
     return _rows(s, o), s["weight"]
 
 
@@ -508,11 +509,11 @@ def _exact_attn(s, c):
     for b, L in enumerate(s["len"]):
         n = start[b + 1] - start[b]
         base, t = L - n, torch.arange(L, device=DEV)
+        if n == 0:
+            continue
         if c["op"] == "weights":
             weight[b, :, :base] *= c["factor"]
             weight[b, :, base:L] = 0
-        if n == 0:
-            continue
         q = s["q"][start[b]:start[b + 1]].double().view(n, H, G, D)
         if c["op"] == "tree":
             bits = s["mask"][start[b]:start[b + 1]].tolist()
