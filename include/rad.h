@@ -466,6 +466,162 @@ int rad_attn_kv4(const rad_kv4_cache *cache, const rad_kv_batch *batch, const vo
                  int64_t workspace_bytes, int32_t dtype, rad_stream_t stream);
 
 /*
+ * rad_kv4_append_at -- rad_kv4_append with the rotary position of each row given apart from its
+ * place in the cache: for drafted trees, whose siblings share a position, and for sequences that
+ * have lost tokens to eviction.
+ *
+ *   position  int32 [rows], 4-byte aligned, read on the device: row r takes the angles of
+ *             position[r]; a row whose position lies outside 0 .. rope->rows - 1 is skipped.
+ *             NULL: each row's place in the cache, as rad_kv4_append.  Without rope unused.
+ */
+int rad_kv4_append_at(const rad_kv4_cache *cache, const rad_kv_batch *batch, const void *k, int64_t ldk,
+                      const void *v, int64_t ldv, const void *q, int64_t ldq, int64_t q_heads, void *q_out,
+                      const rad_rope *rope, const int32_t *position, int rotate, int32_t dtype,
+                      rad_stream_t stream);
+
+/*
+ * rad_attn_kv4_tree -- rad_attn_kv4 for drafted tokens that form a tree (or any other pattern):
+ * a sequence's rows are its last tokens, nodes 0 .. n - 1 at tokens base .. base + n - 1 (base =
+ * seq_len - n).  Row i sees the tokens before base, and token base + j where bit j of its mask is
+ * set (bit j % 64 of word j / 64; an ancestor's and its own, for a tree).
+ *
+ *   mask    uint64 [rows][words], 8-byte aligned.  Bits from n on are not looked at; nodes
+ *           from 64 * words on are not seen.
+ *   words   1 .. RAD_TREE_MAX_WORDS.
+ *   window  > 0: of the tokens before base only those t >= base + c - window, c being the nodes
+ *           that the row sees (a chain no longer than the window gets what rad_attn_kv4 gives).
+ *
+ * Everything else, the workspace among it, as for rad_attn_kv4.  A row that sees no token, or
+ * whose own token would lie before token 0, becomes zeros.
+ */
+#define RAD_TREE_MAX_WORDS 64
+int rad_attn_kv4_tree(const rad_kv4_cache *cache, const rad_kv_batch *batch, const void *q, int64_t q_heads,
+                      float sm_scale, const uint64_t *mask, int64_t words, int64_t window, void *o,
+                      void *workspace, int64_t workspace_bytes, int32_t dtype, rad_stream_t stream);
+
+/*
+ * rad_attn_kv4_weights -- rad_attn_kv4, and the attention weight that each cached token got: for
+ * token t of sequence b and KV head h
+ *
+ *   weight[b][h][t] = factor * weight[b][h][t] + sum of the probabilities that the observed rows
+ *                     of the sequence gave t, over the query heads of h's group.
+ *
+ *   weight   f32 [B][heads][ldw], 16-byte aligned, ldw a multiple of 4 and at least
+ *            max_pages * page_size.  The call's own tokens (those of the sequence's rows) begin
+ *            at 0, whatever is held there.  A token on an absent page gets factor * weight.
+ *            Entries from the sequence's length on, and those of a sequence without rows, are
+ *            left as they were.
+ *   observe  > 0: only the last `observe` rows of each sequence count; 0: every row.
+ *   factor   finite, >= 0; with 0 the entries are not read.
+ *   workspace, workspace_bytes  as for rad_attn_kv4, of the size that
+ *            rad_attn_kv4_weights_workspace gives.
+ *
+ * Rows past max_q count for nothing.  Sums are held in f32, in an unspecified but fixed order.
+ */
+int rad_attn_kv4_weights_workspace(const rad_kv4_cache *cache, const rad_kv_batch *batch, int64_t q_heads,
+                                   int32_t dtype, int64_t *bytes);
+int rad_attn_kv4_weights(const rad_kv4_cache *cache, const rad_kv_batch *batch, const void *q, int64_t q_heads,
+                         float sm_scale, int causal, int64_t window, void *o, float *weight, int64_t ldw,
+                         int64_t observe, float factor, void *workspace, int64_t workspace_bytes,
+                         int32_t dtype, rad_stream_t stream);
+
+/*
+ * rad_kv4_select -- which tokens of each sequence and KV head to keep: the `budget` of greatest
+ * weight, the first `first` and the last `recent` of the sequence always among them.
+ *
+ *   weight       f32 [B][heads][ldw], 16-byte aligned (from rad_attn_kv4_weights, say); ldw a
+ *                multiple of 4, at least max_tokens.
+ *   seq_len      int32 [B], 4-byte aligned, read on the device as clamped to 0 .. max_tokens.
+ *   budget       >= 1, at least first + recent, below 2^30; first, recent >= 0.
+ *   kept         int32 [B][heads][budget] output, 4-byte aligned: the tokens kept, ascending.  Of
+ *                equal weights the lower token is kept; a NaN is below every other weight.
+ *   count        int32 [B] output, 4-byte aligned: min(seq_len, budget), the entries of kept
+ *                that are written; those behind are left as they were.
+ *   kept_weight  f32 [B][heads][ld_kept] output, 16-byte aligned, or NULL: the weights of the
+ *                kept tokens, in their order; ld_kept a multiple of 4, at least budget.
+ *   workspace    device memory, 16-byte aligned, of at least the bytes that
+ *                rad_kv4_select_workspace gives (NULL when that is 0).
+ *
+ * B, heads, max_tokens >= 0; B < 2^22, heads <= 1024, max_tokens < 2^30, B * heads < 2^22.  No
+ * output may overlap another argument.
+ */
+int rad_kv4_select_workspace(int64_t B, int64_t heads, int64_t max_tokens, int64_t *bytes);
+int rad_kv4_select(const float *weight, int64_t ldw, const int32_t *seq_len, int64_t B, int64_t heads,
+                   int64_t max_tokens, int64_t budget, int64_t first, int64_t recent, int32_t *kept,
+                   int32_t *count, float *kept_weight, int64_t ld_kept, void *workspace,
+                   int64_t workspace_bytes, rad_stream_t stream);
+
+/*
+ * rad_kv4_move -- cached tokens (codes and scales) to other places: entry i of a sequence's list
+ * goes from token from[i] of the sequence to token to_start + i of its target pages.
+ *
+ *   cache, batch  where the tokens are; of the batch B, max_pages, block_table and seq_len count.
+ *   from          int32 [B][lists][entries], 4-byte aligned; lists is 1 (every head's tokens move
+ *                 alike) or cache->heads (rad_kv4_select's kept).  An entry outside 0 .. seq_len -
+ *                 1, or on an absent page, moves nothing: its target is left as it was.
+ *   count         int32 [B], 4-byte aligned: entries of each list that are looked at (read as
+ *                 clamped to 0 .. entries).
+ *   to            cache that takes the tokens, of the same heads and D; NULL: `cache` itself.
+ *   to_table      int32 [B][to_pages], 4-byte aligned: the target pages of each sequence; an
+ *                 absent page takes nothing, as no page takes what lies past the table.  NULL (to
+ *                 and to_pages then NULL and 0): in place, over the sequence's own pages.
+ *   to_start      int32 [B], 4-byte aligned, or NULL (0).  Negative targets take nothing.
+ *
+ * In place every token is read before the first is written, and entries is at most
+ * RAD_KV4_MOVE_MAX (an accepted path; longer lists go to pages of their own).  Otherwise no
+ * target page may be one that the call reads, and never may two lists of a call write the
+ * same page.  Only the targets' codes and scales change.  B * heads < 2^22, entries < 2^30.
+ */
+#define RAD_KV4_MOVE_MAX 256
+int rad_kv4_move(const rad_kv4_cache *cache, const rad_kv_batch *batch, const int32_t *from, int64_t lists,
+                 int64_t entries, const int32_t *count, const rad_kv4_cache *to, const int32_t *to_table,
+                 int64_t to_pages, const int32_t *to_start, rad_stream_t stream);
+
+/*
+ * rad_linear_attn -- linear attention with a decay for each head, over a ragged batch (model card
+ * "Qwen3.8-27B IQ8R + DFlash2 -- radiance container", section "How this file was made", lists
+ * linears of layers that mix tokens by a state, ssm_inz and ssm_out, beside those of attention;
+ * the card does not give their mixer: this is the form with one decay a head).  Row by row of a
+ * sequence, for value head h, with the query and key of head h / (heads / qk_heads):
+ *
+ *   S = exp(log_decay[h]) * S + k v^T        (S [D][D], f32: first index the key's)
+ *   o = scale * S^T q
+ *
+ *   q, k       [rows][qk_heads][D] of `dtype`, rows ldq and ldk values apart (>= qk_heads * D).
+ *   v          [rows][heads][D] of `dtype`, rows ldv apart; 16-byte aligned, as are q and k and
+ *              each of their rows.
+ *   o          [rows][heads][D] of `dtype`, dense, 16-byte aligned.
+ *   log_decay  f32 [heads], 4-byte aligned, at most 0 (-inf: nothing is kept).
+ *   state      f32 [B][heads][D][D], 16-byte aligned: the state before the first row; NULL: zeros.
+ *   state_out  the state after the last row, as `state`, which it may be (in place); NULL: not
+ *              kept (a drafted block is verified so, and run again with the rows accepted).  A
+ *              sequence without rows keeps its state.
+ *   q_start    int32 [B + 1], ascending, 4-byte aligned, read on the device: rows q_start[b] ..
+ *              q_start[b + 1] - 1 are sequence b's; rows from q_start[B] on are padding and
+ *              left as they were.  NULL: one row a sequence (rows == B).
+ *   max_q      no sequence has more rows than this (1 when q_start is NULL); one that has more
+ *              is taken as ending after max_q rows.
+ *   workspace  device memory, 16-byte aligned, of at least the bytes that
+ *              rad_linear_attn_workspace gives for the same sizes (NULL when that is 0).
+ *
+ * D is 64, 128 or 256; heads a multiple of qk_heads, at most 1024; B, rows < 2^22; B * heads < 2^22.
+ * scale is finite.  The state and all sums are held in f32; RAD_DT_F32 values are
+ * multiplied in f32.  For the 16-bit types the weights of the rows of a chunk and the state meet the
+ * matrix cores as pairs of 16-bit parts (16 bits at least).
+ */
+typedef struct rad_linear {
+    const void *q, *k, *v;
+    int64_t ldq, ldk, ldv;
+    const float *log_decay;
+    const int32_t *q_start;
+    int64_t B, rows, max_q, qk_heads, heads, D;
+    int32_t dtype;
+} rad_linear;
+int rad_linear_attn_workspace(const rad_linear *in, int64_t *bytes);
+int rad_linear_attn(const rad_linear *in, const float *state, float *state_out, float scale, void *o,
+                    void *workspace, int64_t workspace_bytes, rad_stream_t stream);
+
+/*
  * rad_probe_mfma_i8 -- a measurement aid, not a step of the layer: what the
  * int8 matrix cores sustain on given operand bytes.  Its callers are
  * benchmarks that price a contraction against the rate the chip reaches on

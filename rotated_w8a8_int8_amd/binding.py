@@ -40,9 +40,13 @@ RAD_PROBE_MAX_KSTEPS = 1073741824
 EXPORTS = ("rad_fwht128", "rad_quant_act_i8", "rad_w8a8_gemv", "rad_w8a8_gemm", "rad_w8a8_linear",
            "rad_quant_weight_i8", "rad_kv_quant_i8", "rad_kv_dequant_i8", "rad_w8a8_rescore",
            "rad_add_rmsnorm_quant_i8", "rad_kv4_append", "rad_kv4_read", "rad_attn_kv4_workspace",
-           "rad_attn_kv4", "rad_probe_mfma_i8", "rad_strerror")
+           "rad_attn_kv4", "rad_kv4_append_at", "rad_attn_kv4_tree", "rad_attn_kv4_weights_workspace",
+           "rad_attn_kv4_weights", "rad_kv4_select_workspace", "rad_kv4_select", "rad_kv4_move",
+           "rad_linear_attn_workspace", "rad_linear_attn", "rad_probe_mfma_i8", "rad_strerror")
 KV_HEAD_DIMS = (64, 128, 256)
 KV4_PAGE_SIZES = (32, 64, 128, 256)
+RAD_TREE_MAX_WORDS = 64
+RAD_KV4_MOVE_MAX = 256
 # enum rad_dtype
 RAD_DT_F32 = 0
 RAD_DT_BF16 = 1
@@ -104,6 +108,27 @@ class RopeDesc(ctypes.Structure):
     ]
 
 
+class LinearDesc(ctypes.Structure):
+    """struct rad_linear."""
+    _fields_ = [
+        ("q", ctypes.c_void_p),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("ldq", ctypes.c_int64),
+        ("ldk", ctypes.c_int64),
+        ("ldv", ctypes.c_int64),
+        ("log_decay", ctypes.c_void_p),
+        ("q_start", ctypes.c_void_p),
+        ("B", ctypes.c_int64),
+        ("rows", ctypes.c_int64),
+        ("max_q", ctypes.c_int64),
+        ("qk_heads", ctypes.c_int64),
+        ("heads", ctypes.c_int64),
+        ("D", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+    ]
+
+
 _lib = None
 
 
@@ -132,10 +157,25 @@ def lib() -> ctypes.CDLL:
         L.rad_kv4_read.argtypes = [cache, batch, vp, vp, vp]
         L.rad_attn_kv4_workspace.argtypes = [cache, batch, i64, i32, ctypes.POINTER(i64)]
         L.rad_attn_kv4.argtypes = [cache, batch, vp, i64, f32, ci, i64, vp, vp, i64, i32, vp]
+        pi64 = ctypes.POINTER(i64)
+        L.rad_kv4_append_at.argtypes = [cache, batch, vp, i64, vp, i64, vp, i64, i64, vp, ctypes.POINTER(RopeDesc), vp,
+                                        ci, i32, vp]
+        L.rad_attn_kv4_tree.argtypes = [cache, batch, vp, i64, f32, vp, i64, i64, vp, vp, i64, i32, vp]
+        L.rad_attn_kv4_weights_workspace.argtypes = [cache, batch, i64, i32, pi64]
+        L.rad_attn_kv4_weights.argtypes = [cache, batch, vp, i64, f32, ci, i64, vp, vp, i64, i64, f32, vp, i64, i32, vp]
+        L.rad_kv4_select_workspace.argtypes = [i64, i64, i64, pi64]
+        L.rad_kv4_select.argtypes = [vp, i64, vp, i64, i64, i64, i64, i64, i64, vp, vp, vp, i64, vp, i64, vp]
+        L.rad_kv4_move.argtypes = [cache, batch, vp, i64, i64, vp, cache, vp, i64, vp, vp]
+        linear = ctypes.POINTER(LinearDesc)
+        L.rad_linear_attn_workspace.argtypes = [linear, pi64]
+        L.rad_linear_attn.argtypes = [linear, vp, vp, f32, vp, vp, i64, vp]
         for f in (L.rad_fwht128, L.rad_quant_act_i8, L.rad_w8a8_gemv, L.rad_w8a8_gemm,
                   L.rad_w8a8_linear, L.rad_quant_weight_i8, L.rad_kv_quant_i8, L.rad_kv_dequant_i8,
                   L.rad_w8a8_rescore, L.rad_probe_mfma_i8, L.rad_add_rmsnorm_quant_i8, L.rad_kv4_append,
-                  L.rad_kv4_read, L.rad_attn_kv4_workspace, L.rad_attn_kv4):
+                  L.rad_kv4_read, L.rad_attn_kv4_workspace, L.rad_attn_kv4, L.rad_kv4_append_at,
+                  L.rad_attn_kv4_tree, L.rad_attn_kv4_weights_workspace, L.rad_attn_kv4_weights,
+                  L.rad_kv4_select_workspace, L.rad_kv4_select, L.rad_kv4_move, L.rad_linear_attn_workspace,
+                  L.rad_linear_attn):
             f.restype = ci
         L.rad_strerror.argtypes = [ci]
         L.rad_strerror.restype = ctypes.c_char_p
@@ -602,6 +642,11 @@ class KVBatch:
 
 def _head_rows(t, dtype, rows, heads, D, ref, name):
     """[rows][heads][D] values whose token rows may lie apart: address and distance in values."""
+    return _rows_apart(t, dtype, (rows, heads, D), ref.device_index, name)
+
+
+def _rows_apart(t, dtype, shape, index, name):
+    rows, heads, D = shape
     if not isinstance(t, _torch().Tensor) or t.dtype != dtype:
         _values(t, name)
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
@@ -610,8 +655,8 @@ def _head_rows(t, dtype, rows, heads, D, ref, name):
     apart, head, one = t.stride()
     if one != 1 or (head != D and heads > 1):
         raise ValueError("%s must be contiguous in its last two dims" % name)
-    if not t.is_cuda or t.get_device() != ref.device_index:
-        raise ValueError("%s is on %s, the cache on GPU %d" % (name, t.device, ref.device_index))
+    if not t.is_cuda or t.get_device() != index:
+        raise ValueError("%s is on %s, expected GPU %d" % (name, t.device, index))
     return t.data_ptr(), apart if rows > 1 else heads * D
 
 
@@ -621,10 +666,11 @@ def _one_device(cache, batch):
 
 
 def kv4_append(cache: KV4Cache, batch: KVBatch, k, v, q=None, rope=None, rope_style: int = 0, rotate: bool = True,
-               q_out=None):
+               q_out=None, position=None):
     """Append ``k`` and ``v`` [rows][heads][D] to the cache at their positions, turned by ``rope`` (f32
     [positions][dim]: dim/2 cosines, then dim/2 sines) and rotated per 128; returns the queries ``q``
-    [rows][q_heads][D] turned alike (q.k kept), or None."""
+    [rows][q_heads][D] turned alike (q.k kept), or None.  ``position`` int32 [rows]: the row of ``rope`` for each
+    row, where it is not its place in the cache (drafted trees, sequences that have lost tokens)."""
     torch = _torch()
     rows, H, D = batch.rows, cache.heads, cache.D
     _one_device(cache, batch)
@@ -646,8 +692,13 @@ def kv4_append(cache: KV4Cache, batch: KVBatch, k, v, q=None, rope=None, rope_st
             raise ValueError("rope must be a 2-D tensor")
         table = RopeDesc(_ptr(rope, torch.float32, rope.shape, cache.k_codes, "rope"), rope.shape[0], rope.shape[1],
                          rope_style)
-    _enqueue("rad_kv4_append", cache.device_index, lib().rad_kv4_append, cache._desc, batch._desc, kp, ldk, vp, ldv,
-             qp, ldq, q_heads, op, table, 1 if rotate else 0, dt)
+    if position is None:
+        _enqueue("rad_kv4_append", cache.device_index, lib().rad_kv4_append, cache._desc, batch._desc, kp, ldk, vp, ldv,
+                 qp, ldq, q_heads, op, table, 1 if rotate else 0, dt)
+    else:
+        pp = _ptr(position, torch.int32, (rows,), cache.k_codes, "position")
+        _enqueue("rad_kv4_append_at", cache.device_index, lib().rad_kv4_append_at, cache._desc, batch._desc, kp, ldk,
+                 vp, ldv, qp, ldq, q_heads, op, table, pp, 1 if rotate else 0, dt)
     return q_out
 
 
@@ -666,21 +717,39 @@ def kv4_read(cache: KV4Cache, batch: KVBatch, k=None, v=None):
     return k, v
 
 
-def attn_kv4_workspace(cache: KV4Cache, batch: KVBatch, q_heads: int, dtype) -> int:
-    """Bytes of workspace that attn_kv4 needs for these sizes."""
-    key = (cache.heads, cache.page_size, cache.D, q_heads, dtype)
+def _workspace_bytes(name, cache, batch, q_heads, dtype):
+    """Bytes that an attention call needs for these sizes, asked for once a batch."""
+    key = (name, cache.heads, cache.page_size, cache.D, q_heads, dtype)
     if key not in batch._workspace:
         n = ctypes.c_int64(0)
-        _check(lib().rad_attn_kv4_workspace(cache._desc, batch._desc, q_heads, _dtypes()[dtype], ctypes.byref(n)),
-               "rad_attn_kv4_workspace")
+        _check(getattr(lib(), name)(cache._desc, batch._desc, q_heads, _dtypes()[dtype], ctypes.byref(n)), name)
         batch._workspace[key] = n.value
     return batch._workspace[key]
 
 
-def attn_kv4(cache: KV4Cache, batch: KVBatch, q, sm_scale: float, causal: bool = True, window: int = 0, o=None,
-             workspace=None):
-    """Attention of ``q`` [rows][q_heads][D] over the paged 4-bit cache; rows that see nothing give zeros."""
+def _workspace(workspace, n, ref):
+    """Address and bytes of a call's workspace, made here where the caller has none, and the tensor itself."""
     torch = _torch()
+    if workspace is not None:
+        return _ptr(workspace, torch.uint8, workspace.shape, ref, "workspace"), workspace.numel(), workspace
+    if not n:
+        return None, 0, None
+    workspace = torch.empty((n,), dtype=torch.uint8, device=ref.device)
+    return workspace.data_ptr(), n, workspace
+
+
+def attn_kv4_workspace(cache: KV4Cache, batch: KVBatch, q_heads: int, dtype) -> int:
+    """Bytes of workspace that attn_kv4 and attn_kv4_tree need for these sizes."""
+    return _workspace_bytes("rad_attn_kv4_workspace", cache, batch, q_heads, dtype)
+
+
+def attn_kv4_weights_workspace(cache: KV4Cache, batch: KVBatch, q_heads: int, dtype) -> int:
+    """Bytes of workspace that attn_kv4_weights needs for these sizes."""
+    return _workspace_bytes("rad_attn_kv4_weights_workspace", cache, batch, q_heads, dtype)
+
+
+def _queries(cache, batch, q, o):
+    """Checked queries and outputs of an attention call: dtype code, addresses, outputs."""
     dt = _values(q, "q")
     shape, dtype = q.shape, q.dtype
     if len(shape) != 3 or shape[0] != batch.rows or shape[2] != cache.D:
@@ -688,15 +757,162 @@ def attn_kv4(cache: KV4Cache, batch: KVBatch, q, sm_scale: float, causal: bool =
     _one_device(cache, batch)
     qp = _ptr(q, dtype, shape, cache.k_codes, "q")
     if o is None:
-        o = torch.empty_like(q)
-    op = _ptr(o, dtype, shape, cache.k_codes, "o")
-    n = attn_kv4_workspace(cache, batch, shape[1], dtype)
-    wp, size = None, 0
-    if workspace is not None:
-        wp, size = _ptr(workspace, torch.uint8, workspace.shape, cache.k_codes, "workspace"), workspace.numel()
-    elif n:
-        workspace = torch.empty((n,), dtype=torch.uint8, device=q.device)
-        wp, size = workspace.data_ptr(), n
-    _enqueue("rad_attn_kv4", cache.device_index, lib().rad_attn_kv4, cache._desc, batch._desc, qp, shape[1], sm_scale,
+        o = _torch().empty_like(q)
+    return dt, qp, _ptr(o, dtype, shape, cache.k_codes, "o"), o
+
+
+def attn_kv4(cache: KV4Cache, batch: KVBatch, q, sm_scale: float, causal: bool = True, window: int = 0, o=None,
+             workspace=None):
+    """Attention of ``q`` [rows][q_heads][D] over the paged 4-bit cache; rows that see nothing give zeros."""
+    dt, qp, op, o = _queries(cache, batch, q, o)
+    wp, size, workspace = _workspace(workspace, attn_kv4_workspace(cache, batch, q.shape[1], q.dtype), q)
+    _enqueue("rad_attn_kv4", cache.device_index, lib().rad_attn_kv4, cache._desc, batch._desc, qp, q.shape[1], sm_scale,
              1 if causal else 0, window, op, wp, size, dt)
     return o
+
+
+def attn_kv4_tree(cache: KV4Cache, batch: KVBatch, q, mask, sm_scale: float, window: int = 0, o=None, workspace=None):
+    """Attention for trees of drafted tokens, a sequence's rows being its last tokens: row i sees the tokens before
+    them, and drafted token j where bit j of its ``mask`` (int64 [rows][words], bit j % 64 of word j // 64) is
+    set."""
+    torch = _torch()
+    dt, qp, op, o = _queries(cache, batch, q, o)
+    words = mask.shape[1] if isinstance(mask, torch.Tensor) and mask.dim() == 2 else -1
+    mp = _ptr(mask, torch.int64, (batch.rows, words), cache.k_codes, "mask")
+    wp, size, workspace = _workspace(workspace, attn_kv4_workspace(cache, batch, q.shape[1], q.dtype), q)
+    _enqueue("rad_attn_kv4_tree", cache.device_index, lib().rad_attn_kv4_tree, cache._desc, batch._desc, qp, q.shape[1],
+             sm_scale, mp, words, window, op, wp, size, dt)
+    return o
+
+
+def _weight_rows(t, B, heads, tokens, ref, name):
+    """f32 [B][heads][tokens or more] on ref's GPU: address and values a head."""
+    torch = _torch()
+    n = t.shape[2] if isinstance(t, torch.Tensor) and t.dim() == 3 else -1
+    p = _ptr(t, torch.float32, (B, heads, n), ref, name)
+    if n < tokens:
+        raise ValueError("%s has room for %d tokens, %d are needed" % (name, n, tokens))
+    return p, n
+
+
+def attn_kv4_weights(cache: KV4Cache, batch: KVBatch, q, weight, sm_scale: float, causal: bool = True, window: int = 0,
+                     observe: int = 0, factor: float = 1.0, o=None, workspace=None):
+    """Attention, and ``weight`` f32 [B][heads][tokens] = ``factor`` * weight + the probabilities that the last
+    ``observe`` rows (0: every row) of each sequence gave each token, summed over the query heads of the group (the
+    call's own tokens begin at 0; tokens a multiple of 4, at least max_pages * page_size).  Returns (o, weight)."""
+    dt, qp, op, o = _queries(cache, batch, q, o)
+    B, max_pages = batch.block_table.shape
+    tp, ldw = _weight_rows(weight, B, cache.heads, max_pages * cache.page_size, cache.k_codes, "weight")
+    wp, size, workspace = _workspace(workspace, attn_kv4_weights_workspace(cache, batch, q.shape[1], q.dtype), q)
+    _enqueue("rad_attn_kv4_weights", cache.device_index, lib().rad_attn_kv4_weights, cache._desc, batch._desc, qp,
+             q.shape[1], sm_scale, 1 if causal else 0, window, op, tp, ldw, observe, factor, wp, size, dt)
+    return o, weight
+
+
+def kv4_select_workspace(B: int, heads: int, max_tokens: int) -> int:
+    """Bytes of workspace that kv4_select needs for these sizes."""
+    n = ctypes.c_int64(0)
+    _check(lib().rad_kv4_select_workspace(B, heads, max_tokens, ctypes.byref(n)), "rad_kv4_select_workspace")
+    return n.value
+
+
+def kv4_select(batch: KVBatch, weight, budget: int, first: int = 0, recent: int = 0, kept=None, count=None,
+               kept_weight=None, workspace=None):
+    """The ``budget`` tokens of greatest ``weight`` (f32 [B][heads][tokens]) of each of the batch's sequences and
+    heads, the first ``first`` and last ``recent`` always among them: ``kept`` int32 [B][heads][budget], ascending,
+    ``count`` int32 [B] of them, and their weights (f32 [B][heads][budget to the next multiple of 4 or more])."""
+    torch = _torch()
+    B, ref = batch.block_table.shape[0], batch.block_table
+    heads = weight.shape[1] if isinstance(weight, torch.Tensor) and weight.dim() == 3 else -1
+    tp, ldw = _weight_rows(weight, B, heads, 0, ref, "weight")
+    if kept is None:
+        kept = torch.empty((B, heads, budget), dtype=torch.int32, device=ref.device)
+    if count is None:
+        count = torch.empty((B,), dtype=torch.int32, device=ref.device)
+    if kept_weight is None:
+        kept_weight = torch.empty((B, heads, (budget + 3) // 4 * 4), dtype=torch.float32, device=ref.device)
+    kp = _ptr(kept, torch.int32, (B, heads, budget), ref, "kept")
+    cp = _ptr(count, torch.int32, (B,), ref, "count")
+    gp, ldk = _weight_rows(kept_weight, B, heads, budget, ref, "kept_weight")
+    key = ("rad_kv4_select", heads, ldw)
+    if key not in batch._workspace:
+        batch._workspace[key] = kv4_select_workspace(B, heads, ldw)
+    wp, size, workspace = _workspace(workspace, batch._workspace[key], weight)
+    _enqueue("rad_kv4_select", ref.get_device(), lib().rad_kv4_select, tp, ldw, batch.seq_len.data_ptr(), B, heads, ldw,
+             budget, first, recent, kp, cp, gp, ldk, wp, size)
+    return kept, count, kept_weight
+
+
+def kv4_move(cache: KV4Cache, batch: KVBatch, source, count, to: KV4Cache = None, to_table=None, to_start=None):
+    """Move cached tokens: entry i of ``source`` (int32 [B][entries], or [B][heads][entries] with a list a head), of
+    which ``count`` int32 [B] are looked at, goes to token ``to_start`` (int32 [B], default 0) + i of the pages
+    ``to_table`` int32 [B][pages] of ``to`` (default: the same cache).  Without ``to_table`` in place, at most
+    RAD_KV4_MOVE_MAX entries a list."""
+    torch = _torch()
+    _one_device(cache, batch)
+    B, ref = batch.block_table.shape[0], cache.k_codes
+    dims = source.dim() if isinstance(source, torch.Tensor) else 0
+    if dims not in (2, 3):
+        raise ValueError("source must be a 2-D or 3-D tensor")
+    entries = source.shape[-1]
+    fp = _ptr(source, torch.int32, (B, entries) if dims == 2 else (B, cache.heads, entries), ref, "source")
+    cp = _ptr(count, torch.int32, (B,), ref, "count")
+    tp, pages = None, 0
+    if to_table is not None:
+        pages = to_table.shape[1] if isinstance(to_table, torch.Tensor) and to_table.dim() == 2 else -1
+        tp = _ptr(to_table, torch.int32, (B, pages), ref, "to_table")
+    elif to is not None:
+        raise ValueError("another cache needs to_table")
+    if to is not None and to.device_index != cache.device_index:
+        raise ValueError("the target cache is on GPU %d, the cache on GPU %d" % (to.device_index, cache.device_index))
+    sp = None if to_start is None else _ptr(to_start, torch.int32, (B,), ref, "to_start")
+    _enqueue("rad_kv4_move", cache.device_index, lib().rad_kv4_move, cache._desc, batch._desc, fp,
+             1 if dims == 2 else cache.heads, entries, cp, None if to is None else to._desc, tp, pages, sp)
+
+
+_linear_bytes = {}                              # sizes of a call -> bytes of its workspace
+
+
+def linear_attn(q, k, v, log_decay, state=None, state_out=None, q_start=None, max_q=None, scale: float = 1.0, o=None,
+                workspace=None):
+    """Linear attention with a decay for each head: per row S = exp(log_decay[h]) * S + k v^T, o = scale * S^T q.
+
+    ``q``, ``k`` [rows][qk_heads][D] and ``v`` [rows][heads][D] (f32, bf16 or f16; token rows may lie apart),
+    ``log_decay`` f32 [heads], ``q_start`` int32 [B + 1] (None: one row a sequence), ``max_q``: no sequence has more
+    rows.  ``state`` f32 [B][heads][D][D] before the first row (None: zeros); ``state_out`` takes the state after the
+    last (the same tensor: in place; None: it is not kept).  Returns (o, state_out)."""
+    torch = _torch()
+    dt, dtype = _values(v, "v"), v.dtype
+    if v.dim() != 3 or not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q, k and v must be 3-D")
+    rows, heads, D = v.shape
+    qk_heads, index = q.shape[1], v.get_device()
+    vp, ldv = _rows_apart(v, dtype, (rows, heads, D), index, "v")
+    qp, ldq = _rows_apart(q, dtype, (rows, qk_heads, D), index, "q")
+    kp, ldk = _rows_apart(k, dtype, (rows, qk_heads, D), index, "k")
+    B = rows
+    sp = None
+    if q_start is not None:
+        if not isinstance(q_start, torch.Tensor) or q_start.dim() != 1 or q_start.shape[0] < 1:
+            raise ValueError("q_start must be a 1-D tensor")
+        B = q_start.shape[0] - 1
+        sp = _ptr(q_start, torch.int32, (B + 1,), v, "q_start")
+    gp = _ptr(log_decay, torch.float32, (heads,), v, "log_decay")
+    shape = (B, heads, D, D)
+    ip = None if state is None else _ptr(state, torch.float32, shape, v, "state")
+    np_ = None if state_out is None else _ptr(state_out, torch.float32, shape, v, "state_out")
+    if o is None:
+        o = torch.empty((rows, heads, D), dtype=dtype, device=v.device)
+    op = _ptr(o, dtype, (rows, heads, D), v, "o")
+    max_q = 1 if q_start is None else rows if max_q is None else int(max_q)
+    d = LinearDesc(qp, kp, vp, ldq, ldk, ldv, gp, sp, B, rows, max_q, qk_heads, heads, D, dt)
+    key = (B, rows, max_q, heads, D, dt, q_start is None)
+    if key not in _linear_bytes:
+        n = ctypes.c_int64(0)
+        _check(lib().rad_linear_attn_workspace(d, ctypes.byref(n)), "rad_linear_attn_workspace")
+        if len(_linear_bytes) > 4096:
+            _linear_bytes.clear()
+        _linear_bytes[key] = n.value
+    wp, size, workspace = _workspace(workspace, _linear_bytes[key], v)
+    _enqueue("rad_linear_attn", index, lib().rad_linear_attn, d, ip, np_, scale, op, wp, size)
+    return o, state_out

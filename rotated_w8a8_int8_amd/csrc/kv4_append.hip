@@ -125,6 +125,12 @@ __device__ __forceinline__ float head_max(float a) {
     return a;
 }
 
+// Row of the angle table for a row of the call at token t (AT: by its given position), and
+// whether the table has it.
+template <bool AT>
+__device__ __forceinline__ int angle_row(const Kv4New &nw, int64_t row, int t) { return AT ? nw.position[row] : t; }
+__device__ __forceinline__ bool has_angles(const Kv4New &nw, int at) { return !nw.rope || (at >= 0 && at < nw.rope_rows); }
+
 // One head vector v of a token (kind 0: query, 1: key, 2: value, head h of its kind), by D / 8
 // lanes: the turned query stored, or scale and keys' codes; returns the lane's eight codes.
 template <int DT, int D>
@@ -179,7 +185,7 @@ constexpr int kRunsApart = D == 64 ? 32 : 64;
 
 // One row per sequence: blockIdx.x the row, blockIdx.y 256 / L heads of it (queries, keys,
 // values), D / 8 lanes each.  A value's lane puts its eight codes into the octet's dwords itself.
-template <int DT, int D>
+template <int DT, int D, bool AT>
 __global__ __launch_bounds__(256) void kv4_append_one_kernel(Kv4Cache c, KvBatch b, Kv4New nw) {
     constexpr int L = D / 8;
     const int lane = threadIdx.x % L, row = blockIdx.x, hx = blockIdx.y * (256 / L) + threadIdx.x / L;
@@ -191,8 +197,8 @@ __global__ __launch_bounds__(256) void kv4_append_one_kernel(Kv4Cache c, KvBatch
     const int64_t base = row * (kind == 0 ? nw.ldq : kind == 1 ? nw.ldk : nw.ldv) + static_cast<int64_t>(h) * D;
     const void *src = kind == 0 ? nw.q : kind == 1 ? nw.k : nw.v;
     const Runs v{load4<DT>(src, base + d0), load4<DT>(src, base + d1)};
-    const int t = kv_len(b, row) - 1;
-    if (t < 0 || (nw.rope && t >= nw.rope_rows)) return;
+    const int t = kv_len(b, row) - 1, at = angle_row<AT>(nw, row, t);
+    if (t < 0 || !has_angles(nw, at)) return;
     const int page = kv_page(b, row, t, c.pages), off = t & ((1 << c.page_shift) - 1), sh = 4 * (t & 7);
     const bool merge = kind == 2 && page >= 0;
     uint4 *oct = nullptr, lo{}, hi{};
@@ -201,7 +207,7 @@ __global__ __launch_bounds__(256) void kv4_append_one_kernel(Kv4Cache c, KvBatch
         lo = oct[d0 >> 2];
         hi = oct[d1 >> 2];
     }
-    const Angles ang = nw.rope && kind < 2 ? angles<D>(nw.rope + static_cast<int64_t>(t) * nw.rope_dim, nw.rope_dim, nw.rope_style, d0, d1)
+    const Angles ang = nw.rope && kind < 2 ? angles<D>(nw.rope + static_cast<int64_t>(at) * nw.rope_dim, nw.rope_dim, nw.rope_style, d0, d1)
                                            : Angles{};
     const float sign = D % 128 == 0 && nw.rotate ? fwht_lane_sign(lane & 15) : 1.0f;
     const uint32_t w = append_head<DT, D>(c, nw, v, ang, kind, h, base, row, page, off, lane, d0, d1, sign);
@@ -218,10 +224,11 @@ __global__ __launch_bounds__(256) void kv4_append_one_kernel(Kv4Cache c, KvBatch
 // there; blockIdx.y: `span` groups of HPB heads of the q_heads + 2 * heads in the order
 // queries, keys, values.  A thread's token, and with it its angles, stays while the heads
 // go by, the next head's values being on their way.
-template <int DT, int D>
+template <int DT, int D, bool AT>
 __global__ __launch_bounds__(256) void kv4_append_kernel(Kv4Cache c, KvBatch b, Kv4New nw, int chunk, int span) {
     constexpr int L = D / 8, HPB = 32 / L;
     __shared__ uint32_t codes[HPB][8][L];                 // [head][token of the octet][lane]: 8 codes of a lane
+    __shared__ int live[AT ? 8 : 1];                      // tokens of the octet that are appended
     const int lane = threadIdx.x % L, tok = (threadIdx.x / L) % 8, hs = threadIdx.x / (8 * L);
     const int d0 = first_dim<D>(lane), d1 = d0 + kRunsApart<D>;
     const int H = c.heads, HQ = nw.q_heads, heads = HQ + 2 * H;
@@ -245,11 +252,13 @@ __global__ __launch_bounds__(256) void kv4_append_kernel(Kv4Cache c, KvBatch b, 
         for (; rr.first + (p - pos0) < seq_end; p = (p | 7) + 1) {
             const int octet = p >> 3;                         // tokens p .. min(last, 8 * octet + 7)
             const int t = octet * 8 + tok;
-            const bool here = t >= p && t <= last && (!nw.rope || t < nw.rope_rows);
             const int64_t trow = rr.first + (t - pos0);
+            const bool mine = t >= p && t <= last;
+            const int at = !AT || mine ? angle_row<AT>(nw, trow, t) : 0;
+            const bool here = mine && has_angles(nw, at);
             const int page = kv_page(b, seq, octet * 8, c.pages);
             const int off = (octet * 8) & ((1 << c.page_shift) - 1);
-            const Angles ang = here && nw.rope ? angles<D>(nw.rope + static_cast<int64_t>(t) * nw.rope_dim, nw.rope_dim, nw.rope_style, d0, d1)
+            const Angles ang = here && nw.rope ? angles<D>(nw.rope + static_cast<int64_t>(at) * nw.rope_dim, nw.rope_dim, nw.rope_style, d0, d1)
                                                : Angles{};
             auto base_of = [&](int hx) {
                 return hx < HQ ? trow * nw.ldq + static_cast<int64_t>(hx) * D
@@ -277,6 +286,7 @@ __global__ __launch_bounds__(256) void kv4_append_kernel(Kv4Cache c, KvBatch b, 
                 if ((hb + 1) * HPB <= HQ + H || page < 0) continue;   // no values among the workgroup's heads
                 __syncthreads();                              // the group before is read
                 if (kind == 2) codes[hs][tok][lane] = w;
+                if (AT && hs == 0 && lane == 0) live[tok] = here;
                 __syncthreads();
                 if (kind == 2) {
                     // one thread per dword: dimension d of head hs, the octet's eight tokens
@@ -287,7 +297,7 @@ __global__ __launch_bounds__(256) void kv4_append_kernel(Kv4Cache c, KvBatch b, 
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const int tj = octet * 8 + j;
-                        const bool on = tj >= p && tj <= last && (!nw.rope || tj < nw.rope_rows);
+                        const bool on = AT ? live[AT ? j : 0] : tj >= p && tj <= last && has_angles(nw, tj);
                         word |= ((codes[hs][j][ln] >> nib) & 15u) << (4 * j);
                         mask |= on ? 15u << (4 * j) : 0u;
                     }
@@ -301,12 +311,12 @@ __global__ __launch_bounds__(256) void kv4_append_kernel(Kv4Cache c, KvBatch b, 
     }
 }
 
-template <int DT, int D>
+template <int DT, int D, bool AT>
 hipError_t append_d(const Kv4Cache &c, const KvBatch &b, const Kv4New &n, hipStream_t st) {
     const int heads = n.q_heads + 2 * c.heads;
     if (!b.q_start) {
         const dim3 grid(b.rows, (heads * (D / 8) + 255) / 256);
-        hipLaunchKernelGGL((kv4_append_one_kernel<DT, D>), grid, dim3(256), 0, st, c, b, n);
+        hipLaunchKernelGGL((kv4_append_one_kernel<DT, D, AT>), grid, dim3(256), 0, st, c, b, n);
         return hipGetLastError();
     }
     // Rows a workgroup: an octet where sequences have that many, else as many as they have on
@@ -322,14 +332,20 @@ hipError_t append_d(const Kv4Cache &c, const KvBatch &b, const Kv4New &n, hipStr
     const int64_t all = static_cast<int64_t>((b.rows + chunk - 1) / chunk) * groups;
     const int span = static_cast<int>(all <= kFew ? 1 : all >= kSpan * kFew ? kSpan : all / kFew);
     const dim3 grid((b.rows + chunk - 1) / chunk, (groups + span - 1) / span);
-    hipLaunchKernelGGL((kv4_append_kernel<DT, D>), grid, dim3(256), 0, st, c, b, n, chunk, span);
+    hipLaunchKernelGGL((kv4_append_kernel<DT, D, AT>), grid, dim3(256), 0, st, c, b, n, chunk, span);
     return hipGetLastError();
 }
-template <int DT>
+template <int DT, bool AT>
 hipError_t append_t(const Kv4Cache &c, const KvBatch &b, const Kv4New &n, hipStream_t st) {
-    if (c.D == 64) return append_d<DT, 64>(c, b, n, st);
-    if (c.D == 128) return append_d<DT, 128>(c, b, n, st);
-    return append_d<DT, 256>(c, b, n, st);
+    if (c.D == 64) return append_d<DT, 64, AT>(c, b, n, st);
+    if (c.D == 128) return append_d<DT, 128, AT>(c, b, n, st);
+    return append_d<DT, 256, AT>(c, b, n, st);
+}
+template <bool AT>
+hipError_t append(const Kv4Cache &c, const KvBatch &b, const Kv4New &n, int dtype, hipStream_t st) {
+    if (dtype == kDtF32) return append_t<kDtF32, AT>(c, b, n, st);
+    if (dtype == kDtBf16) return append_t<kDtBf16, AT>(c, b, n, st);
+    return append_t<kDtF16, AT>(c, b, n, st);
 }
 
 // One (row, head) vector by D / 8 lanes, eight consecutive values each.
@@ -371,9 +387,7 @@ __global__ __launch_bounds__(256) void kv4_read_kernel(Kv4Cache c, KvBatch b, ui
 }  // namespace
 
 hipError_t launch_kv4_append(const Kv4Cache &c, const KvBatch &b, const Kv4New &n, int dtype, hipStream_t st) {
-    if (dtype == kDtF32) return append_t<kDtF32>(c, b, n, st);
-    if (dtype == kDtBf16) return append_t<kDtBf16>(c, b, n, st);
-    return append_t<kDtF16>(c, b, n, st);
+    return n.rope && n.position ? append<true>(c, b, n, dtype, st) : append<false>(c, b, n, dtype, st);
 }
 
 hipError_t launch_kv4_read(const Kv4Cache &c, const KvBatch &b, uint16_t *k, uint16_t *v, hipStream_t st) {

@@ -29,6 +29,7 @@ struct Kv4New {
     const float *rope;
     int64_t rope_rows;
     int rope_dim, rope_style, rotate;
+    const int32_t *position;     // angles of each row, or null: by its place in the cache
 };
 
 hipError_t launch_kv4_append(const Kv4Cache &c, const KvBatch &b, const Kv4New &n, int dtype, hipStream_t st);
@@ -41,9 +42,55 @@ struct Kv4Attn {
     float sm_scale;
     int causal, window;      // window 0: none
     void *workspace;
+    float2 *stats;           // [rows][q_heads]: reference exponent, 1 / normaliser (0: sees nothing); or null
+    const uint64_t *mask;    // trees: [rows][words]
+    int words;
 };
 bool kv4_attn_fits(const Kv4Cache &c, const KvBatch &b, int q_heads);     // one launch holds the call
 int64_t kv4_attn_workspace(const Kv4Cache &c, const KvBatch &b, int q_heads, int dtype);
 hipError_t launch_kv4_attn(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, int dtype, hipStream_t st);
+hipError_t launch_kv4_attn_tree(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, int dtype, hipStream_t st);
+
+// Attention weights of the cached tokens, from the rows' statistics (Kv4Attn::stats).
+struct Kv4Weights {
+    float *weight;
+    int64_t ldw;
+    int observe;             // last rows that count; 0: all
+    float factor;
+};
+hipError_t launch_kv4_weights(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, const Kv4Weights &w, int dtype, hipStream_t st);
+
+struct Kv4Select {
+    const float *weight;
+    int64_t ldw;
+    const int32_t *seq_len;
+    int B, heads, max_tokens, budget, first, recent;
+    int32_t *kept, *count;
+    float *kept_weight;
+    int64_t ld_kept;
+};
+int64_t kv4_select_workspace(int64_t B, int64_t heads, int64_t max_tokens);
+hipError_t launch_kv4_select(const Kv4Select &s, void *workspace, hipStream_t st);
+
+struct Kv4Move {
+    const int32_t *from, *count, *to_table, *to_start;
+    int lists, entries, to_pages;      // to_table null: in place
+};
+hipError_t launch_kv4_move(const Kv4Cache &c, const KvBatch &b, const Kv4Cache &to, const Kv4Move &m, hipStream_t st);
+
+// Linear attention (include/rad.h, rad_linear).
+struct Linear {
+    const void *q, *k, *v;
+    int64_t ldq, ldk, ldv;
+    const float *log_decay;
+    const int32_t *q_start;
+    int B, rows, max_q, qk_heads, heads, D;
+    const float *state;
+    float *state_out;
+    float scale;
+    void *o;
+};
+int64_t linear_workspace(const Linear &l, int dtype);
+hipError_t launch_linear(const Linear &l, int dtype, void *workspace, hipStream_t st);
 
 }  // namespace rad
