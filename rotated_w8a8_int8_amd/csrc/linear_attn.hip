@@ -81,10 +81,270 @@ __global__ __launch_bounds__(256) void recurrent_kernel(Linear l) {
         for (int i = 0; i < R; ++i) store4<kDtF32, true>(l.state_out, at + static_cast<int64_t>(i) * D, s[i]);
 }
 
+// ---- chunks of 32 rows ---------------------------------------------------------
+//
+// With a = exp(g), S the state before a chunk and i, j its rows from 0:
+//
+//   O = (Q K^T . a^(i - j) [j <= i]) V + a^(i + 1) Q S,   S' = a^n S + K^T (a^(n - 1 - j) V)
+//
+// A wave holds 32 of the head's value columns of the state, [D][32] in accumulators, and
+// does all four products for them, transposed so that what one product leaves is what the
+// next takes, lane by lane:
+//
+//   P^T [32 j][32 i] = K Q^T           a lane comes out with 16 rows j of one column i,
+//   O^T [32 v][32 i] = V^T P^T         which are the second operand's rows here
+//                    + S^T Q^T         and a lane's dims of one column v the first operand's
+//   S [D][32 v]     += K^T (a.. V)     V as read for O^T, aged
+//
+// Rows r = 8 q + 4 g + e of a tile (q = 0 .. 3, g = lane / 32, e = 0 .. 3) are held by lane half
+// g.  Value column r of the wave is v = 16 g + 4 q + e, so that a lane stores 16
+// consecutive values of a row.
+//
+// A sequence is cut into `segs` segments, a workgroup each: where it has several, a first
+// kernel works out what each adds to the state, a second hands the states on, and the last
+// one begins each segment with its state.
+typedef float f16v __attribute__((ext_vector_type(16)));
+typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+typedef unsigned int u4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u2 __attribute__((ext_vector_type(2)));
+
+constexpr int kChunk = 32;
+constexpr float kLog2e = 1.44269504088896340736f;
+template <int D>
+constexpr int kLinWaves = D >= 128 ? 4 : 2;              // of 32 value columns
+template <int D>
+constexpr int kSlices = D / (32 * kLinWaves<D>);         // workgroups a head
+
+struct Segments {
+    int segs;
+    float *states;            // [B][heads][segs][D][D]: state before each segment (segs > 1)
+};
+
+// The segment's rows: all whole chunks but the sequence's last.
+struct SegRows {
+    int first, n;             // rows of the call
+    bool last;
+};
+__device__ __forceinline__ SegRows segment_rows(const Rows &r, int segs, int seg) {
+    const int chunks = (r.n + kChunk - 1) / kChunk, each = (chunks + segs - 1) / segs * kChunk;
+    const int lo = min(seg * each, r.n), hi = min(lo + each, r.n);
+    return SegRows{r.first + lo, hi - lo, seg == segs - 1};
+}
+
+// a^k, a = 2^l2
+__device__ __forceinline__ float power(float l2, int k) { return __builtin_amdgcn_exp2f(l2 * static_cast<float>(k)); }
+__device__ __forceinline__ float log2_decay(const Linear &l, int h) { return fmaxf(l.log_decay[h] * kLog2e, -1e30f); }
+
+// State columns of a wave: lane r = lane % 32 holds column v(r), rows 32 T + 8 q + 4 g + e in s[T][4 q + e].
+__device__ __forceinline__ int value_of(int r) { return 16 * ((r >> 2) & 1) + 4 * (r >> 3) + (r & 3); }
+template <int D>
+__device__ __forceinline__ void load_state(f16v (&s)[D / 32], const float *from, int g, int col) {
+#pragma unroll
+    for (int T = 0; T < D / 32; ++T)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[T][i] = from ? from[static_cast<int64_t>(32 * T + 8 * (i >> 2) + 4 * g + (i & 3)) * D + col] : 0.0f;
+}
+template <int D>
+__device__ __forceinline__ void store_state(const f16v (&s)[D / 32], float *to, int g, int col) {
+#pragma unroll
+    for (int T = 0; T < D / 32; ++T)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) to[static_cast<int64_t>(32 * T + 8 * (i >> 2) + 4 * g + (i & 3)) * D + col] = s[T][i];
+}
+
+// Ages of a chunk of n rows, as a lane meets its rows j = 8 q + 4 g + e.
+struct Ages {
+    float w[16], all;         // a^(n - 1 - j), 0 from row n on; a^n
+    __device__ __forceinline__ void set(float l2, int n, int g) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int j = 8 * (i >> 2) + 4 * g + (i & 3);
+            w[i] = j < n ? power(l2, n - 1 - j) : 0.0f;
+        }
+        all = power(l2, n);
+    }
+};
+
+// ---- f32 products -----------------------------------------------------------------
+//
+// 32x32x2 matrix operations (154 TFLOP/s where the 16-bit ones reach 1228): 160 of them a wave and chunk
+// for D = 128.  They read two values a lane and take 64 cycles, so that tiles lie in LDS as they come, f32.
+template <int D>
+struct TileF32 {
+    float q[kChunk][D + 4], k[kChunk][D + 4], v[kChunk][32 * kLinWaves<D> + 4];
+    f16v p[kLinWaves<D>][64];                             // shares of P^T, by dims of the products
+};
+
+template <int DT, int D, bool OUT>
+__global__ __launch_bounds__(64 * kLinWaves<D>, D == 256 ? 1 : 2) void chunk_f32_kernel(Linear l, Segments sg) {
+    constexpr int NW = kLinWaves<D>, NT = 64 * NW, VC = 32 * NW, NS = kSlices<D>, PQ = D / (NT / 2);
+    __shared__ TileF32<D> tile;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int g = lane >> 5, col = lane & 31;
+    const int seq = blockIdx.x / sg.segs, seg = blockIdx.x % sg.segs, h = blockIdx.y / NS, v0 = VC * (blockIdx.y % NS);
+    const int hk = h / (l.heads / l.qk_heads);
+    const Rows rows = linear_rows(l, seq);
+    const SegRows sr = segment_rows(rows, sg.segs, seg);
+    const int64_t pair = static_cast<int64_t>(seq) * l.heads + h, mat = static_cast<int64_t>(D) * D;
+    float *const kept = sg.states + (pair * sg.segs + seg) * mat;
+    const int vcol = v0 + 32 * wave + value_of(col);
+    if (OUT && rows.n == 0 && (!l.state_out || l.state == l.state_out)) return;
+    if (!OUT && sr.last) return;
+
+    f16v s[D / 32];
+    load_state<D>(s, OUT ? (sg.segs > 1 ? kept : l.state ? l.state + pair * mat : nullptr) : nullptr, g, vcol);
+    const float l2 = log2_decay(l, h), from = power(l2, col + 1);
+    float near[16];                                       // a^(i - j) of the lane's column i = col
+    Ages age;
+    age.set(l2, kChunk, g);
+    if (OUT)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int j = 8 * (i >> 2) + 4 * g + (i & 3);
+            near[i] = j <= col ? power(l2, col - j) : 0.0f;
+        }
+
+    const int br = 4 * (tid & 7), bc = 4 * (tid >> 3);
+    float4 bq[PQ][4], bk[PQ][4], bv[4];
+    auto fetch = [&](int c0) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const bool on = c0 + br + x < sr.n;
+            const int64_t row = sr.first + c0 + br + x;
+            const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int y = 0; y < PQ; ++y) {
+                const int d = bc + (NT / 2) * y;
+                bk[y][x] = on ? load4<DT>(l.k, row * l.ldk + static_cast<int64_t>(hk) * D + d) : none;
+                if (OUT) bq[y][x] = on ? load4<DT>(l.q, row * l.ldq + static_cast<int64_t>(hk) * D + d) : none;
+            }
+            bv[x] = on ? load4<DT>(l.v, row * l.ldv + static_cast<int64_t>(h) * D + v0 + bc) : none;
+        }
+    };
+    // value column v of a wave lies at its r: 4 of them in a row stay together
+    const int vr = 32 * (bc >> 5) + 8 * ((bc >> 2) & 3) + 4 * ((bc >> 4) & 1);
+    auto put = [&]() {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+#pragma unroll
+            for (int y = 0; y < PQ; ++y) {
+                *reinterpret_cast<float4 *>(&tile.k[br + x][bc + (NT / 2) * y]) = bk[y][x];
+                if (OUT) *reinterpret_cast<float4 *>(&tile.q[br + x][bc + (NT / 2) * y]) = bq[y][x];
+            }
+            *reinterpret_cast<float4 *>(&tile.v[br + x][vr]) = bv[x];
+        }
+    };
+    fetch(0);
+    for (int c0 = 0; c0 < sr.n; c0 += kChunk) {
+        const int n = min(kChunk, sr.n - c0);
+        __syncthreads();                                  // the tile before is read
+        put();
+        __syncthreads();
+        if (c0 + kChunk < sr.n) fetch(c0 + kChunk);
+        if (n < kChunk) age.set(l2, n, g);
+        if (OUT) {
+            // P^T: each wave sums over its share of the dims, all of them add the shares up
+            f16v p{};
+#pragma unroll
+            for (int m = 0; m < D / NW / 8; ++m) {
+                const int d = D / NW * wave + 8 * m + 4 * g;
+                const float4 a = *reinterpret_cast<const float4 *>(&tile.k[col][d]), b = *reinterpret_cast<const float4 *>(&tile.q[col][d]);
+                p = __builtin_amdgcn_mfma_f32_32x32x2f32(a.x, b.x, p, 0, 0, 0);
+                p = __builtin_amdgcn_mfma_f32_32x32x2f32(a.y, b.y, p, 0, 0, 0);
+                p = __builtin_amdgcn_mfma_f32_32x32x2f32(a.z, b.z, p, 0, 0, 0);
+                p = __builtin_amdgcn_mfma_f32_32x32x2f32(a.w, b.w, p, 0, 0, 0);
+            }
+            tile.p[wave][lane] = p;
+            // S^T Q^T meanwhile
+            f16v o{};
+#pragma unroll
+            for (int T = 0; T < D / 32; ++T)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float4 b = *reinterpret_cast<const float4 *>(&tile.q[col][32 * T + 8 * q + 4 * g]);
+                    o = __builtin_amdgcn_mfma_f32_32x32x2f32(s[T][4 * q], b.x, o, 0, 0, 0);
+                    o = __builtin_amdgcn_mfma_f32_32x32x2f32(s[T][4 * q + 1], b.y, o, 0, 0, 0);
+                    o = __builtin_amdgcn_mfma_f32_32x32x2f32(s[T][4 * q + 2], b.z, o, 0, 0, 0);
+                    o = __builtin_amdgcn_mfma_f32_32x32x2f32(s[T][4 * q + 3], b.w, o, 0, 0, 0);
+                }
+            __syncthreads();
+            p = tile.p[0][lane];
+#pragma unroll
+            for (int x = 1; x < NW; ++x) p += tile.p[x][lane];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                p[i] *= near[i];
+                o[i] *= from;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                o = __builtin_amdgcn_mfma_f32_32x32x2f32(tile.v[8 * (i >> 2) + 4 * g + (i & 3)][32 * wave + col], p[i], o, 0, 0, 0);
+            if (col < n) {
+                const int64_t at = (static_cast<int64_t>(sr.first + c0 + col) * l.heads + h) * D + v0 + 32 * wave + 16 * g;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    store4<DT>(l.o, at + 4 * q, make_float4(o[4 * q] * l.scale, o[4 * q + 1] * l.scale, o[4 * q + 2] * l.scale, o[4 * q + 3] * l.scale));
+            }
+        }
+#pragma unroll
+        for (int T = 0; T < D / 32; ++T) s[T] *= age.all;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int j = 8 * (i >> 2) + 4 * g + (i & 3);
+            const float b = tile.v[j][32 * wave + col] * age.w[i];
+#pragma unroll
+            for (int T = 0; T < D / 32; ++T) s[T] = __builtin_amdgcn_mfma_f32_32x32x2f32(tile.k[j][32 * T + col], b, s[T], 0, 0, 0);
+        }
+    }
+    if (!OUT) store_state<D>(s, kept, g, vcol);
+    else if (l.state_out && sr.last) store_state<D>(s, l.state_out + pair * mat, g, vcol);
+}
+
+// States before each segment, in place of what each adds: blockIdx.x: sequence * heads + head, blockIdx.y: 1024 values.
+__global__ __launch_bounds__(256) void states_kernel(Linear l, Segments sg) {
+    const int64_t pair = blockIdx.x;
+    const int seq = static_cast<int>(pair / l.heads), h = static_cast<int>(pair % l.heads);
+    const Rows rows = linear_rows(l, seq);
+    const int64_t mat = static_cast<int64_t>(l.D) * l.D, at = blockIdx.y * 1024 + 4 * threadIdx.x;
+    const float l2 = log2_decay(l, h);
+    float *w = sg.states + pair * sg.segs * mat + at;
+    float4 s = l.state ? load4<kDtF32>(l.state, pair * mat + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int seg = 0; seg < sg.segs; ++seg) {
+        const float4 add = seg + 1 < sg.segs ? load4<kDtF32>(w, seg * mat) : s;
+        store4<kDtF32>(w, seg * mat, s);
+        const float a = power(l2, segment_rows(rows, sg.segs, seg).n);
+        s = make_float4(fmaf(a, s.x, add.x), fmaf(a, s.y, add.y), fmaf(a, s.z, add.z), fmaf(a, s.w, add.w));
+    }
+}
+
+// Segments a sequence: as many as give each CU two workgroups, of 256 rows at least.
+template <int D>
+int segments(const Linear &l) {
+    const int64_t wgs = static_cast<int64_t>(l.B) * l.heads * kSlices<D>, most = l.max_q / 256, want = 512 / wgs;
+    return static_cast<int>(want < 1 || most < 1 ? 1 : want < most ? want : most);
+}
+// Few rows are done one by one.
+template <int D>
+bool row_by_row(const Linear &l) { return l.max_q <= 4; }
+
 template <int DT, int D>
-hipError_t launch_d(const Linear &l, void *, hipStream_t st) {
-    hipLaunchKernelGGL((recurrent_kernel<DT, D>), dim3(l.B, l.heads * (D / kSlice)), dim3(256), 0, st, l);
-    return hipGetLastError();
+hipError_t launch_d(const Linear &l, void *ws, hipStream_t st) {
+    if (row_by_row<D>(l)) {
+        hipLaunchKernelGGL((recurrent_kernel<DT, D>), dim3(l.B, l.heads * (D / kSlice)), dim3(256), 0, st, l);
+        return hipGetLastError();
+    }
+    const Segments sg{segments<D>(l), static_cast<float *>(ws)};
+    const dim3 grid(static_cast<uint32_t>(l.B) * sg.segs, l.heads * kSlices<D>), block(64 * kLinWaves<D>);
+    auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid, block, 0, st, l, sg);
+        return hipGetLastError();
+    };
+    if (sg.segs > 1) {
+        if (hipError_t e = go(chunk_f32_kernel<DT, D, false>); e != hipSuccess) return e;
+        hipLaunchKernelGGL(states_kernel, dim3(l.B * l.heads, D * D / 1024), dim3(256), 0, st, l, sg);
+        if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    }
+    return go(chunk_f32_kernel<DT, D, true>);
 }
 template <int DT>
 hipError_t launch_t(const Linear &l, void *ws, hipStream_t st) {
@@ -92,10 +352,17 @@ hipError_t launch_t(const Linear &l, void *ws, hipStream_t st) {
     if (l.D == 128) return launch_d<DT, 128>(l, ws, st);
     return launch_d<DT, 256>(l, ws, st);
 }
+template <int D>
+int64_t workspace_d(const Linear &l) {
+    const int segs = row_by_row<D>(l) ? 1 : segments<D>(l);
+    return segs > 1 ? static_cast<int64_t>(l.B) * l.heads * segs * D * D * 4 : 0;
+}
 
 }  // namespace
 
-int64_t linear_workspace(const Linear &, int) { return 0; }
+int64_t linear_workspace(const Linear &l, int) {
+    return l.D == 64 ? workspace_d<64>(l) : l.D == 128 ? workspace_d<128>(l) : workspace_d<256>(l);
+}
 
 hipError_t launch_linear(const Linear &l, int dtype, void *workspace, hipStream_t st) {
     if (dtype == kDtF32) return launch_t<kDtF32>(l, workspace, st);
