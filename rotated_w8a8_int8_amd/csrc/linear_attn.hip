@@ -4,6 +4,8 @@
 //
 // Row by row (single tokens): a workgroup holds 64 of a head's D value columns, D / 16
 // of the key's rows a thread, four columns each, and passes over its part of the state once.
+#include <type_traits>
+
 #include "layer_launch.h"
 #include "value_types.h"
 
@@ -105,6 +107,7 @@ __global__ __launch_bounds__(256) void recurrent_kernel(Linear l) {
 // one begins each segment with its state.
 typedef float f16v __attribute__((ext_vector_type(16)));
 typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef unsigned int u4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u2 __attribute__((ext_vector_type(2)));
 
@@ -300,6 +303,235 @@ __global__ __launch_bounds__(64 * kLinWaves<D>, D == 256 ? 1 : 2) void chunk_f32
     else if (l.state_out && sr.last) store_state<D>(s, l.state_out + pair * mat, g, vcol);
 }
 
+// ---- 16-bit products ---------------------------------------------------------------
+//
+// 32x32x16 matrix operations, 8 values a lane.  Rows (and dims) of a step of 16 are taken in the order
+// 16 m + 8 b + 4 g + e -> 16 m + 8 g + 4 b + e that accumulators have, so that a lane's values lie together;
+// K and V are transposed on their way into LDS, 4 x 4 values a thread.  q, k and v are exact.  P and
+// S are taken as two 16-bit parts (bf16 16 bits, f16 22), aged values as as many as make the
+// state good to 2^-22 or better (bf16 three, f16 two).  f16 parts are taken at the power of two that puts the
+// largest of a wave's 32 columns in [2^14, 2^15): what is 2^-17 of that keeps 22 bits.
+template <int DT>
+__device__ __forceinline__ f16v mma(u4 a, u4 b, f16v c) {
+    if constexpr (DT == kDtBf16) return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8, a), __builtin_bit_cast(b8, b), c, 0, 0, 0);
+    else return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, a), __builtin_bit_cast(h8, b), c, 0, 0, 0);
+}
+// Eight values to the type; what that leaves of them.
+template <int DT>
+__device__ __forceinline__ u4 part8(float (&x)[8]) {
+    u4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float a = x[2 * i], b = x[2 * i + 1];
+        if constexpr (DT == kDtBf16) {
+            typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+            r[i] = __builtin_bit_cast(uint32_t, b2{static_cast<__bf16>(a), static_cast<__bf16>(b)});
+        } else {
+            typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+            r[i] = __builtin_bit_cast(uint32_t, h2{static_cast<_Float16>(a), static_cast<_Float16>(b)});
+        }
+        x[2 * i] = a - widen16<DT>(r[i] & 0xFFFFu);
+        x[2 * i + 1] = b - widen16<DT>(r[i] >> 16);
+    }
+    return r;
+}
+// Exponent that takes a wave's largest magnitude to [2^14, 2^15), at most `most` (what meets the products
+// in f32 is taken along and has to stay finite); 0 for bf16, whose range is f32's.
+template <int DT, int N>
+__device__ __forceinline__ int room(const float (&x)[N], int most) {
+    if constexpr (DT == kDtBf16) return 0;
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) m = fmaxf(m, fabsf(x[i]));
+    m = wave_max_f32(m);
+    return m > 0.0f ? min(15 - __builtin_amdgcn_frexp_expf(m), most) : 0;
+}
+__device__ __forceinline__ float pow2(int e) { return __builtin_amdgcn_ldexpf(1.0f, e); }
+
+template <int D, bool OUT>
+struct Tile16 {
+    uint16_t q[OUT ? kChunk : 1][D + 8], k[OUT ? kChunk : 1][D + 8];      // [row][dim]
+    uint16_t kt[D][kChunk + 8], vt[32 * kLinWaves<D>][kChunk + 8];        // [dim][row], [value column][row]
+};
+// Place of four values in a row of the order above.
+__device__ __forceinline__ int place(int i) { return (i & ~15) + 8 * ((i >> 2) & 1) + 4 * ((i >> 3) & 1); }
+// Four rows of four values -> four columns of four.
+__device__ __forceinline__ void turn4(const u2 (&x)[4], u2 (&y)[4]) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const uint32_t sel = c & 1 ? 0x07060302u : 0x05040100u;
+        y[c] = u2{__builtin_amdgcn_perm(x[1][c >> 1], x[0][c >> 1], sel), __builtin_amdgcn_perm(x[3][c >> 1], x[2][c >> 1], sel)};
+    }
+}
+
+template <int DT, int D, bool OUT>
+__global__ __launch_bounds__(64 * kLinWaves<D>, D == 256 ? 1 : 2) void chunk_kernel(Linear l, Segments sg) {
+    constexpr int NW = kLinWaves<D>, NT = 64 * NW, VC = 32 * NW, NS = kSlices<D>, PQ = D / (NT / 2), NA = DT == kDtBf16 ? 3 : 2;
+    __shared__ Tile16<D, OUT> tiles[2];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int g = lane >> 5, col = lane & 31;
+    const int seq = blockIdx.x / sg.segs, seg = blockIdx.x % sg.segs, h = blockIdx.y / NS, v0 = VC * (blockIdx.y % NS);
+    const int hk = h / (l.heads / l.qk_heads);
+    const Rows rows = linear_rows(l, seq);
+    const SegRows sr = segment_rows(rows, sg.segs, seg);
+    const int64_t pair = static_cast<int64_t>(seq) * l.heads + h, mat = static_cast<int64_t>(D) * D;
+    float *const kept = sg.states + (pair * sg.segs + seg) * mat;
+    const int vcol = v0 + 32 * wave + value_of(col);
+    if (OUT && rows.n == 0 && (!l.state_out || l.state == l.state_out)) return;
+    if (!OUT && sr.last) return;
+
+    const int br = 4 * (tid & 7), bc = 4 * (tid >> 3);
+    u2 bq[PQ][4], bk[PQ][4], bv[4];
+    auto fetch = [&](int c0) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const bool on = c0 + br + x < sr.n;
+            const int64_t row = sr.first + c0 + br + x;
+            auto four = [&](const void *base, int64_t at) { return on ? *reinterpret_cast<const u2 *>(static_cast<const uint16_t *>(base) + at) : u2{0u, 0u}; };
+#pragma unroll
+            for (int y = 0; y < PQ; ++y) {
+                const int64_t d = static_cast<int64_t>(hk) * D + bc + (NT / 2) * y;
+                bk[y][x] = four(l.k, row * l.ldk + d);
+                if (OUT) bq[y][x] = four(l.q, row * l.ldq + d);
+            }
+            bv[x] = four(l.v, row * l.ldv + static_cast<int64_t>(h) * D + v0 + bc);
+        }
+    };
+    const int vr = 32 * (bc >> 5) + 8 * ((bc >> 2) & 3) + 4 * ((bc >> 4) & 1), at_r = place(br);
+    auto put = [&](Tile16<D, OUT> &t) {
+        u2 y4[4];
+#pragma unroll
+        for (int y = 0; y < PQ; ++y) {
+            const int d = bc + (NT / 2) * y;
+            if (OUT)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    *reinterpret_cast<u2 *>(&t.k[br + x][place(d)]) = bk[y][x];
+                    *reinterpret_cast<u2 *>(&t.q[br + x][place(d)]) = bq[y][x];
+                }
+            turn4(bk[y], y4);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) *reinterpret_cast<u2 *>(&t.kt[d + x][at_r]) = y4[x];
+        }
+        turn4(bv, y4);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) *reinterpret_cast<u2 *>(&t.vt[vr + x][at_r]) = y4[x];
+    };
+    fetch(0);
+    f16v s[D / 32];
+    load_state<D>(s, OUT ? (sg.segs > 1 ? kept : l.state ? l.state + pair * mat : nullptr) : nullptr, g, vcol);
+    const float l2 = log2_decay(l, h), from = power(l2, col + 1);
+    float near[16];                                       // a^(i - j) of the lane's column i = col
+    Ages age;
+    age.set(l2, kChunk, g);
+    if (OUT)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int j = 8 * (i >> 2) + 4 * g + (i & 3);
+            near[i] = j <= col ? power(l2, col - j) : 0.0f;
+        }
+    int es = 0;                                           // the state is 2^-es s
+    put(tiles[0]);
+    __syncthreads();
+    for (int c0 = 0, at = 0; c0 < sr.n; c0 += kChunk, at ^= 1) {
+        const Tile16<D, OUT> &t = tiles[at];
+        const int n = min(kChunk, sr.n - c0);
+        const bool more = c0 + kChunk < sr.n;
+        if (more) fetch(c0 + kChunk);
+        u4 vf[2];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) vf[m] = *reinterpret_cast<const u4 *>(&t.vt[32 * wave + col][16 * m + 8 * g]);
+        if (OUT) {
+            u4 qf[D / 16];
+#pragma unroll
+            for (int m = 0; m < D / 16; ++m) qf[m] = *reinterpret_cast<const u4 *>(&t.q[col][16 * m + 8 * g]);
+            f16v p{};
+#pragma unroll
+            for (int m = 0; m < D / 16; ++m) p = mma<DT>(*reinterpret_cast<const u4 *>(&t.k[col][16 * m + 8 * g]), qf[m], p);
+            float big = 0.0f;
+            int ef = 0;
+            if constexpr (DT == kDtF16) {
+#pragma unroll
+                for (int T = 0; T < D / 32; ++T)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) big = fmaxf(big, fabsf(s[T][i]));
+                const float one[1] = {big};
+                ef = room<DT>(one, 127);
+            }
+            const float fs = pow2(ef);
+            f16v o{};
+#pragma unroll
+            for (int T = 0; T < D / 32; ++T)
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    float x[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = DT == kDtF16 ? s[T][8 * m + i] * fs : s[T][8 * m + i];
+                    const u4 hi = part8<DT>(x), lo = part8<DT>(x);
+                    o = mma<DT>(lo, qf[2 * T + m], o);
+                    o = mma<DT>(hi, qf[2 * T + m], o);
+                }
+            float pw[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) pw[i] = p[i] * near[i];
+            const int ep = room<DT>(pw, 64);
+            const float fo = DT == kDtF16 ? __builtin_amdgcn_ldexpf(from, ep - ef - es) : from, fp = pow2(ep);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] *= fo;
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = DT == kDtF16 ? pw[8 * m + i] * fp : pw[8 * m + i];
+                const u4 hi = part8<DT>(x), lo = part8<DT>(x);
+                o = mma<DT>(vf[m], lo, o);
+                o = mma<DT>(vf[m], hi, o);
+            }
+            if (col < n) {
+                const int64_t to = (static_cast<int64_t>(sr.first + c0 + col) * l.heads + h) * D + v0 + 32 * wave + 16 * g;
+                const float f = DT == kDtF16 ? __builtin_amdgcn_ldexpf(l.scale, -ep) : l.scale;
+                u4 y[2];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i >> 2][i & 3] = round16<DT>(o[2 * i] * f) | round16<DT>(o[2 * i + 1] * f) << 16;
+                u4 *q = reinterpret_cast<u4 *>(static_cast<uint16_t *>(l.o) + to);
+                q[0] = y[0];
+                q[1] = y[1];
+            }
+        }
+        if (n < kChunk) age.set(l2, n, g);
+        float aged[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) aged[i] = widen16<DT>(i & 1 ? vf[i >> 3][(i & 7) >> 1] >> 16 : vf[i >> 3][(i & 7) >> 1] & 0xFFFFu) * age.w[i];
+        const int ea = room<DT>(aged, 32);
+        const float fa = pow2(ea), keep = DT == kDtF16 ? __builtin_amdgcn_ldexpf(age.all, ea - es) : age.all;
+        es = ea;
+#pragma unroll
+        for (int T = 0; T < D / 32; ++T) s[T] *= keep;
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            float x[8];
+            u4 part[NA];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = DT == kDtF16 ? aged[8 * m + i] * fa : aged[8 * m + i];
+#pragma unroll
+            for (int y = 0; y < NA; ++y) part[y] = part8<DT>(x);
+#pragma unroll
+            for (int T = 0; T < D / 32; ++T) {
+                const u4 kf = *reinterpret_cast<const u4 *>(&t.kt[32 * T + col][16 * m + 8 * g]);
+#pragma unroll
+                for (int y = NA - 1; y >= 0; --y) s[T] = mma<DT>(kf, part[y], s[T]);
+            }
+        }
+        if (more) put(tiles[at ^ 1]);
+        __syncthreads();
+    }
+    if (DT == kDtF16)
+#pragma unroll
+        for (int T = 0; T < D / 32; ++T) s[T] *= pow2(-es);
+    if (!OUT) store_state<D>(s, kept, g, vcol);
+    else if (l.state_out && sr.last) store_state<D>(s, l.state_out + pair * mat, g, vcol);
+}
+
 // States before each segment, in place of what each adds: blockIdx.x: sequence * heads + head, blockIdx.y: 1024 values.
 __global__ __launch_bounds__(256) void states_kernel(Linear l, Segments sg) {
     const int64_t pair = blockIdx.x;
@@ -339,12 +571,16 @@ hipError_t launch_d(const Linear &l, void *ws, hipStream_t st) {
         hipLaunchKernelGGL(kernel, grid, block, 0, st, l, sg);
         return hipGetLastError();
     };
+    auto chunks = [&](auto out) {
+        if constexpr (DT == kDtF32) return go(chunk_f32_kernel<DT, D, decltype(out)::value>);
+        else return go(chunk_kernel<DT, D, decltype(out)::value>);
+    };
     if (sg.segs > 1) {
-        if (hipError_t e = go(chunk_f32_kernel<DT, D, false>); e != hipSuccess) return e;
+        if (hipError_t e = chunks(std::false_type{}); e != hipSuccess) return e;
         hipLaunchKernelGGL(states_kernel, dim3(l.B * l.heads, D * D / 1024), dim3(256), 0, st, l, sg);
         if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     }
-    return go(chunk_f32_kernel<DT, D, true>);
+    return chunks(std::true_type{});
 }
 template <int DT>
 hipError_t launch_t(const Linear &l, void *ws, hipStream_t st) {
