@@ -512,7 +512,7 @@ int rad_attn_kv4_tree(const rad_kv4_cache *cache, const rad_kv_batch *batch, con
  *            Entries from the sequence's length on, and those of a sequence without rows, are
  *            left as they were.
  *   observe  > 0: only the last `observe` rows of each sequence count; 0: every row.
- *   factor   finite, >= 0; with 0 the entries are not read.
+ *   factor   finite, >= 0; with 0 what the entries held does not matter.
  *   workspace, workspace_bytes  as for rad_attn_kv4, of the size that
  *            rad_attn_kv4_weights_workspace gives.
  *
@@ -537,8 +537,8 @@ int rad_attn_kv4_weights(const rad_kv4_cache *cache, const rad_kv_batch *batch, 
  *                equal weights the lower token is kept; a NaN is below every other weight.
  *   count        int32 [B] output, 4-byte aligned: min(seq_len, budget), the entries of kept
  *                that are written; those behind are left as they were.
- *   kept_weight  f32 [B][heads][ld_kept] output, 16-byte aligned, or NULL: the weights of the
- *                kept tokens, in their order; ld_kept a multiple of 4, at least budget.
+ *   kept_weight  f32 [B][heads][ld_kept] output, 4-byte aligned, or NULL: the weights of the
+ *                kept tokens, in their order; ld_kept at least budget.
  *   workspace    device memory, 16-byte aligned, of at least the bytes that
  *                rad_kv4_select_workspace gives (NULL when that is 0).
  *

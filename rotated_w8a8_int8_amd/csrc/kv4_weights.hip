@@ -16,139 +16,252 @@
 namespace rad {
 namespace {
 
-// A token's keys and their f16 levels, D / 2 dims a lane.
+// A step's key codes: D / 2 dims of token lane % 32, and its scale.
 template <int D>
-struct Keys {
-    u4 f[D / 16];
-    float scale;
+struct Codes {
+    u4 k[D / 64];
+    uint16_t scale;
 };
 template <int D>
-__device__ __forceinline__ void load_keys(Keys<D> &k, const Kv4Cache &c, int64_t tok, int g, int r) {
+__device__ __forceinline__ void load_codes(Codes<D> &s, const Kv4Cache &c, int64_t tok, int g, int r) {
     const u4 *p = reinterpret_cast<const u4 *>(c.k_codes + (tok + r) * (D / 2) + g * (D / 4));
 #pragma unroll
-    for (int j = 0; j < D / 64; ++j) {
-        const u4 x = p[j];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) k.f[4 * j + i] = levels8(x[i]);
-    }
-    k.scale = f16_widen(c.k_scale[tok + r]);
+    for (int j = 0; j < D / 64; ++j) s.k[j] = p[j];
+    s.scale = c.k_scale[tok + r];
 }
 
-// What a pair's row brings to its scores: their factor, reference exponent, 1 / normaliser, position.
+// What a pair's row brings to its scores: their factor, reference exponent, 1 / normaliser, position.  A row
+// that sees nothing, and a pair that is none, has no statistics: it counts 0 times 2^0.
 struct PairRow {
     float f, m, inv;
     int pos;
 };
 
-// blockIdx.x: sequence * parts + part, blockIdx.y: KV head.  Wave w of part x takes steps 4 x + w, 4 (x + parts) + w, ..
+// The sequence as the call counts it: its rows row0 .. row1 - 1 are observed.
+struct Observed {
+    RowRange rr;
+    int len, base, pair0, pair1;
+    __device__ __forceinline__ Observed(const KvBatch &b, const Kv4Attn &a, const Kv4Weights &w, int heads, int seq)
+        : rr(kv_rows(b, seq)), len(kv_len(b, seq)), base(len - rr.n) {
+        const int G = a.q_heads / heads, row0 = w.observe > 0 ? max(0, rr.n - w.observe) : 0;
+        pair0 = row0 * G;
+        pair1 = max(min(rr.n, b.max_q), row0) * G;
+    }
+};
+
 template <int DT, int D>
-__global__ __launch_bounds__(256) void weights_kernel(Kv4Cache c, KvBatch b, Kv4Attn a, Kv4Weights w, int parts) {
+struct Tile {                                             // 32 pairs as the matrix operations take them
+    u4 hi[D / 16][64], lo[DT == kDtF32 ? D / 16 : 1][64];
+    PairRow row[32];
+    int far;                                              // a reference exponent past kNear is among them
+};
+// Eight threads a pair, D / 8 dims each: queries to f16, their largest value in [2^9, 2^10) as in attn_wide_kernel.
+template <int DT, int D>
+__device__ __forceinline__ void stage(Tile<DT, D> &t, const Kv4Attn &a, const Observed &ob, int h, int G, int p0) {
+    constexpr int N = D / 64;                             // runs of 8 dims
+    const int r = threadIdx.x >> 3, c = threadIdx.x & 7, cp = p0 + r;
+    const bool used = cp < ob.pair1;
+    const int ci = used ? cp / G : 0, cg = used ? cp % G : 0;
+    const int64_t at = static_cast<int64_t>(ob.rr.first + ci) * a.q_heads + h * G + cg;
+    float x[N][8], big = 0.0f;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const float4 u = load4<DT>(a.q, at * D + 8 * (N * c + n)), v = load4<DT>(a.q, at * D + 8 * (N * c + n) + 4);
+        x[n][0] = u.x; x[n][1] = u.y; x[n][2] = u.z; x[n][3] = u.w;
+        x[n][4] = v.x; x[n][5] = v.y; x[n][6] = v.z; x[n][7] = v.w;
+    }
+    const float2 st = a.stats[at];
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(x[n][i]));
+    big = fmaxf(big, lane_xor<1>(big));
+    big = fmaxf(big, lane_xor<2>(big));
+    big = fmaxf(big, lane_xor<4>(big));
+    const int e = big > 0.0f ? 10 - __builtin_amdgcn_frexp_expf(big) : 0;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[n][i] = used ? __builtin_amdgcn_ldexpf(x[n][i], e) : 0.0f;
+        const int d = 8 * (N * c + n), slot = (d >= D / 2 ? 32 : 0) + r, j = (d & (D / 2 - 1)) >> 3;
+        if constexpr (DT == kDtF32) {
+            u4 hi, lo;
+            f16_split8(x[n], hi, lo);
+            t.hi[j][slot] = hi;
+            t.lo[j][slot] = lo;
+        } else {
+            t.hi[j][slot] = f16_pack8(x[n]);
+        }
+    }
+    const bool on = used && ob.base + ci >= 0 && st.y > 0.0f;
+    if (c == 0) {
+        t.row[r] = PairRow{on ? score_factor(a.sm_scale, e) : 0.0f, on ? st.x : 0.0f, on ? st.y : 0.0f, ob.base + ci};
+        if (on && fabsf(st.x) > kNear) t.far = 1;
+    }
+}
+
+// A pair's probability of a token: s its product with the key, ks the key's scale.
+__device__ __forceinline__ float probability(const PairRow &r, float s, float ks, bool far, bool causal, int window, int t) {
+    float x = fmaf(s * ks, r.f, -r.m);
+    if (far) x = fminf(x, most_power(r.m));
+    const bool on = (!causal || t <= r.pos) && (window == 0 || t > r.pos - window);
+    return on ? __builtin_amdgcn_exp2f(x) * r.inv : 0.0f;
+}
+// One lane's tokens: the sum of the two lanes that share one, added to what is there.
+__device__ __forceinline__ void add_weight(const Kv4Weights &w, float *row, const Observed &ob, int t, int g, float total, float old) {
+    total += __shfl_xor(total, 32);
+    if (g == 0 && t < ob.len) row[t] = (w.factor != 0.0f && t < ob.base ? w.factor * old : 0.0f) + total;
+}
+
+// At most 8 NQ pairs: queries stay in registers, the steps of a wave go through a ring of kRing on
+// their way.  Rows 8 q + .. of the products are looked at for q < NQ alone.  blockIdx.x: sequence * parts
+// + part, blockIdx.y: KV head; wave w of part x takes steps 4 x + w, 4 (x + parts) + w, ..
+constexpr int kRing = 4;
+template <int DT, int D, int NQ>
+__global__ __launch_bounds__(256, NQ == 4 || D == 256 || (D == 128 && DT == kDtF32) ? 2 : 3) void weights_few_kernel(Kv4Cache c, KvBatch b, Kv4Attn a, Kv4Weights w, int parts) {
     constexpr int NK = D / 16;
     constexpr bool SP = DT == kDtF32;
-    __shared__ PairRow rows[kWaves][32];
+    __shared__ Tile<DT, D> tile;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 5, col = lane & 31;
     const int h = blockIdx.y, G = a.q_heads / c.heads;
     const int seq = blockIdx.x / parts, part = blockIdx.x % parts;
-    const RowRange rr = kv_rows(b, seq);
-    if (rr.n == 0) return;
-    const int len = kv_len(b, seq), base = len - rr.n;
-    const int row0 = w.observe > 0 ? max(0, rr.n - w.observe) : 0, row1 = min(rr.n, b.max_q);
-    const int pair0 = row0 * G, pair1 = max(row1, row0) * G;
-    const Pages pages(c, b, seq, h, (len + 31) >> 5);
-
-    u4 qf[NK], ql[SP ? NK : 1];
-    bool far = false;
-    // tile of pairs p0 ..: queries to f16 (as in attn_wide_kernel), rows to LDS
-    auto load_tile = [&](int p0) {
-        const int cp = p0 + col;
-        const bool used = cp < pair1;
-        const int ci = used ? cp / G : row0, cg = used ? cp % G : 0;
-        const int64_t qrow = (static_cast<int64_t>(rr.first + ci) * a.q_heads + h * G + cg) * D;
-        float qv[NK][8], big = 0.0f;
-#pragma unroll
-        for (int j = 0; j < NK; ++j) {
-            const int64_t at = qrow + g * (D / 2) + 8 * j;
-            const float4 x = load4<DT>(a.q, at), y = load4<DT>(a.q, at + 4);
-            qv[j][0] = x.x; qv[j][1] = x.y; qv[j][2] = x.z; qv[j][3] = x.w;
-            qv[j][4] = y.x; qv[j][5] = y.y; qv[j][6] = y.z; qv[j][7] = y.w;
-        }
-        const float2 st = a.stats[qrow / D];
-#pragma unroll
-        for (int j = 0; j < NK; ++j)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(qv[j][i]));
-        big = fmaxf(big, __shfl_xor(big, 32));
-        const int e = big > 0.0f ? 10 - __builtin_amdgcn_frexp_expf(big) : 0;
-#pragma unroll
-        for (int j = 0; j < NK; ++j) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) qv[j][i] = used ? __builtin_amdgcn_ldexpf(qv[j][i], e) : 0.0f;
-            if constexpr (SP) f16_split8(qv[j], qf[j], ql[j]);
-            else qf[j] = f16_pack8(qv[j]);
-        }
-        // a row that sees nothing has no statistics: it counts 0 times 1
-        const bool on = used && base + ci >= 0 && st.y > 0.0f;
-        far = __any(on && fabsf(st.x) > kNear);
-        if (g == 0)
-            rows[wave][col] = PairRow{on ? score_factor(a.sm_scale, e) : 0.0f, on ? st.x : 0.0f, on ? st.y : 0.0f, base + ci};
-        __builtin_amdgcn_wave_barrier();
+    const Observed ob(b, a, w, c.heads, seq);
+    if (ob.rr.n == 0) return;
+    const Pages pages(c, b, seq, h, (ob.len + 31) >> 5);
+    const int stride = 4 * parts;
+    int step = 4 * part + wave;
+    Codes<D> ring[kRing];
+    int page[kRing + 1];
+    float old[kRing];
+    float *const row = w.weight + (static_cast<int64_t>(seq) * c.heads + h) * w.ldw;
+    const int most = w.factor != 0.0f ? static_cast<int>(w.ldw) - 1 : 0;          // what is there does not matter: one line of it
+    auto load = [&](int k, int p, int st) {
+        load_codes<D>(ring[k], c, pages.token(p, st), g, col);
+        old[k] = row[min((st << 5) + col, most)];
     };
-    const bool one = pair1 - pair0 <= 32;
-    if (one && pair1 > pair0) load_tile(pair0);
-
-    for (int step = 4 * part + wave; step < pages.end; step += 4 * parts) {
-        const int t0 = step << 5, t = t0 + col, page = pages.id(step);
-        float total = 0.0f;
-        if (page >= 0 && page < c.pages) {
-            Keys<D> k;
-            load_keys<D>(k, c, pages.token(page, step), g, col);
-            // rows before the step's first token see none of it
-            int p0 = pair0;
-            if (a.causal && t0 > base + row0) p0 += (t0 - base - row0) * G & ~31;
-            for (; p0 < pair1; p0 += 32) {
-                if (!one) load_tile(p0);
+#pragma unroll
+    for (int k = 0; k < kRing + 1; ++k) page[k] = pages.id(step + k * stride);
+#pragma unroll
+    for (int k = 0; k < kRing - 1; ++k) load(k, page[k], step + k * stride);
+    if (threadIdx.x == 0) tile.far = 0;
+    __syncthreads();
+    stage<DT, D>(tile, a, ob, h, G, ob.pair0);
+    __syncthreads();
+    u4 qf[NK], ql[SP ? NK : 1];
+#pragma unroll
+    for (int j = 0; j < NK; ++j) {
+        qf[j] = tile.hi[j][lane];
+        if constexpr (SP) ql[j] = tile.lo[j][lane];
+    }
+    PairRow rows[4 * NQ];
+#pragma unroll
+    for (int i = 0; i < 4 * NQ; ++i) rows[i] = tile.row[8 * (i >> 2) + 4 * g + (i & 3)];
+    const bool far = tile.far;
+    while (step < pages.end) {
+#pragma unroll
+        for (int k = 0; k < kRing; ++k) {
+            constexpr int ahead = kRing - 1;
+            load((k + ahead) % kRing, page[ahead], step + ahead * stride);
+            const int t0 = step << 5, now = page[0];
+#pragma unroll
+            for (int i = 0; i < kRing; ++i) page[i] = page[i + 1];
+            page[kRing] = pages.id(step + (kRing + 1) * stride);
+            float total = 0.0f;
+            if (now >= 0 && now < c.pages) {
                 f16v s;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) s[i] = 0.0f;
 #pragma unroll
                 for (int j = 0; j < NK; ++j) {
-                    if constexpr (SP) s = mma32(ql[j], k.f[j], s);
-                    s = mma32(qf[j], k.f[j], s);
+                    const u4 kf = levels8(ring[k].k[j >> 2][j & 3]);
+                    if constexpr (SP) s = mma32(ql[j], kf, s);
+                    s = mma32(qf[j], kf, s);
                 }
-                float sum = 0.0f;
+                const float ks = f16_widen(ring[k].scale);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const PairRow r = rows[wave][8 * (i >> 2) + 4 * g + (i & 3)];
-                    float x = fmaf(s[i] * k.scale, r.f, -r.m);
-                    if (far) x = fminf(x, most_power(r.m));
-                    const bool on = (!a.causal || t <= r.pos) && (a.window == 0 || t > r.pos - a.window);
-                    sum += on ? __builtin_amdgcn_exp2f(x) * r.inv : 0.0f;
-                }
-                total += sum;
+                for (int i = 0; i < 4 * NQ; ++i) total += probability(rows[i], s[i], ks, far, a.causal, a.window, t0 + col);
             }
-        }
-        total += __shfl_xor(total, 32);
-        if (g == 0 && t < len) {
-            float *at = w.weight + (static_cast<int64_t>(seq) * c.heads + h) * w.ldw + t;
-            const float old = w.factor != 0.0f && t < base ? w.factor * *at : 0.0f;
-            *at = old + total;
+            add_weight(w, row, ob, t0 + col, g, total, old[k]);
+            step += stride;
+            if (step >= pages.end) break;
         }
     }
 }
 
-template <int DT>
-hipError_t launch_t(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, const Kv4Weights &w, hipStream_t st) {
+// More pairs: a workgroup's waves take a step each and meet the tiles of pairs together, which are staged through LDS.
+template <int DT, int D>
+__global__ __launch_bounds__(256, 2) void weights_many_kernel(Kv4Cache c, KvBatch b, Kv4Attn a, Kv4Weights w, int parts) {
+    constexpr int NK = D / 16;
+    constexpr bool SP = DT == kDtF32;
+    __shared__ Tile<DT, D> tiles[2];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int g = lane >> 5, col = lane & 31;
+    const int h = blockIdx.y, G = a.q_heads / c.heads;
+    const int seq = blockIdx.x / parts, part = blockIdx.x % parts;
+    const Observed ob(b, a, w, c.heads, seq);
+    if (ob.rr.n == 0) return;
+    const Pages pages(c, b, seq, h, (ob.len + 31) >> 5);
+    float *const row = w.weight + (static_cast<int64_t>(seq) * c.heads + h) * w.ldw;
+    if (threadIdx.x == 0) tiles[0].far = tiles[1].far = 0;
+    for (int first = 4 * part; first < pages.end; first += 4 * parts) {
+        const int step = first + wave, t = (step << 5) + col, page = pages.id(step);
+        const bool here = page >= 0 && page < c.pages;
+        Codes<D> codes;
+        load_codes<D>(codes, c, pages.token(page, step), g, col);
+        const float old = row[min(t, w.factor != 0.0f ? static_cast<int>(w.ldw) - 1 : 0)];
+        // rows before the first token see none of the four steps
+        int p0 = ob.pair0;
+        if (a.causal && (first << 5) - ob.base > 0) p0 += max(0, ((first << 5) - ob.base) * G - ob.pair0) & ~31;
+        __syncthreads();                                  // the last steps' tiles are read
+        if (p0 < ob.pair1) stage<DT, D>(tiles[0], a, ob, h, G, p0);
+        __syncthreads();
+        u4 kf[NK];
+#pragma unroll
+        for (int j = 0; j < NK; ++j) kf[j] = levels8(codes.k[j >> 2][j & 3]);
+        const float ks = f16_widen(codes.scale);
+        float total = 0.0f;
+        for (int at = 0; p0 < ob.pair1; p0 += 32, at ^= 1) {
+            if (p0 + 32 < ob.pair1) stage<DT, D>(tiles[at ^ 1], a, ob, h, G, p0 + 32);
+            const Tile<DT, D> &tile = tiles[at];
+            f16v s;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < NK; ++j) {
+                if constexpr (SP) s = mma32(tile.lo[j][lane], kf[j], s);
+                s = mma32(tile.hi[j][lane], kf[j], s);
+            }
+            float sum = 0.0f;
+            const bool far = tile.far;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sum += probability(tile.row[8 * (i >> 2) + 4 * g + (i & 3)], s[i], ks, far, a.causal, a.window, t);
+            total += sum;
+            __syncthreads();
+        }
+        add_weight(w, row, ob, t, g, here ? total : 0.0f, old);
+    }
+}
+
+template <int DT, int D>
+hipError_t launch_d(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, const Kv4Weights &w, hipStream_t st) {
     const int64_t steps = ((static_cast<int64_t>(b.max_pages) << b.page_shift) + 31) >> 5, all = static_cast<int64_t>(b.B) * c.heads;
     const int64_t most = (steps + 3) / 4, even = 2048 / all;
     const int parts = static_cast<int>(even < 1 ? 1 : even < most ? even : most);
     if (parts == 0) return hipSuccess;
     const dim3 grid(static_cast<uint32_t>(b.B) * parts, c.heads), block(64 * kWaves);
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, st, c, b, a, w, parts); };
-    if (c.D == 64) go(weights_kernel<DT, 64>);
-    else if (c.D == 128) go(weights_kernel<DT, 128>);
-    else go(weights_kernel<DT, 256>);
+    const int64_t rows = w.observe > 0 && w.observe < b.max_q ? w.observe : b.max_q, pairs = rows * (a.q_heads / c.heads);
+    if (pairs <= 8) go(weights_few_kernel<DT, D, 1>);
+    else if (D <= 128 && pairs <= 32) go(weights_few_kernel<DT, D <= 128 ? D : 64, 4>);
+    else go(weights_many_kernel<DT, D>);
     return hipGetLastError();
+}
+template <int DT>
+hipError_t launch_t(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, const Kv4Weights &w, hipStream_t st) {
+    if (c.D == 64) return launch_d<DT, 64>(c, b, a, w, st);
+    if (c.D == 128) return launch_d<DT, 128>(c, b, a, w, st);
+    return launch_d<DT, 256>(c, b, a, w, st);
 }
 
 }  // namespace

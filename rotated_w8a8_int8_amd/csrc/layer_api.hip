@@ -365,14 +365,14 @@ int rad_kv4_select(const float *weight, int64_t ldw, const int32_t *seq_len, int
     const int rc = check_select(B, heads, max_tokens);
     if (rc < 0) return rc;
     if (budget < 1 || first < 0 || recent < 0 || ldw < max_tokens || ldw % 4 != 0) return RAD_E_SHAPE;
-    if (kept_weight && (ld_kept < budget || ld_kept % 4 != 0)) return RAD_E_SHAPE;
+    if (kept_weight && ld_kept < budget) return RAD_E_SHAPE;
     if (budget >= kMaxTokens || first > budget || recent > budget - first || ldw > kI32Max || ld_kept > kI32Max) return RAD_E_RANGE;
     if (rc) return RAD_OK;
     const int64_t need = rad::kv4_select_workspace(B, heads, max_tokens);
     if (workspace_bytes < need) return RAD_E_RANGE;
     if ((max_tokens > 0 && !weight) || !seq_len || !kept || !count || (need > 0 && !workspace)) return RAD_E_NULL;
     if (!aligned(weight, 16) || !aligned(seq_len, 4) || !aligned(kept, 4) || !aligned(count, 4) ||
-        !aligned(kept_weight, 16) || !aligned(workspace, 16))
+        !aligned(kept_weight, 4) || !aligned(workspace, 16))
         return RAD_E_ALIGN;
     const int64_t pairs = B * heads;
     const Span in[] = {span(weight, pairs * ldw * 4), span(seq_len, B * 4)};

@@ -45,7 +45,7 @@ def run_select(torch, seq_len, heads, budget, first, recent, kind, seed=0, width
     w = make_weights(rng, kind, (len(seq_len), heads, n))
     batch = C.device_batch(torch, np.zeros((len(seq_len), width), np.int32), seq_len, None, len(seq_len))
     kept = torch.full((len(seq_len), heads, budget), -7, dtype=torch.int32, device="cuda")
-    kw = torch.full((len(seq_len), heads, (budget + 7) // 4 * 4), 77.0, device="cuda")
+    kw = torch.full((len(seq_len), heads, budget + seed % 3), 77.0, device="cuda")
     _, count, _ = B.kv4_select(batch, C.put(torch, w), budget, first, recent, kept=kept, kept_weight=kw)
     kept, kw, count = kept.cpu().numpy(), kw.cpu().numpy(), count.cpu().numpy()
     for b, L in enumerate(np.clip(seq_len, 0, n)):

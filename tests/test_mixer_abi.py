@@ -128,13 +128,13 @@ def test_workspaces():
 @pytest.mark.parametrize("kw,rc", [
     (dict(seqs=-1), B.RAD_E_SHAPE), (dict(heads=-1), B.RAD_E_SHAPE), (dict(tokens=-1), B.RAD_E_SHAPE),
     (dict(budget=0), B.RAD_E_SHAPE), (dict(first=-1), B.RAD_E_SHAPE), (dict(recent=-1), B.RAD_E_SHAPE),
-    (dict(ldw=499), B.RAD_E_SHAPE), (dict(ldw=502), B.RAD_E_SHAPE), (dict(ldk=60), B.RAD_E_SHAPE), (dict(ldk=66), B.RAD_E_SHAPE),
+    (dict(ldw=499), B.RAD_E_SHAPE), (dict(ldw=502), B.RAD_E_SHAPE), (dict(ldk=63), B.RAD_E_SHAPE),
     (dict(seqs=1 << 22), B.RAD_E_RANGE), (dict(heads=1025), B.RAD_E_RANGE), (dict(seqs=1 << 12, heads=1024), B.RAD_E_RANGE),
     (dict(tokens=1 << 30, ldw=1 << 30), B.RAD_E_RANGE), (dict(budget=1 << 30, ldk=1 << 30), B.RAD_E_RANGE),
     (dict(first=60), B.RAD_E_RANGE), (dict(first=65, recent=0), B.RAD_E_RANGE), (dict(ldw=1 << 31), B.RAD_E_RANGE),
     (dict(w=None), B.RAD_E_NULL), (dict(n=None), B.RAD_E_NULL), (dict(kept=None), B.RAD_E_NULL), (dict(count=None), B.RAD_E_NULL),
     (dict(w=P[0] + 4), B.RAD_E_ALIGN), (dict(n=P[1] + 2), B.RAD_E_ALIGN), (dict(kept=P[2] + 1), B.RAD_E_ALIGN),
-    (dict(count=P[3] + 2), B.RAD_E_ALIGN), (dict(kw=P[4] + 8), B.RAD_E_ALIGN),
+    (dict(count=P[3] + 2), B.RAD_E_ALIGN), (dict(kw=P[4] + 2), B.RAD_E_ALIGN),
     (dict(kept=P[0]), B.RAD_E_ALIAS), (dict(count=P[2] + 64), B.RAD_E_ALIAS), (dict(kw=P[0] + 1024), B.RAD_E_ALIAS),
     (dict(count=P[1]), B.RAD_E_ALIAS), (dict(seqs=0, w=None, n=None, kept=None, count=None), B.RAD_OK),
     (dict(heads=0, w=None), B.RAD_OK),
