@@ -5,7 +5,10 @@
 // found digit by digit, 11, 11 and 10 bits: a histogram of the keys that share the digits
 // so far, from its top down to where the budget ends.  Every key above it is kept, and of
 // those equal to it the first ones.  The list comes out in order because a wave takes a run
-// of tokens and knows from the waves before it how many it follows.
+// of tokens and knows from the runs before it how many it follows.
+//
+// Up to 65536 tokens a workgroup holds a sequence and head's keys in registers.  Longer ones are cut
+// into slices, a workgroup each, and the digits found between launches.
 #include "layer_launch.h"
 #include "rad_device.h"
 
@@ -18,9 +21,10 @@ __device__ __forceinline__ uint32_t key_of(float w) {
     return u >> 31 ? ~u : u | 0x80000000u;
 }
 
-constexpr int kSelThreads = 1024, kSelWaves = kSelThreads / 64, kBins = 2048;
+constexpr int kBins = 2048;
+constexpr int kShift[3] = {21, 10, 0}, kBits[3] = {11, 11, 10};
 
-// Sums over the lanes above this one, and over all lanes.
+// Sums over this lane and those above it.
 __device__ __forceinline__ int wave_suffix(int v, int lane) {
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
@@ -30,98 +34,348 @@ __device__ __forceinline__ int wave_suffix(int v, int lane) {
     return v;
 }
 
-// One workgroup per (head, sequence).
-__global__ __launch_bounds__(kSelThreads) void select_kernel(Kv4Select s) {
-    __shared__ int hist[kBins];
-    __shared__ int part[kSelWaves];
-    __shared__ int found[2];                                  // digit, keys above it
-    __shared__ int above[kSelWaves], equal[kSelWaves];
+// A (sequence, head)'s task: tokens lo .. hi - 1 compete for `need` places, those outside are kept.
+struct Task {
+    int L, n, lo, hi, need;
+    int64_t pair;
+    const float *w;
+    __device__ __forceinline__ Task(const Kv4Select &s, int seq, int h)
+        : L(min(max(s.seq_len[seq], 0), s.max_tokens)), n(min(L, s.budget)), lo(s.first), hi(L - s.recent),
+          need(n - s.first - s.recent), pair(static_cast<int64_t>(seq) * s.heads + h), w(s.weight + pair * s.ldw) {}
+    __device__ __forceinline__ bool competes(int t) const { return t >= lo && t < hi; }
+};
+
+// The keys of four tokens from t on (t a multiple of 4): 16 bytes, those past the sequence aside.
+__device__ __forceinline__ uint4 keys4(const Task &k, int t) {
+    const float4 w = t < k.L ? *reinterpret_cast<const float4 *>(k.w + t) : make_float4(0.f, 0.f, 0.f, 0.f);
+    return make_uint4(key_of(w.x), key_of(w.y), key_of(w.z), key_of(w.w));
+}
+
+// Digit d with as many keys in higher digits as `over` < rest <= over + its own, of C counts a digit
+// (the lowest thread has the lowest digits); by a workgroup of W waves, 2048 / (64 W) digits a thread.
+template <int W, class Count>
+__device__ __forceinline__ void find_digit(int rest, int (&part)[W], int (&found)[2], Count count) {
+    constexpr int N = kBins / (64 * W);
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int h = blockIdx.y, seq = blockIdx.x;
-    const int L = min(max(s.seq_len[seq], 0), s.max_tokens), n = min(L, s.budget);
-    const int64_t pair = static_cast<int64_t>(seq) * s.heads + h;
-    const float *w = s.weight + pair * s.ldw;
-    int32_t *kept = s.kept + pair * s.budget;
-    float *kw = s.kept_weight ? s.kept_weight + pair * s.ld_kept : nullptr;
-    if (h == 0 && tid == 0) s.count[seq] = n;
-    if (n == L) {                                             // everything is kept
-        for (int t = tid; t < L; t += kSelThreads) {
-            kept[t] = t;
-            if (kw) kw[t] = w[t];
+    int c[N], all = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        c[i] = count(N * tid + i);
+        all += c[i];
+    }
+    const int sum = wave_suffix(all, lane);
+    if (lane == 0) part[wave] = sum;
+    if (tid == 0) found[0] = found[1] = 0;
+    __syncthreads();
+    int over = sum - all;
+    for (int x = wave + 1; x < W; ++x) over += part[x];
+#pragma unroll
+    for (int i = N - 1; i >= 0; --i) {
+        if (rest > over && rest <= over + c[i]) found[0] = N * tid + i, found[1] = over;
+        over += c[i];
+    }
+    __syncthreads();
+}
+
+// The kept tokens among 256 in a row (four a lane), behind `ups` and `ties` of them that came before.
+__device__ __forceinline__ void list256(const Kv4Select &s, const Task &k, int t, uint4 w4, uint32_t least, int rest, int &ups, int &ties) {
+    const int lane = threadIdx.x & 63;
+    const uint32_t key[4] = {w4.x, w4.y, w4.z, w4.w};
+    bool up[4], tie[4];
+    int u = 0, e = 0, all_u = 0, all_e = 0;
+    const uint64_t before = (uint64_t(1) << lane) - 1;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const bool on = t + c < k.L, free = k.competes(t + c) && k.need > 0;
+        up[c] = on && (!k.competes(t + c) || (free && key[c] > least));
+        tie[c] = on && free && key[c] == least;
+        const uint64_t mu = __ballot(up[c]), mt = __ballot(tie[c]);
+        u += __popcll(mu & before);
+        e += __popcll(mt & before);
+        all_u += __popcll(mu);
+        all_e += __popcll(mt);
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        if (up[c] || (tie[c] && ties + e < rest)) {
+            const int at = ups + u + min(ties + e, rest);
+            s.kept[k.pair * s.budget + at] = t + c;
+            if (s.kept_weight) s.kept_weight[k.pair * s.ld_kept + at] = k.w[t + c];
         }
+        u += up[c];
+        e += tie[c];
+    }
+    ups += all_u;
+    ties += all_e;
+}
+__device__ __forceinline__ void count256(const Task &k, int t, uint4 w4, uint32_t least, int &ups, int &ties) {
+    const uint32_t key[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const bool on = t + c < k.L, free = k.competes(t + c) && k.need > 0;
+        ups += __popcll(__ballot(on && (!k.competes(t + c) || (free && key[c] > least))));
+        ties += __popcll(__ballot(on && free && key[c] == least));
+    }
+}
+
+// ---- keys in registers ---------------------------------------------------------
+//
+// One workgroup per (sequence, head), 4 NV keys a thread.  Weights crowd into few digits (a binade is four of
+// them), so a digit has eight counters, by lane.
+constexpr int kSelWaves = 16, kCopies = 8;
+// A token's number, hidden from the compiler, which would keep what it once found out about each
+// (whether it competes: 64 of them spilled 430 scalar registers).
+__device__ __forceinline__ int anew(int t) {
+    asm volatile("" : "+v"(t));
+    return t;
+}
+template <int NV>
+__global__ __launch_bounds__(64 * kSelWaves) void select_kernel(Kv4Select s) {
+    __shared__ int hist[kBins * kCopies];
+    __shared__ int part[kSelWaves], found[2], above[kSelWaves], equal[kSelWaves];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const Task k(s, blockIdx.x, blockIdx.y);
+    if (blockIdx.y == 0 && tid == 0) s.count[blockIdx.x] = k.n;
+    const int t0 = wave * (256 * NV) + 4 * lane;              // a wave's run: NV times 256 tokens
+    uint4 w[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) w[i] = keys4(k, t0 + 256 * i);
+    uint32_t least = 0, known = 0;
+    int rest = k.L > k.n ? k.need : 0;
+    if (k.L > k.n) {
+#pragma unroll
+        for (int pass = 0; pass < 3; ++pass) {
+            for (int i = tid; i < kBins * kCopies; i += 64 * kSelWaves) hist[i] = 0;
+            __syncthreads();
+            if (rest > 0)
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const uint32_t key[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                    const int t = anew(t0 + 256 * i);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        if (k.competes(t + c) && (key[c] & known) == least)
+                            atomicAdd(&hist[(key[c] >> kShift[pass] & ((1u << kBits[pass]) - 1)) * kCopies + (lane & (kCopies - 1))], 1);
+                    }
+                }
+            __syncthreads();
+            find_digit<kSelWaves>(rest, part, found, [&](int d) {
+                const int4 a = *reinterpret_cast<const int4 *>(&hist[kCopies * d]), b = *reinterpret_cast<const int4 *>(&hist[kCopies * d + 4]);
+                return a.x + a.y + a.z + a.w + b.x + b.y + b.z + b.w;
+            });
+            least |= static_cast<uint32_t>(found[0]) << kShift[pass];
+            known |= ((1u << kBits[pass]) - 1) << kShift[pass];
+            rest -= found[1];
+            __syncthreads();
+        }
+    }
+    int ups = 0, ties = 0;
+    if (k.L > k.n) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            count256(k, anew(t0 + 256 * i), w[i], least, ups, ties);
+        }
+        if (lane == 0) above[wave] = ups, equal[wave] = ties;
+        __syncthreads();
+        ups = ties = 0;
+        for (int x = 0; x < wave; ++x) ups += above[x], ties += equal[x];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            list256(s, k, anew(t0 + 256 * i), w[i], anew(least), rest, ups, ties);
+        }
+    } else {
+        for (int t = tid; t < k.L; t += 64 * kSelWaves) {      // everything is kept
+            s.kept[k.pair * s.budget + t] = t;
+            if (s.kept_weight) s.kept_weight[k.pair * s.ld_kept + t] = k.w[t];
+        }
+    }
+}
+
+// ---- slices ----------------------------------------------------------------------
+//
+// blockIdx.x: sequence * slices + slice, blockIdx.y: head.  Launch p = 0 .. 2 counts the p-th digit of
+// its slice's keys that share the digits found; launch 3 lists.  Each finds the digit before it from
+// every slice's counts; slice 0 keeps it for the launches after that.  Of a slice's keys those above the
+// digits found so far are counted on the way.
+constexpr int kSliceWaves = 4, kSliceCopies = 4, kMostSlices = 64;
+struct Slices {
+    int slices, each;                 // tokens a slice, a multiple of 256 * kSliceWaves
+    int *hist;                        // [3][pairs][slices][kBins]
+    int *above;                       // [2][pairs][slices]: keys above the first digit, above the second
+    int *state;                       // [2][pairs][2]: digits found, places left among the keys that share them
+    int64_t pairs;
+};
+template <int PASS>
+__global__ __launch_bounds__(64 * kSliceWaves) void slice_kernel(Kv4Select s, Slices sl) {
+    __shared__ int hist[PASS < 3 ? kBins * kSliceCopies : 1];
+    __shared__ int part[kSliceWaves], found[2], sums[kSliceWaves][2];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, slice = blockIdx.x % sl.slices, seq = blockIdx.x / sl.slices;
+    const Task k(s, seq, blockIdx.y);
+    if (PASS == 0 && slice == 0 && blockIdx.y == 0 && tid == 0) s.count[seq] = k.n;
+    const int t0 = slice * sl.each, t1 = min(t0 + sl.each, k.L);
+    if (k.L == k.n) {                                         // everything is kept
+        if (PASS == 3)
+            for (int t = t0 + tid; t < t1; t += 64 * kSliceWaves) {
+                s.kept[k.pair * s.budget + t] = t;
+                if (s.kept_weight) s.kept_weight[k.pair * s.ld_kept + t] = k.w[t];
+            }
         return;
     }
-    // the tokens that weights decide about, and how many of them are kept
-    const int lo = s.first, hi = L - s.recent, need = n - s.first - s.recent;
-    uint32_t prefix = 0, known = 0;                           // digits found, and their bits
-    int rest = need;                                          // keys still wanted among those that share them
-#pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-        for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+    auto hists = [&](int pass) { return sl.hist + (static_cast<int64_t>(pass) * sl.pairs + k.pair) * sl.slices * kBins; };
+    uint32_t least = 0, known = 0;
+    int rest = k.need;
+    if (PASS > 0) {
+        if (PASS > 1) {
+            const int *st = sl.state + ((PASS - 2) * sl.pairs + k.pair) * 2;
+            least = static_cast<uint32_t>(st[0]);
+            rest = st[1];
+        }
+        for (int p = 0; p < PASS; ++p) known |= ((1u << kBits[p]) - 1) << kShift[p];
+        const int *from = hists(PASS - 1);
+        constexpr int N = kBins / (64 * kSliceWaves);
+        int c[N] = {};
+#pragma unroll 4
+        for (int x = 0; x < sl.slices; ++x)
+#pragma unroll
+            for (int i = 0; i < N; i += 4) {
+                const int4 v = *reinterpret_cast<const int4 *>(from + static_cast<int64_t>(x) * kBins + N * tid + i);
+                c[i] += v.x; c[i + 1] += v.y; c[i + 2] += v.z; c[i + 3] += v.w;
+            }
+        find_digit<kSliceWaves>(rest, part, found, [&](int d) { return c[d % N]; });
+        least |= static_cast<uint32_t>(found[0]) << kShift[PASS - 1];
+        rest -= found[1];
+        if (PASS < 3) {
+            if (slice == 0 && tid == 0) {
+                int *st = sl.state + ((PASS - 1) * sl.pairs + k.pair) * 2;
+                st[0] = static_cast<int>(least);
+                st[1] = rest;
+            }
+            // this slice's keys above the digit
+            int up = 0;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (N * tid + i > found[0]) up += from[static_cast<int64_t>(slice) * kBins + N * tid + i];
+            up = wave_suffix(up, lane);
+            if (lane == 0) sums[wave][0] = up;
+            __syncthreads();
+            if (tid == 0) sl.above[((PASS - 1) * sl.pairs + k.pair) * sl.slices + slice] = sums[0][0] + sums[1][0] + sums[2][0] + sums[3][0];
+        }
+    }
+    if constexpr (PASS < 3) {
+        for (int i = tid; i < kBins * kSliceCopies; i += 64 * kSliceWaves) hist[i] = 0;
         __syncthreads();
+        auto count = [&](int t, uint4 w4) {
+            const uint32_t key[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if (t + c < t1 && k.competes(t + c) && (PASS == 0 || (key[c] & known) == least))
+                    atomicAdd(&hist[(key[c] >> kShift[PASS] & ((1u << kBits[PASS]) - 1)) * kSliceCopies + (lane & (kSliceCopies - 1))], 1);
+            }
+        };
+        constexpr int kStep = 4 * 64 * kSliceWaves;
         if (rest > 0)
-            for (int t = lo + tid; t < hi; t += kSelThreads) {
-                const uint32_t k = key_of(w[t]);
-                if ((k & known) == prefix) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1)], 1);
+            for (int t = t0 + 4 * tid; t < t1; t += 8 * kStep) {
+                uint4 w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = keys4(k, t + kStep * i);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) count(t + kStep * i, w[i]);
             }
         __syncthreads();
-        // digit d with keys in digits above it < rest <= those and its own
-        const int h1 = hist[2 * tid + 1], h0 = hist[2 * tid], sum = wave_suffix(h0 + h1, lane);
-        if (lane == 0) part[wave] = sum;
-        if (tid == 0) found[0] = found[1] = 0;
-        __syncthreads();
-        int over = sum - h0 - h1;                             // keys in the digits of higher threads
-        for (int x = wave + 1; x < kSelWaves; ++x) over += part[x];
-        if (rest > over && rest <= over + h1) found[0] = 2 * tid + 1, found[1] = over;
-        else if (rest > over + h1 && rest <= over + h1 + h0) found[0] = 2 * tid, found[1] = over + h1;
-        __syncthreads();
-        prefix |= static_cast<uint32_t>(found[0]) << shift;
-        known |= ((1u << bits) - 1) << shift;
-        rest -= found[1];
-        __syncthreads();
-    }
-    // rest: how many of the keys equal to prefix are kept.  A wave's run of tokens, whole lines of 64
-    const int run = ((L + 63) / 64 + kSelWaves - 1) / kSelWaves * 64, t0 = wave * run, t1 = min(t0 + run, L);
-    auto look = [&](int t, bool &up, bool &tie) {
-        const bool on = t < t1, sure = t < lo || t >= hi;
-        const uint32_t k = on && need > 0 ? key_of(w[t]) : 0u;
-        up = on && (sure || (need > 0 && k > prefix));
-        tie = on && !sure && need > 0 && k == prefix;
-    };
-    int ups = 0, ties = 0;
-    for (int t = t0; t < t1; t += 64) {
-        bool up, tie;
-        look(t + lane, up, tie);
-        ups += __popcll(__ballot(up));
-        ties += __popcll(__ballot(tie));
-    }
-    if (lane == 0) above[wave] = ups, equal[wave] = ties;
-    __syncthreads();
-    ups = ties = 0;
-    for (int x = 0; x < wave; ++x) ups += above[x], ties += equal[x];
-    const uint64_t before = (uint64_t(1) << lane) - 1;
-    for (int t = t0; t < t1; t += 64) {
-        bool up, tie;
-        look(t + lane, up, tie);
-        const uint64_t mu = __ballot(up), mt = __ballot(tie);
-        const int tb = ties + __popcll(mt & before), at = ups + __popcll(mu & before) + min(tb, rest);
-        if (up || (tie && tb < rest)) {
-            kept[at] = t + lane;
-            if (kw) kw[at] = w[t + lane];
+        int *to = hists(PASS) + static_cast<int64_t>(slice) * kBins;
+        for (int d = tid; d < kBins; d += 64 * kSliceWaves) {
+            const int4 a = *reinterpret_cast<const int4 *>(&hist[kSliceCopies * d]);
+            to[d] = a.x + a.y + a.z + a.w;
         }
-        ups += __popcll(mu);
-        ties += __popcll(mt);
+    } else {
+        // kept and equal ones in the slices before: tokens that are always kept, then by the three digits
+        int ups = 0, ties = 0;
+        if (tid < slice) {
+            ups = sl.above[k.pair * sl.slices + tid] + sl.above[(sl.pairs + k.pair) * sl.slices + tid];
+            ties = hists(2)[static_cast<int64_t>(tid) * kBins + found[0]];
+        }
+        const int least3 = found[0];
+        for (int x = 0; x < slice; ++x)
+            for (int d = least3 + 1 + tid; d < (1 << kBits[2]); d += 64 * kSliceWaves) ups += hists(2)[static_cast<int64_t>(x) * kBins + d];
+        ups = wave_suffix(ups, lane);
+        ties = wave_suffix(ties, lane);
+        if (lane == 0) sums[wave][0] = ups, sums[wave][1] = ties;
+        __syncthreads();
+        // before t0, tokens below lo and from hi on are kept whatever they weigh
+        ups = min(t0, k.lo) + max(0, t0 - max(k.hi, k.lo));
+        ties = 0;
+        for (int x = 0; x < kSliceWaves; ++x) ups += sums[x][0], ties += sums[x][1];
+        __syncthreads();
+        // a wave's run of the slice
+        const int run = sl.each / kSliceWaves, r0 = t0 + wave * run, r1 = min(r0 + run, t1);
+        int u = 0, e = 0;
+        constexpr int N = 8;                                  // loads on their way together
+        for (int t = r0; t < r1; t += 256 * N) {
+            uint4 w[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) w[i] = keys4(k, t + 256 * i + 4 * lane);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (t + 256 * i < r1) count256(k, t + 256 * i + 4 * lane, w[i], least, u, e);
+        }
+        if (lane == 0) sums[wave][0] = u, sums[wave][1] = e;
+        __syncthreads();
+        for (int x = 0; x < wave; ++x) ups += sums[x][0], ties += sums[x][1];
+        for (int t = r0; t < r1; t += 256 * N) {
+            uint4 w[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) w[i] = keys4(k, t + 256 * i + 4 * lane);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (t + 256 * i < r1) list256(s, k, t + 256 * i + 4 * lane, w[i], least, rest, ups, ties);
+        }
     }
+}
+
+// Tokens that a workgroup's registers hold; sequences that may be longer are cut into slices.
+constexpr int kMostHeld = 64 * kSelWaves * 4 * 16;
+
+Slices make_slices(int64_t pairs, int64_t max_tokens, void *workspace) {
+    constexpr int kUnit = 256 * kSliceWaves;
+    Slices sl{};
+    sl.pairs = pairs;
+    const int64_t most = (max_tokens + 8191) / 8192, want = pairs < 1024 ? 1024 / pairs : 1;
+    const int64_t n = most < want ? most : want < kMostSlices ? want : kMostSlices;
+    const int64_t each = ((max_tokens + n - 1) / n + kUnit - 1) / kUnit * kUnit;
+    sl.each = static_cast<int>(each);
+    sl.slices = static_cast<int>((max_tokens + each - 1) / each);
+    sl.hist = static_cast<int *>(workspace);
+    sl.above = sl.hist ? sl.hist + 3 * pairs * sl.slices * kBins : nullptr;
+    sl.state = sl.above ? sl.above + 2 * pairs * sl.slices : nullptr;
+    return sl;
 }
 
 }  // namespace
 
-int64_t kv4_select_workspace(int64_t, int64_t, int64_t) { return 0; }
+int64_t kv4_select_workspace(int64_t B, int64_t heads, int64_t max_tokens) {
+    if (max_tokens <= kMostHeld) return 0;
+    const Slices sl = make_slices(B * heads, max_tokens, nullptr);
+    return 4 * (sl.pairs * sl.slices * (3 * kBins + 2) + 4 * sl.pairs);
+}
 
-hipError_t launch_kv4_select(const Kv4Select &s, void *, hipStream_t st) {
-    hipLaunchKernelGGL(select_kernel, dim3(s.B, s.heads), dim3(kSelThreads), 0, st, s);
-    return hipGetLastError();
+hipError_t launch_kv4_select(const Kv4Select &s, void *workspace, hipStream_t st) {
+    if (s.max_tokens <= kMostHeld) {
+        auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(s.B, s.heads), dim3(64 * kSelWaves), 0, st, s); };
+        if (s.max_tokens <= 4096) go(select_kernel<1>);
+        else if (s.max_tokens <= 16384) go(select_kernel<4>);
+        else if (s.max_tokens <= 32768 + 8192) go(select_kernel<10>);
+        else go(select_kernel<16>);
+        return hipGetLastError();
+    }
+    const Slices sl = make_slices(static_cast<int64_t>(s.B) * s.heads, s.max_tokens, workspace);
+    auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(s.B) * sl.slices, s.heads), dim3(64 * kSliceWaves), 0, st, s, sl);
+        return hipGetLastError();
+    };
+    if (hipError_t e = go(slice_kernel<0>); e != hipSuccess) return e;
+    if (hipError_t e = go(slice_kernel<1>); e != hipSuccess) return e;
+    if (hipError_t e = go(slice_kernel<2>); e != hipSuccess) return e;
+    return go(slice_kernel<3>);
 }
 
 }  // namespace rad
