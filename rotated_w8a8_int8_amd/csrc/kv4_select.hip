@@ -77,50 +77,64 @@ __device__ __forceinline__ void find_digit(int rest, int (&part)[W], int (&found
     __syncthreads();
 }
 
-// The kept tokens among 256 in a row (four a lane), behind `ups` and `ties` of them that came before.
-__device__ __forceinline__ void list256(const Kv4Select &s, const Task &k, int t, uint4 w4, uint32_t least, int rest, int &ups, int &ties) {
-    const int lane = threadIdx.x & 63;
-    const uint32_t key[4] = {w4.x, w4.y, w4.z, w4.w};
-    bool up[4], tie[4];
-    int u = 0, e = 0, all_u = 0, all_e = 0;
-    const uint64_t before = (uint64_t(1) << lane) - 1;
+// A lane's tokens of four in a row: bit c of the low four where token t + c is kept whatever the ties, bit 4 + c
+// where its key is the least one.
+__device__ __forceinline__ uint32_t look4(const Task &k, int t, uint4 w, uint32_t least) {
+    const uint32_t key[4] = {w.x, w.y, w.z, w.w};
+    uint32_t m = 0;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-        const bool on = t + c < k.L, free = k.competes(t + c) && k.need > 0;
-        up[c] = on && (!k.competes(t + c) || (free && key[c] > least));
-        tie[c] = on && free && key[c] == least;
-        const uint64_t mu = __ballot(up[c]), mt = __ballot(tie[c]);
-        u += __popcll(mu & before);
-        e += __popcll(mt & before);
-        all_u += __popcll(mu);
-        all_e += __popcll(mt);
+        const bool free = k.competes(t + c);
+        const bool up = t + c < k.L && (!free || (k.need > 0 && key[c] > least)), tie = free && k.need > 0 && key[c] == least;
+        m |= (up ? 1u << c : 0u) | (tie ? 16u << c : 0u);
     }
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        if (up[c] || (tie[c] && ties + e < rest)) {
-            const int at = ups + u + min(ties + e, rest);
-            s.kept[k.pair * s.budget + at] = t + c;
-            if (s.kept_weight) s.kept_weight[k.pair * s.ld_kept + at] = k.w[t + c];
-        }
-        u += up[c];
-        e += tie[c];
-    }
-    ups += all_u;
-    ties += all_e;
+    return m;
 }
-__device__ __forceinline__ void count256(const Task &k, int t, uint4 w4, uint32_t least, int &ups, int &ties) {
-    const uint32_t key[4] = {w4.x, w4.y, w4.z, w4.w};
+// How many of each kind, in the halves of a word (256 tokens a wave at most, so they stay apart).
+__device__ __forceinline__ int counts(uint32_t m) { return __popc(m & 15u) | __popc(m >> 4) << 16; }
+
+// Inclusive sum over the lanes of a wave.
+__device__ __forceinline__ int wave_scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);     // row_shr 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);    // row_bcast 15
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);    // row_bcast 31
+    return v;
+}
+
+// The kept tokens among 256 in a row (four a lane), behind `ups` and `ties` of them that came before.
+__device__ __forceinline__ void list256(const Kv4Select &s, const Task &k, int t, uint4 w, uint32_t least, int rest, int &ups, int &ties) {
+    const uint32_t m = look4(k, t, w, least);
+    const int mine = counts(m), sum = wave_scan(mine), all = __builtin_amdgcn_readlane(sum, 63);
+    int u = ups + ((sum - mine) & 0xFFFF), e = ties + ((sum - mine) >> 16);
+    if (m)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        const bool on = t + c < k.L, free = k.competes(t + c) && k.need > 0;
-        ups += __popcll(__ballot(on && (!k.competes(t + c) || (free && key[c] > least))));
-        ties += __popcll(__ballot(on && free && key[c] == least));
-    }
+        for (int c = 0; c < 4; ++c) {
+            const bool up = m >> c & 1, tie = m >> (4 + c) & 1;
+            if (up || (tie && e < rest)) {
+                const int at = u + min(e, rest);
+                s.kept[k.pair * s.budget + at] = t + c;
+                if (s.kept_weight) s.kept_weight[k.pair * s.ld_kept + at] = k.w[t + c];
+            }
+            u += up;
+            e += tie;
+        }
+    ups += all & 0xFFFF;
+    ties += all >> 16;
+}
+// Their numbers alone, a lane's own.
+__device__ __forceinline__ void count4(const Task &k, int t, uint4 w, uint32_t least, int &ups, int &ties) {
+    const int c = counts(look4(k, t, w, least));
+    ups += c & 0xFFFF;
+    ties += c >> 16;
 }
 
 // ---- keys in registers ---------------------------------------------------------
 //
-// One workgroup per (sequence, head), 4 NV keys a thread.  Weights crowd into few digits (a binade is four of
+// blockIdx.x: sequence * shares + share, blockIdx.y: head; 4 NV keys a thread.  Every share finds the least
+// key, and lists its share of each wave's run (64 runs of 32768 tokens: 36 us with one share).  Weights crowd into few digits (a binade is four of
 // them), so a digit has eight counters, by lane.
 constexpr int kSelWaves = 16, kCopies = 8;
 // A token's number, hidden from the compiler, which would keep what it once found out about each
@@ -130,12 +144,13 @@ __device__ __forceinline__ int anew(int t) {
     return t;
 }
 template <int NV>
-__global__ __launch_bounds__(64 * kSelWaves) void select_kernel(Kv4Select s) {
+__global__ __launch_bounds__(64 * kSelWaves) void select_kernel(Kv4Select s, int shares) {
     __shared__ int hist[kBins * kCopies];
     __shared__ int part[kSelWaves], found[2], above[kSelWaves], equal[kSelWaves];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const Task k(s, blockIdx.x, blockIdx.y);
-    if (blockIdx.y == 0 && tid == 0) s.count[blockIdx.x] = k.n;
+    const int seq = blockIdx.x / shares, share = blockIdx.x % shares, i0 = NV * share / shares, i1 = NV * (share + 1) / shares;
+    const Task k(s, seq, blockIdx.y);
+    if (share == 0 && blockIdx.y == 0 && tid == 0) s.count[seq] = k.n;
     const int t0 = wave * (256 * NV) + 4 * lane;              // a wave's run: NV times 256 tokens
     uint4 w[NV];
 #pragma unroll
@@ -169,22 +184,27 @@ __global__ __launch_bounds__(64 * kSelWaves) void select_kernel(Kv4Select s) {
             __syncthreads();
         }
     }
-    int ups = 0, ties = 0;
     if (k.L > k.n) {
+        int ups = 0, ties = 0, u0 = 0, e0 = 0;                // of the wave's run; of it before the share
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            count256(k, anew(t0 + 256 * i), w[i], least, ups, ties);
+            if (i == i0) u0 = ups, e0 = ties;
+            count4(k, anew(t0 + 256 * i), w[i], least, ups, ties);
         }
+        ups = wave_suffix(ups, lane);
+        ties = wave_suffix(ties, lane);
         if (lane == 0) above[wave] = ups, equal[wave] = ties;
+        ups = __builtin_amdgcn_readfirstlane(wave_suffix(u0, lane));
+        ties = __builtin_amdgcn_readfirstlane(wave_suffix(e0, lane));
         __syncthreads();
-        ups = ties = 0;
         for (int x = 0; x < wave; ++x) ups += above[x], ties += equal[x];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
+            if (i < i0 || i >= i1) continue;
             list256(s, k, anew(t0 + 256 * i), w[i], anew(least), rest, ups, ties);
         }
     } else {
-        for (int t = tid; t < k.L; t += 64 * kSelWaves) {      // everything is kept
+        for (int t = tid + 64 * kSelWaves * share; t < k.L; t += 64 * kSelWaves * shares) {      // everything is kept
             s.kept[k.pair * s.budget + t] = t;
             if (s.kept_weight) s.kept_weight[k.pair * s.ld_kept + t] = k.w[t];
         }
@@ -197,7 +217,7 @@ __global__ __launch_bounds__(64 * kSelWaves) void select_kernel(Kv4Select s) {
 // its slice's keys that share the digits found; launch 3 lists.  Each finds the digit before it from
 // every slice's counts; slice 0 keeps it for the launches after that.  Of a slice's keys those above the
 // digits found so far are counted on the way.
-constexpr int kSliceWaves = 4, kSliceCopies = 4, kMostSlices = 64;
+constexpr int kSliceWaves = 16, kSliceCopies = 4, kMostSlices = 64;
 struct Slices {
     int slices, each;                 // tokens a slice, a multiple of 256 * kSliceWaves
     int *hist;                        // [3][pairs][slices][kBins]
@@ -223,7 +243,7 @@ __global__ __launch_bounds__(64 * kSliceWaves) void slice_kernel(Kv4Select s, Sl
     }
     auto hists = [&](int pass) { return sl.hist + (static_cast<int64_t>(pass) * sl.pairs + k.pair) * sl.slices * kBins; };
     uint32_t least = 0, known = 0;
-    int rest = k.need;
+    int rest = k.need, ups = 0, ties = 0;                     // above and equal to the least key in the slices before
     if (PASS > 0) {
         if (PASS > 1) {
             const int *st = sl.state + ((PASS - 2) * sl.pairs + k.pair) * 2;
@@ -233,17 +253,31 @@ __global__ __launch_bounds__(64 * kSliceWaves) void slice_kernel(Kv4Select s, Sl
         for (int p = 0; p < PASS; ++p) known |= ((1u << kBits[p]) - 1) << kShift[p];
         const int *from = hists(PASS - 1);
         constexpr int N = kBins / (64 * kSliceWaves);
-        int c[N] = {};
-#pragma unroll 4
-        for (int x = 0; x < sl.slices; ++x)
+        int c[N] = {}, cb[N] = {};                            // all slices' counts, those of the slices before
+#pragma unroll 8
+        for (int x = 0; x < sl.slices; ++x) {
+            const bool before = PASS == 3 && x < slice;
 #pragma unroll
-            for (int i = 0; i < N; i += 4) {
-                const int4 v = *reinterpret_cast<const int4 *>(from + static_cast<int64_t>(x) * kBins + N * tid + i);
-                c[i] += v.x; c[i + 1] += v.y; c[i + 2] += v.z; c[i + 3] += v.w;
+            for (int i = 0; i < N; i += 2) {
+                const int2 v = *reinterpret_cast<const int2 *>(from + static_cast<int64_t>(x) * kBins + N * tid + i);
+                c[i] += v.x;
+                c[i + 1] += v.y;
+                if (PASS == 3) {
+                    cb[i] += before ? v.x : 0;
+                    cb[i + 1] += before ? v.y : 0;
+                }
             }
+        }
         find_digit<kSliceWaves>(rest, part, found, [&](int d) { return c[d % N]; });
         least |= static_cast<uint32_t>(found[0]) << kShift[PASS - 1];
         rest -= found[1];
+        if (PASS == 3) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                ups += N * tid + i > found[0] ? cb[i] : 0;
+                ties += N * tid + i == found[0] ? cb[i] : 0;
+            }
+        }
         if (PASS < 3) {
             if (slice == 0 && tid == 0) {
                 int *st = sl.state + ((PASS - 1) * sl.pairs + k.pair) * 2;
@@ -258,7 +292,11 @@ __global__ __launch_bounds__(64 * kSliceWaves) void slice_kernel(Kv4Select s, Sl
             up = wave_suffix(up, lane);
             if (lane == 0) sums[wave][0] = up;
             __syncthreads();
-            if (tid == 0) sl.above[((PASS - 1) * sl.pairs + k.pair) * sl.slices + slice] = sums[0][0] + sums[1][0] + sums[2][0] + sums[3][0];
+            if (tid == 0) {
+                up = 0;
+                for (int x = 0; x < kSliceWaves; ++x) up += sums[x][0];
+                sl.above[((PASS - 1) * sl.pairs + k.pair) * sl.slices + slice] = up;
+            }
         }
     }
     if constexpr (PASS < 3) {
@@ -274,12 +312,12 @@ __global__ __launch_bounds__(64 * kSliceWaves) void slice_kernel(Kv4Select s, Sl
         };
         constexpr int kStep = 4 * 64 * kSliceWaves;
         if (rest > 0)
-            for (int t = t0 + 4 * tid; t < t1; t += 8 * kStep) {
-                uint4 w[8];
+            for (int t = t0 + 4 * tid; t < t1; t += 4 * kStep) {
+                uint4 w[4];                                   // loads on their way together
 #pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = keys4(k, t + kStep * i);
+                for (int i = 0; i < 4; ++i) w[i] = keys4(k, t + kStep * i);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) count(t + kStep * i, w[i]);
+                for (int i = 0; i < 4; ++i) count(t + kStep * i, w[i]);
             }
         __syncthreads();
         int *to = hists(PASS) + static_cast<int64_t>(slice) * kBins;
@@ -288,15 +326,7 @@ __global__ __launch_bounds__(64 * kSliceWaves) void slice_kernel(Kv4Select s, Sl
             to[d] = a.x + a.y + a.z + a.w;
         }
     } else {
-        // kept and equal ones in the slices before: tokens that are always kept, then by the three digits
-        int ups = 0, ties = 0;
-        if (tid < slice) {
-            ups = sl.above[k.pair * sl.slices + tid] + sl.above[(sl.pairs + k.pair) * sl.slices + tid];
-            ties = hists(2)[static_cast<int64_t>(tid) * kBins + found[0]];
-        }
-        const int least3 = found[0];
-        for (int x = 0; x < slice; ++x)
-            for (int d = least3 + 1 + tid; d < (1 << kBits[2]); d += 64 * kSliceWaves) ups += hists(2)[static_cast<int64_t>(x) * kBins + d];
+        if (tid < slice) ups += sl.above[k.pair * sl.slices + tid] + sl.above[(sl.pairs + k.pair) * sl.slices + tid];
         ups = wave_suffix(ups, lane);
         ties = wave_suffix(ties, lane);
         if (lane == 0) sums[wave][0] = ups, sums[wave][1] = ties;
@@ -309,15 +339,17 @@ __global__ __launch_bounds__(64 * kSliceWaves) void slice_kernel(Kv4Select s, Sl
         // a wave's run of the slice
         const int run = sl.each / kSliceWaves, r0 = t0 + wave * run, r1 = min(r0 + run, t1);
         int u = 0, e = 0;
-        constexpr int N = 8;                                  // loads on their way together
+        constexpr int N = 4;
         for (int t = r0; t < r1; t += 256 * N) {
             uint4 w[N];
 #pragma unroll
             for (int i = 0; i < N; ++i) w[i] = keys4(k, t + 256 * i + 4 * lane);
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                if (t + 256 * i < r1) count256(k, t + 256 * i + 4 * lane, w[i], least, u, e);
+                if (t + 256 * i < r1) count4(k, t + 256 * i + 4 * lane, w[i], least, u, e);
         }
+        u = wave_suffix(u, lane);
+        e = wave_suffix(e, lane);
         if (lane == 0) sums[wave][0] = u, sums[wave][1] = e;
         __syncthreads();
         for (int x = 0; x < wave; ++x) ups += sums[x][0], ties += sums[x][1];
@@ -360,7 +392,9 @@ int64_t kv4_select_workspace(int64_t B, int64_t heads, int64_t max_tokens) {
 
 hipError_t launch_kv4_select(const Kv4Select &s, void *workspace, hipStream_t st) {
     if (s.max_tokens <= kMostHeld) {
-        auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(s.B, s.heads), dim3(64 * kSelWaves), 0, st, s); };
+        const int64_t pairs = static_cast<int64_t>(s.B) * s.heads;
+        const int shares = s.max_tokens <= 4096 || pairs > 128 ? 1 : pairs > 64 ? 2 : 4;
+        auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(s.B * shares, s.heads), dim3(64 * kSelWaves), 0, st, s, shares); };
         if (s.max_tokens <= 4096) go(select_kernel<1>);
         else if (s.max_tokens <= 16384) go(select_kernel<4>);
         else if (s.max_tokens <= 32768 + 8192) go(select_kernel<10>);
