@@ -187,10 +187,24 @@ constexpr int kMostScanned = 512;
 struct Plan {
     int tm, target, min_chunk, split;     // rows a tile; workgroups wanted; least steps a part; 0: one part a tile
     int pieces, items, slots;             // bounds a KV head: workgroups, tiles in several parts, parts of those
+    int per;                              // pieces of a KV head that one of its XCDs takes; 0: no matter which
 };
 struct Piece {
     int seq, tile, part, parts, slot;     // parts 0: none.  slot: place among the parts kept apart
 };
+
+// Workgroups go to the eight XCDs in turn, each with an L2 of its own.  Where tiles share codes, a KV head's
+// pieces stay on one XCD (on 8 / heads of them in turn, where there are fewer heads), the tiles of a part
+// side by side: 64 rows over 199936 tokens read their codes from beyond L2 ten times otherwise (307 us).
+struct Place {
+    int x, h;
+};
+__host__ __device__ __forceinline__ int common8(int heads) { return heads & 1 ? 1 : heads & 2 ? 2 : heads & 4 ? 4 : 8; }
+__device__ __forceinline__ Place piece_place(const Plan &pl, int heads) {
+    if (pl.per == 0) return Place{static_cast<int>(blockIdx.x), static_cast<int>(blockIdx.y)};
+    const int g = common8(heads), xcd = blockIdx.x & 7, j = blockIdx.x >> 3;
+    return Place{j * (8 / g) + xcd / g, static_cast<int>(blockIdx.y) * g + xcd % g};
+}
 
 // Rows of a sequence that a call handles, and what they see together.
 struct SeqWork {
@@ -270,10 +284,10 @@ __device__ __forceinline__ Piece find_piece(const KvBatch &b, const Kv4Attn &a, 
         const int tiles = (s.n * G + pl.tm - 1) / pl.tm, steps = steps_of(s.lo, s.hi);
         const int chunk = chunk_of(static_cast<uint64_t>(tiles) * static_cast<uint32_t>(steps), pl, heads);
         const int parts = pl.split ? max(1, (steps + chunk - 1) / chunk) : 1;
-        const int tile = ITEMS ? x : x / parts, slot = ITEMS ? x * parts : x;
-        if (tile >= tiles || (ITEMS && parts == 1)) return Piece{0, 0, 0, 0, 0};
+        const int part = ITEMS || tiles == 0 ? 0 : x / tiles, tile = ITEMS || tiles == 0 ? x : x % tiles, slot = tile * parts + part;
+        if (tile >= tiles || part >= parts || (ITEMS && parts == 1)) return Piece{0, 0, 0, 0, 0};
         if (parts > 1 && slot + (ITEMS ? parts : 1) > pl.slots) return Piece{0, 0, 0, 0, 0};
-        return Piece{0, tiles - 1 - tile, ITEMS ? 0 : x % parts, parts, slot};
+        return Piece{0, tiles - 1 - tile, part, parts, slot};
     }
     if (b.B > kMostScanned) return ITEMS ? Piece{0, 0, 0, 0, 0} : find_uncut<TREE>(b, a, pl, G, x);
     uint64_t total = 0;
@@ -309,13 +323,13 @@ __device__ __forceinline__ Piece find_piece(const KvBatch &b, const Kv4Attn &a, 
             p.parts = __builtin_amdgcn_readlane(parts, src);
             const int local = x - (before + __builtin_amdgcn_readlane(sum - mine, src));
             const int slot0 = kept + __builtin_amdgcn_readlane(sum_keep - keep, src);
-            const int tile = ITEMS ? local : local / p.parts;
-            p.part = ITEMS ? 0 : local % p.parts;
+            const int n = __builtin_amdgcn_readlane(tiles, src), tile = ITEMS ? local : local % n;
+            p.part = ITEMS ? 0 : local / n;
             p.slot = slot0 + tile * p.parts + p.part;
             // holds for every ascending q_start; another must not leave the workspace
             if (p.parts > 1 && (p.slot < 0 || p.slot + (ITEMS ? p.parts : 1) > pl.slots)) break;
             // the last rows of a causal prompt see most: they go first
-            p.tile = __builtin_amdgcn_readlane(tiles, src) - 1 - tile;
+            p.tile = n - 1 - tile;
             return p;
         }
         before += __builtin_amdgcn_readlane(sum, 63);
@@ -494,8 +508,9 @@ __global__ __launch_bounds__(256, D == 128 && HL != 2 ? 3 : 2) void attn_kernel(
     __shared__ float lds_o[TG][TM][D + 4], lds_ml[TG][TM][2];
     const int lane = threadIdx.x & 63, tg = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 4, col = lane & 15;
-    const int h = blockIdx.y, G = a.q_heads / c.heads;
-    const Piece pc = find_piece<false, TREE>(b, a, pl, c.heads, G, blockIdx.x);
+    const Place place = ONCE ? Place{static_cast<int>(blockIdx.x), static_cast<int>(blockIdx.y)} : piece_place(pl, c.heads);
+    const int h = place.h, G = a.q_heads / c.heads;
+    const Piece pc = find_piece<false, TREE>(b, a, pl, c.heads, G, place.x);
     if (pc.parts == 0) return;
     const int seq = __builtin_amdgcn_readfirstlane(pc.seq);
     const Share sh = wave_share<TM, TREE>(b, a, pc, seq, G, tg);
@@ -747,8 +762,9 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(Kv4Cache c, KvBatch b
     __shared__ float lds_o[TG][TM][D + 4], lds_ml[TG][TM][2];
     const int lane = threadIdx.x & 63, tg = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 5, col = lane & 31;
-    const int h = blockIdx.y, G = a.q_heads / c.heads;
-    const Piece pc = find_piece<false, TREE>(b, a, pl, c.heads, G, blockIdx.x);
+    const Place place = piece_place(pl, c.heads);
+    const int h = place.h, G = a.q_heads / c.heads;
+    const Piece pc = find_piece<false, TREE>(b, a, pl, c.heads, G, place.x);
     if (pc.parts == 0) return;
     const int seq = __builtin_amdgcn_readfirstlane(pc.seq);
     const Share sh = wave_share<TM, TREE>(b, a, pc, seq, G, tg);
@@ -987,7 +1003,7 @@ Plan make_plan(const KvBatch &b, int heads, int G, int tm, int target, int min_c
     // 20.5 against 17.4 us; 64 of 3900 34.6 against 42.9 us).
     const int64_t whole = kWaves * (tiles < 64 ? 8 : tiles < 256 ? 16 : 32);
     target = 2 * tiles <= target ? target - static_cast<int>(tiles) : 2 * target;
-    Plan p{tm, target, min_chunk, 0, 0, 0, 0};
+    Plan p{tm, target, min_chunk, 0, 0, 0, 0, 0};
     p.split = b.B <= kMostScanned && steps > whole;
     const int64_t even = (target + heads - 1) / heads, cuts = (steps + min_chunk - 1) / min_chunk;
     const int64_t extra = p.split ? (even < rows * cuts ? even : rows * cuts) : 0;
@@ -1019,6 +1035,10 @@ Shape attn_shape(const KvBatch &b, const Kv4Cache &c, int q_heads) {
     // tokens 50 us at 3 a CU, 60 at 6, 68 at 9)
     const int held = !s.once || c.D == 256 ? 2 : c.D == 128 ? 3 : 5;
     s.plan = make_plan(b, c.heads, G, tm, 256 * held, kWaves);
+    if (!s.once) {
+        const int each = 8 / common8(c.heads), per = (s.plan.pieces + each - 1) / each;
+        if (static_cast<int64_t>(per) * 8 * 64 * kWaves < int64_t(1) << 32) s.plan.per = per;
+    }
     s.cols = static_cast<int>(pairs < tm ? pairs : tm);
     s.sums = static_cast<int64_t>(c.heads) * s.plan.slots * s.cols * c.D * 4;
     s.stats = static_cast<int64_t>(c.heads) * s.plan.slots * s.cols * 8;
@@ -1029,7 +1049,7 @@ template <int DT, int D, bool TREE>
 hipError_t launch_d(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, hipStream_t st) {
     const Shape s = attn_shape(b, c, a.q_heads);
     float *part_o = static_cast<float *>(a.workspace), *part_ml = part_o + s.sums / 4;
-    const dim3 grid(s.plan.pieces, c.heads), block(64 * kWaves);
+    const dim3 grid = s.plan.per ? dim3(8 * s.plan.per, c.heads / common8(c.heads)) : dim3(s.plan.pieces, c.heads), block(64 * kWaves);
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, st, c, b, a, s.plan, s.cols, part_o, part_ml); };
     constexpr int HL = DT == kDtF32 ? 2 : 0;
     if (s.once) {
