@@ -316,22 +316,27 @@ __device__ __forceinline__ f16v mma(u4 a, u4 b, f16v c) {
     if constexpr (DT == kDtBf16) return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8, a), __builtin_bit_cast(b8, b), c, 0, 0, 0);
     else return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, a), __builtin_bit_cast(h8, b), c, 0, 0, 0);
 }
+// Two values to the type, in a word.
+template <int DT>
+__device__ __forceinline__ uint32_t pack16(float a, float b) {
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    if constexpr (DT == kDtBf16) {
+        typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, b2));
+    } else {
+        typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+        return __builtin_bit_cast(uint32_t, h2{static_cast<_Float16>(a), static_cast<_Float16>(b)});
+    }
+}
 // Eight values to the type; what that leaves of them.
 template <int DT>
 __device__ __forceinline__ u4 part8(float (&x)[8]) {
     u4 r;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float a = x[2 * i], b = x[2 * i + 1];
-        if constexpr (DT == kDtBf16) {
-            typedef __bf16 b2 __attribute__((ext_vector_type(2)));
-            r[i] = __builtin_bit_cast(uint32_t, b2{static_cast<__bf16>(a), static_cast<__bf16>(b)});
-        } else {
-            typedef _Float16 h2 __attribute__((ext_vector_type(2)));
-            r[i] = __builtin_bit_cast(uint32_t, h2{static_cast<_Float16>(a), static_cast<_Float16>(b)});
-        }
-        x[2 * i] = a - widen16<DT>(r[i] & 0xFFFFu);
-        x[2 * i + 1] = b - widen16<DT>(r[i] >> 16);
+        r[i] = pack16<DT>(x[2 * i], x[2 * i + 1]);
+        x[2 * i] -= widen16<DT>(r[i] & 0xFFFFu);
+        x[2 * i + 1] -= widen16<DT>(r[i] >> 16);
     }
     return r;
 }
@@ -346,6 +351,7 @@ __device__ __forceinline__ int room(const float (&x)[N], int most) {
     m = wave_max_f32(m);
     return m > 0.0f ? min(15 - __builtin_amdgcn_frexp_expf(m), most) : 0;
 }
+constexpr float kLazy = 0x1p-20f;
 __device__ __forceinline__ float pow2(int e) { return __builtin_amdgcn_ldexpf(1.0f, e); }
 
 template <int D, bool OUT>
@@ -382,20 +388,28 @@ __global__ __launch_bounds__(64 * kLinWaves<D>, D == 256 ? 1 : 2) void chunk_ker
 
     const int br = 4 * (tid & 7), bc = 4 * (tid >> 3);
     u2 bq[PQ][4], bk[PQ][4], bv[4];
+    // the thread's block of the next chunk: four values from column bc of rows br .. br + 3
+    const int64_t row0 = sr.first + br;
+    const uint16_t *pk = static_cast<const uint16_t *>(l.k) + row0 * l.ldk + hk * D + bc;
+    const uint16_t *pq = static_cast<const uint16_t *>(l.q) + row0 * l.ldq + hk * D + bc;
+    const uint16_t *pv = static_cast<const uint16_t *>(l.v) + row0 * l.ldv + h * D + v0 + bc;
     auto fetch = [&](int c0) {
+        auto rows4 = [&](auto on) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const bool on = c0 + br + x < sr.n;
-            const int64_t row = sr.first + c0 + br + x;
-            auto four = [&](const void *base, int64_t at) { return on ? *reinterpret_cast<const u2 *>(static_cast<const uint16_t *>(base) + at) : u2{0u, 0u}; };
+            for (int x = 0; x < 4; ++x) {
+                auto four = [&](const uint16_t *at) { return on(x) ? *reinterpret_cast<const u2 *>(at) : u2{0u, 0u}; };
 #pragma unroll
-            for (int y = 0; y < PQ; ++y) {
-                const int64_t d = static_cast<int64_t>(hk) * D + bc + (NT / 2) * y;
-                bk[y][x] = four(l.k, row * l.ldk + d);
-                if (OUT) bq[y][x] = four(l.q, row * l.ldq + d);
+                for (int y = 0; y < PQ; ++y) {
+                    bk[y][x] = four(pk + x * l.ldk + (NT / 2) * y);
+                    if (OUT) bq[y][x] = four(pq + x * l.ldq + (NT / 2) * y);
+                }
+                bv[x] = four(pv + x * l.ldv);
             }
-            bv[x] = four(l.v, row * l.ldv + static_cast<int64_t>(h) * D + v0 + bc);
-        }
+        };
+        rows4([&](int x) { return c0 + br + x < sr.n; });
+        pk += kChunk * l.ldk;
+        pq += kChunk * l.ldq;
+        pv += kChunk * l.ldv;
     };
     const int vr = 32 * (bc >> 5) + 8 * ((bc >> 2) & 3) + 4 * ((bc >> 4) & 1), at_r = place(br);
     auto put = [&](Tile16<D, OUT> &t) {
@@ -420,7 +434,7 @@ __global__ __launch_bounds__(64 * kLinWaves<D>, D == 256 ? 1 : 2) void chunk_ker
     fetch(0);
     f16v s[D / 32];
     load_state<D>(s, OUT ? (sg.segs > 1 ? kept : l.state ? l.state + pair * mat : nullptr) : nullptr, g, vcol);
-    const float l2 = log2_decay(l, h), from = power(l2, col + 1);
+    const float l2 = log2_decay(l, h), from = power(l2, col + 1) * l.scale;
     float near[16];                                       // a^(i - j) of the lane's column i = col
     Ages age;
     age.set(l2, kChunk, g);
@@ -428,9 +442,11 @@ __global__ __launch_bounds__(64 * kLinWaves<D>, D == 256 ? 1 : 2) void chunk_ker
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const int j = 8 * (i >> 2) + 4 * g + (i & 3);
-            near[i] = j <= col ? power(l2, col - j) : 0.0f;
+            near[i] = j <= col ? power(l2, col - j) * l.scale : 0.0f;
         }
-    int es = 0;                                           // the state is 2^-es s
+    // The state is a^aged_by 2^-es s.  Where the products have f32's range (bf16) it ages by the count of
+    // rows alone, and is multiplied out once that comes to kLazy.
+    int es = 0, aged_by = 0;
     put(tiles[0]);
     __syncthreads();
     for (int c0 = 0, at = 0; c0 < sr.n; c0 += kChunk, at ^= 1) {
@@ -475,7 +491,7 @@ __global__ __launch_bounds__(64 * kLinWaves<D>, D == 256 ? 1 : 2) void chunk_ker
 #pragma unroll
             for (int i = 0; i < 16; ++i) pw[i] = p[i] * near[i];
             const int ep = room<DT>(pw, 64);
-            const float fo = DT == kDtF16 ? __builtin_amdgcn_ldexpf(from, ep - ef - es) : from, fp = pow2(ep);
+            const float fo = __builtin_amdgcn_ldexpf(from * power(l2, aged_by), ep - ef - es), fp = pow2(ep);
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[i] *= fo;
 #pragma unroll
@@ -489,10 +505,10 @@ __global__ __launch_bounds__(64 * kLinWaves<D>, D == 256 ? 1 : 2) void chunk_ker
             }
             if (col < n) {
                 const int64_t to = (static_cast<int64_t>(sr.first + c0 + col) * l.heads + h) * D + v0 + 32 * wave + 16 * g;
-                const float f = DT == kDtF16 ? __builtin_amdgcn_ldexpf(l.scale, -ep) : l.scale;
                 u4 y[2];
+                const float f = pow2(-ep);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i >> 2][i & 3] = round16<DT>(o[2 * i] * f) | round16<DT>(o[2 * i + 1] * f) << 16;
+                for (int i = 0; i < 8; ++i) y[i >> 2][i & 3] = DT == kDtF16 ? pack16<DT>(o[2 * i] * f, o[2 * i + 1] * f) : pack16<DT>(o[2 * i], o[2 * i + 1]);
                 u4 *q = reinterpret_cast<u4 *>(static_cast<uint16_t *>(l.o) + to);
                 q[0] = y[0];
                 q[1] = y[1];
@@ -503,16 +519,22 @@ __global__ __launch_bounds__(64 * kLinWaves<D>, D == 256 ? 1 : 2) void chunk_ker
 #pragma unroll
         for (int i = 0; i < 16; ++i) aged[i] = widen16<DT>(i & 1 ? vf[i >> 3][(i & 7) >> 1] >> 16 : vf[i >> 3][(i & 7) >> 1] & 0xFFFFu) * age.w[i];
         const int ea = room<DT>(aged, 32);
-        const float fa = pow2(ea), keep = DT == kDtF16 ? __builtin_amdgcn_ldexpf(age.all, ea - es) : age.all;
-        es = ea;
+        aged_by += n;
+        const float gone = power(l2, aged_by);
+        if (DT == kDtF16 || gone < kLazy) {
+            const float keep = __builtin_amdgcn_ldexpf(gone, ea - es);
 #pragma unroll
-        for (int T = 0; T < D / 32; ++T) s[T] *= keep;
+            for (int T = 0; T < D / 32; ++T) s[T] *= keep;
+            aged_by = 0;
+            es = ea;
+        }
+        const float fa = __builtin_amdgcn_ldexpf(power(-l2, aged_by), es);
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
             float x[8];
             u4 part[NA];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = DT == kDtF16 ? aged[8 * m + i] * fa : aged[8 * m + i];
+            for (int i = 0; i < 8; ++i) x[i] = aged[8 * m + i] * fa;
 #pragma unroll
             for (int y = 0; y < NA; ++y) part[y] = part8<DT>(x);
 #pragma unroll
@@ -525,9 +547,8 @@ __global__ __launch_bounds__(64 * kLinWaves<D>, D == 256 ? 1 : 2) void chunk_ker
         if (more) put(tiles[at ^ 1]);
         __syncthreads();
     }
-    if (DT == kDtF16)
 #pragma unroll
-        for (int T = 0; T < D / 32; ++T) s[T] *= pow2(-es);
+    for (int T = 0; T < D / 32; ++T) s[T] *= __builtin_amdgcn_ldexpf(power(l2, aged_by), -es);
     if (!OUT) store_state<D>(s, kept, g, vcol);
     else if (l.state_out && sr.last) store_state<D>(s, l.state_out + pair * mat, g, vcol);
 }
@@ -549,23 +570,26 @@ __global__ __launch_bounds__(256) void states_kernel(Linear l, Segments sg) {
     }
 }
 
-// Segments a sequence: as many as give each CU two workgroups, of 256 rows at least.
-template <int D>
+// Segments a sequence: as many as fill the chip once (an 8192-row bf16 prompt of 40 heads takes 176 us with 12,
+// 196 with 9, 207 with 19; six f32 sequences of up to 1500 rows and 32 heads of 64 112 us with five, 228 with
+// two), of 128 rows at least (600 rows 36 us, 53 with 256).
+template <int DT, int D>
 int segments(const Linear &l) {
-    const int64_t wgs = static_cast<int64_t>(l.B) * l.heads * kSlices<D>, most = l.max_q / 256, want = 512 / wgs;
+    constexpr int kHeld = D == 256 ? 256 : D == 128 ? 512 : DT == kDtF32 ? 1024 : 768;
+    const int64_t wgs = static_cast<int64_t>(l.B) * l.heads * kSlices<D>, most = l.max_q / 128, want = kHeld / wgs;
     return static_cast<int>(want < 1 || most < 1 ? 1 : want < most ? want : most);
 }
-// Few rows are done one by one.
-template <int D>
-bool row_by_row(const Linear &l) { return l.max_q <= 4; }
+// Few rows are done one by one: 32 sequences of 8 bf16 rows and 16 heads of 128 take 17 us either way, f32 18 and 25 us.
+template <int DT>
+bool row_by_row(const Linear &l) { return l.max_q <= (DT == kDtF32 ? 12 : 8); }
 
 template <int DT, int D>
 hipError_t launch_d(const Linear &l, void *ws, hipStream_t st) {
-    if (row_by_row<D>(l)) {
+    if (row_by_row<DT>(l)) {
         hipLaunchKernelGGL((recurrent_kernel<DT, D>), dim3(l.B, l.heads * (D / kSlice)), dim3(256), 0, st, l);
         return hipGetLastError();
     }
-    const Segments sg{segments<D>(l), static_cast<float *>(ws)};
+    const Segments sg{segments<DT, D>(l), static_cast<float *>(ws)};
     const dim3 grid(static_cast<uint32_t>(l.B) * sg.segs, l.heads * kSlices<D>), block(64 * kLinWaves<D>);
     auto go = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, grid, block, 0, st, l, sg);
@@ -588,16 +612,16 @@ hipError_t launch_t(const Linear &l, void *ws, hipStream_t st) {
     if (l.D == 128) return launch_d<DT, 128>(l, ws, st);
     return launch_d<DT, 256>(l, ws, st);
 }
-template <int D>
-int64_t workspace_d(const Linear &l) {
-    const int segs = row_by_row<D>(l) ? 1 : segments<D>(l);
-    return segs > 1 ? static_cast<int64_t>(l.B) * l.heads * segs * D * D * 4 : 0;
+template <int DT>
+int64_t workspace_t(const Linear &l) {
+    const int64_t segs = row_by_row<DT>(l) ? 1 : l.D == 64 ? segments<DT, 64>(l) : l.D == 128 ? segments<DT, 128>(l) : segments<DT, 256>(l);
+    return segs > 1 ? static_cast<int64_t>(l.B) * l.heads * segs * l.D * l.D * 4 : 0;
 }
 
 }  // namespace
 
-int64_t linear_workspace(const Linear &l, int) {
-    return l.D == 64 ? workspace_d<64>(l) : l.D == 128 ? workspace_d<128>(l) : workspace_d<256>(l);
+int64_t linear_workspace(const Linear &l, int dtype) {
+    return dtype == kDtF32 ? workspace_t<kDtF32>(l) : dtype == kDtBf16 ? workspace_t<kDtBf16>(l) : workspace_t<kDtF16>(l);
 }
 
 hipError_t launch_linear(const Linear &l, int dtype, void *workspace, hipStream_t st) {
