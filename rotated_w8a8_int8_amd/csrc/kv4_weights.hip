@@ -55,18 +55,16 @@ struct Tile {                                             // 32 pairs as the mat
     PairRow row[32];
     int far;                                              // a reference exponent past kNear is among them
 };
-// Eight threads a pair, D / 8 dims each: queries to f16, their largest value in [2^9, 2^10) as in attn_wide_kernel.
+// Eight threads a pair, D / 8 dims each (lane8 the thread's place): queries to f16, their largest value in [2^9,
+// 2^10) as in attn_wide_kernel, and the pair's row.  at: the pair's index in [rows][q_heads]; ci: its row of the sequence.
 template <int DT, int D>
-__device__ __forceinline__ void stage(Tile<DT, D> &t, const Kv4Attn &a, const Observed &ob, int h, int G, int p0) {
+__device__ __forceinline__ PairRow ready(const Kv4Attn &a, const Observed &ob, int64_t at, int ci, bool used, int lane8, u4 (&hi)[D / 64],
+                                         u4 (&lo)[D / 64]) {
     constexpr int N = D / 64;                             // runs of 8 dims
-    const int r = threadIdx.x >> 3, c = threadIdx.x & 7, cp = p0 + r;
-    const bool used = cp < ob.pair1;
-    const int ci = used ? cp / G : 0, cg = used ? cp % G : 0;
-    const int64_t at = static_cast<int64_t>(ob.rr.first + ci) * a.q_heads + h * G + cg;
     float x[N][8], big = 0.0f;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-        const float4 u = load4<DT>(a.q, at * D + 8 * (N * c + n)), v = load4<DT>(a.q, at * D + 8 * (N * c + n) + 4);
+        const float4 u = load4<DT>(a.q, at * D + 8 * (N * lane8 + n)), v = load4<DT>(a.q, at * D + 8 * (N * lane8 + n) + 4);
         x[n][0] = u.x; x[n][1] = u.y; x[n][2] = u.z; x[n][3] = u.w;
         x[n][4] = v.x; x[n][5] = v.y; x[n][6] = v.z; x[n][7] = v.w;
     }
@@ -83,20 +81,28 @@ __device__ __forceinline__ void stage(Tile<DT, D> &t, const Kv4Attn &a, const Ob
     for (int n = 0; n < N; ++n) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[n][i] = used ? __builtin_amdgcn_ldexpf(x[n][i], e) : 0.0f;
-        const int d = 8 * (N * c + n), slot = (d >= D / 2 ? 32 : 0) + r, j = (d & (D / 2 - 1)) >> 3;
-        if constexpr (DT == kDtF32) {
-            u4 hi, lo;
-            f16_split8(x[n], hi, lo);
-            t.hi[j][slot] = hi;
-            t.lo[j][slot] = lo;
-        } else {
-            t.hi[j][slot] = f16_pack8(x[n]);
-        }
+        if constexpr (DT == kDtF32) f16_split8(x[n], hi[n], lo[n]);
+        else hi[n] = f16_pack8(x[n]);
     }
     const bool on = used && ob.base + ci >= 0 && st.y > 0.0f;
+    return PairRow{on ? score_factor(a.sm_scale, e) : 0.0f, on ? st.x : 0.0f, on ? st.y : 0.0f, ob.base + ci};
+}
+template <int DT, int D>
+__device__ __forceinline__ void stage(Tile<DT, D> &t, const Kv4Attn &a, const Observed &ob, int h, int G, int p0) {
+    const int r = threadIdx.x >> 3, c = threadIdx.x & 7, cp = p0 + r;
+    const bool used = cp < ob.pair1;
+    const int ci = used ? cp / G : 0, cg = used ? cp % G : 0;
+    u4 hi[D / 64], lo[D / 64];
+    const PairRow pr = ready<DT, D>(a, ob, static_cast<int64_t>(ob.rr.first + ci) * a.q_heads + h * G + cg, ci, used, c, hi, lo);
+#pragma unroll
+    for (int n = 0; n < D / 64; ++n) {
+        const int d = 8 * (D / 64 * c + n), slot = (d >= D / 2 ? 32 : 0) + r, j = (d & (D / 2 - 1)) >> 3;
+        t.hi[j][slot] = hi[n];
+        if constexpr (DT == kDtF32) t.lo[j][slot] = lo[n];
+    }
     if (c == 0) {
-        t.row[r] = PairRow{on ? score_factor(a.sm_scale, e) : 0.0f, on ? st.x : 0.0f, on ? st.y : 0.0f, ob.base + ci};
-        if (on && fabsf(st.x) > kNear) t.far = 1;
+        t.row[r] = pr;
+        if (fabsf(pr.m) > kNear) t.far = 1;
     }
 }
 
@@ -189,12 +195,50 @@ __global__ __launch_bounds__(256, NQ == 4 || D == 256 || (D == 128 && DT == kDtF
     }
 }
 
-// More pairs: a workgroup's waves take a step each and meet the tiles of pairs together, which are staged through LDS.
+// More pairs: their queries are made ready once (pairs_kernel), as f16 in the order in which a lane takes them,
+// and their rows; every wave reads them as they lie.  A KV head's pairs follow each other row by row.
 template <int DT, int D>
+struct Pairs {
+    u4 *hi, *lo;                      // [heads][rows * G][D / 16][2]: eight dims each
+    PairRow *row;                     // [heads][rows * G]
+    int64_t each;                     // rows * G
+    __host__ __device__ Pairs(void *p, int64_t rows, int heads, int G) : each(rows * G) {
+        row = static_cast<PairRow *>(p);
+        hi = reinterpret_cast<u4 *>(row + each * heads);
+        lo = hi + each * heads * (D / 8);
+    }
+};
+// Eight threads a pair, D / 8 dims each; blockIdx.x: 32 pairs, blockIdx.y: KV head.
+template <int DT, int D>
+__global__ __launch_bounds__(256) void pairs_kernel(Kv4Cache c, KvBatch b, Kv4Attn a, Kv4Weights w) {
+    const int h = blockIdx.y, G = a.q_heads / c.heads, lane8 = threadIdx.x & 7;
+    const Pairs<DT, D> to(w.pairs, b.rows, c.heads, G);
+    const int64_t cp = static_cast<int64_t>(blockIdx.x) * 32 + (threadIdx.x >> 3);
+    const int row = static_cast<int>(min(cp / G, static_cast<int64_t>(b.rows) - 1)), seq = kv_seq_of(b, row);
+    if (cp >= to.each || seq < 0) return;
+    const Observed ob(b, a, w, c.heads, seq);
+    const int64_t mine = cp - static_cast<int64_t>(ob.rr.first) * G;
+    if (mine < ob.pair0 || mine >= ob.pair1) return;
+    u4 hi[D / 64], lo[D / 64];
+    const PairRow r = ready<DT, D>(a, ob, static_cast<int64_t>(row) * a.q_heads + h * G + cp % G, row - ob.rr.first, true, lane8, hi, lo);
+    const int64_t at = h * to.each + cp;
+#pragma unroll
+    for (int n = 0; n < D / 64; ++n) {
+        const int d = 8 * (D / 64 * lane8 + n), half = d >= D / 2, j = (d & (D / 2 - 1)) >> 3;
+        to.hi[at * (D / 8) + 2 * j + half] = hi[n];
+        if constexpr (DT == kDtF32) to.lo[at * (D / 8) + 2 * j + half] = lo[n];
+    }
+    if (lane8 == 0) to.row[at] = r;
+}
+
+// SPLIT 1: a wave takes a step and all its tiles of pairs; 4: the workgroup's waves take every fourth tile of one
+// step, and their sums meet in LDS.
+template <int DT, int D, int SPLIT>
 __global__ __launch_bounds__(256, 2) void weights_many_kernel(Kv4Cache c, KvBatch b, Kv4Attn a, Kv4Weights w, int parts) {
     constexpr int NK = D / 16;
     constexpr bool SP = DT == kDtF32;
-    __shared__ Tile<DT, D> tiles[2];
+    __shared__ PairRow tile_rows[4][32];
+    __shared__ float sums[SPLIT == 4 ? 4 : 1][32];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 5, col = lane & 31;
     const int h = blockIdx.y, G = a.q_heads / c.heads;
@@ -202,60 +246,92 @@ __global__ __launch_bounds__(256, 2) void weights_many_kernel(Kv4Cache c, KvBatc
     const Observed ob(b, a, w, c.heads, seq);
     if (ob.rr.n == 0) return;
     const Pages pages(c, b, seq, h, (ob.len + 31) >> 5);
+    const Pairs<DT, D> from(w.pairs, b.rows, c.heads, G);
+    const int64_t pair_at = h * from.each + static_cast<int64_t>(ob.rr.first) * G;
     float *const row = w.weight + (static_cast<int64_t>(seq) * c.heads + h) * w.ldw;
-    if (threadIdx.x == 0) tiles[0].far = tiles[1].far = 0;
-    for (int first = 4 * part; first < pages.end; first += 4 * parts) {
-        const int step = first + wave, t = (step << 5) + col, page = pages.id(step);
+    for (int first = 4 / SPLIT * part; first < pages.end; first += 4 / SPLIT * parts) {
+        const int step = SPLIT == 4 ? first : first + wave, t = (step << 5) + col, page = pages.id(step);
         const bool here = page >= 0 && page < c.pages;
         Codes<D> codes;
         load_codes<D>(codes, c, pages.token(page, step), g, col);
         const float old = row[min(t, w.factor != 0.0f ? static_cast<int>(w.ldw) - 1 : 0)];
-        // rows before the first token see none of the four steps
+        // rows before the first token see none of the step
         int p0 = ob.pair0;
-        if (a.causal && (first << 5) - ob.base > 0) p0 += max(0, ((first << 5) - ob.base) * G - ob.pair0) & ~31;
-        __syncthreads();                                  // the last steps' tiles are read
-        if (p0 < ob.pair1) stage<DT, D>(tiles[0], a, ob, h, G, p0);
-        __syncthreads();
+        if (a.causal && (step << 5) - ob.base > 0) p0 += max(0, ((step << 5) - ob.base) * G - ob.pair0) & ~31;
+        if (SPLIT == 4) p0 += 32 * wave;
         u4 kf[NK];
 #pragma unroll
         for (int j = 0; j < NK; ++j) kf[j] = levels8(codes.k[j >> 2][j & 3]);
         const float ks = f16_widen(codes.scale);
         float total = 0.0f;
-        for (int at = 0; p0 < ob.pair1; p0 += 32, at ^= 1) {
-            if (p0 + 32 < ob.pair1) stage<DT, D>(tiles[at ^ 1], a, ob, h, G, p0 + 32);
-            const Tile<DT, D> &tile = tiles[at];
-            f16v s;
+        if (here)
+            for (; p0 < ob.pair1; p0 += 32 * SPLIT) {
+                const int cp = min(p0 + col, ob.pair1 - 1);
+                const int64_t at = (pair_at + cp) * (D / 8) + g;
+                u4 hi[NK], lo[SP ? NK : 1];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[i] = 0.0f;
+                for (int j = 0; j < NK; ++j) {
+                    hi[j] = from.hi[at + 2 * j];
+                    if constexpr (SP) lo[j] = from.lo[at + 2 * j];
+                }
+                PairRow r = from.row[pair_at + cp];
+                if (p0 + col >= ob.pair1) r.inv = 0.0f;       // past the last pair: its scores again, which count nothing
+                const bool far = __any(fabsf(r.m) > kNear);
+                if (g == 0) tile_rows[wave][col] = r;
+                __builtin_amdgcn_wave_barrier();
+                f16v s;
 #pragma unroll
-            for (int j = 0; j < NK; ++j) {
-                if constexpr (SP) s = mma32(tile.lo[j][lane], kf[j], s);
-                s = mma32(tile.hi[j][lane], kf[j], s);
+                for (int i = 0; i < 16; ++i) s[i] = 0.0f;
+#pragma unroll
+                for (int j = 0; j < NK; ++j) {
+                    if constexpr (SP) s = mma32(lo[j], kf[j], s);
+                    s = mma32(hi[j], kf[j], s);
+                }
+                float sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sum += probability(tile_rows[wave][8 * (i >> 2) + 4 * g + (i & 3)], s[i], ks, far, a.causal, a.window, t);
+                total += sum;
+                __builtin_amdgcn_wave_barrier();
             }
-            float sum = 0.0f;
-            const bool far = tile.far;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) sum += probability(tile.row[8 * (i >> 2) + 4 * g + (i & 3)], s[i], ks, far, a.causal, a.window, t);
-            total += sum;
+        if (SPLIT == 4) {
+            total += __shfl_xor(total, 32);
+            if (g == 0) sums[wave][col] = total;
             __syncthreads();
+            total = 0.5f * (sums[0][col] + sums[1][col] + sums[2][col] + sums[3][col]);      // add_weight adds both halves
+            __syncthreads();
+            if (wave != 0) continue;
         }
-        add_weight(w, row, ob, t, g, here ? total : 0.0f, old);
+        add_weight(w, row, ob, t, g, total, old);
     }
 }
+
+// Pairs of a sequence and KV head that a call observes at most.
+int64_t most_pairs(const KvBatch &b, int G, int observe) { return static_cast<int64_t>(observe > 0 && observe < b.max_q ? observe : b.max_q) * G; }
+// Pairs that weights_few_kernel holds.
+template <int D>
+constexpr int kFew = D == 256 ? 8 : 32;
 
 template <int DT, int D>
 hipError_t launch_d(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, const Kv4Weights &w, hipStream_t st) {
     const int64_t steps = ((static_cast<int64_t>(b.max_pages) << b.page_shift) + 31) >> 5, all = static_cast<int64_t>(b.B) * c.heads;
-    const int64_t most = (steps + 3) / 4, even = 2048 / all;
-    const int parts = static_cast<int>(even < 1 ? 1 : even < most ? even : most);
-    if (parts == 0) return hipSuccess;
-    const dim3 grid(static_cast<uint32_t>(b.B) * parts, c.heads), block(64 * kWaves);
-    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, st, c, b, a, w, parts); };
-    const int64_t rows = w.observe > 0 && w.observe < b.max_q ? w.observe : b.max_q, pairs = rows * (a.q_heads / c.heads);
-    if (pairs <= 8) go(weights_few_kernel<DT, D, 1>);
-    else if (D <= 128 && pairs <= 32) go(weights_few_kernel<DT, D <= 128 ? D : 64, 4>);
-    else go(weights_many_kernel<DT, D>);
-    return hipGetLastError();
+    if (steps == 0) return hipSuccess;
+    const int G = a.q_heads / c.heads;
+    // workgroups, of `held` steps each: about 2048, fewer where there are fewer steps
+    auto go = [&](auto kernel, int held) {
+        const int64_t most = (steps + held - 1) / held, even = 2048 / all;
+        const int parts = static_cast<int>(even < 1 ? 1 : even < most ? even : most);
+        hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(b.B) * parts, c.heads), dim3(64 * kWaves), 0, st, c, b, a, w, parts);
+        return hipGetLastError();
+    };
+    const int64_t pairs = most_pairs(b, G, w.observe);
+    if (pairs <= 8) return go(weights_few_kernel<DT, D, 1>, 4);
+    if (pairs <= kFew<D>) return go(weights_few_kernel<DT, D <= 128 ? D : 64, 4>, 4);
+    const int64_t each = static_cast<int64_t>(b.rows) * G;
+    hipLaunchKernelGGL((pairs_kernel<DT, D>), dim3(static_cast<uint32_t>((each + 31) / 32), c.heads), dim3(256), 0, st, c, b, a, w);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    // few steps: four waves to a step
+    if ((steps + 3) / 4 * all >= 1024) return go(weights_many_kernel<DT, D, 1>, 4);
+    return go(weights_many_kernel<DT, D, 4>, 1);
 }
 template <int DT>
 hipError_t launch_t(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, const Kv4Weights &w, hipStream_t st) {
@@ -265,6 +341,12 @@ hipError_t launch_t(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, const
 }
 
 }  // namespace
+
+int64_t kv4_weights_workspace(const Kv4Cache &c, const KvBatch &b, int q_heads, int dtype) {
+    const int64_t pairs = static_cast<int64_t>(b.rows) * q_heads, most = static_cast<int64_t>(b.max_q) * (q_heads / c.heads);
+    if (most <= (c.D == 256 ? kFew<256> : kFew<128>)) return 0;
+    return pairs * (c.D * (dtype == kDtF32 ? 4 : 2) + static_cast<int64_t>(sizeof(PairRow)));
+}
 
 hipError_t launch_kv4_weights(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, const Kv4Weights &w, int dtype, hipStream_t st) {
     if (dtype == kDtF32) return launch_t<kDtF32>(c, b, a, w, st);

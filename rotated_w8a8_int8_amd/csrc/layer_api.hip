@@ -228,8 +228,12 @@ struct Extra {
 int64_t stats_at(const rad_kv4_cache *c, const rad_kv_batch *b, int64_t q_heads, int32_t dtype) {
     return (rad::kv4_attn_workspace(cache_args(c), batch_args(c, b), static_cast<int>(q_heads), dtype) + 15) / 16 * 16;
 }
+// Behind them what the second pass makes ready.
+int64_t pairs_at(const rad_kv4_cache *c, const rad_kv_batch *b, int64_t q_heads, int32_t dtype) {
+    return stats_at(c, b, q_heads, dtype) + (b->rows * q_heads * 8 + 15) / 16 * 16;
+}
 int64_t weights_workspace(const rad_kv4_cache *c, const rad_kv_batch *b, int64_t q_heads, int32_t dtype) {
-    return stats_at(c, b, q_heads, dtype) + b->rows * q_heads * 8;
+    return pairs_at(c, b, q_heads, dtype) + rad::kv4_weights_workspace(cache_args(c), batch_args(c, b), static_cast<int>(q_heads), dtype);
 }
 
 int attend(const rad_kv4_cache *cache, const rad_kv_batch *batch, const void *q, int64_t q_heads, float sm_scale, int causal,
@@ -270,7 +274,8 @@ int attend(const rad_kv4_cache *cache, const rad_kv_batch *batch, const void *q,
     const hipError_t err = rad::launch_kv4_attn(ca, ba, at, dtype, st);
     if (err != hipSuccess || !x.weights) return hip_status(err);
     const int observe = x.observe < batch->rows ? static_cast<int>(x.observe) : 0;
-    return hip_status(rad::launch_kv4_weights(ca, ba, at, rad::Kv4Weights{x.weight, x.ldw, observe, x.factor}, dtype, st));
+    void *pairs = static_cast<char *>(workspace) + pairs_at(cache, batch, q_heads, dtype);
+    return hip_status(rad::launch_kv4_weights(ca, ba, at, rad::Kv4Weights{x.weight, x.ldw, observe, x.factor, pairs}, dtype, st));
 }
 
 // Sizes of the selection; 1 when there is nothing to select.

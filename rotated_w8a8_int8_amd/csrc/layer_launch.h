@@ -57,7 +57,9 @@ struct Kv4Weights {
     int64_t ldw;
     int observe;             // last rows that count; 0: all
     float factor;
+    void *pairs;             // queries made ready, where a call has many (kv4_weights_workspace)
 };
+int64_t kv4_weights_workspace(const Kv4Cache &c, const KvBatch &b, int q_heads, int dtype);
 hipError_t launch_kv4_weights(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, const Kv4Weights &w, int dtype, hipStream_t st);
 
 struct Kv4Select {
