@@ -21,7 +21,7 @@
 // 8192 f32 tokens of 40 query and 8 KV heads of 128 take 94 us, 4.4 TB/s of the
 // 412 MB it moves, its mix of reads and writes being a copy's (4.9 TB/s); one
 // token of 8 sequences 3.1 us, 8 x 16 bf16 tokens 7.9 us.  The read-back is a
-// stream: 12 us for the 8192 tokens.
+// stream: 11 us for the 8192 tokens.
 #include "kv4.h"
 #include "rotate_quant.h"
 
@@ -384,6 +384,66 @@ __global__ __launch_bounds__(256) void kv4_read_kernel(Kv4Cache c, KvBatch b, ui
     reinterpret_cast<uint4 *>(v + idx * D)[lane] = eight(vw, vs);
 }
 
+// Sequences of many rows: a wave reads an octet of tokens of a head at once, its values' dwords once for all
+// eight (one token at a time reads them eight times: 8 sequences of 4096 rows 45 us, 31 us so).  blockIdx.x: 8 rows, of which
+// a wave takes the octets that begin there, blockIdx.y: four heads.
+template <int D>
+__global__ __launch_bounds__(256) void kv4_read_octets_kernel(Kv4Cache c, KvBatch b, uint16_t *__restrict__ k, uint16_t *__restrict__ v) {
+    constexpr int NV = D / 64, KB = D / 16;                   // dims of values and bytes of keys a lane
+    const int lane = threadIdx.x & 63, h = blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (h >= c.heads) return;
+    const int row_end = min(static_cast<int>(blockIdx.x + 1) * 8, b.rows);
+    for (int row = blockIdx.x * 8; row < row_end;) {
+        const SeqOfRow found = kv_seq_of_wave(b, row);
+        if (found.seq < 0) {
+            ++row;
+            continue;
+        }
+        const RowRange rr = found.rr;
+        const int pos0 = found.len - rr.n, seq_end = min(rr.first + rr.n, row_end), last = pos0 + rr.n - 1;
+        int p = max(pos0 + (row - rr.first), 0);              // the first row here that begins an octet or the tokens
+        if ((p & 7) != 0 && p != max(pos0, 0)) p = (p | 7) + 1;
+        for (; rr.first + (p - pos0) < seq_end; p = (p | 7) + 1) {
+            const int t0 = p & ~7, page = kv_page(b, found.seq, t0, c.pages);
+            if (page < 0) continue;
+            const int64_t vec = ((static_cast<int64_t>(page) * c.heads + h) << c.page_shift) + (t0 & ((1 << c.page_shift) - 1));
+            const int64_t out = (static_cast<int64_t>(rr.first + (t0 - pos0)) * c.heads + h) * D, next = static_cast<int64_t>(c.heads) * D;
+            // keys: token lane / 8, D / 8 dims
+            const int e = lane >> 3, te = t0 + e;
+            uint32_t kw[KB / 4], vw[NV];
+            const uint32_t *kp = reinterpret_cast<const uint32_t *>(c.k_codes + (vec + e) * (D / 2) + KB * (lane & 7));
+            const uint32_t *vp = reinterpret_cast<const uint32_t *>(c.v_codes) + (vec >> 3) * D + NV * lane;
+#pragma unroll
+            for (int i = 0; i < KB / 4; ++i) kw[i] = kp[i];
+#pragma unroll
+            for (int i = 0; i < NV; ++i) vw[i] = vp[i];
+            const float ks = f16_widen(c.k_scale[vec + e]);
+            const uint4 vs8 = *reinterpret_cast<const uint4 *>(c.v_scale + vec);
+            const uint32_t vs[4] = {vs8.x, vs8.y, vs8.z, vs8.w};
+            auto pair = [](f2v x, float s) { return bf16_round(x[0] * s) | (bf16_round(x[1] * s) << 16); };
+            if (te >= p && te <= last) {
+#pragma unroll
+                for (int i = 0; i < KB / 4; ++i)
+                    reinterpret_cast<uint4 *>(k + out + e * next)[KB / 4 * (lane & 7) + i] =
+                        make_uint4(pair(e2m1_pair<0>(kw[i]), ks), pair(e2m1_pair<1>(kw[i]), ks), pair(e2m1_pair<2>(kw[i]), ks),
+                                   pair(e2m1_pair<3>(kw[i]), ks));
+            }
+            // values: the lane's NV dims of each token
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (t0 + j < p || t0 + j > last) continue;
+                const float s = f16_widen(j & 1 ? vs[j >> 1] >> 16 : vs[j >> 1] & 0xFFFFu);
+                auto value = [&](int i) { return bf16_round(e2m1_pair<0>(vw[i] >> (4 * j))[0] * s); };
+                uint16_t *at = v + out + j * next + NV * lane;
+                if constexpr (NV == 1) *at = static_cast<uint16_t>(value(0));
+                else if constexpr (NV == 2) *reinterpret_cast<uint32_t *>(at) = value(0) | value(1) << 16;
+                else *reinterpret_cast<uint2 *>(at) = make_uint2(value(0) | value(1) << 16, value(2) | value(3) << 16);
+            }
+        }
+        row = rr.first + rr.n;
+    }
+}
+
 }  // namespace
 
 hipError_t launch_kv4_append(const Kv4Cache &c, const KvBatch &b, const Kv4New &n, int dtype, hipStream_t st) {
@@ -391,6 +451,14 @@ hipError_t launch_kv4_append(const Kv4Cache &c, const KvBatch &b, const Kv4New &
 }
 
 hipError_t launch_kv4_read(const Kv4Cache &c, const KvBatch &b, uint16_t *k, uint16_t *v, hipStream_t st) {
+    // few rows take more workgroups one by one (256 rows of 8 heads 3.3 us, 4.6 us by octets)
+    if (b.q_start && b.rows / b.B >= 8 && static_cast<int64_t>(b.rows) * c.heads >= 8192) {
+        const dim3 grid((b.rows + 7) / 8, (c.heads + 3) / 4), block(256);
+        if (c.D == 64) hipLaunchKernelGGL(kv4_read_octets_kernel<64>, grid, block, 0, st, c, b, k, v);
+        else if (c.D == 128) hipLaunchKernelGGL(kv4_read_octets_kernel<128>, grid, block, 0, st, c, b, k, v);
+        else hipLaunchKernelGGL(kv4_read_octets_kernel<256>, grid, block, 0, st, c, b, k, v);
+        return hipGetLastError();
+    }
     const int per = 2048 / c.D;
     const dim3 grid(static_cast<uint32_t>((static_cast<int64_t>(b.rows) * c.heads + per - 1) / per)), block(256);
     if (c.D == 64) hipLaunchKernelGGL(kv4_read_kernel<64>, grid, block, 0, st, c, b, k, v);

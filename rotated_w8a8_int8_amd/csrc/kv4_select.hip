@@ -135,8 +135,8 @@ __device__ __forceinline__ void count4(const Task &k, int t, uint4 w, uint32_t l
 //
 // blockIdx.x: sequence * shares + share, blockIdx.y: head; 4 NV keys a thread.  Every share finds the least
 // key, and lists its share of each wave's run (64 runs of 32768 tokens: 36 us with one share).  Weights crowd into few digits (a binade is four of
-// them), so a digit has eight counters, by lane.
-constexpr int kSelWaves = 16, kCopies = 8;
+// them), so a digit has eight counters, by lane (two where there are few keys).
+constexpr int kSelWaves = 16;
 // A token's number, hidden from the compiler, which would keep what it once found out about each
 // (whether it competes: 64 of them spilled 430 scalar registers).
 __device__ __forceinline__ int anew(int t) {
@@ -145,6 +145,7 @@ __device__ __forceinline__ int anew(int t) {
 }
 template <int NV>
 __global__ __launch_bounds__(64 * kSelWaves) void select_kernel(Kv4Select s, int shares) {
+    constexpr int kCopies = NV == 1 ? 2 : 8;
     __shared__ int hist[kBins * kCopies];
     __shared__ int part[kSelWaves], found[2], above[kSelWaves], equal[kSelWaves];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -175,8 +176,13 @@ __global__ __launch_bounds__(64 * kSelWaves) void select_kernel(Kv4Select s, int
                 }
             __syncthreads();
             find_digit<kSelWaves>(rest, part, found, [&](int d) {
-                const int4 a = *reinterpret_cast<const int4 *>(&hist[kCopies * d]), b = *reinterpret_cast<const int4 *>(&hist[kCopies * d + 4]);
-                return a.x + a.y + a.z + a.w + b.x + b.y + b.z + b.w;
+                int c = 0;
+#pragma unroll
+                for (int x = 0; x < kCopies; x += 2) {
+                    const int2 a = *reinterpret_cast<const int2 *>(&hist[kCopies * d + x]);
+                    c += a.x + a.y;
+                }
+                return c;
             });
             least |= static_cast<uint32_t>(found[0]) << kShift[pass];
             known |= ((1u << kBits[pass]) - 1) << kShift[pass];
