@@ -351,7 +351,7 @@ __device__ __forceinline__ int room(const float (&x)[N], int most) {
     m = wave_max_f32(m);
     return m > 0.0f ? min(15 - __builtin_amdgcn_frexp_expf(m), most) : 0;
 }
-constexpr float kLazy = 0x1p-20f;
+constexpr float kLazy = 0x1p-8f;
 __device__ __forceinline__ float pow2(int e) { return __builtin_amdgcn_ldexpf(1.0f, e); }
 
 template <int D, bool OUT>

@@ -77,6 +77,24 @@ def test_select_of_many_sequences(torch):
     run_select(torch, rng.integers(0, 400, 700), 2, 100, 2, 30, "spread", seed=2)
 
 
+def test_select_of_many_long_sequences(torch):
+    # more (sequence, head) pairs than slices are wanted for
+    rng = np.random.default_rng(6)
+    n, L, heads, budget = 550, 66048, 2, 500
+    w = torch.rand((n, heads, L), device="cuda")
+    seq_len = rng.integers(60000, L + 1, n)
+    batch = C.device_batch(torch, np.zeros((n, L // 32), np.int32), seq_len, None, n)
+    kept, count, kw = B.kv4_select(batch, w, budget, 2, 30)
+    assert torch.all(count == budget)
+    for b in (0, 17, 311, n - 1):
+        for h in range(heads):
+            x = w[b, h].cpu().numpy()
+            want = X.select(x, int(seq_len[b]), budget, 2, 30)
+            assert np.array_equal(kept[b, h].cpu().numpy(), want) and np.array_equal(kw[b, h, :budget].cpu().numpy(), x[want])
+    # every list ascends, and its least weight is no less than what a sort puts there
+    assert torch.all(kept[..., 1:] > kept[..., :-1])
+
+
 def test_lengths_past_the_room_are_cut_to_it(torch):
     run_select(torch, [500, 96, 97], 1, 20, 1, 2, "spread", seed=4, width=3)
 
