@@ -604,7 +604,8 @@ int rad_kv4_move(const rad_kv4_cache *cache, const rad_kv_batch *batch, const in
  *   workspace  device memory, 16-byte aligned, of at least the bytes that
  *              rad_linear_attn_workspace gives for the same sizes (NULL when that is 0).
  *
- * D is 64, 128 or 256; heads a multiple of qk_heads, at most 1024; B, rows < 2^22; B * heads < 2^22.
+ * D is 64, 128 or 256; heads a multiple of qk_heads, at most 1024; B, rows < 2^22; B * heads < 2^22; and
+ * one launch holds fewer than 2^24 workgroups of 128 rows and more of a head's 128 values (2^25 for D = 64).
  * scale is finite.  The state and all sums are held in f32; RAD_DT_F32 values are
  * multiplied in f32.  For the 16-bit types the weights of the rows of a chunk and the state meet the
  * matrix cores as pairs of 16-bit parts (16 bits at least).

@@ -285,6 +285,13 @@ int check_select(int64_t B, int64_t heads, int64_t max_tokens) {
     return B == 0 || heads == 0 ? 1 : RAD_OK;
 }
 
+rad::Linear linear_args(const rad_linear *in, const float *state, float *state_out, float scale, void *o) {
+    const int64_t most = in->q_start ? (in->max_q < in->rows ? in->max_q : in->rows) : 1;
+    return rad::Linear{in->q, in->k, in->v, in->ldq, in->ldk, in->ldv, in->log_decay, in->q_start, static_cast<int>(in->B),
+                       static_cast<int>(in->rows), static_cast<int>(most), static_cast<int>(in->qk_heads),
+                       static_cast<int>(in->heads), static_cast<int>(in->D), state, state_out, scale, o};
+}
+
 // Sizes of linear attention; 1 when there is neither a row nor a state to hand on.
 int check_linear(const rad_linear *in) {
     if (!in) return RAD_E_NULL;
@@ -296,13 +303,8 @@ int check_linear(const rad_linear *in) {
     if (in->ldq < nk || in->ldk < nk || in->ldv < in->heads * in->D) return RAD_E_SHAPE;
     if (in->ldq > kI32Max || in->ldk > kI32Max || in->ldv > kI32Max) return RAD_E_RANGE;
     if (!in->q_start && in->rows != in->B) return RAD_E_SHAPE;
-    return in->B == 0 ? 1 : RAD_OK;
-}
-rad::Linear linear_args(const rad_linear *in, const float *state, float *state_out, float scale, void *o) {
-    const int64_t most = in->q_start ? (in->max_q < in->rows ? in->max_q : in->rows) : 1;
-    return rad::Linear{in->q, in->k, in->v, in->ldq, in->ldk, in->ldv, in->log_decay, in->q_start, static_cast<int>(in->B),
-                       static_cast<int>(in->rows), static_cast<int>(most), static_cast<int>(in->qk_heads),
-                       static_cast<int>(in->heads), static_cast<int>(in->D), state, state_out, scale, o};
+    if (in->B == 0) return 1;
+    return rad::linear_fits(linear_args(in, nullptr, nullptr, 1.0f, nullptr), in->dtype) ? RAD_OK : RAD_E_RANGE;
 }
 }  // namespace
 

@@ -92,6 +92,7 @@ struct Linear {
     float scale;
     void *o;
 };
+bool linear_fits(const Linear &l, int dtype);      // one launch holds the call
 int64_t linear_workspace(const Linear &l, int dtype);
 hipError_t launch_linear(const Linear &l, int dtype, void *workspace, hipStream_t st);
 

@@ -102,9 +102,11 @@ __global__ __launch_bounds__(256) void recurrent_kernel(Linear l) {
 // g.  Value column r of the wave is v = 16 g + 4 q + e, so that a lane stores 16
 // consecutive values of a row.
 //
-// A sequence is cut into `segs` segments, a workgroup each: where it has several, a first
+// A sequence is cut into segments of `each` rows, a workgroup each: where it has several, a first
 // kernel works out what each adds to the state, a second hands the states on, and the last
-// one begins each segment with its state.
+// one begins each segment with its state.  Sequence b's segments have the places from
+// q_start[b] / each + b on, which leaves room for max(1, ceil(n / each)) of them, so that places
+// need no other sequence's length (empty sequences at the end have the last places).
 typedef float f16v __attribute__((ext_vector_type(16)));
 typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
@@ -119,19 +121,53 @@ template <int D>
 constexpr int kSlices = D / (32 * kLinWaves<D>);         // workgroups a head
 
 struct Segments {
-    int segs;
-    float *states;            // [B][heads][segs][D][D]: state before each segment (segs > 1)
+    int each, places;         // rows a segment, a multiple of kChunk; places a head
+    float *states;            // [places][heads][D][D]: state before each segment of a sequence of several
 };
+__device__ __forceinline__ int first_place(const Linear &l, const Segments &sg, int seq) {
+    return min((l.q_start ? l.q_start[seq] : seq) / sg.each, sg.places - l.B) + seq;
+}
 
-// The segment's rows: all whole chunks but the sequence's last.
+// What a workgroup takes: all rows are whole chunks but the sequence's last.
 struct SegRows {
-    int first, n;             // rows of the call
+    int seq, first, n;        // the sequence; the call's rows
+    int segs;                 // the sequence's segments; 0: nothing lies in this place
     bool last;
 };
-__device__ __forceinline__ SegRows segment_rows(const Rows &r, int segs, int seg) {
-    const int chunks = (r.n + kChunk - 1) / kChunk, each = (chunks + segs - 1) / segs * kChunk;
-    const int lo = min(seg * each, r.n), hi = min(lo + each, r.n);
-    return SegRows{r.first + lo, hi - lo, seg == segs - 1};
+// Segment seg of a sequence.
+__device__ __forceinline__ SegRows segment_rows(const Linear &l, const Segments &sg, int seq, int seg) {
+    const Rows r = linear_rows(l, seq);
+    const int segs = max(1, (r.n + sg.each - 1) / sg.each), lo = min(seg * sg.each, r.n);
+    return SegRows{seq, r.first + lo, min(sg.each, r.n - lo), seg < segs ? segs : 0, seg == segs - 1};
+}
+// The segment in a place: its sequence is the last one whose first place is not past it; 64 are looked at a trip.
+// Every lane of the wave calls it and gets the same answer.
+__device__ __forceinline__ SegRows segment_in(const Linear &l, const Segments &sg, int place) {
+    int seq = 0;
+    for (int n = l.B; n > 1;) {                               // it lies in [seq, seq + n)
+        const int each = (n + 63) >> 6, i = (threadIdx.x & 63) * each;
+        const int at = max(__popcll(__ballot(i < n && first_place(l, sg, seq + min(i, n - 1)) <= place)) - 1, 0) * each;
+        seq += at;
+        n = min(each, n - at);
+    }
+    seq = __builtin_amdgcn_readfirstlane(seq);
+    const int seg = place - first_place(l, sg, seq);
+    return seg >= 0 ? segment_rows(l, sg, seq, seg) : SegRows{seq, 0, 0, 0, false};
+}
+
+// What a workgroup is about.  Workgroups go to the eight XCDs in turn: those that read the same queries and keys
+// (slices of a head, heads that share a key head) follow each other on one, where its L2 serves them
+// (8192 bf16 rows of 16 heads of 256: 292 us, 435 us spread over the XCDs).
+struct Item {
+    int place, hk, h, slice;
+};
+__device__ __forceinline__ Item item_of(const Linear &l, const Segments &sg, int slices) {
+    const int each = l.heads / l.qk_heads, sub = each * slices, x = blockIdx.x;
+    const int u = x / (8 * sub) * 8 + (x & 7), j = (x >> 3) % sub, hk = u / sg.places;
+    return Item{u % sg.places, hk, hk * each + j / slices, j % slices};
+}
+int64_t items(const Linear &l, const Segments &sg, int slices) {
+    return (static_cast<int64_t>(sg.places) * l.qk_heads + 7) / 8 * 8 * (l.heads / l.qk_heads) * slices;
 }
 
 // a^k, a = 2^l2
@@ -184,18 +220,18 @@ __global__ __launch_bounds__(64 * kLinWaves<D>, D == 256 ? 1 : 2) void chunk_f32
     __shared__ TileF32<D> tile;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 5, col = lane & 31;
-    const int seq = blockIdx.x / sg.segs, seg = blockIdx.x % sg.segs, h = blockIdx.y / NS, v0 = VC * (blockIdx.y % NS);
-    const int hk = h / (l.heads / l.qk_heads);
-    const Rows rows = linear_rows(l, seq);
-    const SegRows sr = segment_rows(rows, sg.segs, seg);
-    const int64_t pair = static_cast<int64_t>(seq) * l.heads + h, mat = static_cast<int64_t>(D) * D;
-    float *const kept = sg.states + (pair * sg.segs + seg) * mat;
+    const Item it = item_of(l, sg, NS);
+    if (it.hk >= l.qk_heads) return;
+    const int h = it.h, v0 = VC * it.slice, hk = it.hk;
+    const SegRows sr = segment_in(l, sg, it.place);
+    const int64_t pair = static_cast<int64_t>(sr.seq) * l.heads + h, mat = static_cast<int64_t>(D) * D;
+    float *const kept = sg.states + (static_cast<int64_t>(it.place) * l.heads + h) * mat;
     const int vcol = v0 + 32 * wave + value_of(col);
-    if (OUT && rows.n == 0 && (!l.state_out || l.state == l.state_out)) return;
-    if (!OUT && sr.last) return;
+    if (sr.segs == 0 || (!OUT && sr.last)) return;
+    if (OUT && sr.n == 0 && (!l.state_out || l.state == l.state_out)) return;
 
     f16v s[D / 32];
-    load_state<D>(s, OUT ? (sg.segs > 1 ? kept : l.state ? l.state + pair * mat : nullptr) : nullptr, g, vcol);
+    load_state<D>(s, OUT ? (sr.segs > 1 ? kept : l.state ? l.state + pair * mat : nullptr) : nullptr, g, vcol);
     const float l2 = log2_decay(l, h), from = power(l2, col + 1);
     float near[16];                                       // a^(i - j) of the lane's column i = col
     Ages age;
@@ -376,15 +412,15 @@ __global__ __launch_bounds__(64 * kLinWaves<D>, D == 256 ? 1 : 2) void chunk_ker
     __shared__ Tile16<D, OUT> tiles[2];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 5, col = lane & 31;
-    const int seq = blockIdx.x / sg.segs, seg = blockIdx.x % sg.segs, h = blockIdx.y / NS, v0 = VC * (blockIdx.y % NS);
-    const int hk = h / (l.heads / l.qk_heads);
-    const Rows rows = linear_rows(l, seq);
-    const SegRows sr = segment_rows(rows, sg.segs, seg);
-    const int64_t pair = static_cast<int64_t>(seq) * l.heads + h, mat = static_cast<int64_t>(D) * D;
-    float *const kept = sg.states + (pair * sg.segs + seg) * mat;
+    const Item it = item_of(l, sg, NS);
+    if (it.hk >= l.qk_heads) return;
+    const int h = it.h, v0 = VC * it.slice, hk = it.hk;
+    const SegRows sr = segment_in(l, sg, it.place);
+    const int64_t pair = static_cast<int64_t>(sr.seq) * l.heads + h, mat = static_cast<int64_t>(D) * D;
+    float *const kept = sg.states + (static_cast<int64_t>(it.place) * l.heads + h) * mat;
     const int vcol = v0 + 32 * wave + value_of(col);
-    if (OUT && rows.n == 0 && (!l.state_out || l.state == l.state_out)) return;
-    if (!OUT && sr.last) return;
+    if (sr.segs == 0 || (!OUT && sr.last)) return;
+    if (OUT && sr.n == 0 && (!l.state_out || l.state == l.state_out)) return;
 
     const int br = 4 * (tid & 7), bc = 4 * (tid >> 3);
     u2 bq[PQ][4], bk[PQ][4], bv[4];
@@ -433,7 +469,7 @@ __global__ __launch_bounds__(64 * kLinWaves<D>, D == 256 ? 1 : 2) void chunk_ker
     };
     fetch(0);
     f16v s[D / 32];
-    load_state<D>(s, OUT ? (sg.segs > 1 ? kept : l.state ? l.state + pair * mat : nullptr) : nullptr, g, vcol);
+    load_state<D>(s, OUT ? (sr.segs > 1 ? kept : l.state ? l.state + pair * mat : nullptr) : nullptr, g, vcol);
     const float l2 = log2_decay(l, h), from = power(l2, col + 1) * l.scale;
     float near[16];                                       // a^(i - j) of the lane's column i = col
     Ages age;
@@ -557,27 +593,40 @@ __global__ __launch_bounds__(64 * kLinWaves<D>, D == 256 ? 1 : 2) void chunk_ker
 __global__ __launch_bounds__(256) void states_kernel(Linear l, Segments sg) {
     const int64_t pair = blockIdx.x;
     const int seq = static_cast<int>(pair / l.heads), h = static_cast<int>(pair % l.heads);
-    const Rows rows = linear_rows(l, seq);
-    const int64_t mat = static_cast<int64_t>(l.D) * l.D, at = blockIdx.y * 1024 + 4 * threadIdx.x;
-    const float l2 = log2_decay(l, h);
-    float *w = sg.states + pair * sg.segs * mat + at;
+    const int segs = segment_rows(l, sg, seq, 0).segs;
+    if (segs == 1) return;                                    // its state is read where it is
+    const int64_t mat = static_cast<int64_t>(l.D) * l.D, next = mat * l.heads, at = blockIdx.y * 1024 + 4 * threadIdx.x;
+    const float a = power(log2_decay(l, h), sg.each);         // the last segment's is of no use here
+    float *w = sg.states + first_place(l, sg, seq) * next + h * mat + at;
     float4 s = l.state ? load4<kDtF32>(l.state, pair * mat + at) : make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int seg = 0; seg < sg.segs; ++seg) {
-        const float4 add = seg + 1 < sg.segs ? load4<kDtF32>(w, seg * mat) : s;
-        store4<kDtF32>(w, seg * mat, s);
-        const float a = power(l2, segment_rows(rows, sg.segs, seg).n);
+    for (int seg = 0; seg < segs; ++seg, w += next) {
+        const float4 add = seg + 1 < segs ? load4<kDtF32>(w, 0) : s;
+        store4<kDtF32>(w, 0, s);
         s = make_float4(fmaf(a, s.x, add.x), fmaf(a, s.y, add.y), fmaf(a, s.z, add.z), fmaf(a, s.w, add.w));
     }
 }
 
-// Segments a sequence: as many as fill the chip once (an 8192-row bf16 prompt of 40 heads takes 176 us with 12,
-// 196 with 9, 207 with 19; six f32 sequences of up to 1500 rows and 32 heads of 64 112 us with five, 228 with
-// two), of 128 rows at least (600 rows 36 us, 53 with 256).
+// Rows a segment: so many that the segments fill the chip once (an 8192-row bf16 prompt of 40 heads takes 176 us
+// with 12, 196 with 9, 207 with 19; 8 x 1000 rows 147 us whole, 207 us in halves), 128 at least (600 rows
+// 36 us, 53 with 256).  Places that stay empty count too: 288 workgroups of which 32 had nothing to do took 440 us
+// where the 256 others take 296.
 template <int DT, int D>
-int segments(const Linear &l) {
+Segments make_segments(const Linear &l, void *ws) {
     constexpr int kHeld = D == 256 ? 256 : D == 128 ? 512 : DT == kDtF32 ? 1024 : 768;
-    const int64_t wgs = static_cast<int64_t>(l.B) * l.heads * kSlices<D>, most = l.max_q / 128, want = kHeld / wgs;
-    return static_cast<int>(want < 1 || most < 1 ? 1 : want < most ? want : most);
+    const int64_t a_head = kHeld / (l.heads * kSlices<D>), all = static_cast<int64_t>(l.B) * l.max_q;
+    int64_t even;
+    if (10 * static_cast<int64_t>(l.rows) >= 9 * all) {
+        const int64_t segs = a_head / l.B > 1 ? a_head / l.B : 1;
+        even = (l.max_q + segs - 1) / segs;
+    } else {
+        const int64_t segs = a_head - (l.B - 1) / 2 > 1 ? a_head - (l.B - 1) / 2 : 1;
+        even = (l.rows + segs - 1) / segs;
+    }
+    const int64_t most = (static_cast<int64_t>(l.max_q) + kChunk - 1) / kChunk * kChunk;
+    const int64_t each = ((even > 128 ? even : 128) + kChunk - 1) / kChunk * kChunk;
+    Segments sg{static_cast<int>(each < most ? each : most), 0, static_cast<float *>(ws)};
+    sg.places = (l.rows + sg.each - 1) / sg.each + l.B - 1;
+    return sg;
 }
 // Few rows are done one by one: 32 sequences of 8 bf16 rows and 16 heads of 128 take 17 us either way, f32 18 and 25 us.
 template <int DT>
@@ -589,8 +638,8 @@ hipError_t launch_d(const Linear &l, void *ws, hipStream_t st) {
         hipLaunchKernelGGL((recurrent_kernel<DT, D>), dim3(l.B, l.heads * (D / kSlice)), dim3(256), 0, st, l);
         return hipGetLastError();
     }
-    const Segments sg{segments<DT, D>(l), static_cast<float *>(ws)};
-    const dim3 grid(static_cast<uint32_t>(l.B) * sg.segs, l.heads * kSlices<D>), block(64 * kLinWaves<D>);
+    const Segments sg = make_segments<DT, D>(l, ws);
+    const dim3 grid(static_cast<uint32_t>(items(l, sg, kSlices<D>))), block(64 * kLinWaves<D>);
     auto go = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, grid, block, 0, st, l, sg);
         return hipGetLastError();
@@ -599,7 +648,7 @@ hipError_t launch_d(const Linear &l, void *ws, hipStream_t st) {
         if constexpr (DT == kDtF32) return go(chunk_f32_kernel<DT, D, decltype(out)::value>);
         else return go(chunk_kernel<DT, D, decltype(out)::value>);
     };
-    if (sg.segs > 1) {
+    if (l.max_q > sg.each) {
         if (hipError_t e = chunks(std::false_type{}); e != hipSuccess) return e;
         hipLaunchKernelGGL(states_kernel, dim3(l.B * l.heads, D * D / 1024), dim3(256), 0, st, l, sg);
         if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
@@ -612,13 +661,30 @@ hipError_t launch_t(const Linear &l, void *ws, hipStream_t st) {
     if (l.D == 128) return launch_d<DT, 128>(l, ws, st);
     return launch_d<DT, 256>(l, ws, st);
 }
+template <int DT, int D>
+bool fits_d(const Linear &l) {
+    return row_by_row<DT>(l) || items(l, make_segments<DT, D>(l, nullptr), kSlices<D>) * 64 * kLinWaves<D> < int64_t(1) << 32;
+}
+template <int DT>
+bool fits_t(const Linear &l) {
+    return l.D == 64 ? fits_d<DT, 64>(l) : l.D == 128 ? fits_d<DT, 128>(l) : fits_d<DT, 256>(l);
+}
+template <int DT, int D>
+int64_t workspace_d(const Linear &l) {
+    if (row_by_row<DT>(l)) return 0;
+    const Segments sg = make_segments<DT, D>(l, nullptr);
+    return l.max_q > sg.each ? static_cast<int64_t>(sg.places) * l.heads * D * D * 4 : 0;
+}
 template <int DT>
 int64_t workspace_t(const Linear &l) {
-    const int64_t segs = row_by_row<DT>(l) ? 1 : l.D == 64 ? segments<DT, 64>(l) : l.D == 128 ? segments<DT, 128>(l) : segments<DT, 256>(l);
-    return segs > 1 ? static_cast<int64_t>(l.B) * l.heads * segs * l.D * l.D * 4 : 0;
+    return l.D == 64 ? workspace_d<DT, 64>(l) : l.D == 128 ? workspace_d<DT, 128>(l) : workspace_d<DT, 256>(l);
 }
 
 }  // namespace
+
+bool linear_fits(const Linear &l, int dtype) {
+    return dtype == kDtF32 ? fits_t<kDtF32>(l) : dtype == kDtBf16 ? fits_t<kDtBf16>(l) : fits_t<kDtF16>(l);
+}
 
 int64_t linear_workspace(const Linear &l, int dtype) {
     return dtype == kDtF32 ? workspace_t<kDtF32>(l) : dtype == kDtBf16 ? workspace_t<kDtBf16>(l) : workspace_t<kDtF16>(l);

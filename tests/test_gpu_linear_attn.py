@@ -85,6 +85,14 @@ def test_ragged_rows(torch, new, D, dtype):
 
 
 @pytest.mark.parametrize("dtype", C.DTYPES)
+@pytest.mark.parametrize("new,pad", [([256, 0, 128, 0, 0], 0), ([0, 0, 384, 128], 0), ([512], 0), ([129, 127, 0], 128), ([0, 700, 1, 0, 33], 5),
+                                     ([128] * 9, 0), ([20] * 40 + [300], 1)])
+def test_sequences_of_whole_segments_and_none(torch, new, pad, dtype):
+    print("segments", new, pad, dtype, flush=True)
+    run(torch, new, 4, 2, 64, dtype, seed=len(new), pad=pad)
+
+
+@pytest.mark.parametrize("dtype", C.DTYPES)
 @pytest.mark.parametrize("n", [1000, 2049])
 def test_prompts(torch, n, dtype):
     print("prompt", n, dtype, flush=True)
