@@ -51,10 +51,10 @@ __device__ __forceinline__ uint4 keys4(const Task &k, int t) {
     return make_uint4(key_of(w.x), key_of(w.y), key_of(w.z), key_of(w.w));
 }
 
-// Digit d with as many keys in higher digits as `over` < rest <= over + its own, of C counts a digit
+// found: digit d with as many keys in higher digits as `over` < rest <= over + its own, over, and its own, of C counts a digit
 // (the lowest thread has the lowest digits); by a workgroup of W waves, 2048 / (64 W) digits a thread.
 template <int W, class Count>
-__device__ __forceinline__ void find_digit(int rest, int (&part)[W], int (&found)[2], Count count) {
+__device__ __forceinline__ void find_digit(int rest, int (&part)[W], int (&found)[3], Count count) {
     constexpr int N = kBins / (64 * W);
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     int c[N], all = 0;
@@ -65,13 +65,13 @@ __device__ __forceinline__ void find_digit(int rest, int (&part)[W], int (&found
     }
     const int sum = wave_suffix(all, lane);
     if (lane == 0) part[wave] = sum;
-    if (tid == 0) found[0] = found[1] = 0;
+    if (tid == 0) found[0] = found[1] = found[2] = 0;
     __syncthreads();
     int over = sum - all;
     for (int x = wave + 1; x < W; ++x) over += part[x];
 #pragma unroll
     for (int i = N - 1; i >= 0; --i) {
-        if (rest > over && rest <= over + c[i]) found[0] = N * tid + i, found[1] = over;
+        if (rest > over && rest <= over + c[i]) found[0] = N * tid + i, found[1] = over, found[2] = c[i];
         over += c[i];
     }
     __syncthreads();
@@ -133,10 +133,11 @@ __device__ __forceinline__ void count4(const Task &k, int t, uint4 w, uint32_t l
 
 // ---- keys in registers ---------------------------------------------------------
 //
-// blockIdx.x: sequence * shares + share, blockIdx.y: head; 4 NV keys a thread.  Every share finds the least
-// key, and lists its share of each wave's run (64 runs of 32768 tokens: 36 us with one share).  Weights crowd into few digits (a binade is four of
-// them), so a digit has eight counters, by lane (two where there are few keys).
-constexpr int kSelWaves = 16;
+// blockIdx.x: sequence * shares + share, blockIdx.y: head; 4 NV keys a thread, 4096 tokens in a row at a time.  Every
+// share finds the least key, and lists its share of the tokens (64 sequences of 32768 tokens: 36 us with one
+// share).  Weights crowd into few digits (a binade is four of them), so a digit has four counters, by lane; the
+// keys that share the first digit are few and go on in LDS, where kHeldKeys hold them (32 us without).
+constexpr int kSelWaves = 16, kRun = 256 * kSelWaves, kHeldKeys = 4096;
 // A token's number, hidden from the compiler, which would keep what it once found out about each
 // (whether it competes: 64 of them spilled 430 scalar registers).
 __device__ __forceinline__ int anew(int t) {
@@ -145,75 +146,122 @@ __device__ __forceinline__ int anew(int t) {
 }
 template <int NV>
 __global__ __launch_bounds__(64 * kSelWaves) void select_kernel(Kv4Select s, int shares) {
-    constexpr int kCopies = NV == 1 ? 2 : 8;
+    constexpr int kCopies = NV == 1 ? 2 : 4, kBlocks = NV * kSelWaves;       // blocks of 256 tokens
     __shared__ int hist[kBins * kCopies];
-    __shared__ int part[kSelWaves], found[2], above[kSelWaves], equal[kSelWaves];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int seq = blockIdx.x / shares, share = blockIdx.x % shares, i0 = NV * share / shares, i1 = NV * (share + 1) / shares;
+    __shared__ uint32_t held[kHeldKeys];
+    __shared__ int part[kSelWaves], found[3], n_held, ups_of[kBlocks], ties_of[kBlocks];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int seq = blockIdx.x / shares, share = blockIdx.x % shares;
     const Task k(s, seq, blockIdx.y);
     if (share == 0 && blockIdx.y == 0 && tid == 0) s.count[seq] = k.n;
-    const int t0 = wave * (256 * NV) + 4 * lane;              // a wave's run: NV times 256 tokens
-    uint4 w[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) w[i] = keys4(k, t0 + 256 * i);
-    uint32_t least = 0, known = 0;
-    int rest = k.L > k.n ? k.need : 0;
-    if (k.L > k.n) {
-#pragma unroll
-        for (int pass = 0; pass < 3; ++pass) {
-            for (int i = tid; i < kBins * kCopies; i += 64 * kSelWaves) hist[i] = 0;
-            __syncthreads();
-            if (rest > 0)
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const uint32_t key[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-                    const int t = anew(t0 + 256 * i);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        if (k.competes(t + c) && (key[c] & known) == least)
-                            atomicAdd(&hist[(key[c] >> kShift[pass] & ((1u << kBits[pass]) - 1)) * kCopies + (lane & (kCopies - 1))], 1);
-                    }
-                }
-            __syncthreads();
-            find_digit<kSelWaves>(rest, part, found, [&](int d) {
-                int c = 0;
-#pragma unroll
-                for (int x = 0; x < kCopies; x += 2) {
-                    const int2 a = *reinterpret_cast<const int2 *>(&hist[kCopies * d + x]);
-                    c += a.x + a.y;
-                }
-                return c;
-            });
-            least |= static_cast<uint32_t>(found[0]) << kShift[pass];
-            known |= ((1u << kBits[pass]) - 1) << kShift[pass];
-            rest -= found[1];
-            __syncthreads();
-        }
-    }
-    if (k.L > k.n) {
-        int ups = 0, ties = 0, u0 = 0, e0 = 0;                // of the wave's run; of it before the share
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (i == i0) u0 = ups, e0 = ties;
-            count4(k, anew(t0 + 256 * i), w[i], least, ups, ties);
-        }
-        ups = wave_suffix(ups, lane);
-        ties = wave_suffix(ties, lane);
-        if (lane == 0) above[wave] = ups, equal[wave] = ties;
-        ups = __builtin_amdgcn_readfirstlane(wave_suffix(u0, lane));
-        ties = __builtin_amdgcn_readfirstlane(wave_suffix(e0, lane));
-        __syncthreads();
-        for (int x = 0; x < wave; ++x) ups += above[x], ties += equal[x];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (i < i0 || i >= i1) continue;
-            list256(s, k, anew(t0 + 256 * i), w[i], anew(least), rest, ups, ties);
-        }
-    } else {
-        for (int t = tid + 64 * kSelWaves * share; t < k.L; t += 64 * kSelWaves * shares) {      // everything is kept
+    if (k.L == k.n) {                                         // everything is kept
+        for (int t = tid + 64 * kSelWaves * share; t < k.L; t += 64 * kSelWaves * shares) {
             s.kept[k.pair * s.budget + t] = t;
             if (s.kept_weight) s.kept_weight[k.pair * s.ld_kept + t] = k.w[t];
         }
+        return;
+    }
+    const int t0 = 256 * wave + 4 * lane, runs = (k.L + kRun - 1) / kRun;
+    uint4 w[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) w[i] = keys4(k, t0 + kRun * i);
+    uint32_t least = 0, known = 0;
+    int rest = k.need;
+    bool few = false;                                         // the keys still in question are in `held`
+    if (tid == 0) n_held = 0;
+#pragma unroll
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = kShift[pass], mask = (1 << kBits[pass]) - 1;
+        for (int i = tid; i < (few ? kBins : kBins * kCopies); i += 64 * kSelWaves) hist[i] = 0;
+        __syncthreads();
+        if (few) {
+            for (int i = tid; i < found[2]; i += 64 * kSelWaves)
+                if ((held[i] & known) == least) atomicAdd(&hist[held[i] >> shift & mask], 1);
+        } else if (rest > 0) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (i >= runs) continue;
+                const uint32_t key[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                const int t = anew(t0 + kRun * i);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (k.competes(t + c) && (key[c] & known) == least)
+                        atomicAdd(&hist[(key[c] >> shift & mask) * kCopies + (lane & (kCopies - 1))], 1);
+            }
+        }
+        const int before = few ? found[2] : 0;
+        __syncthreads();
+        find_digit<kSelWaves>(rest, part, found, [&](int d) {
+            if (few) return hist[d];
+            int c = 0;
+#pragma unroll
+            for (int x = 0; x < kCopies; x += 2) {
+                const int2 a = *reinterpret_cast<const int2 *>(&hist[kCopies * d + x]);
+                c += a.x + a.y;
+            }
+            return c;
+        });
+        least |= static_cast<uint32_t>(found[0]) << shift;
+        known |= static_cast<uint32_t>(mask) << shift;
+        rest -= found[1];
+        const int same = found[2];
+        __syncthreads();
+        if (few) {
+            if (tid == 0) found[2] = before;                  // the list stays as long as it is
+        } else if (pass == 0 && same <= kHeldKeys) {
+            few = true;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (i >= runs) continue;
+                const uint32_t key[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                const int t = anew(t0 + kRun * i);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (k.competes(t + c) && (key[c] & known) == least) held[atomicAdd(&n_held, 1)] = key[c];
+            }
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (i >= runs) continue;
+        int ups = 0, ties = 0;
+        count4(k, anew(t0 + kRun * i), w[i], least, ups, ties);
+        const int sum = wave_scan(ups | ties << 16);
+        if (lane == 63) {
+            ups_of[i * kSelWaves + wave] = sum & 0xFFFF;
+            ties_of[i * kSelWaves + wave] = sum >> 16;
+        }
+    }
+    __syncthreads();
+    if (wave == 0) {                                          // of the blocks before each
+        int u[NV / 4 + 1], e[NV / 4 + 1], all_u = 0, all_e = 0;
+        constexpr int N = (kBlocks + 63) / 64;
+#pragma unroll
+        for (int x = 0; x < N; ++x) {
+            const int at = N * lane + x;
+            u[x] = at < runs * kSelWaves ? ups_of[at] : 0;
+            e[x] = at < runs * kSelWaves ? ties_of[at] : 0;
+            all_u += u[x];
+            all_e += e[x];
+        }
+        all_u = wave_scan(all_u) - all_u;
+        all_e = wave_scan(all_e) - all_e;
+#pragma unroll
+        for (int x = 0; x < N; ++x) {
+            const int at = N * lane + x;
+            if (at < runs * kSelWaves) ups_of[at] = all_u, ties_of[at] = all_e;
+            all_u += u[x];
+            all_e += e[x];
+        }
+    }
+    __syncthreads();
+    const int i0 = runs * share / shares, i1 = runs * (share + 1) / shares;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (i < i0 || i >= i1) continue;
+        int ups = ups_of[i * kSelWaves + wave], ties = ties_of[i * kSelWaves + wave];
+        list256(s, k, anew(t0 + kRun * i), w[i], anew(least), rest, ups, ties);
     }
 }
 
@@ -234,7 +282,7 @@ struct Slices {
 template <int PASS>
 __global__ __launch_bounds__(64 * kSliceWaves) void slice_kernel(Kv4Select s, Slices sl) {
     __shared__ int hist[PASS < 3 ? kBins * kSliceCopies : 1];
-    __shared__ int part[kSliceWaves], found[2], sums[kSliceWaves][2];
+    __shared__ int part[kSliceWaves], found[3], sums[kSliceWaves][2];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, slice = blockIdx.x % sl.slices, seq = blockIdx.x / sl.slices;
     const Task k(s, seq, blockIdx.y);
     if (PASS == 0 && slice == 0 && blockIdx.y == 0 && tid == 0) s.count[seq] = k.n;
