@@ -295,6 +295,16 @@ __global__ __launch_bounds__(64 * kSliceWaves) void slice_kernel(Kv4Select s, Sl
             }
         return;
     }
+    // the first keys are asked for before the digits are looked for: PASS < 3 takes 4096 tokens at a time, the list
+    // a run a wave
+    constexpr int N = 4, kStep = PASS < 3 ? 4 * 64 * kSliceWaves : 256;
+    const int run = sl.each / kSliceWaves, r0 = PASS < 3 ? t0 + 4 * tid : t0 + wave * run + 4 * lane;
+    uint4 w[N];
+    auto load = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = keys4(k, t + kStep * i);
+    };
+    load(r0);
     auto hists = [&](int pass) { return sl.hist + (static_cast<int64_t>(pass) * sl.pairs + k.pair) * sl.slices * kBins; };
     uint32_t least = 0, known = 0;
     int rest = k.need, ups = 0, ties = 0;                     // above and equal to the least key in the slices before
@@ -364,14 +374,11 @@ __global__ __launch_bounds__(64 * kSliceWaves) void slice_kernel(Kv4Select s, Sl
                     atomicAdd(&hist[(key[c] >> kShift[PASS] & ((1u << kBits[PASS]) - 1)) * kSliceCopies + (lane & (kSliceCopies - 1))], 1);
             }
         };
-        constexpr int kStep = 4 * 64 * kSliceWaves;
         if (rest > 0)
-            for (int t = t0 + 4 * tid; t < t1; t += 4 * kStep) {
-                uint4 w[4];                                   // loads on their way together
+            for (int t = r0; t < t1; t += N * kStep) {
+                if (t != r0) load(t);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = keys4(k, t + kStep * i);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) count(t + kStep * i, w[i]);
+                for (int i = 0; i < N; ++i) count(t + kStep * i, w[i]);
             }
         __syncthreads();
         int *to = hists(PASS) + static_cast<int64_t>(slice) * kBins;
@@ -390,42 +397,38 @@ __global__ __launch_bounds__(64 * kSliceWaves) void slice_kernel(Kv4Select s, Sl
         ties = 0;
         for (int x = 0; x < kSliceWaves; ++x) ups += sums[x][0], ties += sums[x][1];
         __syncthreads();
-        // a wave's run of the slice
-        const int run = sl.each / kSliceWaves, r0 = t0 + wave * run, r1 = min(r0 + run, t1);
+        const int r1 = min(t0 + (wave + 1) * run, t1);        // the end of the wave's run
         int u = 0, e = 0;
-        constexpr int N = 4;
-        for (int t = r0; t < r1; t += 256 * N) {
-            uint4 w[N];
-#pragma unroll
-            for (int i = 0; i < N; ++i) w[i] = keys4(k, t + 256 * i + 4 * lane);
+        for (int t = r0; t - 4 * lane < r1; t += N * kStep) {
+            if (t != r0) load(t);
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                if (t + 256 * i < r1) count4(k, t + 256 * i + 4 * lane, w[i], least, u, e);
+                if (t - 4 * lane + kStep * i < r1) count4(k, t + kStep * i, w[i], least, u, e);
         }
         u = wave_suffix(u, lane);
         e = wave_suffix(e, lane);
         if (lane == 0) sums[wave][0] = u, sums[wave][1] = e;
         __syncthreads();
         for (int x = 0; x < wave; ++x) ups += sums[x][0], ties += sums[x][1];
-        for (int t = r0; t < r1; t += 256 * N) {
-            uint4 w[N];
-#pragma unroll
-            for (int i = 0; i < N; ++i) w[i] = keys4(k, t + 256 * i + 4 * lane);
+        const bool once = run <= N * kStep;                   // the run is still in registers
+        for (int t = r0; t - 4 * lane < r1; t += N * kStep) {
+            if (!once) load(t);
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                if (t + 256 * i < r1) list256(s, k, t + 256 * i + 4 * lane, w[i], least, rest, ups, ties);
+                if (t - 4 * lane + kStep * i < r1) list256(s, k, t + kStep * i, w[i], least, rest, ups, ties);
         }
     }
 }
 
 // Tokens that a workgroup's registers hold; sequences that may be longer are cut into slices.
+constexpr int kSliceTokens = 16384;
 constexpr int kMostHeld = 64 * kSelWaves * 4 * 16;
 
 Slices make_slices(int64_t pairs, int64_t max_tokens, void *workspace) {
     constexpr int kUnit = 256 * kSliceWaves;
     Slices sl{};
     sl.pairs = pairs;
-    const int64_t most = (max_tokens + 8191) / 8192, want = pairs < 1024 ? 1024 / pairs : 1;
+    const int64_t most = (max_tokens + kSliceTokens - 1) / kSliceTokens, want = pairs < 1024 ? 1024 / pairs : 1;
     const int64_t n = most < want ? most : want < kMostSlices ? want : kMostSlices;
     const int64_t each = ((max_tokens + n - 1) / n + kUnit - 1) / kUnit * kUnit;
     sl.each = static_cast<int>(each);
