@@ -36,6 +36,10 @@ __device__ __forceinline__ TokenRange seen(int pos, int len, int causal, int win
 
 // ---- trees ------------------------------------------------------------------
 //
+// Bound as the causal form is: 64 nodes over 199936 tokens (262 GFLOP, bf16) take 300 us and 5.9 us for
+// the join, 0.87 PFLOP/s; 8 trees of up to 60 nodes over up to 16000 tokens 82 + 9.2 us; 8 nodes over 500 tokens
+// 11.7 us, latency.
+//
 // A sequence's n rows are nodes 0 .. n - 1, at tokens base .. base + n - 1.  Every row sees the tokens
 // before base (from `lo` on, where there is a window); among the nodes its mask decides, a bit
 // a node.  Only the steps that hold nodes look at masks: two bytes for eight tokens.
@@ -195,7 +199,7 @@ struct Piece {
 
 // Workgroups go to the eight XCDs in turn, each with an L2 of its own.  Where tiles share codes, a KV head's
 // pieces stay on one XCD (on 8 / heads of them in turn, where there are fewer heads), the tiles of a part
-// side by side: 64 rows over 199936 tokens read their codes from beyond L2 ten times otherwise (307 us).
+// side by side (8 trees of up to 60 nodes over 16000 tokens 87 -> 82 us, an 8192-token prompt 850 -> 844 us).
 struct Place {
     int x, h;
 };
@@ -275,8 +279,10 @@ __device__ __forceinline__ Piece find_uncut(const KvBatch &b, const Kv4Attn &a, 
 }
 
 // The x-th piece of a KV head (ITEMS false), or the x-th tile in several parts (true).
-// Every lane of the wave calls it and gets the same answer.
-template <bool ITEMS, bool TREE>
+// Every lane of the wave calls it and gets the same answer.  ONCE: a sequence is one tile, so that no order
+// of tiles matters, and the count of tiles, held early, would be the one register too many (64 decoding
+// sequences of up to 16000 tokens, bf16: 94 us, 96 us with it in scratch).
+template <bool ITEMS, bool ONCE, bool TREE>
 __device__ __forceinline__ Piece find_piece(const KvBatch &b, const Kv4Attn &a, const Plan &pl, int heads, int G, int x) {
     const int lane = threadIdx.x & 63;
     if (b.B == 1) {
@@ -284,8 +290,14 @@ __device__ __forceinline__ Piece find_piece(const KvBatch &b, const Kv4Attn &a, 
         const int tiles = (s.n * G + pl.tm - 1) / pl.tm, steps = steps_of(s.lo, s.hi);
         const int chunk = chunk_of(static_cast<uint64_t>(tiles) * static_cast<uint32_t>(steps), pl, heads);
         const int parts = pl.split ? max(1, (steps + chunk - 1) / chunk) : 1;
-        const int part = ITEMS || tiles == 0 ? 0 : x / tiles, tile = ITEMS || tiles == 0 ? x : x % tiles, slot = tile * parts + part;
-        if (tile >= tiles || part >= parts || (ITEMS && parts == 1)) return Piece{0, 0, 0, 0, 0};
+        int part, tile, slot;
+        if constexpr (ITEMS || ONCE) {
+            part = ITEMS ? 0 : x % parts, tile = ITEMS ? x : x / parts, slot = ITEMS ? x * parts : x;
+            if (tile >= tiles || (ITEMS && parts == 1)) return Piece{0, 0, 0, 0, 0};
+        } else {
+            if (tiles == 0 || x / tiles >= parts) return Piece{0, 0, 0, 0, 0};
+            part = x / tiles, tile = x % tiles, slot = tile * parts + part;
+        }
         if (parts > 1 && slot + (ITEMS ? parts : 1) > pl.slots) return Piece{0, 0, 0, 0, 0};
         return Piece{0, tiles - 1 - tile, part, parts, slot};
     }
@@ -323,13 +335,20 @@ __device__ __forceinline__ Piece find_piece(const KvBatch &b, const Kv4Attn &a, 
             p.parts = __builtin_amdgcn_readlane(parts, src);
             const int local = x - (before + __builtin_amdgcn_readlane(sum - mine, src));
             const int slot0 = kept + __builtin_amdgcn_readlane(sum_keep - keep, src);
-            const int n = __builtin_amdgcn_readlane(tiles, src), tile = ITEMS ? local : local % n;
-            p.part = ITEMS ? 0 : local / n;
+            int tile;
+            if constexpr (ITEMS || ONCE) {
+                tile = ITEMS ? local : local / p.parts;
+                p.part = ITEMS ? 0 : local % p.parts;
+            } else {
+                const int n = __builtin_amdgcn_readlane(tiles, src);
+                tile = local % n;
+                p.part = local / n;
+            }
             p.slot = slot0 + tile * p.parts + p.part;
             // holds for every ascending q_start; another must not leave the workspace
             if (p.parts > 1 && (p.slot < 0 || p.slot + (ITEMS ? p.parts : 1) > pl.slots)) break;
             // the last rows of a causal prompt see most: they go first
-            p.tile = n - 1 - tile;
+            p.tile = __builtin_amdgcn_readlane(tiles, src) - 1 - tile;
             return p;
         }
         before += __builtin_amdgcn_readlane(sum, 63);
@@ -510,7 +529,7 @@ __global__ __launch_bounds__(256, D == 128 && HL != 2 ? 3 : 2) void attn_kernel(
     const int g = lane >> 4, col = lane & 15;
     const Place place = ONCE ? Place{static_cast<int>(blockIdx.x), static_cast<int>(blockIdx.y)} : piece_place(pl, c.heads);
     const int h = place.h, G = a.q_heads / c.heads;
-    const Piece pc = find_piece<false, TREE>(b, a, pl, c.heads, G, place.x);
+    const Piece pc = find_piece<false, ONCE, TREE>(b, a, pl, c.heads, G, place.x);
     if (pc.parts == 0) return;
     const int seq = __builtin_amdgcn_readfirstlane(pc.seq);
     const Share sh = wave_share<TM, TREE>(b, a, pc, seq, G, tg);
@@ -764,7 +783,7 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(Kv4Cache c, KvBatch b
     const int g = lane >> 5, col = lane & 31;
     const Place place = piece_place(pl, c.heads);
     const int h = place.h, G = a.q_heads / c.heads;
-    const Piece pc = find_piece<false, TREE>(b, a, pl, c.heads, G, place.x);
+    const Piece pc = find_piece<false, false, TREE>(b, a, pl, c.heads, G, place.x);
     if (pc.parts == 0) return;
     const int seq = __builtin_amdgcn_readfirstlane(pc.seq);
     const Share sh = wave_share<TM, TREE>(b, a, pc, seq, G, tg);
@@ -944,7 +963,7 @@ __global__ __launch_bounds__(512) void attn_join_kernel(Kv4Cache c, KvBatch b, K
     __shared__ f4 lds_o[N][L];
     __shared__ float lds_ml[N][2];
     const int h = blockIdx.y, G = a.q_heads / c.heads;
-    const Piece pc = find_piece<true, TREE>(b, a, pl, c.heads, G, blockIdx.x);
+    const Piece pc = find_piece<true, false, TREE>(b, a, pl, c.heads, G, blockIdx.x);
     if (pc.parts == 0) return;
     const SeqWork sw = seq_work<TREE>(b, a, pc.seq);
     const int64_t first = (static_cast<int64_t>(h) * pl.slots + pc.slot) * cols;
