@@ -6,6 +6,10 @@
 // dwords of its own dimensions, D/64 a lane, from which it takes a nibble each.  Octets
 // that the list fills only partly are merged with what is there.
 //
+// Bound by memory and by what its layout brings along: 8 sequences' 4096 of 17000 tokens (8 heads of 128, 34 MB
+// in and out) take 41 us, 140 MB at 3.4 TB/s, as nearly every octet of values is read for two of its tokens
+// and a key's 64 bytes are half a line; 16384 of 199999 tokens 23 us, 256 of 1000 4 us.
+//
 // Into pages of their own the octets are independent.  In place a workgroup has all
 // of a sequence and head's octets (at most 33): it reads them all, meets, and writes.
 #include "kv4.h"

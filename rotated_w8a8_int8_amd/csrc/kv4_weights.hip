@@ -11,6 +11,11 @@
 //   S [32 pairs][32 tokens] = Q K^T, 32x32x16 matrix operations; a lane comes out with 16
 //   pairs of one token, so that pairs are summed within the lane, and the two lanes of a
 //   token meet once at the end.  Nothing is atomic: a token belongs to one wave.
+//
+// Few rows leave it to the memory: 32 bf16 rows over up to 30000 tokens each read 222 MB of
+// keys and move 27 MB of weights in 66 us, 3.8 TB/s; 4096 tokens of one row take 5 us, latency.  Many rows are
+// bound by a SIMD's vector work, about eight instructions and an exponent a pair and token: 288 f32 rows of
+// 48 heads over 2913 tokens 92 us and 7 us for their pairs, beside 53 us for the attention.
 #include "kv4_attn.h"
 
 namespace rad {

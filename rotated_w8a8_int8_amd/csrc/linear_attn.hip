@@ -3,7 +3,12 @@
 //   S = exp(g) S + k v^T,  o = scale S^T q, row by row; S [D][D] in f32.
 //
 // Row by row (single tokens): a workgroup holds 64 of a head's D value columns, D / 16
-// of the key's rows a thread, four columns each, and passes over its part of the state once.
+// of the key's rows a thread, four columns each, and passes over its part of the state once:
+// 64 bf16 tokens of 40 heads of 128 stream 338 MB in 56 to 62 us, 5.4 to 6.0 TB/s.
+//
+// Prompts in chunks of 32 rows: 8192 bf16 rows of 40 heads of 128 take 112 us for the outputs,
+// 56 us for what the segments add and 11 us for their states, 625 MB in all at 3.5 TB/s, with 48% of a
+// SIMD's cycles on vector and 28% on matrix instructions; f16 180 us, f32 417 us (its matrix operations 260).
 #include <type_traits>
 
 #include "layer_launch.h"
