@@ -13,7 +13,7 @@
 //   token meet once at the end.  Nothing is atomic: a token belongs to one wave.
 //
 // Few rows leave it to the memory: 32 bf16 rows over up to 30000 tokens each read 222 MB of
-// keys and move 27 MB of weights in 66 us, 3.8 TB/s; 4096 tokens of one row take 5 us, latency.  Many rows are
+// keys and move 27 MB of weights in 56 us, 4.4 TB/s; 4096 tokens of one row take 5 us, latency.  Many rows are
 // bound by a SIMD's vector work, about eight instructions and an exponent a pair and token: 288 f32 rows of
 // 48 heads over 2913 tokens 92 us and 7 us for their pairs, beside 53 us for the attention.
 #include "kv4_attn.h"
@@ -124,24 +124,47 @@ __device__ __forceinline__ void add_weight(const Kv4Weights &w, float *row, cons
     if (g == 0 && t < ob.len) row[t] = (w.factor != 0.0f && t < ob.base ? w.factor * old : 0.0f) + total;
 }
 
+// How the workgroups of a KV head share the steps, four at a time.  even 0: `parts` to every sequence.  Else (2 to 64
+// sequences) parts of equal length, about `even` of them, found from all lengths: even + B workgroups hold them.
+struct Split {
+    int even, parts;
+};
+struct PartOf {
+    int seq, part, parts;                                 // parts 0: none
+};
+// Every lane of the wave calls it and gets the same answer.
+__device__ __forceinline__ PartOf part_of(const KvBatch &b, const Split &sp, int x) {
+    if (sp.even == 0) return PartOf{x / sp.parts, x % sp.parts, sp.parts};
+    const int lane = threadIdx.x & 63, i = min(lane, b.B - 1);
+    const int fours = lane < b.B && kv_rows(b, i).n > 0 ? (kv_len(b, i) + 127) >> 7 : 0;
+    const int all = __builtin_amdgcn_readlane(wave_scan(fours), 63), each = max(1, (all + sp.even - 1) / sp.even);
+    const int parts = (fours + each - 1) / each, sum = wave_scan(parts);
+    const uint64_t hit = __ballot(x >= sum - parts && x < sum);
+    if (hit == 0) return PartOf{0, 0, 0};
+    const int src = __builtin_ctzll(hit);
+    return PartOf{src, x - __builtin_amdgcn_readlane(sum - parts, src), __builtin_amdgcn_readlane(parts, src)};
+}
+
 // At most 8 NQ pairs: queries stay in registers, the steps of a wave go through a ring of kRing on
-// their way.  Rows 8 q + .. of the products are looked at for q < NQ alone.  blockIdx.x: sequence * parts
-// + part, blockIdx.y: KV head; wave w of part x takes steps 4 x + w, 4 (x + parts) + w, ..
+// their way.  Rows 8 q + .. of the products are looked at for q < NQ alone.  blockIdx.x: a part,
+// blockIdx.y: KV head; wave w of part x takes steps 4 x + w, 4 (x + parts) + w, ..
 constexpr int kRing = 4;
 template <int DT, int D, int NQ>
-__global__ __launch_bounds__(256, NQ == 4 || D == 256 || (D == 128 && DT == kDtF32) ? 2 : 3) void weights_few_kernel(Kv4Cache c, KvBatch b, Kv4Attn a, Kv4Weights w, int parts) {
+__global__ __launch_bounds__(256, NQ == 4 || D == 256 || (D == 128 && DT == kDtF32) ? 2 : 3) void weights_few_kernel(Kv4Cache c, KvBatch b, Kv4Attn a, Kv4Weights w, Split split) {
     constexpr int NK = D / 16;
     constexpr bool SP = DT == kDtF32;
     __shared__ Tile<DT, D> tile;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 5, col = lane & 31;
     const int h = blockIdx.y, G = a.q_heads / c.heads;
-    const int seq = blockIdx.x / parts, part = blockIdx.x % parts;
+    const PartOf mine = part_of(b, split, blockIdx.x);
+    if (mine.parts == 0) return;
+    const int seq = mine.seq;
     const Observed ob(b, a, w, c.heads, seq);
     if (ob.rr.n == 0) return;
     const Pages pages(c, b, seq, h, (ob.len + 31) >> 5);
-    const int stride = 4 * parts;
-    int step = 4 * part + wave;
+    const int stride = 4 * mine.parts;
+    int step = 4 * mine.part + wave;
     Codes<D> ring[kRing];
     int page[kRing + 1];
     float old[kRing];
@@ -328,9 +351,25 @@ hipError_t launch_d(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, const
         hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(b.B) * parts, c.heads), dim3(64 * kWaves), 0, st, c, b, a, w, parts);
         return hipGetLastError();
     };
+    // few pairs: several sequences by their lengths, in one round of the workgroups that 256 CUs hold, half a part a
+    // sequence more than even counted in (bf16, one row each: 32 of up to 30000 tokens 156 -> 148 us a call, 8 of
+    // 2000 20.3 -> 18.9; four rows, 16 of 8000 54 -> 44; two rounds 150, 19.2 and 46)
+    auto go_few = [&](auto kernel, int held) {
+        const int64_t most = (steps + 3) / 4, even = 2048 / all;
+        Split sp{0, static_cast<int>(even < 1 ? 1 : even < most ? even : most)};
+        int64_t pieces = static_cast<int64_t>(b.B) * sp.parts;
+        if (b.B > 1 && b.B <= 64 && most > 1) {
+            const int64_t round = 256 * held / c.heads, half = (round + 1) / 2, share = round - b.B / 2 > half ? round - b.B / 2 : half;
+            sp.even = static_cast<int>(share < 1 ? 1 : share < b.B * most ? share : b.B * most);
+            pieces = sp.even + b.B;
+        }
+        hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(pieces), c.heads), dim3(64 * kWaves), 0, st, c, b, a, w, sp);
+        return hipGetLastError();
+    };
     const int64_t pairs = most_pairs(b, G, w.observe);
-    if (pairs <= 8) return go(weights_few_kernel<DT, D, 1>, 4);
-    if (pairs <= kFew<D>) return go(weights_few_kernel<DT, D <= 128 ? D : 64, 4>, 4);
+    constexpr int held = D == 256 || (D == 128 && DT == kDtF32) ? 2 : 3;
+    if (pairs <= 8) return go_few(weights_few_kernel<DT, D, 1>, held);
+    if (pairs <= kFew<D>) return go_few(weights_few_kernel<DT, D <= 128 ? D : 64, 4>, 2);
     const int64_t each = static_cast<int64_t>(b.rows) * G;
     hipLaunchKernelGGL((pairs_kernel<DT, D>), dim3(static_cast<uint32_t>((each + 31) / 32), c.heads), dim3(256), 0, st, c, b, a, w);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;

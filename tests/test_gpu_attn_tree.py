@@ -190,6 +190,15 @@ def test_weights_of_a_long_context(torch):
     run_weights(torch, [4, 2], [6000, 2500], 1, 2, 64, 32, "bf16", factor=0.5, seed=2)
 
 
+@pytest.mark.parametrize("sequences", [2, 63, 64, 65])
+def test_weights_of_sequences_of_very_different_lengths(torch, sequences):
+    # up to 64 sequences share the workgroups by their lengths
+    ctx = [3000] + [(37 * i) % 150 for i in range(sequences - 2)] + [700]
+    new = [1] + [i % 3 for i in range(sequences - 2)] + [2]
+    run_weights(torch, new, ctx, 2, 2, 64, 32, "f16", factor=0.5, seed=sequences, pad=1)
+    run_weights(torch, [1] * sequences, ctx, 1, 20, 64, 64, "bf16", seed=sequences, one=True)
+
+
 def test_weights_on_absent_pages(torch):
     def edit(table, pages):
         table[0, 1], table[1, 0] = -1, pages + 3
