@@ -6,9 +6,10 @@
 // dwords of its own dimensions, D/64 a lane, from which it takes a nibble each.  Octets
 // that the list fills only partly are merged with what is there.
 //
-// Bound by memory and by what its layout brings along: 8 sequences' 4096 of 17000 tokens (8 heads of 128, 34 MB
-// in and out) take 41 us, 140 MB at 3.4 TB/s, as nearly every octet of values is read for two of its tokens
-// and a key's 64 bytes are half a line; 16384 of 199999 tokens 23 us, 256 of 1000 4 us.
+// Bound by the trips to memory of an octet (list, page, codes, a scale of two bytes from each of 16 lines) more than
+// by bytes: 8 sequences' 4096 of 13000 tokens (8 heads of 128) take 32 us for 44 MB fetched and 35 MB written; the
+// loads of the eight entries one behind the other took 41 us, several octets a wave with the next one's places
+// looked up ahead the same 32.  16384 of 199999 tokens 19 us, 256 of 1000 3.2 us.
 //
 // Into pages of their own the octets are independent.  In place a workgroup has all
 // of a sequence and head's octets (at most 33): it reads them all, meets, and writes.
@@ -36,6 +37,10 @@ __device__ __forceinline__ int64_t source_of(const Kv4Cache &c, const KvBatch &b
     return page < 0 ? -1 : ((static_cast<int64_t>(page) * c.heads + h) << c.page_shift) + (t & ((1 << c.page_shift) - 1));
 }
 
+__device__ __forceinline__ int64_t lane_of(int64_t v, int lane) {
+    return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), lane)) |
+           static_cast<int64_t>(__builtin_amdgcn_readlane(static_cast<int>(v >> 32), lane)) << 32;
+}
 template <int D>
 __device__ __forceinline__ void read_octet(Octet<D> &o, const Kv4Cache &c, const KvBatch &b, const int32_t *list, int seq, int h, int len, int i0, int n) {
     constexpr int KB = D / 16, NV = D / 64;                   // bytes of a key and dwords of values a lane
@@ -47,25 +52,31 @@ __device__ __forceinline__ void read_octet(Octet<D> &o, const Kv4Cache &c, const
     for (int j = 0; j < 8; ++j) o.mask |= moves >> j & 1 ? 15u << (4 * j) : 0u;
     o.scales = 0;
     if (lane < 8 && mine >= 0) o.scales = c.k_scale[mine] | static_cast<uint32_t>(c.v_scale[mine]) << 16;
-    const int64_t ke = __shfl(mine, lane >> 3);
-    if (ke >= 0) {
-        const uint8_t *p = c.k_codes + ke * (D / 2) + KB * (lane & 7);
-        if constexpr (D == 64) o.key[0].x = *reinterpret_cast<const uint32_t *>(p);
-        else {
+    if (moves == 0) return;
+    // entries that do not move read another's, so that every load is under way before the first is waited for
+    const int64_t some = lane_of(mine, __builtin_ctzll(moves)), ke = __shfl(mine, lane >> 3);
+    const uint8_t *p = c.k_codes + (ke >= 0 ? ke : some) * (D / 2) + KB * (lane & 7);
+    if constexpr (D == 64) o.key[0].x = *reinterpret_cast<const uint32_t *>(p);
+    else {
 #pragma unroll
-            for (int x = 0; x < D / 128; ++x) o.key[x] = reinterpret_cast<const uint2 *>(p)[x];
-        }
+        for (int x = 0; x < D / 128; ++x) o.key[x] = reinterpret_cast<const uint2 *>(p)[x];
     }
-#pragma unroll
-    for (int x = 0; x < NV; ++x) o.value[x] = 0;
+    uint32_t v[8][NV];
+    int shift[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const int64_t ve = __shfl(mine, j);
-        if (ve < 0) continue;
-        const uint32_t *p = reinterpret_cast<const uint32_t *>(c.v_codes) + (ve >> 3) * D + NV * lane;
-        const int sh = 4 * static_cast<int>(ve & 7);
+        const int64_t ve = moves >> j & 1 ? lane_of(mine, j) : some;
+        const uint32_t *q = reinterpret_cast<const uint32_t *>(c.v_codes) + (ve >> 3) * D + NV * lane;
+        shift[j] = 4 * static_cast<int>(ve & 7);
 #pragma unroll
-        for (int x = 0; x < NV; ++x) o.value[x] |= ((p[x] >> sh) & 15u) << (4 * j);
+        for (int x = 0; x < NV; ++x) v[j][x] = q[x];
+    }
+#pragma unroll
+    for (int x = 0; x < NV; ++x) {
+        o.value[x] = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o.value[x] |= ((v[j][x] >> shift[j]) & 15u) << (4 * j);
+        o.value[x] &= o.mask;
     }
 }
 
