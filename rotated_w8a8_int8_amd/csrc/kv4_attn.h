@@ -44,10 +44,10 @@ __device__ __forceinline__ TokenRange seen(int pos, int len, int causal, int win
 // before base (from `lo` on, where there is a window); among the nodes its mask decides, a bit
 // a node.  Only the steps that hold nodes look at masks: two bytes for eight tokens.
 
-// Bits of nodes j .. j + 7 of a mask of `bytes` bytes (bits outside it are 0).
-__device__ __forceinline__ uint32_t mask_bits8(const uint8_t *mask, int bytes, int j) {
+// Bits of nodes j .. j + 7 of the mask of `bytes` bytes from mask[first] on (bits outside it are 0).
+__device__ __forceinline__ uint32_t mask_bits8(const uint8_t *mask, uint32_t first, int bytes, int j) {
     const int at = j >> 3;                                    // floor, for negative j too
-    const uint32_t lo = at >= 0 && at < bytes ? mask[at] : 0u, hi = at >= -1 && at + 1 < bytes ? mask[at + 1] : 0u;
+    const uint32_t lo = at >= 0 && at < bytes ? mask[first + at] : 0u, hi = at >= -1 && at + 1 < bytes ? mask[first + at + 1] : 0u;
     return ((lo | hi << 8) >> (j & 7)) & 0xFFu;
 }
 // Nodes from `from` to n - 1 that a row sees.
@@ -539,7 +539,11 @@ __global__ __launch_bounds__(256, D == 128 && HL != 2 ? 3 : 2) void attn_kernel(
     const bool used = cp < sh.pairs;
     const int ci = used ? cp / G : 0, cg = used ? cp % G : 0;
     const TokenRange tr = used ? seen_by<TREE>(b, a, sh, seq, ci) : sh.tile_r;
-    const uint8_t *const mask = TREE ? reinterpret_cast<const uint8_t *>(a.mask + static_cast<int64_t>(sh.first_row + ci) * a.words) : nullptr;
+    // Bytes of the masks, fewer than 2^22 rows of at most 64 words, count in 32 bits: as an address it is a register
+    // too many (32 chains of three, 16000 tokens: 64 us, 61 us so; attn_wide_kernel has no such limit, and
+    // 8 nodes over 500 tokens lose 0.3 us to it).
+    const uint8_t *const masks = reinterpret_cast<const uint8_t *>(a.mask);
+    const uint32_t mask = TREE ? static_cast<uint32_t>(sh.first_row + ci) * static_cast<uint32_t>(8 * a.words) : 0u;
     const int64_t qrow = (static_cast<int64_t>(sh.first_row + ci) * a.q_heads + h * G + cg) * D;
     // the query's values are asked for first, then the first steps
     float qv[NK][8];
@@ -616,7 +620,7 @@ __global__ __launch_bounds__(256, D == 128 && HL != 2 ? 3 : 2) void attn_kernel(
         }
         if (step < sh.open_lo || step >= sh.open_hi) {
             const int t0 = (step << 5) + 8 * g;
-            const uint32_t bits = TREE ? mask_bits8(mask, 8 * a.words, t0 - sh.pos0) : 0u;
+            const uint32_t bits = TREE ? mask_bits8(masks, mask, 8 * a.words, t0 - sh.pos0) : 0u;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const bool on = t0 + i >= tr.lo && t0 + i < tr.hi && (!TREE || t0 + i < sh.pos0 || (bits >> i & 1));
@@ -859,8 +863,8 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(Kv4Cache c, KvBatch b
         for (int i = 0; i < 16; ++i) s[i] = times_half(st[i], cur.ks[i >> 3], i & 7);
         if (step < sh.open_lo || step >= sh.open_hi) {
             const int t0 = (step << 5) + 8 * g;
-            const uint32_t bits = TREE ? mask_bits8(mask, 8 * a.words, t0 - sh.pos0) |
-                                             mask_bits8(mask, 8 * a.words, t0 + 16 - sh.pos0) << 8 : 0u;
+            const uint32_t bits = TREE ? mask_bits8(mask, 0, 8 * a.words, t0 - sh.pos0) |
+                                             mask_bits8(mask, 0, 8 * a.words, t0 + 16 - sh.pos0) << 8 : 0u;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const int t = t0 + 16 * (i >> 3) + (i & 7);
