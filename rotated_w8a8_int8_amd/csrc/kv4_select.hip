@@ -210,7 +210,7 @@ __global__ __launch_bounds__(64 * kSelWaves) void select_kernel(Kv4Select s, int
         __syncthreads();
         if (few) {
             if (tid == 0) found[2] = before;                  // the list stays as long as it is
-        } else if (pass == 0 && same <= kHeldKeys) {
+        } else if (pass == 0 && rest > 0 && same <= kHeldKeys) {       // with no place left no digit was found: `same` counts nothing
             few = true;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
