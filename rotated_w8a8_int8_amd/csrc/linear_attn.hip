@@ -196,13 +196,15 @@ __device__ __forceinline__ void store_state(const f16v (&s)[D / 32], float *to, 
         for (int i = 0; i < 16; ++i) to[static_cast<int64_t>(32 * T + 8 * (i >> 2) + 4 * g + (i & 3)) * D + col] = s[T][i];
 }
 
-// Ages of a chunk of n rows, as a lane meets its rows j = 8 q + 4 g + e.
+// A lane's i-th row of a chunk, j = 8 q + 4 g + e.
+__device__ __forceinline__ int row_of(int i, int g) { return 8 * (i >> 2) + 4 * g + (i & 3); }
+// Ages of a chunk of n rows, as a lane meets its rows.
 struct Ages {
     float w[16], all;         // a^(n - 1 - j), 0 from row n on; a^n
     __device__ __forceinline__ void set(float l2, int n, int g) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const int j = 8 * (i >> 2) + 4 * g + (i & 3);
+            const int j = row_of(i, g);
             w[i] = j < n ? power(l2, n - 1 - j) : 0.0f;
         }
         all = power(l2, n);
@@ -238,15 +240,13 @@ __global__ __launch_bounds__(64 * kLinWaves<D>, D == 256 ? 1 : 2) void chunk_f32
     f16v s[D / 32];
     load_state<D>(s, OUT ? (sr.segs > 1 ? kept : l.state ? l.state + pair * mat : nullptr) : nullptr, g, vcol);
     const float l2 = log2_decay(l, h), from = power(l2, col + 1);
+    auto sees = [&](int i) { return row_of(i, g) <= col; };
     float near[16];                                       // a^(i - j) of the lane's column i = col
     Ages age;
     age.set(l2, kChunk, g);
     if (OUT)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int j = 8 * (i >> 2) + 4 * g + (i & 3);
-            near[i] = j <= col ? power(l2, col - j) : 0.0f;
-        }
+        for (int i = 0; i < 16; ++i) near[i] = sees(i) ? power(l2, col - row_of(i, g)) : 0.0f;
 
     const int br = 4 * (tid & 7), bc = 4 * (tid >> 3);
     float4 bq[PQ][4], bk[PQ][4], bv[4];
@@ -317,7 +317,7 @@ __global__ __launch_bounds__(64 * kLinWaves<D>, D == 256 ? 1 : 2) void chunk_f32
             for (int x = 1; x < NW; ++x) p += tile.p[x][lane];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                p[i] *= near[i];
+                p[i] = sees(i) ? p[i] * near[i] : 0.0f;       // a product with a later row's key may be anything
                 o[i] *= from;
             }
 #pragma unroll
@@ -476,15 +476,13 @@ __global__ __launch_bounds__(64 * kLinWaves<D>, D == 256 ? 1 : 2) void chunk_ker
     f16v s[D / 32];
     load_state<D>(s, OUT ? (sr.segs > 1 ? kept : l.state ? l.state + pair * mat : nullptr) : nullptr, g, vcol);
     const float l2 = log2_decay(l, h), from = power(l2, col + 1) * l.scale;
+    auto sees = [&](int i) { return row_of(i, g) <= col; };
     float near[16];                                       // a^(i - j) of the lane's column i = col
     Ages age;
     age.set(l2, kChunk, g);
     if (OUT)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int j = 8 * (i >> 2) + 4 * g + (i & 3);
-            near[i] = j <= col ? power(l2, col - j) * l.scale : 0.0f;
-        }
+        for (int i = 0; i < 16; ++i) near[i] = sees(i) ? power(l2, col - row_of(i, g)) * l.scale : 0.0f;
     // The state is a^aged_by 2^-es s.  Where the products have f32's range (bf16) it ages by the count of
     // rows alone, and is multiplied out once that comes to kLazy.
     int es = 0, aged_by = 0;
@@ -530,7 +528,7 @@ __global__ __launch_bounds__(64 * kLinWaves<D>, D == 256 ? 1 : 2) void chunk_ker
                 }
             float pw[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) pw[i] = p[i] * near[i];
+            for (int i = 0; i < 16; ++i) pw[i] = sees(i) ? p[i] * near[i] : 0.0f;       // a product with a later row's key may be anything
             const int ep = room<DT>(pw, 64);
             const float fo = __builtin_amdgcn_ldexpf(from * power(l2, aged_by), ep - ef - es), fp = pow2(ep);
 #pragma unroll

@@ -1,0 +1,89 @@
+"""GPU: rad_linear_attn with values that are not finite and products that leave f32's range: nothing reaches an earlier row,
+another sequence, or a head that it has no part in."""
+import numpy as np
+import pytest
+
+import layer_cases as C
+from oracle import layer as O
+from oracle import mixers as X
+from rotated_w8a8_int8_amd import binding as B
+from test_gpu_linear_attn import tolerance
+
+pytestmark = pytest.mark.gpu
+NEW = [70, 9, 40, 33]                                        # rows a sequence, in chunks and segments
+
+
+@pytest.fixture(scope="module")
+def torch():
+    import torch as _t
+    if not _t.cuda.is_available():
+        pytest.fail("GPU tests need a GPU")
+    return _t
+
+
+def inputs(seed, D, dtype, new, heads=4, qk=2):
+    rng = np.random.default_rng(seed)
+    T = sum(new)
+    q, k, v = (O.to_dtype(rng.standard_normal((T, n, D)), dtype) for n in (qk, qk, heads))
+    g = -np.exp2(rng.uniform(-8, -2, heads)).astype(np.float32)
+    S = rng.standard_normal((len(new), heads, D, D)).astype(np.float32)
+    return q, k, v, g, S
+
+
+def call(torch, q, k, v, g, S, dtype, new, scale):
+    o = torch.full(v.shape, 33.0, dtype=C.torch_dtype(torch, dtype), device="cuda")
+    state = torch.full(S.shape, 44.0, device="cuda")
+    B.linear_attn(C.put(torch, q, dtype), C.put(torch, k, dtype), C.put(torch, v, dtype), C.put(torch, g), state=C.put(torch, S),
+                  state_out=state, q_start=C.put(torch, C.ragged(new)), max_q=max(new), scale=scale, o=o)
+    return C.host(o), state.cpu().numpy()
+
+
+def check(got, want, mass, S, want_S, big, dtype, new, D, rows=Ellipsis, states=Ellipsis):
+    """Outputs at `rows` (of rows, heads, columns) and states at `states` (of sequences, heads, key dims, columns)."""
+    to, ts = tolerance(dtype, max(new), D, 1.0, want, mass, want_S, big)
+    off = np.abs(got - want)[rows]
+    assert np.all(off <= to[rows]), "off by %g of the tolerance" % np.nanmax(off / to[rows])
+    off = np.abs(S - want_S)[states]
+    assert np.all(off <= ts[states]), "state off by %g of the tolerance" % np.nanmax(off / ts[states])
+
+
+@pytest.mark.parametrize("D", B.KV_HEAD_DIMS)
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
+@pytest.mark.parametrize("what,dtype", [("q", "f32"), ("q", "bf16"), ("k", "f32"), ("k", "bf16")])
+def test_what_is_not_finite_reaches_no_earlier_row_and_no_other_column(torch, what, bad, D, dtype):
+    print("not finite", what, bad, D, dtype, flush=True)
+    q, k, v, g, S = inputs(D, D, dtype, NEW)
+    start, scale = C.ragged(NEW), D ** -0.5
+    want, want_S, mass, big = X.linear(q, k, v, g, S, start, scale)
+    # a row of the middle of the first sequence, of its first rows, and the last of the third one
+    for seq, at in ((0, 45), (0, 5), (2, 39)):
+        x = {"q": q.copy(), "k": k.copy(), "v": v.copy()}
+        row, column = int(start[seq]) + at, D - 5
+        x[what][row, 1, column] = bad
+        got, state = call(torch, x["q"], x["k"], x["v"], g, S, dtype, NEW, scale)
+        # what it has no part in: other rows (q), heads (k: of the other key head), columns (v), and all that came before
+        clean, clean_S = np.ones(want.shape, bool), np.ones(S.shape, bool)
+        after = slice(row, int(start[seq + 1]))
+        if what == "q":
+            clean[row, 2:] = False
+        elif what == "k":
+            clean[after, 2:], clean_S[seq, 2:] = False, False
+        else:
+            clean[after, 1, column], clean_S[seq, 1, :, column] = False, False
+        check(got, want, mass, state, want_S, big, dtype, NEW, D, clean, clean_S)
+        assert not np.isfinite(got[row, 1 if what == "v" else 2, column]), "the row itself"
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D", B.KV_HEAD_DIMS)
+def test_products_with_later_rows_may_leave_the_range(torch, D, dtype):
+    # finite inputs and finite exact outputs: only a query's product with a later row's key is past 2^128
+    q, k, v, g, S = inputs(D + 1, D, dtype, NEW)
+    start = C.ragged(NEW)
+    for seq, early, late in ((0, 40, 60), (2, 2, 30)):         # rows of one chunk of 32
+        q[start[seq] + early] *= np.float32(2.0 ** 80)
+        k[start[seq] + late] *= np.float32(2.0 ** 60)
+    want, want_S, mass, big = X.linear(q, k, v, g, S, start, 1.0)
+    got, state = call(torch, q, k, v, g, S, dtype, NEW, 1.0)
+    assert np.all(np.abs(want) < 2.0 ** 126)
+    check(got, want, mass, state, want_S, big, dtype, NEW, D)
