@@ -608,7 +608,8 @@ int rad_kv4_move(const rad_kv4_cache *cache, const rad_kv_batch *batch, const in
  * one launch holds fewer than 2^24 workgroups of 128 rows and more of a head's 128 values (2^25 for D = 64).
  * scale is finite.  The state and all sums are held in f32; RAD_DT_F32 values are
  * multiplied in f32.  For the 16-bit types the weights of the rows of a chunk and the state meet the
- * matrix cores as pairs of 16-bit parts (16 bits at least).
+ * matrix cores as pairs of 16-bit parts: bf16 16 bits, f16 22 bits or 2^-39 of the largest weight of the
+ * same row, of the largest value of the same state column, whichever is more.
  */
 typedef struct rad_linear {
     const void *q, *k, *v;

@@ -351,7 +351,8 @@ __global__ __launch_bounds__(64 * kLinWaves<D>, D == 256 ? 1 : 2) void chunk_f32
 // K and V are transposed on their way into LDS, 4 x 4 values a thread.  q, k and v are exact.  P and
 // S are taken as two 16-bit parts (bf16 16 bits, f16 22), aged values as as many as make the
 // state good to 2^-22 or better (bf16 three, f16 two).  f16 parts are taken at the power of two that puts the
-// largest of a wave's 32 columns in [2^14, 2^15): what is 2^-17 of that keeps 22 bits.
+// largest of their column of the state, or of their row's weights, in [2^14, 2^15): what is 2^-17 of that keeps 22
+// bits.  One power for a wave's 32 columns left columns 2^-26 of another's a few bits.
 template <int DT>
 __device__ __forceinline__ f16v mma(u4 a, u4 b, f16v c) {
     if constexpr (DT == kDtBf16) return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8, a), __builtin_bit_cast(b8, b), c, 0, 0, 0);
@@ -381,16 +382,26 @@ __device__ __forceinline__ u4 part8(float (&x)[8]) {
     }
     return r;
 }
-// Exponent that takes a wave's largest magnitude to [2^14, 2^15), at most `most` (what meets the products
-// in f32 is taken along and has to stay finite); 0 for bf16, whose range is f32's.
-template <int DT, int N>
-__device__ __forceinline__ int room(const float (&x)[N], int most) {
-    if constexpr (DT == kDtBf16) return 0;
+// The larger of what the two lanes of a column hold.
+__device__ __forceinline__ float both_max(float m) { return fmaxf(m, __shfl_xor(m, 32)); }
+// Exponent that takes m, the largest magnitude of a column, to [2^14, 2^15), at most `most` (what meets the products
+// in f32 is taken along and has to stay finite).
+__device__ __forceinline__ int room(float m, int most) { return m > 0.0f ? min(15 - __builtin_amdgcn_frexp_expf(m), most) : 0; }
+template <int N>
+__device__ __forceinline__ float largest(const float (&x)[N]) {
     float m = 0.0f;
 #pragma unroll
     for (int i = 0; i < N; ++i) m = fmaxf(m, fabsf(x[i]));
-    m = wave_max_f32(m);
-    return m > 0.0f ? min(15 - __builtin_amdgcn_frexp_expf(m), most) : 0;
+    return both_max(m);
+}
+template <int T>
+__device__ __forceinline__ float largest(const f16v (&s)[T]) {
+    float m = 0.0f;
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(s[t][i]));
+    return both_max(m);
 }
 constexpr float kLazy = 0x1p-8f;
 __device__ __forceinline__ float pow2(int e) { return __builtin_amdgcn_ldexpf(1.0f, e); }
@@ -414,7 +425,9 @@ __device__ __forceinline__ void turn4(const u2 (&x)[4], u2 (&y)[4]) {
 template <int DT, int D, bool OUT>
 __global__ __launch_bounds__(64 * kLinWaves<D>, D == 256 ? 1 : 2) void chunk_kernel(Linear l, Segments sg) {
     constexpr int NW = kLinWaves<D>, NT = 64 * NW, VC = 32 * NW, NS = kSlices<D>, PQ = D / (NT / 2), NA = DT == kDtBf16 ? 3 : 2;
+    constexpr bool kScaled = DT == kDtF16;                // bf16 has f32's range
     __shared__ Tile16<D, OUT> tiles[2];
+    alignas(16) __shared__ float undo[kScaled && OUT ? NW : 1][32];   // of a wave's state columns, what their parts were scaled by
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 5, col = lane & 31;
     const Item it = item_of(l, sg, NS);
@@ -483,9 +496,14 @@ __global__ __launch_bounds__(64 * kLinWaves<D>, D == 256 ? 1 : 2) void chunk_ker
     if (OUT)
 #pragma unroll
         for (int i = 0; i < 16; ++i) near[i] = sees(i) ? power(l2, col - row_of(i, g)) * l.scale : 0.0f;
-    // The state is a^aged_by 2^-es s.  Where the products have f32's range (bf16) it ages by the count of
-    // rows alone, and is multiplied out once that comes to kLazy.
-    int es = 0, aged_by = 0;
+    // The lane's column of the state is a^aged_by 2^-es s.  Where the products have f32's range (bf16) it ages by the
+    // count of rows alone, and is multiplied out once that comes to kLazy.  f16 products add less than 2^54 to a state
+    // (2^22 rows of 2^32 each), so that only one that begins past that may leave no room for its exponent.
+    int es = 0, aged_by = 0, most_es = 32;
+    if constexpr (kScaled) {
+        const float big = largest(s);
+        if (big > 0x1p60f) most_es = min(32, 126 - __builtin_amdgcn_frexp_expf(big));
+    }
     put(tiles[0]);
     __syncthreads();
     for (int c0 = 0, at = 0; c0 < sr.n; c0 += kChunk, at ^= 1) {
@@ -503,17 +521,13 @@ __global__ __launch_bounds__(64 * kLinWaves<D>, D == 256 ? 1 : 2) void chunk_ker
             f16v p{};
 #pragma unroll
             for (int m = 0; m < D / 16; ++m) p = mma<DT>(*reinterpret_cast<const u4 *>(&t.k[col][16 * m + 8 * g]), qf[m], p);
-            float big = 0.0f;
-            int ef = 0;
-            if constexpr (DT == kDtF16) {
-#pragma unroll
-                for (int T = 0; T < D / 32; ++T)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) big = fmaxf(big, fabsf(s[T][i]));
-                const float one[1] = {big};
-                ef = room<DT>(one, 127);
+            float fs = 1.0f;
+            if constexpr (kScaled) {
+                const int ef = room(largest(s), 90);
+                fs = pow2(ef);
+                if (g == 0) undo[wave][col] = pow2(-ef - es);
+                __builtin_amdgcn_wave_barrier();
             }
-            const float fs = pow2(ef);
             f16v o{};
 #pragma unroll
             for (int T = 0; T < D / 32; ++T)
@@ -521,7 +535,7 @@ __global__ __launch_bounds__(64 * kLinWaves<D>, D == 256 ? 1 : 2) void chunk_ker
                 for (int m = 0; m < 2; ++m) {
                     float x[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = DT == kDtF16 ? s[T][8 * m + i] * fs : s[T][8 * m + i];
+                    for (int i = 0; i < 8; ++i) x[i] = kScaled ? s[T][8 * m + i] * fs : s[T][8 * m + i];
                     const u4 hi = part8<DT>(x), lo = part8<DT>(x);
                     o = mma<DT>(lo, qf[2 * T + m], o);
                     o = mma<DT>(hi, qf[2 * T + m], o);
@@ -529,15 +543,22 @@ __global__ __launch_bounds__(64 * kLinWaves<D>, D == 256 ? 1 : 2) void chunk_ker
             float pw[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) pw[i] = sees(i) ? p[i] * near[i] : 0.0f;       // a product with a later row's key may be anything
-            const int ep = room<DT>(pw, 64);
-            const float fo = __builtin_amdgcn_ldexpf(from * power(l2, aged_by), ep - ef - es), fp = pow2(ep);
+            const int ep = kScaled ? room(largest(pw), 64) : 0;
+            const float fo = __builtin_amdgcn_ldexpf(from * power(l2, aged_by), ep), fp = pow2(ep);
+            if constexpr (kScaled)                        // a product's row is a column of the state
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float4 u = *reinterpret_cast<const float4 *>(&undo[wave][8 * q + 4 * g]);
+                    o[4 * q] *= u.x, o[4 * q + 1] *= u.y, o[4 * q + 2] *= u.z, o[4 * q + 3] *= u.w;
+                }
+            __builtin_amdgcn_wave_barrier();
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[i] *= fo;
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
                 float x[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = DT == kDtF16 ? pw[8 * m + i] * fp : pw[8 * m + i];
+                for (int i = 0; i < 8; ++i) x[i] = kScaled ? pw[8 * m + i] * fp : pw[8 * m + i];
                 const u4 hi = part8<DT>(x), lo = part8<DT>(x);
                 o = mma<DT>(vf[m], lo, o);
                 o = mma<DT>(vf[m], hi, o);
@@ -547,7 +568,7 @@ __global__ __launch_bounds__(64 * kLinWaves<D>, D == 256 ? 1 : 2) void chunk_ker
                 u4 y[2];
                 const float f = pow2(-ep);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i >> 2][i & 3] = DT == kDtF16 ? pack16<DT>(o[2 * i] * f, o[2 * i + 1] * f) : pack16<DT>(o[2 * i], o[2 * i + 1]);
+                for (int i = 0; i < 8; ++i) y[i >> 2][i & 3] = kScaled ? pack16<DT>(o[2 * i] * f, o[2 * i + 1] * f) : pack16<DT>(o[2 * i], o[2 * i + 1]);
                 u4 *q = reinterpret_cast<u4 *>(static_cast<uint16_t *>(l.o) + to);
                 q[0] = y[0];
                 q[1] = y[1];
@@ -557,10 +578,10 @@ __global__ __launch_bounds__(64 * kLinWaves<D>, D == 256 ? 1 : 2) void chunk_ker
         float aged[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) aged[i] = widen16<DT>(i & 1 ? vf[i >> 3][(i & 7) >> 1] >> 16 : vf[i >> 3][(i & 7) >> 1] & 0xFFFFu) * age.w[i];
-        const int ea = room<DT>(aged, 32);
+        const int ea = kScaled ? room(largest(aged), most_es) : 0;
         aged_by += n;
         const float gone = power(l2, aged_by);
-        if (DT == kDtF16 || gone < kLazy) {
+        if (kScaled || gone < kLazy) {
             const float keep = __builtin_amdgcn_ldexpf(gone, ea - es);
 #pragma unroll
             for (int T = 0; T < D / 32; ++T) s[T] *= keep;

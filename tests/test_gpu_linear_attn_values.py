@@ -1,5 +1,5 @@
-"""GPU: rad_linear_attn with values that are not finite and products that leave f32's range: nothing reaches an earlier row,
-another sequence, or a head that it has no part in."""
+"""GPU: rad_linear_attn with values that are not finite, products that leave f32's range, and value columns, rows and states of
+very different sizes: nothing reaches an earlier row, another sequence, or a head that it has no part in."""
 import numpy as np
 import pytest
 
@@ -49,7 +49,8 @@ def check(got, want, mass, S, want_S, big, dtype, new, D, rows=Ellipsis, states=
 
 @pytest.mark.parametrize("D", B.KV_HEAD_DIMS)
 @pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
-@pytest.mark.parametrize("what,dtype", [("q", "f32"), ("q", "bf16"), ("k", "f32"), ("k", "bf16")])
+@pytest.mark.parametrize("dtype", C.DTYPES)
+@pytest.mark.parametrize("what", ["q", "k"])
 def test_what_is_not_finite_reaches_no_earlier_row_and_no_other_column(torch, what, bad, D, dtype):
     print("not finite", what, bad, D, dtype, flush=True)
     q, k, v, g, S = inputs(D, D, dtype, NEW)
@@ -87,3 +88,45 @@ def test_products_with_later_rows_may_leave_the_range(torch, D, dtype):
     got, state = call(torch, q, k, v, g, S, dtype, NEW, 1.0)
     assert np.all(np.abs(want) < 2.0 ** 126)
     check(got, want, mass, state, want_S, big, dtype, NEW, D)
+
+
+def columns_of_size(D, lo, hi):
+    """A power of two a value column, from 2^lo to 2^hi, neighbours far apart."""
+    return np.exp2(np.round(np.linspace(lo, hi, D))[np.arange(D) * 37 % D]).astype(np.float32)
+
+
+@pytest.mark.parametrize("dtype", C.DTYPES)
+@pytest.mark.parametrize("D", B.KV_HEAD_DIMS)
+def test_value_columns_of_very_different_sizes(torch, D, dtype):
+    # each column, and its part of the state, is as good as if it were alone
+    q, k, v, g, S = inputs(D + 2, D, dtype, NEW)
+    size = columns_of_size(D, -13, 13)
+    v, S = O.to_dtype(v * size, dtype), S * size
+    scale = 2.0 ** -5
+    want, want_S, mass, big = X.linear(q, k, v, g, S, C.ragged(NEW), scale)
+    got, state = call(torch, q, k, v, g, S, dtype, NEW, scale)
+    keep = np.abs(want) < 6e4                                 # f16 ends there
+    check(got, want, mass, state, want_S, big, dtype, NEW, D, keep)
+
+
+@pytest.mark.parametrize("dtype", C.DTYPES)
+@pytest.mark.parametrize("D", B.KV_HEAD_DIMS)
+def test_query_rows_of_very_different_sizes(torch, D, dtype):
+    q, k, v, g, S = inputs(D + 3, D, dtype, NEW)
+    size = np.exp2(np.round(np.linspace(-13, 13, len(q)))[np.arange(len(q)) * 37 % len(q)])[:, None, None]
+    q = O.to_dtype(q * size, dtype)
+    want, want_S, mass, big = X.linear(q, k, v, g, S, C.ragged(NEW), 2.0 ** -5)
+    got, state = call(torch, q, k, v, g, S, dtype, NEW, 2.0 ** -5)
+    check(got, want, mass, state, want_S, big, dtype, NEW, D, np.abs(want) < 6e4)
+
+
+@pytest.mark.parametrize("dtype", C.DTYPES)
+@pytest.mark.parametrize("size", [2.0 ** 64, 2.0 ** 110, 2.0 ** -64, 2.0 ** -110])
+def test_states_far_from_the_values(torch, size, dtype):
+    # values of 2^-20 meet states of 2^110; outputs come to about 1
+    q, k, v, g, S = inputs(4, 64, dtype, NEW)
+    q[5], q[45] = 0.0, 0.0
+    v, S, scale = O.to_dtype(v * np.float32(2.0 ** -20), dtype), S * np.float32(size), min(1 / size, 1.0)
+    want, want_S, mass, big = X.linear(q, k, v, g, S, C.ragged(NEW), scale)
+    got, state = call(torch, q, k, v, g, S, dtype, NEW, scale)
+    check(got, want, mass, state, want_S, big, dtype, NEW, 64)
