@@ -610,6 +610,8 @@ int rad_kv4_move(const rad_kv4_cache *cache, const rad_kv_batch *batch, const in
  * multiplied in f32.  For the 16-bit types the weights of the rows of a chunk and the state meet the
  * matrix cores as pairs of 16-bit parts: bf16 16 bits, f16 22 bits or 2^-39 of the largest weight of the
  * same row, of the largest value of the same state column, whichever is more.
+ * What is not finite reaches its own row and later ones of its sequence: of q that row of its head, of k
+ * every value of its head, of v its value column.
  */
 typedef struct rad_linear {
     const void *q, *k, *v;

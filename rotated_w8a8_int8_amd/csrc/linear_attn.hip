@@ -117,6 +117,7 @@ typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef unsigned int u4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u2 __attribute__((ext_vector_type(2)));
+typedef unsigned short us2 __attribute__((ext_vector_type(2)));
 
 constexpr int kChunk = 32;
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -211,6 +212,20 @@ struct Ages {
     }
 };
 
+// A value v_j that is not finite reaches rows i >= j of its column, and the state's column; a product with the 0 that hides it
+// from rows before would bring it there.  A chunk that holds one works with 0 in its place, and makes those outputs and the
+// state's column NaN: from_row is the first such row of each of a wave's columns.
+__device__ __forceinline__ void hide_lost(f16v &o, const int *from_row, int g, int col) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] = col >= from_row[row_of(i, g)] ? NAN : o[i];
+}
+__device__ __forceinline__ bool keep_lost(int *from_row, int first, int g, int col) {
+    first = min(first, __shfl_xor(first, 32));
+    if (g == 0) from_row[col] = first;
+    __builtin_amdgcn_wave_barrier();
+    return first < kChunk;
+}
+
 // ---- f32 products -----------------------------------------------------------------
 //
 // 32x32x2 matrix operations (154 TFLOP/s where the 16-bit ones reach 1228): 160 of them a wave and chunk
@@ -219,6 +234,7 @@ template <int D>
 struct TileF32 {
     float q[kChunk][D + 4], k[kChunk][D + 4], v[kChunk][32 * kLinWaves<D> + 4];
     f16v p[kLinWaves<D>][64];                             // shares of P^T, by dims of the products
+    int lost, from_row[kLinWaves<D>][32];                 // the last chunk with a value that is not finite; see hide_lost
 };
 
 template <int DT, int D, bool OUT>
@@ -267,9 +283,11 @@ __global__ __launch_bounds__(64 * kLinWaves<D>, D == 256 ? 1 : 2) void chunk_f32
     };
     // value column v of a wave lies at its r: 4 of them in a row stay together
     const int vr = 32 * (bc >> 5) + 8 * ((bc >> 2) & 3) + 4 * ((bc >> 4) & 1);
-    auto put = [&]() {
+    auto put = [&](int c0) {
+        float zero = 0.0f;                                // NaN where a value is not finite
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
+            if (OUT) zero = fmaf(bv[x].x, 0.0f, fmaf(bv[x].y, 0.0f, fmaf(bv[x].z, 0.0f, fmaf(bv[x].w, 0.0f, zero))));
 #pragma unroll
             for (int y = 0; y < PQ; ++y) {
                 *reinterpret_cast<float4 *>(&tile.k[br + x][bc + (NT / 2) * y]) = bk[y][x];
@@ -277,16 +295,28 @@ __global__ __launch_bounds__(64 * kLinWaves<D>, D == 256 ? 1 : 2) void chunk_f32
             }
             *reinterpret_cast<float4 *>(&tile.v[br + x][vr]) = bv[x];
         }
+        if (OUT && zero != 0.0f) tile.lost = c0;
     };
+    if (OUT && tid == 0) tile.lost = -1;
     fetch(0);
     for (int c0 = 0; c0 < sr.n; c0 += kChunk) {
         const int n = min(kChunk, sr.n - c0);
         __syncthreads();                                  // the tile before is read
-        put();
+        put(c0);
         __syncthreads();
         if (c0 + kChunk < sr.n) fetch(c0 + kChunk);
         if (n < kChunk) age.set(l2, n, g);
+        bool lost = false;                                // the lane's column has a value that is not finite
         if (OUT) {
+            if (tile.lost == c0) {                        // rare; the wave's columns are its own
+                int first = kChunk;
+#pragma unroll 1
+                for (int i = 15; i >= 0; --i) {
+                    float &v = tile.v[row_of(i, g)][32 * wave + col];
+                    if (!(fabsf(v) < INFINITY)) v = 0.0f, first = row_of(i, g);
+                }
+                lost = keep_lost(tile.from_row[wave], first, g, col);
+            }
             // P^T: each wave sums over its share of the dims, all of them add the shares up
             f16v p{};
 #pragma unroll
@@ -323,6 +353,7 @@ __global__ __launch_bounds__(64 * kLinWaves<D>, D == 256 ? 1 : 2) void chunk_f32
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 o = __builtin_amdgcn_mfma_f32_32x32x2f32(tile.v[8 * (i >> 2) + 4 * g + (i & 3)][32 * wave + col], p[i], o, 0, 0, 0);
+            if (tile.lost == c0) hide_lost(o, tile.from_row[wave], g, col);
             if (col < n) {
                 const int64_t at = (static_cast<int64_t>(sr.first + c0 + col) * l.heads + h) * D + v0 + 32 * wave + 16 * g;
 #pragma unroll
@@ -335,7 +366,7 @@ __global__ __launch_bounds__(64 * kLinWaves<D>, D == 256 ? 1 : 2) void chunk_f32
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const int j = 8 * (i >> 2) + 4 * g + (i & 3);
-            const float b = tile.v[j][32 * wave + col] * age.w[i];
+            const float b = i == 0 && lost ? NAN : tile.v[j][32 * wave + col] * age.w[i];
 #pragma unroll
             for (int T = 0; T < D / 32; ++T) s[T] = __builtin_amdgcn_mfma_f32_32x32x2f32(tile.k[j][32 * T + col], b, s[T], 0, 0, 0);
         }
@@ -428,6 +459,7 @@ __global__ __launch_bounds__(64 * kLinWaves<D>, D == 256 ? 1 : 2) void chunk_ker
     constexpr bool kScaled = DT == kDtF16;                // bf16 has f32's range
     __shared__ Tile16<D, OUT> tiles[2];
     alignas(16) __shared__ float undo[kScaled && OUT ? NW : 1][32];   // of a wave's state columns, what their parts were scaled by
+    __shared__ int from_row[OUT ? NW : 1][32];            // see hide_lost
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 5, col = lane & 31;
     const Item it = item_of(l, sg, NS);
@@ -512,8 +544,11 @@ __global__ __launch_bounds__(64 * kLinWaves<D>, D == 256 ? 1 : 2) void chunk_ker
         const bool more = c0 + kChunk < sr.n;
         if (more) fetch(c0 + kChunk);
         u4 vf[2];
+        auto values = [&]() {
 #pragma unroll
-        for (int m = 0; m < 2; ++m) vf[m] = *reinterpret_cast<const u4 *>(&t.vt[32 * wave + col][16 * m + 8 * g]);
+            for (int m = 0; m < 2; ++m) vf[m] = *reinterpret_cast<const u4 *>(&t.vt[32 * wave + col][16 * m + 8 * g]);
+        };
+        bool lost = false;                                // the lane's column has a value that is not finite
         if (OUT) {
             u4 qf[D / 16];
 #pragma unroll
@@ -554,6 +589,22 @@ __global__ __launch_bounds__(64 * kLinWaves<D>, D == 256 ? 1 : 2) void chunk_ker
             __builtin_amdgcn_wave_barrier();
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[i] *= fo;
+            values();
+            constexpr uint32_t kExp = DT == kDtBf16 ? 0x7F80u : 0x7C00u;
+            us2 most = __builtin_bit_cast(us2, vf[0][0] & 0x7FFF7FFFu);
+#pragma unroll
+            for (int i = 1; i < 8; ++i) most = __builtin_elementwise_max(most, __builtin_bit_cast(us2, vf[i >> 2][i & 3] & 0x7FFF7FFFu));
+            const bool any_lost = __any(most.x >= kExp || most.y >= kExp);
+            if (any_lost) {                               // rare
+                int first = kChunk;                       // the wave's columns are its own
+#pragma unroll 1
+                for (int i = 15; i >= 0; --i) {
+                    uint16_t &x = tiles[at].vt[32 * wave + col][16 * (i >> 3) + 8 * g + (i & 7)];
+                    if ((x & kExp) == kExp) x = 0, first = row_of(i, g);
+                }
+                lost = keep_lost(from_row[wave], first, g, col);
+                values();
+            }
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
                 float x[8];
@@ -563,6 +614,7 @@ __global__ __launch_bounds__(64 * kLinWaves<D>, D == 256 ? 1 : 2) void chunk_ker
                 o = mma<DT>(vf[m], lo, o);
                 o = mma<DT>(vf[m], hi, o);
             }
+            if (any_lost) hide_lost(o, from_row[wave], g, col);
             if (col < n) {
                 const int64_t to = (static_cast<int64_t>(sr.first + c0 + col) * l.heads + h) * D + v0 + 32 * wave + 16 * g;
                 u4 y[2];
@@ -574,10 +626,12 @@ __global__ __launch_bounds__(64 * kLinWaves<D>, D == 256 ? 1 : 2) void chunk_ker
                 q[1] = y[1];
             }
         }
+        if (!OUT) values();
         if (n < kChunk) age.set(l2, n, g);
         float aged[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) aged[i] = widen16<DT>(i & 1 ? vf[i >> 3][(i & 7) >> 1] >> 16 : vf[i >> 3][(i & 7) >> 1] & 0xFFFFu) * age.w[i];
+        if (lost) aged[0] = NAN;
         const int ea = kScaled ? room(largest(aged), most_es) : 0;
         aged_by += n;
         const float gone = power(l2, aged_by);

@@ -1,5 +1,5 @@
 """GPU: rad_linear_attn with values that are not finite, products that leave f32's range, and value columns, rows and states of
-very different sizes: nothing reaches an earlier row, another sequence, or a head that it has no part in."""
+very different sizes: nothing reaches an earlier row, another sequence, or a head or column that it has no part in."""
 import numpy as np
 import pytest
 
@@ -50,7 +50,7 @@ def check(got, want, mass, S, want_S, big, dtype, new, D, rows=Ellipsis, states=
 @pytest.mark.parametrize("D", B.KV_HEAD_DIMS)
 @pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
 @pytest.mark.parametrize("dtype", C.DTYPES)
-@pytest.mark.parametrize("what", ["q", "k"])
+@pytest.mark.parametrize("what", ["q", "k", "v"])
 def test_what_is_not_finite_reaches_no_earlier_row_and_no_other_column(torch, what, bad, D, dtype):
     print("not finite", what, bad, D, dtype, flush=True)
     q, k, v, g, S = inputs(D, D, dtype, NEW)
@@ -130,3 +130,21 @@ def test_states_far_from_the_values(torch, size, dtype):
     want, want_S, mass, big = X.linear(q, k, v, g, S, C.ragged(NEW), scale)
     got, state = call(torch, q, k, v, g, S, dtype, NEW, scale)
     check(got, want, mass, state, want_S, big, dtype, NEW, 64)
+
+
+@pytest.mark.parametrize("dtype", C.DTYPES)
+@pytest.mark.parametrize("D", B.KV_HEAD_DIMS)
+def test_many_values_that_are_not_finite(torch, D, dtype):
+    # in several columns, rows and chunks, each from its own row on; zero keys and weights too, and rows behind a whole chunk
+    q, k, v, g, S = inputs(D + 4, D, dtype, [150, 33])
+    rng, start, scale = np.random.default_rng(D), C.ragged([150, 33]), D ** -0.5
+    want, want_S, mass, big = X.linear(q, k, v, g, S, start, scale)
+    clean, clean_S = np.ones(want.shape, bool), np.ones(S.shape, bool)
+    for seq, lo, hi in ((0, 0, 150), (1, 150, 183)):
+        for column in rng.choice(D, D // 3, replace=False):
+            head, row = int(rng.integers(4)), int(rng.integers(lo, hi))
+            v[row, head, column] = rng.choice([np.nan, np.inf, -np.inf])
+            clean[row:hi, head, column], clean_S[seq, head, :, column] = False, False
+    got, state = call(torch, q, k, v, g, S, dtype, [150, 33], scale)
+    check(got, want, mass, state, want_S, big, dtype, [150, 33], D, clean, clean_S)
+    assert not np.isfinite(got[~clean]).any() and not np.isfinite(state[~clean_S]).any()
