@@ -82,14 +82,15 @@ __device__ __forceinline__ PairRow ready(const Kv4Attn &a, const Observed &ob, i
     big = fmaxf(big, lane_xor<2>(big));
     big = fmaxf(big, lane_xor<4>(big));
     const int e = big > 0.0f ? 10 - __builtin_amdgcn_frexp_expf(big) : 0;
+    const bool token = used && ob.base + ci >= 0;             // else its values may be anything: scores of 0
 #pragma unroll
     for (int n = 0; n < N; ++n) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[n][i] = used ? __builtin_amdgcn_ldexpf(x[n][i], e) : 0.0f;
+        for (int i = 0; i < 8; ++i) x[n][i] = token ? __builtin_amdgcn_ldexpf(x[n][i], e) : 0.0f;
         if constexpr (DT == kDtF32) f16_split8(x[n], hi[n], lo[n]);
         else hi[n] = f16_pack8(x[n]);
     }
-    const bool on = used && ob.base + ci >= 0 && st.y > 0.0f;
+    const bool on = token && st.y > 0.0f;
     return PairRow{on ? score_factor(a.sm_scale, e) : 0.0f, on ? st.x : 0.0f, on ? st.y : 0.0f, ob.base + ci};
 }
 template <int DT, int D>
