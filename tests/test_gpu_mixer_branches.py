@@ -1,4 +1,6 @@
-"""GPU: attention weights where rows are no token, whose queries may hold anything."""
+"""GPU: the token mixers at sizes that choose other launches than small calls do: many pairs of rows and heads over many steps,
+selections of several lists a workgroup's share, sequences past one look of a wave; and rows that are no token, whose queries
+may hold anything."""
 import numpy as np
 import pytest
 
@@ -7,6 +9,8 @@ from oracle import layer as O
 from oracle import mixers as X
 from rotated_w8a8_int8_amd import binding as B
 from test_gpu_attn_tree import check
+from test_gpu_kv4_evict import run_select
+from test_gpu_linear_attn import run as run_linear
 
 pytestmark = pytest.mark.gpu
 
@@ -76,3 +80,33 @@ def test_queries_of_rows_that_are_no_token(torch, new, G, dtype, garbage, causal
         garbage = 6e4
     run_weights(torch, new, [-2, 30, -5], 2, G, 64, 32, dtype, causal, 0, 0, 0.5, seed=len(new), pad=3, garbage=garbage)
     run_weights(torch, new, [-2, 30, 5], 2, G, 64, 32, dtype, causal, 0, 0, 0.5, seed=len(new), pad=1, garbage=garbage, max_q=3)
+
+
+@pytest.mark.parametrize("dtype", C.DTYPES)
+@pytest.mark.parametrize("D", B.KV_HEAD_DIMS)
+@pytest.mark.parametrize("causal,window,observe", [(True, 0, 0), (False, 700, 6)])
+def test_weights_of_many_pairs_over_many_steps(torch, D, dtype, causal, window, observe):
+    # a step a wave: 10 rows of 5 heads, 32 (sequence, head) pairs, 129 steps and more
+    print("many", D, dtype, causal, flush=True)
+    run_weights(torch, [10, 7, 10, 0], [4100, 2000, 33, 3500], 8, 7, D, 64, dtype, causal, window, observe, 0.5, seed=D, pad=2)
+
+
+@pytest.mark.parametrize("kind", ["spread", "ties", "odd"])
+@pytest.mark.parametrize("sequences,heads", [(20, 2), (40, 2), (70, 2)])
+def test_selections_of_many_lists(torch, sequences, heads, kind):
+    # 40, 80 and 140 lists of up to 17000 tokens: four, two and one workgroup a list
+    print("lists", sequences, kind, flush=True)
+    rng = np.random.default_rng(sequences)
+    for longest, budget in ((5000, 700), (17000, 4000), (45000, 4001)):
+        run_select(torch, rng.integers(longest // 3, longest, sequences).tolist() + [longest], heads, budget, 4, budget // 5, kind, seed=longest)
+
+
+@pytest.mark.parametrize("dtype", C.DTYPES)
+@pytest.mark.parametrize("sequences", [64, 65, 130, 700])
+def test_linear_attention_of_many_ragged_sequences(torch, sequences, dtype):
+    # a place's sequence is looked for 64 at a time
+    rng = np.random.default_rng(sequences)
+    new = rng.integers(0, 30, sequences)
+    new[rng.choice(sequences, 3, replace=False)] = (200, 129, 400)
+    run_linear(torch, new.tolist(), 2, 1, 64, dtype, seed=sequences, pad=1)
+    run_linear(torch, new.tolist(), 40 if sequences < 200 else 4, 4, 64, dtype, seed=sequences, pad=1, in_place=True)
