@@ -8,6 +8,7 @@ from oracle import layer as O
 from oracle import mixers as X
 from rotated_w8a8_int8_amd import binding as B
 from test_gpu_linear_attn import tolerance
+from test_oracle_linear_parts import STATE_TERM
 
 pytestmark = pytest.mark.gpu
 NEW = [70, 9, 40, 33]                                        # rows a sequence, in chunks and segments
@@ -148,3 +149,39 @@ def test_many_values_that_are_not_finite(torch, D, dtype):
     got, state = call(torch, q, k, v, g, S, dtype, [150, 33], scale)
     check(got, want, mass, state, want_S, big, dtype, [150, 33], D, clean, clean_S)
     assert not np.isfinite(got[~clean]).any() and not np.isfinite(state[~clean_S]).any()
+
+
+@pytest.mark.parametrize("dtype", C.DTYPES)
+@pytest.mark.parametrize("D", B.KV_HEAD_DIMS)
+def test_states_hold_more_than_the_values_type(torch, D, dtype):
+    # rows whose keys are 0 but one row's: nothing is added up, so that each entry shows how well a term is held
+    rng, n, heads = np.random.default_rng(D), 13, 4
+    q, k, v = (O.to_dtype(rng.standard_normal((n, x, D)), dtype) for x in (2, 2, heads))
+    j = int(rng.integers(n))
+    k[np.arange(n) != j] = 0
+    g = -rng.uniform(0.002, 0.01, heads).astype(np.float32)
+    _, state = call(torch, q, k, v, g, np.zeros((1, heads, D, D), np.float32), dtype, [n], 1.0)
+    want = X.linear(q, k, v, g, np.zeros((1, heads, D, D)), np.array([0, n]), 1.0)[1]
+    assert np.all(np.abs(state - want) <= STATE_TERM * np.abs(want) + 1e-30), np.max(np.abs(state - want) / np.maximum(np.abs(want), 1e-30))
+
+
+@pytest.mark.parametrize("dtype", C.DTYPES)
+@pytest.mark.parametrize("D", B.KV_HEAD_DIMS)
+@pytest.mark.parametrize("what", ["q", "k", "v"])
+def test_what_is_not_finite_row_by_row(torch, what, D, dtype):
+    new = [3, 1, 0, 8]
+    q, k, v, g, S = inputs(D + 5, D, dtype, new)
+    start, scale = C.ragged(new), D ** -0.5
+    want, want_S, mass, big = X.linear(q, k, v, g, S, start, scale)
+    x = {"q": q, "k": k, "v": v}
+    x[what][6, 1, 7] = np.nan
+    got, state = call(torch, x["q"], x["k"], x["v"], g, S, dtype, new, scale)
+    clean, clean_S = np.ones(want.shape, bool), np.ones(S.shape, bool)
+    if what == "q":
+        clean[6, 2:] = False
+    elif what == "k":
+        clean[6:, 2:], clean_S[3, 2:] = False, False
+    else:
+        clean[6:, 1, 7], clean_S[3, 1, :, 7] = False, False
+    check(got, want, mass, state, want_S, big, dtype, new, D, clean, clean_S)
+    assert not np.isfinite(got[~clean]).any()
