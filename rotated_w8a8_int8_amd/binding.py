@@ -908,12 +908,14 @@ def linear_attn(q, k, v, log_decay, state=None, state_out=None, q_start=None, ma
     max_q = 1 if q_start is None else rows if max_q is None else int(max_q)
     d = LinearDesc(qp, kp, vp, ldq, ldk, ldv, gp, sp, B, rows, max_q, qk_heads, heads, D, dt)
     key = (B, rows, max_q, heads, D, dt, q_start is None)
-    if key not in _linear_bytes:
+    size = _linear_bytes.get(key)
+    if size is None:
         n = ctypes.c_int64(0)
         _check(lib().rad_linear_attn_workspace(d, ctypes.byref(n)), "rad_linear_attn_workspace")
-        if len(_linear_bytes) > 4096:
+        size = n.value
+        if len(_linear_bytes) > 4096:            # another thread may do so as well: nothing is looked up again
             _linear_bytes.clear()
-        _linear_bytes[key] = n.value
-    wp, size, workspace = _workspace(workspace, _linear_bytes[key], v)
+        _linear_bytes[key] = size
+    wp, size, workspace = _workspace(workspace, size, v)
     _enqueue("rad_linear_attn", index, lib().rad_linear_attn, d, ip, np_, scale, op, wp, size)
     return o, state_out
