@@ -197,6 +197,9 @@ struct Piece {
     int seq, tile, part, parts, slot;     // parts 0: none.  slot: place among the parts kept apart
 };
 
+// Arguments of a kernel below: these, a count of columns and two addresses (see Kv4Attn).
+static_assert(sizeof(Kv4Cache) + sizeof(KvBatch) + sizeof(Kv4Attn) + sizeof(Plan) + 24 <= 192, "three lines");
+
 // Workgroups go to the eight XCDs in turn, each with an L2 of its own.  Where tiles share codes, a KV head's
 // pieces stay on one XCD (on 8 / heads of them in turn, where there are fewer heads), the tiles of a part
 // side by side (8 trees of up to 60 nodes over 16000 tokens 87 -> 82 us, an 8192-token prompt 850 -> 844 us).
@@ -449,7 +452,7 @@ __device__ __forceinline__ TokenRange seen_by(const KvBatch &b, const Kv4Attn &a
     TokenRange r{0, s.pos0 + ci >= 0 ? s.len : 0};
     if (a.window > 0) {
         const int nodes = s.len - s.pos0;
-        const int path = mask_count(a.mask + static_cast<int64_t>(s.first_row + ci) * a.words, a.words, max(0, -s.pos0), nodes);
+        const int path = mask_count(a.mask + static_cast<int64_t>(s.first_row + ci) * a.words(), a.words(), max(0, -s.pos0), nodes);
         r.lo = max(0, min(s.pos0, s.pos0 + path - a.window));    // nodes themselves lie in every window
     }
     return r;
@@ -475,7 +478,7 @@ struct Pages {
 };
 
 // Where a column's sums go: the output, or among the parts kept apart.
-template <int DT, int D>
+template <int DT, int D, bool TREE>
 struct Output {
     const Kv4Attn &a;
     const Plan &pl;
@@ -489,7 +492,7 @@ struct Output {
             const int cp = tile0 + cc;
             const int64_t at = (static_cast<int64_t>(first_row + cp / G) * a.q_heads + h * G + cp % G) * D + d;
             store4<DT>(a.o, at, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-            if (a.stats && d == 0) a.stats[at / D] = make_float2(m, inv);
+            if (!TREE && a.stats && d == 0) a.stats[at / D] = make_float2(m, inv);
         } else {
             const int64_t slot = (static_cast<int64_t>(h) * pl.slots + pc.slot) * cols + cc;
             *reinterpret_cast<f4 *>(part_o + slot * D + d) = o;
@@ -543,7 +546,7 @@ __global__ __launch_bounds__(256, D == 128 && HL != 2 ? 3 : 2) void attn_kernel(
     // too many (32 chains of three, 16000 tokens: 64 us, 61 us so; attn_wide_kernel has no such limit, and
     // 8 nodes over 500 tokens lose 0.3 us to it).
     const uint8_t *const masks = reinterpret_cast<const uint8_t *>(a.mask);
-    const uint32_t mask = TREE ? static_cast<uint32_t>(sh.first_row + ci) * static_cast<uint32_t>(8 * a.words) : 0u;
+    const uint32_t mask = TREE ? static_cast<uint32_t>(sh.first_row + ci) * static_cast<uint32_t>(8 * a.words()) : 0u;
     const int64_t qrow = (static_cast<int64_t>(sh.first_row + ci) * a.q_heads + h * G + cg) * D;
     // the query's values are asked for first, then the first steps
     float qv[NK][8];
@@ -620,7 +623,7 @@ __global__ __launch_bounds__(256, D == 128 && HL != 2 ? 3 : 2) void attn_kernel(
         }
         if (step < sh.open_lo || step >= sh.open_hi) {
             const int t0 = (step << 5) + 8 * g;
-            const uint32_t bits = TREE ? mask_bits8(masks, mask, 8 * a.words, t0 - sh.pos0) : 0u;
+            const uint32_t bits = TREE ? mask_bits8(masks, mask, 8 * a.words(), t0 - sh.pos0) : 0u;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const bool on = t0 + i >= tr.lo && t0 + i < tr.hi && (!TREE || t0 + i < sh.pos0 || (bits >> i & 1));
@@ -692,7 +695,7 @@ __global__ __launch_bounds__(256, D == 128 && HL != 2 ? 3 : 2) void attn_kernel(
 
     // lane (g, c) holds dims 64 j + 16 g .. + 15 of column c: acc[4 j + x][i] is 4 i + x of them
     auto dims4 = [&](int j, int i) { return f4{acc[4 * j][i], acc[4 * j + 1][i], acc[4 * j + 2][i], acc[4 * j + 3][i]}; };
-    const Output<DT, D> out{a, pl, pc, part_o, part_ml, sh.first_row, sh.tile0, cols, h, G};
+    const Output<DT, D, TREE> out{a, pl, pc, part_o, part_ml, sh.first_row, sh.tile0, cols, h, G};
     l = col_sum(l);
     if (g == 0) {
         lds_ml[tg][col][0] = m;
@@ -797,7 +800,7 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(Kv4Cache c, KvBatch b
     const bool used = cp < sh.pairs;
     const int ci = used ? cp / G : 0, cg = used ? cp % G : 0;
     const TokenRange tr = used ? seen_by<TREE>(b, a, sh, seq, ci) : sh.tile_r;
-    const uint8_t *const mask = TREE ? reinterpret_cast<const uint8_t *>(a.mask + static_cast<int64_t>(sh.first_row + ci) * a.words) : nullptr;
+    const uint8_t *const mask = TREE ? reinterpret_cast<const uint8_t *>(a.mask + static_cast<int64_t>(sh.first_row + ci) * a.words()) : nullptr;
     const int64_t qrow = (static_cast<int64_t>(sh.first_row + ci) * a.q_heads + h * G + cg) * D;
     float qv[NK][8];
 #pragma unroll
@@ -863,8 +866,8 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(Kv4Cache c, KvBatch b
         for (int i = 0; i < 16; ++i) s[i] = times_half(st[i], cur.ks[i >> 3], i & 7);
         if (step < sh.open_lo || step >= sh.open_hi) {
             const int t0 = (step << 5) + 8 * g;
-            const uint32_t bits = TREE ? mask_bits8(mask, 0, 8 * a.words, t0 - sh.pos0) |
-                                             mask_bits8(mask, 0, 8 * a.words, t0 + 16 - sh.pos0) << 8 : 0u;
+            const uint32_t bits = TREE ? mask_bits8(mask, 0, 8 * a.words(), t0 - sh.pos0) |
+                                             mask_bits8(mask, 0, 8 * a.words(), t0 + 16 - sh.pos0) << 8 : 0u;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const int t = t0 + 16 * (i >> 3) + (i & 7);
@@ -937,7 +940,7 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(Kv4Cache c, KvBatch b
 
     // lane (g, c): tile x's row 8 q + 4 g + i is dim D / 32 * row + x; four dims in a row from (q, i)
     l += __shfl_xor(l, 32);
-    const Output<DT, D> out{a, pl, pc, part_o, part_ml, sh.first_row, sh.tile0, cols, h, G};
+    const Output<DT, D, TREE> out{a, pl, pc, part_o, part_ml, sh.first_row, sh.tile0, cols, h, G};
     if (g == 0) {
         lds_ml[tg][col][0] = m;
         lds_ml[tg][col][1] = l;
@@ -1009,7 +1012,7 @@ __global__ __launch_bounds__(512) void attn_join_kernel(Kv4Cache c, KvBatch b, K
         const int cp = pc.tile * pl.tm + cc;
         const int64_t at = (static_cast<int64_t>(sw.rr.first + cp / G) * a.q_heads + h * G + cp % G) * D + d;
         store4<DT>(a.o, at, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-        if (a.stats && ln == 0) a.stats[at / D] = make_float2(top, inv);
+        if (!TREE && a.stats && ln == 0) a.stats[at / D] = make_float2(top, inv);
     }
 }
 
@@ -1069,9 +1072,9 @@ Shape attn_shape(const KvBatch &b, const Kv4Cache &c, int q_heads) {
 }
 
 template <int DT, int D, bool TREE>
-hipError_t launch_d(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, hipStream_t st) {
+hipError_t launch_d(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, void *workspace, hipStream_t st) {
     const Shape s = attn_shape(b, c, a.q_heads);
-    float *part_o = static_cast<float *>(a.workspace), *part_ml = part_o + s.sums / 4;
+    float *part_o = static_cast<float *>(workspace), *part_ml = part_o + s.sums / 4;
     const dim3 grid = s.plan.per ? dim3(8 * s.plan.per, c.heads / common8(c.heads)) : dim3(s.plan.pieces, c.heads), block(64 * kWaves);
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, st, c, b, a, s.plan, s.cols, part_o, part_ml); };
     constexpr int HL = DT == kDtF32 ? 2 : 0;
@@ -1094,16 +1097,16 @@ hipError_t launch_d(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, hipSt
 }
 
 template <int DT, bool TREE>
-hipError_t launch_t(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, hipStream_t st) {
-    if (c.D == 64) return launch_d<DT, 64, TREE>(c, b, a, st);
-    if (c.D == 128) return launch_d<DT, 128, TREE>(c, b, a, st);
-    return launch_d<DT, 256, TREE>(c, b, a, st);
+hipError_t launch_t(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, void *workspace, hipStream_t st) {
+    if (c.D == 64) return launch_d<DT, 64, TREE>(c, b, a, workspace, st);
+    if (c.D == 128) return launch_d<DT, 128, TREE>(c, b, a, workspace, st);
+    return launch_d<DT, 256, TREE>(c, b, a, workspace, st);
 }
 template <bool TREE>
-hipError_t launch_attn(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, int dtype, hipStream_t st) {
-    if (dtype == kDtF32) return launch_t<kDtF32, TREE>(c, b, a, st);
-    if (dtype == kDtBf16) return launch_t<kDtBf16, TREE>(c, b, a, st);
-    return launch_t<kDtF16, TREE>(c, b, a, st);
+hipError_t launch_attn(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, void *workspace, int dtype, hipStream_t st) {
+    if (dtype == kDtF32) return launch_t<kDtF32, TREE>(c, b, a, workspace, st);
+    if (dtype == kDtBf16) return launch_t<kDtBf16, TREE>(c, b, a, workspace, st);
+    return launch_t<kDtF16, TREE>(c, b, a, workspace, st);
 }
 
 }  // namespace

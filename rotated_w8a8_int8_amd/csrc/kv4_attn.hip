@@ -13,8 +13,8 @@ int64_t kv4_attn_workspace(const Kv4Cache &c, const KvBatch &b, int q_heads, int
     return s.sums + s.stats;
 }
 
-hipError_t launch_kv4_attn(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, int dtype, hipStream_t st) {
-    return launch_attn<false>(c, b, a, dtype, st);
+hipError_t launch_kv4_attn(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, void *workspace, int dtype, hipStream_t st) {
+    return launch_attn<false>(c, b, a, workspace, dtype, st);
 }
 
 }  // namespace rad

@@ -4,8 +4,8 @@
 
 namespace rad {
 
-hipError_t launch_kv4_attn_tree(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, int dtype, hipStream_t st) {
-    return launch_attn<true>(c, b, a, dtype, st);
+hipError_t launch_kv4_attn_tree(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, void *workspace, int dtype, hipStream_t st) {
+    return launch_attn<true>(c, b, a, workspace, dtype, st);
 }
 
 }  // namespace rad

@@ -266,12 +266,12 @@ int attend(const rad_kv4_cache *cache, const rad_kv_batch *batch, const void *q,
     if (overlap(os, qs) || overlap(ws, qs) || overlap(ws, os) || sp.meets(os) || sp.meets(ws)) return RAD_E_ALIAS;
     if (overlap(ms, os) || overlap(ms, ws) || overlap(wt, qs) || overlap(wt, os) || overlap(wt, ws) || sp.meets(wt)) return RAD_E_ALIAS;
     const int win = window > 0 && window < kMaxTokens ? static_cast<int>(window) : 0;
-    float2 *stats = nullptr;
-    if (x.weights) stats = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + stats_at(cache, batch, q_heads, dtype));
-    const rad::Kv4Attn at{q, o, static_cast<int>(q_heads), sm_scale, causal, win, workspace, stats, x.mask, static_cast<int>(x.words)};
+    rad::Kv4Attn at{q, o, static_cast<int>(q_heads), sm_scale, x.tree ? static_cast<int>(x.words) : causal, win, {nullptr}};
+    if (x.weights) at.stats = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + stats_at(cache, batch, q_heads, dtype));
+    if (x.tree) at.mask = x.mask;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    if (x.tree) return hip_status(rad::launch_kv4_attn_tree(ca, ba, at, dtype, st));
-    const hipError_t err = rad::launch_kv4_attn(ca, ba, at, dtype, st);
+    if (x.tree) return hip_status(rad::launch_kv4_attn_tree(ca, ba, at, workspace, dtype, st));
+    const hipError_t err = rad::launch_kv4_attn(ca, ba, at, workspace, dtype, st);
     if (err != hipSuccess || !x.weights) return hip_status(err);
     const int observe = x.observe < batch->rows ? static_cast<int>(x.observe) : 0;
     void *pairs = static_cast<char *>(workspace) + pairs_at(cache, batch, q_heads, dtype);
