@@ -451,8 +451,14 @@ hipError_t launch_kv4_append(const Kv4Cache &c, const KvBatch &b, const Kv4New &
 }
 
 hipError_t launch_kv4_read(const Kv4Cache &c, const KvBatch &b, uint16_t *k, uint16_t *v, hipStream_t st) {
-    // few rows take more workgroups one by one (256 rows of 8 heads 3.3 us, 4.6 us by octets)
-    if (b.q_start && b.rows / b.B >= 8 && static_cast<int64_t>(b.rows) * c.heads >= 8192) {
+    // Octets where there are 48K vectors of 128 or 24K of 256 and more (8 heads of 128, warm: 8192 vectors 4.9 us, 3.7 one by
+    // one, 32768 7.6 and 6.6, 49152 9.3 and 9.2 or, of 8 sequences, 9.4 and 10.2, 65536 11.2 and 11.8, 262144 of 8 sequences 29
+    // and 38).  A single head leaves three of four waves idle and heads of 64 half of a load's width: there it takes
+    // many, and sequences to be looked for (131072 of one head 21 us and 18, of 64 sequences 21 and 23; 262144 of 64
+    // 20.7 and 19.8, of 8 sequences 20.3 and 20.8).
+    const int64_t values = static_cast<int64_t>(b.rows) * c.heads * c.D;
+    const bool narrow = c.heads == 1 || c.D == 64;
+    if (b.q_start && b.rows / b.B >= 8 && (narrow ? b.B >= 8 && values >= 16 << 20 : values >= 6 << 20)) {
         const dim3 grid((b.rows + 7) / 8, (c.heads + 3) / 4), block(256);
         if (c.D == 64) hipLaunchKernelGGL(kv4_read_octets_kernel<64>, grid, block, 0, st, c, b, k, v);
         else if (c.D == 128) hipLaunchKernelGGL(kv4_read_octets_kernel<128>, grid, block, 0, st, c, b, k, v);
