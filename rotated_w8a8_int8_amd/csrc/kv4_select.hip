@@ -136,8 +136,7 @@ __device__ __forceinline__ void count4(const Task &k, int t, uint4 w, uint32_t l
 // ---- keys in registers ---------------------------------------------------------
 //
 // blockIdx.x: sequence * shares + share, blockIdx.y: head; 4 NV keys a thread, 4096 tokens in a row at a time.  Every
-// share finds the least key, and lists its share of the tokens (64 sequences of 32768 tokens: 36 us with one
-// share).  Weights crowd into few digits (a binade is four of them), so a digit has four counters, by lane; the
+// share finds the least key, and lists its share of the tokens.  Weights crowd into few digits (a binade is four of them), so a digit has four counters, by lane; the
 // keys that share the first digit are few and go on in LDS, where kHeldKeys hold them (32 us without).
 constexpr int kSelWaves = 16, kRun = 256 * kSelWaves, kHeldKeys = 4096;
 // A token's number, hidden from the compiler, which would keep what it once found out about each
@@ -273,7 +272,7 @@ __global__ __launch_bounds__(64 * kSelWaves) void select_kernel(Kv4Select s, int
 // its slice's keys that share the digits found; launch 3 lists.  Each finds the digit before it from
 // every slice's counts; slice 0 keeps it for the launches after that.  Of a slice's keys those above the
 // digits found so far are counted on the way.
-constexpr int kSliceWaves = 16, kSliceCopies = 4, kMostSlices = 64;
+constexpr int kSliceWaves = 16, kSliceCopies = 4, kMostSlices = 64, kManySlices = 96;
 struct Slices {
     int slices, each;                 // tokens a slice, a multiple of 256 * kSliceWaves
     int *hist;                        // [3][pairs][slices][kBins]
@@ -422,8 +421,13 @@ __global__ __launch_bounds__(64 * kSliceWaves) void slice_kernel(Kv4Select s, Sl
     }
 }
 
-// Tokens that a workgroup's registers hold; sequences that may be longer are cut into slices.
+// Tokens of a slice whose list is still in registers when it is written; up to 1024 slices for all lists, as long as a list
+// has no more than 96 of them, whose counts every slice adds up: else 64 longer ones (one list of 1300000 tokens 57 us
+// in 80, 62 in 64, of 2 million 72 us in 123, 66 in 64, of 8 million 373 us in 489, 144 in 64; 8 lists of 2 million 250
+// and 128).
 constexpr int kSliceTokens = 16384;
+// Tokens that a workgroup's registers hold; sequences that may be longer are cut into slices (8 lists of 65536 tokens 35 us
+// held, 33 in slices; 64 of them 43 and 36, 256 of them 64 and 129; 8 of 40960 25 and 32).
 constexpr int kMostHeld = 64 * kSelWaves * 4 * 16;
 
 Slices make_slices(int64_t pairs, int64_t max_tokens, void *workspace) {
@@ -431,7 +435,7 @@ Slices make_slices(int64_t pairs, int64_t max_tokens, void *workspace) {
     Slices sl{};
     sl.pairs = pairs;
     const int64_t most = (max_tokens + kSliceTokens - 1) / kSliceTokens, want = pairs < 1024 ? 1024 / pairs : 1;
-    const int64_t n = most < want ? most : want < kMostSlices ? want : kMostSlices;
+    const int64_t n = most < want && most <= kManySlices ? most : want < kMostSlices ? want : kMostSlices;
     const int64_t each = ((max_tokens + n - 1) / n + kUnit - 1) / kUnit * kUnit;
     sl.each = static_cast<int>(each);
     sl.slices = static_cast<int>((max_tokens + each - 1) / each);
@@ -452,6 +456,10 @@ int64_t kv4_select_workspace(int64_t B, int64_t heads, int64_t max_tokens) {
 hipError_t launch_kv4_select(const Kv4Select &s, void *workspace, hipStream_t st) {
     if (s.max_tokens <= kMostHeld) {
         const int64_t pairs = static_cast<int64_t>(s.B) * s.heads;
+        // As many shares as find a CU of their own (lists of 32768: 8 of them 28 us with one share, 24 with two, 22 with
+        // four, 80 of them 29, 25 and 46, 136 of them 29, 49 and 69).  A list's registers go by its room, in rungs
+        // (8 lists of 32768 tokens 22 us with 40 keys a thread, 23.5 with 64; 32 keys would serve 32768 in 21.7 and
+        // leave 40960, 25.5, to 64, 26.9).
         const int shares = s.max_tokens <= 4096 || pairs > 128 ? 1 : pairs > 64 ? 2 : 4;
         auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(s.B * shares, s.heads), dim3(64 * kSelWaves), 0, st, s, shares); };
         if (s.max_tokens <= 4096) go(select_kernel<1>);

@@ -1,5 +1,5 @@
 """GPU: selection where no place is left for weights to compete for (the first and the recent tokens fill the budget), whatever
-the weights are: more of one kind than the kernel holds in LDS among them."""
+the weights are, more of one kind than the kernel holds in LDS among them; and from lists of millions of tokens."""
 import numpy as np
 import pytest
 
@@ -35,3 +35,15 @@ def test_budgets_that_first_and_recent_tokens_fill(torch, L, room, fill):
             for h in range(2):
                 assert np.array_equal(kept[b, h].cpu().numpy(), want)
                 assert np.array_equal(kw[b, h, :budget].cpu().numpy(), w[b, h, want], equal_nan=True)
+
+
+@pytest.mark.parametrize("L", [1048580, 1560000, 1600001, 5000000])
+def test_lists_of_many_slices(torch, L):
+    print("slices", L, flush=True)
+    rng = np.random.default_rng(L)
+    w = (rng.random((2, 1, (L + 3) // 4 * 4)) ** 8).astype(np.float32)
+    seq_len = [L, L // 2]
+    kept, count, kw = B.kv4_select(C.device_batch(torch, np.zeros((2, 1), np.int32), seq_len, None, 2), C.put(torch, w), 2000, 4, 300)
+    for b, n in enumerate(seq_len):
+        want = X.select(w[b, 0], n, 2000, 4, 300)
+        assert np.array_equal(kept[b, 0].cpu().numpy(), want) and np.array_equal(kw[b, 0, :2000].cpu().numpy(), w[b, 0, want])
