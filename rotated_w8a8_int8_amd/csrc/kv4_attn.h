@@ -206,11 +206,12 @@ static_assert(sizeof(Kv4Cache) + sizeof(KvBatch) + sizeof(Kv4Attn) + sizeof(Plan
 struct Place {
     int x, h;
 };
-__host__ __device__ __forceinline__ int common8(int heads) { return heads & 1 ? 1 : heads & 2 ? 2 : heads & 4 ? 4 : 8; }
+// log2 of the largest power of two up to 8 that divides heads.
+__host__ __device__ __forceinline__ int common8(int heads) { return heads & 1 ? 0 : heads & 2 ? 1 : heads & 4 ? 2 : 3; }
 __device__ __forceinline__ Place piece_place(const Plan &pl, int heads) {
     if (pl.per == 0) return Place{static_cast<int>(blockIdx.x), static_cast<int>(blockIdx.y)};
     const int g = common8(heads), xcd = blockIdx.x & 7, j = blockIdx.x >> 3;
-    return Place{j * (8 / g) + xcd / g, static_cast<int>(blockIdx.y) * g + xcd % g};
+    return Place{(j << (3 - g)) + (xcd >> g), (static_cast<int>(blockIdx.y) << g) + (xcd & ((1 << g) - 1))};
 }
 
 // Rows of a sequence that a call handles, and what they see together.
@@ -297,6 +298,9 @@ __device__ __forceinline__ Piece find_piece(const KvBatch &b, const Kv4Attn &a, 
         if constexpr (ITEMS || ONCE) {
             part = ITEMS ? 0 : x % parts, tile = ITEMS ? x : x / parts, slot = ITEMS ? x * parts : x;
             if (tile >= tiles || (ITEMS && parts == 1)) return Piece{0, 0, 0, 0, 0};
+        } else if (!pl.split) {                               // short calls: no division
+            if (x >= tiles) return Piece{0, 0, 0, 0, 0};
+            part = 0, tile = x, slot = x;
         } else {
             if (tiles == 0 || x / tiles >= parts) return Piece{0, 0, 0, 0, 0};
             part = x / tiles, tile = x % tiles, slot = tile * parts + part;
@@ -342,6 +346,9 @@ __device__ __forceinline__ Piece find_piece(const KvBatch &b, const Kv4Attn &a, 
             if constexpr (ITEMS || ONCE) {
                 tile = ITEMS ? local : local / p.parts;
                 p.part = ITEMS ? 0 : local % p.parts;
+            } else if (!pl.split) {                           // short calls: no division
+                tile = local;
+                p.part = 0;
             } else {
                 const int n = __builtin_amdgcn_readlane(tiles, src);
                 tile = local % n;
@@ -492,12 +499,17 @@ struct Output {
             const int cp = tile0 + cc;
             const int64_t at = (static_cast<int64_t>(first_row + cp / G) * a.q_heads + h * G + cp % G) * D + d;
             store4<DT>(a.o, at, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-            if (!TREE && a.stats && d == 0) a.stats[at / D] = make_float2(m, inv);
         } else {
             const int64_t slot = (static_cast<int64_t>(h) * pl.slots + pc.slot) * cols + cc;
             *reinterpret_cast<f4 *>(part_o + slot * D + d) = o;
             if (d == 0) *reinterpret_cast<float2 *>(part_ml + 2 * slot) = make_float2(m, l);
         }
+    }
+    // the column's statistics, where they are asked for (apart from the outputs, whose loop they slowed down)
+    __device__ __forceinline__ bool wants_stats() const { return !TREE && pc.parts == 1 && a.stats; }
+    __device__ __forceinline__ void put_stats(int cc, float m, float l) const {
+        const int cp = tile0 + cc;
+        a.stats[static_cast<int64_t>(first_row + cp / G) * a.q_heads + h * G + cp % G] = make_float2(m, l > 0.0f ? 1.0f / l : 0.0f);
     }
 };
 // The step groups' sums of n columns become one (each group's taken to the common maximum).
@@ -515,6 +527,13 @@ __device__ __forceinline__ void join_groups(const Out &out, float (&lds_o)[TG][T
             l += lds_ml[k][cc][1] * __builtin_amdgcn_exp2f(lds_ml[k][cc][0] - m);
         }
         out.put(cc, d, o, m, l);
+    }
+    if (out.wants_stats() && static_cast<int>(threadIdx.x) < n) {
+        const int cc = threadIdx.x;
+        float m = kLowest, l = 0.0f;
+        for (int k = 0; k < TG; ++k) m = fmaxf(m, lds_ml[k][cc][0]);
+        for (int k = 0; k < TG; ++k) l += lds_ml[k][cc][1] * __builtin_amdgcn_exp2f(lds_ml[k][cc][0] - m);
+        out.put_stats(cc, m, l);
     }
 }
 
@@ -1062,7 +1081,7 @@ Shape attn_shape(const KvBatch &b, const Kv4Cache &c, int q_heads) {
     const int held = !s.once || c.D == 256 ? 2 : c.D == 128 ? 3 : 5;
     s.plan = make_plan(b, c.heads, G, tm, 256 * held, kWaves);
     if (!s.once) {
-        const int each = 8 / common8(c.heads), per = (s.plan.pieces + each - 1) / each;
+        const int each = 8 >> common8(c.heads), per = (s.plan.pieces + each - 1) / each;
         if (static_cast<int64_t>(per) * 8 * 64 * kWaves < int64_t(1) << 32) s.plan.per = per;
     }
     s.cols = static_cast<int>(pairs < tm ? pairs : tm);
@@ -1075,7 +1094,7 @@ template <int DT, int D, bool TREE>
 hipError_t launch_d(const Kv4Cache &c, const KvBatch &b, const Kv4Attn &a, void *workspace, hipStream_t st) {
     const Shape s = attn_shape(b, c, a.q_heads);
     float *part_o = static_cast<float *>(workspace), *part_ml = part_o + s.sums / 4;
-    const dim3 grid = s.plan.per ? dim3(8 * s.plan.per, c.heads / common8(c.heads)) : dim3(s.plan.pieces, c.heads), block(64 * kWaves);
+    const dim3 grid = s.plan.per ? dim3(8 * s.plan.per, c.heads >> common8(c.heads)) : dim3(s.plan.pieces, c.heads), block(64 * kWaves);
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, st, c, b, a, s.plan, s.cols, part_o, part_ml); };
     constexpr int HL = DT == kDtF32 ? 2 : 0;
     if (s.once) {
