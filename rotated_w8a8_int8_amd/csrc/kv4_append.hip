@@ -183,6 +183,7 @@ __device__ __forceinline__ int first_dim(int lane) { return D == 64 ? 4 * lane :
 template <int D>
 constexpr int kRunsApart = D == 64 ? 32 : 64;
 
+static_assert(sizeof(Kv4Cache) + sizeof(KvBatch) + sizeof(Kv4New) <= 192, "three lines");
 // One row per sequence: blockIdx.x the row, blockIdx.y 256 / L heads of it (queries, keys,
 // values), D / 8 lanes each.  A value's lane puts its eight codes into the octet's dwords itself.
 template <int DT, int D, bool AT>

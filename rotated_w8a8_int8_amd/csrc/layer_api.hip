@@ -127,9 +127,8 @@ int append(const rad_kv4_cache *cache, const rad_kv_batch *batch, const void *k,
         for (int j = 0; j < i; ++j)
             if (overlap(sp.cache[i], sp.cache[j])) return RAD_E_ALIAS;
     if (sp.meets(qo)) return RAD_E_ALIAS;
-    const rad::Kv4New nw{q, k, v, ldq, ldk, ldv, static_cast<int>(q_heads), q_out,
-                         rope ? rope->table : nullptr, rope ? rope->rows : 0, rope ? rope->dim : 0,
-                         rope ? rope->style : 0, rotate, position};
+    const rad::Kv4New nw{q, k, v, ldq, ldk, ldv, static_cast<int>(q_heads), rope ? static_cast<int>(rope->rows) : 0, q_out,
+                         rope ? rope->table : nullptr, rope ? rope->dim : 0, rope ? rope->style : 0, rotate, position};
     return hip_status(rad::launch_kv4_append(cache_args(cache), batch_args(cache, batch), nw, dtype,
                                              static_cast<hipStream_t>(stream)));
 }

@@ -21,13 +21,13 @@ struct KvBatch {
     const int32_t *block_table, *seq_len, *q_start;
     int B, max_pages, rows, max_q, page_shift;
 };
+// With cache and batch 192 bytes, three lines of the memory that a kernel's arguments are fetched from.
 struct Kv4New {
     const void *q, *k, *v;
     int64_t ldq, ldk, ldv;
-    int q_heads;
+    int q_heads, rope_rows;
     void *q_out;
     const float *rope;
-    int64_t rope_rows;
     int rope_dim, rope_style, rotate;
     const int32_t *position;     // angles of each row, or null: by its place in the cache
 };
