@@ -129,7 +129,8 @@ __device__ __forceinline__ float head_max(float a) {
 // whether the table has it.
 template <bool AT>
 __device__ __forceinline__ int angle_row(const Kv4New &nw, int64_t row, int t) { return AT ? nw.position[row] : t; }
-__device__ __forceinline__ bool has_angles(const Kv4New &nw, int at) { return !nw.rope || (at >= 0 && at < nw.rope_rows); }
+template <bool AT>
+__device__ __forceinline__ bool has_angles(const Kv4New &nw, int at) { return !nw.rope || ((!AT || at >= 0) && at < nw.rope_rows); }
 
 // One head vector v of a token (kind 0: query, 1: key, 2: value, head h of its kind), by D / 8
 // lanes: the turned query stored, or scale and keys' codes; returns the lane's eight codes.
@@ -199,7 +200,7 @@ __global__ __launch_bounds__(256) void kv4_append_one_kernel(Kv4Cache c, KvBatch
     const void *src = kind == 0 ? nw.q : kind == 1 ? nw.k : nw.v;
     const Runs v{load4<DT>(src, base + d0), load4<DT>(src, base + d1)};
     const int t = kv_len(b, row) - 1, at = angle_row<AT>(nw, row, t);
-    if (t < 0 || !has_angles(nw, at)) return;
+    if (t < 0 || !has_angles<AT>(nw, at)) return;
     const int page = kv_page(b, row, t, c.pages), off = t & ((1 << c.page_shift) - 1), sh = 4 * (t & 7);
     const bool merge = kind == 2 && page >= 0;
     uint4 *oct = nullptr, lo{}, hi{};
@@ -256,7 +257,7 @@ __global__ __launch_bounds__(256) void kv4_append_kernel(Kv4Cache c, KvBatch b, 
             const int64_t trow = rr.first + (t - pos0);
             const bool mine = t >= p && t <= last;
             const int at = !AT || mine ? angle_row<AT>(nw, trow, t) : 0;
-            const bool here = mine && has_angles(nw, at);
+            const bool here = mine && has_angles<AT>(nw, at);
             const int page = kv_page(b, seq, octet * 8, c.pages);
             const int off = (octet * 8) & ((1 << c.page_shift) - 1);
             const Angles ang = here && nw.rope ? angles<D>(nw.rope + static_cast<int64_t>(at) * nw.rope_dim, nw.rope_dim, nw.rope_style, d0, d1)
@@ -298,7 +299,7 @@ __global__ __launch_bounds__(256) void kv4_append_kernel(Kv4Cache c, KvBatch b, 
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const int tj = octet * 8 + j;
-                        const bool on = AT ? live[AT ? j : 0] : tj >= p && tj <= last && has_angles(nw, tj);
+                        const bool on = AT ? live[AT ? j : 0] : tj >= p && tj <= last && has_angles<AT>(nw, tj);
                         word |= ((codes[hs][j][ln] >> nib) & 15u) << (4 * j);
                         mask |= on ? 15u << (4 * j) : 0u;
                     }
