@@ -569,8 +569,9 @@ int rad_kv4_select(const float *weight, int64_t ldw, const int32_t *seq_len, int
  *
  * In place every token is read before the first is written, and entries is at most
  * RAD_KV4_MOVE_MAX (an accepted path; longer lists go to pages of their own).  Otherwise no
- * target page may be one that the call reads, and never may two lists of a call write the
- * same page.  Only the targets' codes and scales change.  B * heads < 2^22, entries < 2^30.
+ * target page may be one that the call reads; in place none that it reads for another sequence; and
+ * never may lists of two sequences write the same page.  Only the targets' codes and scales change.
+ * B * heads < 2^22, entries < 2^30.
  */
 #define RAD_KV4_MOVE_MAX 256
 int rad_kv4_move(const rad_kv4_cache *cache, const rad_kv_batch *batch, const int32_t *from, int64_t lists,
@@ -610,8 +611,8 @@ int rad_kv4_move(const rad_kv4_cache *cache, const rad_kv_batch *batch, const in
  * multiplied in f32.  For the 16-bit types the weights of the rows of a chunk and the state meet the
  * matrix cores as pairs of 16-bit parts: bf16 16 bits, f16 22 bits or 2^-39 of the largest weight of the
  * same row, of the largest value of the same state column, whichever is more.
- * What is not finite reaches its own row and later ones of its sequence: of q that row of its head, of k
- * every value of its head, of v its value column.
+ * What is not finite reaches its own row and later ones of its sequence: of q that row of the heads that
+ * read it, of k every value of the heads that read it, of v its value column.
  */
 typedef struct rad_linear {
     const void *q, *k, *v;

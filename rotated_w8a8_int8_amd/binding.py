@@ -820,8 +820,9 @@ def kv4_select(batch: KVBatch, weight, budget: int, first: int = 0, recent: int 
                kept_weight=None, workspace=None):
     """The ``budget`` tokens of greatest ``weight`` (f32 [B][heads][tokens]) of each of the batch's sequences and
     heads, the first ``first`` and last ``recent`` always among them: ``kept`` int32 [B][heads][budget], ascending,
-    ``count`` int32 [B] of them, and their weights (f32 [B][heads][budget or more];
-    by default as many as a ``weight`` of the kept tokens takes, a multiple of 4)."""
+    ``count`` int32 [B] of them, and their weights (f32 [B][heads][budget or more], by default to a multiple of 4; entries
+    behind ``count`` are left as they were).  A ``weight`` of the kept tokens' next calls has room for all of their pages:
+    give one as ``kept_weight``."""
     torch = _torch()
     B, ref = batch.block_table.shape[0], batch.block_table
     heads = weight.shape[1] if isinstance(weight, torch.Tensor) and weight.dim() == 3 else -1

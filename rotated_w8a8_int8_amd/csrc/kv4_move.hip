@@ -9,7 +9,8 @@
 // Bound by the trips to memory of an octet (list, page, codes, a scale of two bytes from each of 16 lines) more than
 // by bytes: 8 sequences' 4096 of 13000 tokens (8 heads of 128) take 32 us for 44 MB fetched and 35 MB written; the
 // loads of the eight entries one behind the other took 41 us, several octets a wave with the next one's places
-// looked up ahead the same 32.  16384 of 199999 tokens 19 us, 256 of 1000 3.2 us.
+// looked up ahead the same 32.  16384 of 199999 tokens 19 us, 256 of 1000 3.2 us; in place 8 paths of 8 of 60
+// drafted tokens 3.4 us.
 //
 // Into pages of their own the octets are independent.  In place a workgroup has all
 // of a sequence and head's octets (at most 33): it reads them all, meets, and writes.
@@ -105,14 +106,14 @@ __device__ __forceinline__ void write_octet(const Octet<D> &o, const Kv4Cache &t
     for (int x = 0; x < NV; ++x) q[x] = o.mask == 0xFFFFFFFFu ? o.value[x] : (q[x] & ~o.mask) | o.value[x];
 }
 
-constexpr int kFar = 1 << 30;
+constexpr int kFar = (1 << 30) - 16, kBefore = -(1 << 30);   // past every table's last octet, and before any entry's token
 struct List {
     const int32_t *list;
     int len, n, start;
     __device__ __forceinline__ List(const KvBatch &b, const Kv4Move &m, int seq, int h)
         : list(m.from + (static_cast<int64_t>(seq) * m.lists + (m.lists == 1 ? 0 : h)) * m.entries), len(kv_len(b, seq)),
           n(min(max(m.count[seq], 0), m.entries)),
-          start(m.to_start ? min(max(m.to_start[seq], -kFar), kFar) : 0) {}      // no token lies that far: sums stay in 32 bits
+          start(m.to_start ? min(max(m.to_start[seq], kBefore), kFar) : 0) {}      // no token lies that far: sums stay in 32 bits
 };
 // Page of the octet's targets, or -1.
 __device__ __forceinline__ int target_page(const int32_t *table, int pages, int shift, int octet) {

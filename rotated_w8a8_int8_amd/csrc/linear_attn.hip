@@ -6,9 +6,10 @@
 // of the key's rows a thread, four columns each, and passes over its part of the state once:
 // 64 bf16 tokens of 40 heads of 128 stream 338 MB in 56 to 62 us, 5.4 to 6.0 TB/s.
 //
-// Prompts in chunks of 32 rows: 8192 bf16 rows of 40 heads of 128 take 112 us for the outputs,
-// 56 us for what the segments add and 11 us for their states, 625 MB in all at 3.5 TB/s, with 48% of a
-// SIMD's cycles on vector and 28% on matrix instructions; f16 180 us, f32 417 us (its matrix operations 260).
+// Prompts in chunks of 32 rows: 8192 bf16 rows of 40 heads of 128 take 117 us for the outputs,
+// 58 us for what the segments add and 11 us for their states (profiled; 169 us a call), 625 MB in all, 3.7 TB/s of a
+// call, with 52% of the cycles of a SIMD of a busy CU on vector and 33% on matrix instructions while outputs are made; f16
+// 185 us a call, f32 420 us (its matrix operations 260).
 #include <type_traits>
 
 #include "layer_launch.h"
@@ -163,7 +164,7 @@ __device__ __forceinline__ SegRows segment_in(const Linear &l, const Segments &s
 
 // What a workgroup is about.  Workgroups go to the eight XCDs in turn: those that read the same queries and keys
 // (slices of a head, heads that share a key head) follow each other on one, where its L2 serves them
-// (8192 bf16 rows of 16 heads of 256: 292 us, 435 us spread over the XCDs).
+// (8192 bf16 rows of 16 heads of 256: 292 us, 435 us spread over the XCDs, when this was chosen).
 struct Item {
     int place, hk, h, slice;
 };
@@ -685,9 +686,16 @@ __global__ __launch_bounds__(256) void states_kernel(Linear l, Segments sg) {
 }
 
 // Rows a segment: so many that the segments fill the chip once (an 8192-row bf16 prompt of 40 heads takes 176 us
-// with 12, 196 with 9, 207 with 19; 8 x 1000 rows 147 us whole, 207 us in halves), 128 at least (600 rows
-// 36 us, 53 with 256).  Places that stay empty count too: 288 workgroups of which 32 had nothing to do took 440 us
-// where the 256 others take 296.
+// with 12, 196 with 9, 207 with 19; 8 x 1000 rows 147 us whole, 207 us in halves, when this was chosen), 128 at least
+// (600 rows 36 us, 53 with 256).  Places that stay empty count too: 288 workgroups of which 32 had nothing to do took
+// 440 us where the 256 others take 296.
+//
+// Sequences within a tenth of the longest's length share the segments evenly; else these are sized by all rows (bf16, 40
+// heads of 128: 8 x 1000 rows 148 us so, 312 by all rows; 4 of 500 to 1000 rows 78 us by all rows, 92 evenly; 4 ragged of up to
+// 1500 91 and 118), less half a workgroup for each sequence but the first, whose last segment is short (6 ragged 146 us; 149
+// with none less, 176 with a whole one; 4 91, 91 and 98).  Where that leaves one segment the longest sequence goes whole: 8
+// ragged of up to 1500 rows take 225 us, 156 with none less, and of many single rows and one long sequence
+// only that one's heads keep workgroups busy.
 template <int DT, int D>
 Segments make_segments(const Linear &l, void *ws) {
     constexpr int kHeld = D == 256 ? 256 : D == 128 ? 512 : DT == kDtF32 ? 1024 : 768;
