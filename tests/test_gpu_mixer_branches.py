@@ -110,3 +110,12 @@ def test_linear_attention_of_many_ragged_sequences(torch, sequences, dtype):
     new[rng.choice(sequences, 3, replace=False)] = (200, 129, 400)
     run_linear(torch, new.tolist(), 2, 1, 64, dtype, seed=sequences, pad=1)
     run_linear(torch, new.tolist(), 40 if sequences < 200 else 4, 4, 64, dtype, seed=sequences, pad=1, in_place=True)
+
+
+@pytest.mark.parametrize("dtype", C.DTYPES)
+@pytest.mark.parametrize("rows", [3, 40])
+def test_weights_of_more_sequences_than_are_looked_at_by_all(torch, rows, dtype):
+    # past 512 sequences no context is cut, and tiles are found another way
+    rng = np.random.default_rng(rows)
+    new = rng.integers(0, rows, 600)
+    run_weights(torch, new.tolist(), rng.integers(-3, 70, 600).tolist(), 1, 2, 64, 32, dtype, True, 0, 0, 0.5, seed=rows, pad=2)
