@@ -540,7 +540,8 @@ int rad_attn_kv4_weights(const rad_kv4_cache *cache, const rad_kv_batch *batch, 
  *   kept_weight  f32 [B][heads][ld_kept] output, 4-byte aligned, or NULL: the weights of the
  *                kept tokens, in their order; ld_kept at least budget.
  *   workspace    device memory, 16-byte aligned, of at least the bytes that
- *                rad_kv4_select_workspace gives (NULL when that is 0).
+ *                rad_kv4_select_workspace gives (NULL when that is 0); one for each call that
+ *                may run at the same time.
  *
  * B, heads, max_tokens >= 0; B < 2^22, heads <= 1024, max_tokens < 2^30, B * heads < 2^22.  No
  * output may overlap another argument.
@@ -603,7 +604,8 @@ int rad_kv4_move(const rad_kv4_cache *cache, const rad_kv_batch *batch, const in
  *   max_q      no sequence has more rows than this (1 when q_start is NULL); one that has more
  *              is taken as ending after max_q rows.
  *   workspace  device memory, 16-byte aligned, of at least the bytes that
- *              rad_linear_attn_workspace gives for the same sizes (NULL when that is 0).
+ *              rad_linear_attn_workspace gives for the same sizes (NULL when that is 0); one for
+ *              each call that may run at the same time.
  *
  * D is 64, 128 or 256; heads a multiple of qk_heads, at most 1024; B, rows < 2^22; B * heads < 2^22; and
  * one launch holds fewer than 2^24 workgroups of 128 rows and more of a head's 128 values (2^25 for D = 64).

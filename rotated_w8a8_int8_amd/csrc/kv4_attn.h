@@ -238,18 +238,6 @@ __device__ __forceinline__ SeqWork seq_work(const KvBatch &b, const Kv4Attn &a, 
 }
 __device__ __forceinline__ int steps_of(int lo, int hi) { return hi > lo ? ((hi + 31) >> 5) - (lo >> 5) : 0; }
 
-// Inclusive sum over the lanes of a wave: inside rows of 16, then row 0 into 1 and 2 into
-// 3, then rows 0 .. 1 into 2 .. 3.
-__device__ __forceinline__ int wave_scan(int v) {
-    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);     // row_shr 1, 2, 4, 8
-    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);    // row_bcast 15
-    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);    // row_bcast 31
-    return v;
-}
-
 // Steps a part: about `target` parts over all sequences and KV heads, rounded up.
 __device__ __forceinline__ int chunk_of(uint64_t total, const Plan &pl, int heads) {
     const uint64_t all = total * static_cast<uint32_t>(heads) + static_cast<uint32_t>(pl.target - 1);

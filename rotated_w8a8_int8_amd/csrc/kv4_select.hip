@@ -95,17 +95,6 @@ __device__ __forceinline__ uint32_t look4(const Task &k, int t, uint4 w, uint32_
 // How many of each kind, in the halves of a word (256 tokens a wave at most, so they stay apart).
 __device__ __forceinline__ int counts(uint32_t m) { return __popc(m & 15u) | __popc(m >> 4) << 16; }
 
-// Inclusive sum over the lanes of a wave.
-__device__ __forceinline__ int wave_scan(int v) {
-    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);     // row_shr 1, 2, 4, 8
-    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);    // row_bcast 15
-    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);    // row_bcast 31
-    return v;
-}
-
 // The kept tokens among 256 in a row (four a lane), behind `ups` and `ties` of them that came before.
 __device__ __forceinline__ void list256(const Kv4Select &s, const Task &k, int t, uint4 w, uint32_t least, int rest, int &ups, int &ties) {
     const uint32_t m = look4(k, t, w, least);

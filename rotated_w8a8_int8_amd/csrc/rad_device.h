@@ -107,6 +107,18 @@ __device__ __forceinline__ float wave_max_f32(float v) {
     return fmaxf(fmaxf(r0, r1), fmaxf(r2, r3));
 }
 
+// Inclusive sum over the lanes of a wave: inside rows of 16, then row 0 into 1 and 2 into
+// 3, then rows 0 .. 1 into 2 .. 3.
+__device__ __forceinline__ int wave_scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);     // row_shr 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);    // row_bcast 15
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);    // row_bcast 31
+    return v;
+}
+
 // 4 x int8 dot products of a 16-byte chunk pair, exact int32.
 __device__ __forceinline__ int dot16_i8(v4i a, v4i b, int acc) {
     acc = __builtin_amdgcn_sdot4(a.x, b.x, acc, false);
